@@ -20,7 +20,8 @@ __all__ = [
     "sgemm_device_error", "sgemm_set_wait_limit", "sgemm_release_workspace",
     "sgemm_version", "sgemm_ffma_static_scratch", "sgemm_timing_enable",
     "sgemm_timing_read", "sgemm_launch_count", "sgemm_probe_tf32_rate", "gemm",
-    "exported_symbols",
+    "exported_symbols", "TYPE_F32", "TYPE_BF16", "TYPE_E4M3", "TYPE_E5M2",
+    "sgemm_fp8_quantize", "fp8_quantize",
 ]
 
 SGEMM_OK = 0
@@ -38,6 +39,11 @@ PATH_TF32 = 3
 PATH_GEMV = 4
 ACT_NONE = 0
 ACT_RELU = 1
+
+TYPE_F32 = 0
+TYPE_BF16 = 1
+TYPE_E4M3 = 2
+TYPE_E5M2 = 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libsgemm_gb300.so"
@@ -103,6 +109,8 @@ def _declare(lib):
     lib.sgemm_launch_count.restype = i64
     lib.sgemm_ffma_static_scratch.argtypes = gemm_args + [i32]
     lib.sgemm_ffma_static_scratch.restype = i32
+    lib.sgemm_fp8_quantize.argtypes = [i64, i64, vp, i32, i64, i32, i32, vp, i32, i64, vp, i64, vp]
+    lib.sgemm_fp8_quantize.restype = i32
 
 
 def load():
@@ -127,7 +135,7 @@ def exported_symbols(lib=None):
             "sgemm_status_string", "sgemm_device_error",
             "sgemm_set_wait_limit", "sgemm_release_workspace", "sgemm_version",
             "sgemm_ffma_static_scratch", "sgemm_timing_enable", "sgemm_timing_read",
-            "sgemm_launch_count", "sgemm_probe_tf32_rate"]
+            "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize"]
 
 
 def _b(t: str) -> bytes:
@@ -275,3 +283,77 @@ def gemm(A, B, C, transA="N", transB="N", alpha=1.0, beta=0.0, path=PATH_AUTO, s
     if st != SGEMM_OK:
         raise SgemmError(st)
     return C
+
+
+_types = None
+
+
+def _type_of(dtype):
+    """The library's type code of a torch dtype (None: not one of its types)."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
+                  torch.float8_e4m3fn: TYPE_E4M3, torch.float8_e5m2: TYPE_E5M2}
+    return _types.get(dtype)
+
+
+def _matrix(name, t, types):
+    """(address, type, leading dimension) of a 2-D row-major CUDA tensor."""
+    code = _type_of(t.dtype)
+    if code not in types or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of a type the call takes")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.data_ptr(), code, (ld if rows > 1 and ld > cols else max(cols, 1))
+
+
+def _current_stream(device):
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def sgemm_fp8_quantize(rows, cols, X, x_type, ldx, group_rows, group_cols, Q, q_type, ldq, S, lds,
+                       stream=None) -> int:
+    """Codes Q and scales S of the rows x cols matrix X; device addresses (int)."""
+    return load().sgemm_fp8_quantize(rows, cols, X, x_type, ldx, group_rows, group_cols, Q, q_type,
+                                     ldq, S, lds, _stream(stream))
+
+
+def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
+    """(codes, scales) of a 2-D float32 or bfloat16 CUDA tensor, with one scale for
+    each group of 1 x 128, 128 x 1 or 128 x 128 values.
+
+    Codes are of ``dtype`` (torch.float8_e4m3fn by default, or float8_e5m2);
+    scales are float32, of shape (ceil(cols / 128), rows), (ceil(rows / 128),
+    cols) or (ceil(rows / 128), ceil(cols / 128)).  ``Q`` and ``S`` take
+    buffers to write into.  Asynchronous on ``stream`` (default: torch's current
+    stream on X's device); raises SgemmError on any non-zero status.
+    """
+    import torch
+
+    px, tx, ldx = _matrix("X", X, (TYPE_F32, TYPE_BF16))
+    rows, cols = X.shape
+    gr, gc = group
+    if Q is None:
+        Q = torch.empty((rows, cols), device=X.device, dtype=dtype or torch.float8_e4m3fn)
+    elif Q.shape != X.shape or (dtype is not None and dtype != Q.dtype):
+        raise ValueError("Q must have X's shape and the given dtype")
+    pq, tq, ldq = _matrix("Q", Q, (TYPE_E4M3, TYPE_E5M2))
+    row_blocks, col_blocks = (rows + 127) // 128, (cols + 127) // 128
+    shape = ((col_blocks, rows) if gr == 1 else
+             (row_blocks, cols) if gc == 1 else (row_blocks, col_blocks))
+    if S is None:
+        S = torch.empty(shape, device=X.device, dtype=torch.float32)
+    elif S.shape != shape:
+        raise ValueError(f"S must have shape {shape}")
+    ps, _, lds = _matrix("S", S, (TYPE_F32,))
+    if Q.device != X.device or S.device != X.device:
+        raise ValueError("X, Q and S must be on one device")
+    st = load().sgemm_fp8_quantize(rows, cols, px, tx, ldx, gr, gc, pq, tq, ldq, ps, lds,
+                                   _current_stream(X.device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_fp8_quantize")
+    return Q, S

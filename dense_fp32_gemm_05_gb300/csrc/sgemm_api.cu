@@ -62,7 +62,8 @@ static int device_state(DeviceState **out) {
 
 // Returns a workspace of at least `bytes` private to (device, stream, slot).
 // It is allocated and, when it must grow, freed in stream order on `stream`.
-int workspace(cudaStream_t stream, size_t bytes, void **out, int which) {
+int workspace(cudaStream_t stream, size_t bytes, void **out, int which, bool *fresh) {
+    if (fresh) *fresh = false;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
@@ -77,6 +78,7 @@ int workspace(cudaStream_t stream, size_t bytes, void **out, int which) {
             return SGEMM_ERR_NOMEM;
         }
         slot = {p, want};
+        if (fresh) *fresh = true;
     }
     *out = slot.first;
     return SGEMM_OK;
@@ -114,7 +116,16 @@ void timing_mark(cudaStream_t s, bool begin) {
     }
 }
 
-static int launch_status() {
+int usable_device(int *sms) {
+    DeviceState *d = nullptr;
+    const int st = device_state(&d);
+    if (st != SGEMM_OK) return st;
+    if (!(d->cc_major == 10 && d->cc_minor == 3)) return SGEMM_ERR_UNSUPPORTED;
+    *sms = d->sms;
+    return SGEMM_OK;
+}
+
+int launch_status() {
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) return SGEMM_OK;
     if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction)

@@ -51,13 +51,22 @@ int tc_take_device_error();
 
 // Sets the bounded-wait limit (ns; 0 = default).
 void tc_set_wait_limit(uint64_t ns);
+uint64_t tc_wait_limit();
 
 // Measurement hook: records an event before (begin = true) or after the main
 // kernel launch on `s` when timing is enabled (no-op otherwise).
 void timing_mark(cudaStream_t s, bool begin);
 
 // Library-owned per-(device, stream, slot) workspace, grown on demand.
-int workspace(cudaStream_t stream, size_t bytes, void **out, int which = 0);
+// `fresh`, if given, tells whether this call allocated it.
+int workspace(cudaStream_t stream, size_t bytes, void **out, int which = 0, bool *fresh = nullptr);
+
+// The SM count of the current device; SGEMM_ERR_UNSUPPORTED unless it is of
+// compute capability 10.3.
+int usable_device(int *sms);
+
+// The status of the launch just made.
+int launch_status();
 
 // The whole device-pointer GEMM call (checks, quick returns, selector, launch).
 int gemm_impl(char ta, char tb, int64_t M, int64_t N, int64_t K, float alpha, const float *A,

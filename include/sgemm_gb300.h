@@ -387,6 +387,54 @@ int sgemm_ffma_static_scratch(char transA, char transB, int64_t M, int64_t N, in
 /* Library version, 100*major + minor. */
 int sgemm_version(void);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating point: quantisation.
+ *
+ * A quantised matrix is two arrays: codes (one byte each, E4M3 or E5M2) and
+ * fp32 scales, one for each group of the codes; value = code * scale.  Groups
+ * are 128 long along the dimension that a product sums over:
+ *
+ *   group_rows x group_cols   scale of the element (r, c)
+ *      1 x 128                S[(c / 128) * lds + r]            lds >= rows
+ *    128 x 1                  S[(r / 128) * lds + c]            lds >= cols
+ *    128 x 128                S[(r / 128) * lds + c / 128]      lds >= ceil(cols / 128)
+ *
+ * (the scales of vector groups lie block of the sum after block of the sum,
+ * rows or columns of the result next to each other).  The last group of a
+ * row, column or block may be shorter than 128.
+ */
+typedef enum {
+    SGEMM_TYPE_F32 = 0,
+    SGEMM_TYPE_BF16 = 1,
+    SGEMM_TYPE_E4M3 = 2,   /* 4 exponent, 3 mantissa bits; largest 448, NaN, no infinity */
+    SGEMM_TYPE_E5M2 = 3    /* 5 exponent, 2 mantissa bits; largest 57344, infinity, NaN  */
+} sgemm_type;
+
+/*
+ * sgemm_fp8_quantize - codes and scales of a rows x cols matrix X (row-major,
+ * leading dimension ldx, SGEMM_TYPE_F32 or SGEMM_TYPE_BF16):
+ *
+ *   scale = max(amax / L, 2^-126), amax the largest |x| of the group's finite
+ *           values, L the largest value of q_type
+ *   code  = x * (1 / scale), rounded to nearest even
+ *
+ * each operation in fp32, rounded to nearest.  NaN gives NaN; an infinity
+ * gives infinity in E5M2 and NaN in E4M3; neither enters amax.
+ *
+ *   group_rows, group_cols   (1, 128), (128, 1) or (128, 128)
+ *   Q      codes, row-major, leading dimension ldq >= cols, of q_type
+ *          (SGEMM_TYPE_E4M3 or SGEMM_TYPE_E5M2); a ldq and base that are
+ *          multiples of 16 let sgemm_fp8 read the codes in place
+ *   S      scales, laid out as above with lds
+ *
+ * Any alignment of X's elements, any leading dimensions.  Q and S may not
+ * overlap X.  No workspace.  rows or cols zero: nothing is done.  Returns
+ * SGEMM_OK, a negative argument index or an sgemm_status.
+ */
+int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx,
+                       int group_rows, int group_cols, void *Q, int q_type, int64_t ldq,
+                       float *S, int64_t lds, sgemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,66 @@
+"""Argument checks of the 8-bit entry points (no GPU: every case fails before
+anything is launched), and the plain evaluation that the GPU tests compare
+with, against closed forms."""
+import numpy as np
+import pytest
+
+import dense_fp32_gemm_05_gb300 as sg
+from tests import fp8_plain as fp
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from dense_fp32_gemm_05_gb300 import build
+    build.build()
+    sg.load()
+
+
+P = 1 << 20      # never dereferenced
+F32, BF16, E4M3, E5M2 = sg.TYPE_F32, sg.TYPE_BF16, sg.TYPE_E4M3, sg.TYPE_E5M2
+
+
+@pytest.mark.parametrize("change,want", [
+    ({0: -1}, -1), ({0: 2 ** 31}, -1), ({1: -1}, -2), ({1: 2 ** 31 - 1}, -2), ({2: 0}, -3),
+    ({2: P + 2}, -3), ({3: E4M3}, -4), ({3: 9}, -4), ({4: 255}, -5), ({5: 2}, -6), ({6: 64}, -7),
+    ({5: 1, 6: 1}, -7), ({7: 0}, -8), ({8: F32}, -9), ({9: 255}, -10), ({10: 0}, -11),
+    ({10: P + 1}, -11), ({11: 9}, -12), ({5: 128, 6: 1, 11: 255}, -12), ({5: 128, 11: 1}, -12),
+])
+def test_quantize_refusals(change, want):
+    args = [10, 256, P, F32, 256, 1, 128, P, E4M3, 256, P, 10]
+    for i, v in change.items():
+        args[i] = v
+    assert sg.sgemm_fp8_quantize(*args) == want
+
+
+def test_quantize_of_nothing_is_ok():
+    assert sg.sgemm_fp8_quantize(0, 5, 0, F32, 5, 1, 128, 0, E4M3, 5, 0, 1) == 0
+    assert sg.sgemm_fp8_quantize(5, 0, 0, BF16, 1, 128, 128, 0, E5M2, 1, 0, 1) == 0
+
+
+def test_formats():
+    t = fp.TABLE["e4m3"]
+    assert t[0x7e] == 448.0 and t[0x08] == 2.0 ** -6 and t[0x01] == 2.0 ** -9 and np.isnan(t[0xff])
+    t = fp.TABLE["e5m2"]
+    assert t[0x7b] == 57344.0 and t[0x04] == 2.0 ** -14 and t[0x01] == 2.0 ** -16 and t[0xfc] == -np.inf
+    for f in ("e4m3", "e5m2"):
+        v = fp.TABLE[f]
+        ok = ~np.isnan(v)
+        assert np.array_equal(fp.encode(v[ok], f), np.arange(256, dtype=np.uint8)[ok])
+
+
+def test_formats_agree_with_torch():
+    import torch
+    c = torch.arange(256, dtype=torch.uint8)
+    for f, d in (("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)):
+        assert np.array_equal(c.view(d).float().numpy().astype(np.float64), fp.TABLE[f], equal_nan=True)
+        x = (torch.rand(4000, generator=torch.Generator().manual_seed(3)) - 0.5) * 2 * fp.LARGEST[f]
+        assert np.array_equal(x.to(d).view(torch.uint8).numpy(), fp.encode(x.numpy(), f))
+
+
+def test_plain_quantize_closed_form():
+    x = np.zeros((2, 130), np.float32)
+    x[0, 0], x[1, 129] = 896.0, -1.75
+    codes, s = fp.quantize(x, (1, 128), "e4m3")
+    assert s.shape == (2, 2) and s[0, 0] == 2.0 and s[1, 1] == np.float32(1.75) / np.float32(448)
+    assert s[0, 1] == s[1, 0] == np.float32(2.0 ** -126)
+    assert codes[0, 0] == 0x7e and codes[1, 129] == 0xfe and not codes[0, 1:].any()
