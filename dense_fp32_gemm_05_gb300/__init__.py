@@ -21,7 +21,7 @@ __all__ = [
     "sgemm_version", "sgemm_ffma_static_scratch", "sgemm_timing_enable",
     "sgemm_timing_read", "sgemm_launch_count", "sgemm_probe_tf32_rate", "gemm",
     "exported_symbols", "TYPE_F32", "TYPE_BF16", "TYPE_E4M3", "TYPE_E5M2",
-    "sgemm_fp8_quantize", "fp8_quantize",
+    "sgemm_fp8_quantize", "fp8_quantize", "sgemm_fp8", "sgemm_fp8_plan", "fp8_gemm",
 ]
 
 SGEMM_OK = 0
@@ -111,6 +111,11 @@ def _declare(lib):
     lib.sgemm_ffma_static_scratch.restype = i32
     lib.sgemm_fp8_quantize.argtypes = [i64, i64, vp, i32, i64, i32, i32, vp, i32, i64, vp, i64, vp]
     lib.sgemm_fp8_quantize.restype = i32
+    lib.sgemm_fp8.argtypes = [c, c, i64, i64, i64, f32, vp, i32, i64, vp, i32, i64, vp, i32, i64, vp,
+                              i32, i64, f32, vp, i32, i64, vp]
+    lib.sgemm_fp8.restype = i32
+    lib.sgemm_fp8_plan.argtypes = [i64, i64, i64, i32, ip, ip, ip]
+    lib.sgemm_fp8_plan.restype = i32
 
 
 def load():
@@ -135,7 +140,8 @@ def exported_symbols(lib=None):
             "sgemm_status_string", "sgemm_device_error",
             "sgemm_set_wait_limit", "sgemm_release_workspace", "sgemm_version",
             "sgemm_ffma_static_scratch", "sgemm_timing_enable", "sgemm_timing_read",
-            "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize"]
+            "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize",
+            "sgemm_fp8", "sgemm_fp8_plan"]
 
 
 def _b(t: str) -> bytes:
@@ -357,3 +363,59 @@ def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_fp8_quantize")
     return Q, S
+
+
+def sgemm_fp8(transA, transB, M, N, K, alpha, A, a_type, lda, SA, a_group, ldsa, B, b_type, ldb, SB,
+              b_group, ldsb, beta, C, c_type, ldc, stream=None) -> int:
+    """C = alpha*op(A)*op(B) + beta*C with quantised A and B; device addresses (int)."""
+    return load().sgemm_fp8(_b(transA), _b(transB), M, N, K, alpha, A, a_type, lda, SA, a_group, ldsa,
+                            B, b_type, ldb, SB, b_group, ldsb, beta, C, c_type, ldc, _stream(stream))
+
+
+def sgemm_fp8_plan(M, N, K, num_sms=152):
+    """The 8-bit product's tile and cluster size, without a GPU: (status, dict)."""
+    outs = [ctypes.c_int(0) for _ in range(3)]
+    st = load().sgemm_fp8_plan(M, N, K, num_sms, *[ctypes.byref(o) for o in outs])
+    return st, {k: o.value for k, o in zip(("tile_m", "tile_n", "ksplit"), outs)}
+
+
+def fp8_gemm(A, SA, B, SB, C, transA="N", transB="T", alpha=1.0, beta=0.0, a_group=1, b_group=128,
+             stream=None):
+    """C = alpha*op(A)*op(B) + beta*C of quantised operands; C is updated in place and returned.
+
+    A and B are 2-D CUDA tensors of codes (float8_e4m3fn or float8_e5m2) holding the
+    STORED arrays, SA and SB their float32 scales as ``fp8_quantize`` lays them
+    out; C is float32 or bfloat16.  ``a_group`` 1: A has a scale for each row of
+    op(A) and 128 of the sum (groups of 1 x 128 for transA 'N', 128 x 1 for 'T');
+    128: for each 128 x 128 block.  ``b_group`` likewise.  A linear layer's forward
+    product is the default layout, x (1 x 128) times W^T (128 x 128 blocks).
+    Asynchronous on ``stream`` (default: torch's current stream on C's device);
+    raises SgemmError on any non-zero status.
+    """
+    pa, a_type, lda = _matrix("A", A, (TYPE_E4M3, TYPE_E5M2))
+    pb, b_type, ldb = _matrix("B", B, (TYPE_E4M3, TYPE_E5M2))
+    pc, c_type, ldc = _matrix("C", C, (TYPE_F32, TYPE_BF16))
+    psa, _, ldsa = _matrix("SA", SA, (TYPE_F32,))
+    psb, _, ldsb = _matrix("SB", SB, (TYPE_F32,))
+    ta, tb = transA.upper(), transB.upper()
+    M, N = C.shape
+    K = A.shape[1] if ta == "N" else A.shape[0]
+    kb = (K + 127) // 128
+    if A.shape != ((M, K) if ta == "N" else (K, M)) or B.shape != ((K, N) if tb == "N" else (N, K)):
+        raise ValueError("the shapes of A, B and C do not fit together")
+
+    def blocks(t):
+        return ((t.shape[0] + 127) // 128, (t.shape[1] + 127) // 128)
+
+    if SA.shape != ((kb, M) if a_group == 1 else blocks(A)) or \
+            SB.shape != ((kb, N) if b_group == 1 else blocks(B)):
+        raise ValueError("the scales' shapes do not fit the operands and their groups")
+    device = C.device
+    if not (A.device == B.device == SA.device == SB.device == device):
+        raise ValueError("the operands must be on one device")
+    st = load().sgemm_fp8(ta.encode(), tb.encode(), M, N, K, alpha, pa, a_type, lda, psa, a_group, ldsa,
+                          pb, b_type, ldb, psb, b_group, ldsb, beta, pc, c_type, ldc,
+                          _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_fp8")
+    return C

@@ -1,0 +1,678 @@
+// Matrix product of two quantised operands (8-bit codes, one fp32 scale for
+// each group of 128 along the sum):
+//
+//   C(m,n) = alpha * sum_b sA(m,b) sB(b,n) P_b(m,n) + beta * C(m,n),
+//   P_b(m,n) = sum over the 128 k of block b of A(m,k) B(k,n)
+//
+// P_b is what tcgen05.mma kind::f8f6f4 adds up in tensor memory (products of
+// codes are exact in fp32); the scales differ from block to block, so each
+// P_b is brought into registers once and added there with its scales.
+//
+// Orientation: the MMA's M (tensor-memory lanes) is the result's N, its N
+// (columns) is the result's M.  A warp then holds 32 neighbouring columns of C
+// for each row m, so that C is stored straight from registers, whole sectors
+// at a time; and few rows (decode) become a narrow MMA, BY = 16 .. 128 columns,
+// against 128 rows of the weights.
+//
+// Kernel (352 threads; one CTA per SM):
+//   warp 0      TMA producer: per block of 128 k one 128 x 128 tile of B (the
+//               "X" operand) and a BY x 128 tile of A ("Y") into a ring of
+//               stages.  Either operand may be stored along k or across it
+//               (MN-major descriptors read the tile as it lies);
+//   warp 1      tensor memory, and one lane that issues the 4 MMAs of a block
+//               into one of two buffers of BY columns;
+//   warp 2      the block's scales, sA(m,b) for each column (times sB where
+//               that is one value for the CTA's 128 rows), in a small ring;
+//   warps 3-10  add a block's P_b to the accumulators: tcgen05.ld, then one
+//               fused multiply-add for each value (two where both operands
+//               have a scale for each row).  128 x BY fp32 accumulators live in
+//               their registers: warp w has lanes 32 (w % 4) .. + 31 and half
+//               of the columns.  They release the buffer as soon as it is read.
+// Each CTA walks tiles of C (grouped raster), the rings run on across tiles.
+//
+// Few tiles: a cluster of KS CTAs shares a tile's blocks in contiguous ranges
+// and adds the partial sums through distributed shared memory in ascending
+// order, each CTA its share of the columns: no workspace, no atomics.
+//
+// Every wait is bounded, as in the tensor-core GEMM: on expiry the device error
+// word is set, the role stops, copies and MMAs in flight are waited for (again
+// bounded) and the CTA frees its tensor memory and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "fp8.cuh"
+#include "fp8_plan.h"
+#include "plan.h"
+#include "ptx_util.cuh"
+#include "tc_gemm.h"
+#include "tc_ptx.cuh"
+
+namespace sgemm_gb300 {
+namespace fp8g {
+
+using namespace tc;
+
+constexpr int BX = 128;                    // rows of X (columns of C) per CTA
+constexpr int BK = fp8::GROUP;             // k per block
+constexpr int X_BYTES = BX * BK;
+constexpr int PROMOTERS = 8;               // warps 3..10
+constexpr int THREADS = 32 * (3 + PROMOTERS);
+constexpr int MAX_STAGES = 12;
+constexpr int SCALE_SLOTS = 4;
+constexpr int SMEM_MAX = 232448;           // opt-in dynamic shared memory per block
+constexpr int BAR_BYTES = 512;
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+__device__ unsigned int g_error;           // sticky device error word of this path
+
+struct Params {
+    void *C;
+    int64_t ldc;
+    int c_bf16;
+    int M, N;
+    float alpha, beta;
+    const float *SX, *SY;                  // scales of B (X) and A (Y)
+    int64_t x_mn, x_k, y_mn, y_k;          // strides of the scales along N / M (per group) and per block of k
+    int y_shift;                           // a scale of A for each 1 << y_shift rows
+    int x_mnmajor, y_mnmajor;              // operand stored across k
+    int y_bytes;                           // bytes of Y per stage
+    uint32_t idesc;
+    int tiles_x, tiles_y, group_y;
+    int nkb;                               // blocks of 128 k
+    int stages, ksplit;
+    unsigned long long wait_ns;
+};
+
+// Tile u of the grouped raster: group_y tile rows of C at a time, so that the
+// tiles in flight share operand panels in L2.
+__device__ __forceinline__ void tile_of(const Params &p, int u, int &tx, int &ty) {
+    const int per = p.group_y * p.tiles_x;
+    const int g = u / per, r = u - g * per;
+    const int h = min(p.group_y, p.tiles_y - g * p.group_y);
+    tx = r / h;
+    ty = g * p.group_y + (r - tx * h);
+}
+
+__device__ __forceinline__ float load_c(const Params &p, int64_t at) {
+    return p.c_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.C)[at])
+                    : static_cast<const float *>(p.C)[at];
+}
+
+// alpha * acc, or fma(alpha, acc, beta * c), rounded once to C's type
+__device__ __forceinline__ void store_c(const Params &p, int m, int n, float acc) {
+    const int64_t at = (int64_t)m * p.ldc + n;
+    const float v = p.beta == 0.0f ? __fmul_rn(p.alpha, acc)
+                                   : __fmaf_rn(p.alpha, acc, __fmul_rn(p.beta, load_c(p, at)));
+    if (p.c_bf16) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
+    else static_cast<float *>(p.C)[at] = v;
+}
+
+// A CTA's own address of `local` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// BY: columns of the MMA (rows of C) per tile.  XVEC: B has a scale for each
+// of its rows (else one for the CTA's 128).
+template <int BY, bool XVEC>
+__global__ void __launch_bounds__(THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+                    const Params p) {
+    constexpr int PC = BY / 2;                     // columns per promoting thread
+    constexpr int CH = PC < 16 ? PC : 16;          // columns per tensor-memory load
+    constexpr uint32_t COLS = 2 * BY < 32 ? 32 : 2 * BY;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int stage_bytes = X_BYTES + p.y_bytes;
+    const uint32_t smem0 = smem_u32(smem);
+    float *scales = reinterpret_cast<float *>(smem + p.stages * stage_bytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + SCALE_SLOTS * BY);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * MAX_STAGES + 4 + 2 * SCALE_SLOTS);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+    auto tfull = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + b); };
+    auto tempty = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
+    auto sfull = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + 4 + s); };
+    auto sempty = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + 4 + SCALE_SLOTS + s); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ks = p.ksplit;
+    const int rank = ks > 1 ? (int)cluster_rank() : 0;
+    const int group = (int)blockIdx.x / ks, groups = (int)gridDim.x / ks;
+    const int kb0 = (int)((int64_t)p.nkb * rank / ks), kb1 = (int)((int64_t)p.nkb * (rank + 1) / ks);
+    const int units = p.tiles_x * p.tiles_y;
+    const uint64_t lim = p.wait_ns;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), PROMOTERS);
+        }
+        for (int s = 0; s < SCALE_SLOTS; ++s) {
+            mbar_init(sfull(s), 1);
+            mbar_init(sempty(s), PROMOTERS);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&tm_x);
+        prefetch_map(&tm_y);
+    }
+    if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();                                    // a copy of an operand may precede this kernel
+
+    float2 acc[PC / 2];
+    bool ok = true;
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int s = 0, filled = 0;
+            uint32_t ph = 1;                       // an empty stage's first wait passes
+            for (int u = group; ok && u < units; u += groups) {
+                int tx, ty;
+                tile_of(p, u, tx, ty);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_for(empty(s), ph, lim, &g_error)) { ok = false; break; }
+                    const uint32_t x = smem0 + (uint32_t)(s * stage_bytes), y = x + X_BYTES;
+                    mbar_expect_tx(full(s), (uint32_t)stage_bytes);
+                    if (p.x_mnmajor) tma_load_2d(x, &tm_x, full(s), tx * BX, kb * BK);
+                    else tma_load_2d(x, &tm_x, full(s), kb * BK, tx * BX);
+                    if (p.y_mnmajor) {
+                        tma_load_2d(y, &tm_y, full(s), ty * BY, kb * BK);
+                        if (BY > 128) tma_load_2d(y + X_BYTES, &tm_y, full(s), ty * BY + 128, kb * BK);
+                    } else {
+                        tma_load_2d(y, &tm_y, full(s), kb * BK, ty * BY);
+                    }
+                    ++filled;
+                    if (++s == p.stages) { s = 0; ph ^= 1; }
+                }
+            }
+            // copies in flight land before the CTA's shared memory goes (on an
+            // early stop nobody else has waited for them)
+            for (int i = 0; i < min(filled, p.stages); ++i) {
+                if (s == 0) { s = p.stages; ph ^= 1; }
+                --s;
+                mbar_wait_for(full(s), ph ^ 1u, kDrainNs, &g_error);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int s = 0, b = 0, issued = 0;
+            uint32_t ph = 0, bph = 1;
+            const uint32_t x_step = p.x_mnmajor ? 4096u >> 4 : 32u >> 4;
+            const uint32_t y_step = p.y_mnmajor ? 4096u >> 4 : 32u >> 4;
+            for (int u = group; ok && u < units; u += groups) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait_for(tempty(b), bph, lim, &g_error) ||
+                        !mbar_wait_for(full(s), ph, lim, &g_error)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t x = smem0 + (uint32_t)(s * stage_bytes), y = x + X_BYTES;
+                    const uint64_t dx = smem_desc_8bit(x, X_BYTES), dy = smem_desc_8bit(y, X_BYTES);
+                    const uint32_t d = tmem + (uint32_t)(b * BY);
+#pragma unroll
+                    for (int i = 0; i < BK / 32; ++i)
+                        umma_8bit<false>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
+                    umma_commit(empty(s));
+                    umma_commit(tfull(b));
+                    ++issued;
+                    if (++s == p.stages) { s = 0; ph ^= 1; }
+                    if (++b == 2) { b = 0; bph ^= 1; }
+                }
+            }
+            // MMAs retire before tensor memory is freed
+            if (issued > 0) {
+                const int last = (issued - 1) & 1;
+                mbar_wait_for(tfull(last), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ scales
+        constexpr int J = (BY + 31) / 32;          // columns per lane
+        constexpr int AHEAD = 4;                   // blocks loaded at a time
+        int slot = 0;
+        uint32_t ph = 1;
+        for (int u = group; ok && u < units; u += groups) {
+            int tx, ty;
+            tile_of(p, u, tx, ty);
+            const float *sx = XVEC ? nullptr : p.SX + (int64_t)tx * p.x_mn;   // BX = the block's width
+            float v[AHEAD][J], w[AHEAD];
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const bool in = kb + a < kb1;
+                    w[a] = !XVEC && in ? __ldg(sx + (int64_t)(kb + a) * p.x_k) : 1.0f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const int m = ty * BY + 32 * j + lane;
+                        v[a][j] = in && m < p.M && 32 * j + lane < BY
+                                      ? __ldg(p.SY + (int64_t)(m >> p.y_shift) * p.y_mn + (int64_t)(kb + a) * p.y_k)
+                                      : 0.0f;
+                    }
+                }
+            };
+            fetch(kb0);
+            for (int kb = kb0; ok && kb < kb1; kb += AHEAD) {
+                float t[AHEAD][J];
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+                    for (int j = 0; j < J; ++j) t[a][j] = XVEC ? v[a][j] : __fmul_rn(v[a][j], w[a]);
+                fetch(kb + AHEAD);
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    if (kb + a >= kb1) break;
+                    if (!mbar_wait_for(sempty(slot), ph, lim, &g_error)) { ok = false; break; }
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+                        if (32 * j + lane < BY) scales[slot * BY + 32 * j + lane] = t[a][j];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sfull(slot));
+                    if (++slot == SCALE_SLOTS) { slot = 0; ph ^= 1; }
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ promotion and epilogue
+        const int q = warp & 3, half = (warp - 3) >> 2;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
+        int b = 0, slot = 0;
+        uint32_t bph = 0, sph = 0;
+        for (int u = group; ok && u < units; u += groups) {
+            int tx, ty;
+            tile_of(p, u, tx, ty);
+            const int n = tx * BX + q * 32 + lane;
+            const float *sx = p.SX + (XVEC ? (int64_t)min(n, p.N - 1) : 0);
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            float sx_next = XVEC ? __ldg(sx + (int64_t)kb0 * p.x_k) : 0.0f;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const float2 sx2 = make_float2(sx_next, sx_next);
+                if (XVEC && kb + 1 < kb1) sx_next = __ldg(sx + (int64_t)(kb + 1) * p.x_k);
+                ok = mbar_wait_for(sfull(slot), sph, lim, &g_error) &&
+                     mbar_wait_for(tfull(b), bph, lim, &g_error);
+                if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                tc_fence_after();
+                const float *sc = scales + slot * BY + half * PC;
+                uint32_t r[2][CH];
+                tmem_ld_async(taddr + (uint32_t)(b * BY), r[0]);
+#pragma unroll
+                for (int c = 0; c < PC / CH; ++c) {
+                    tmem_ld_wait(r[c & 1]);
+                    if (c + 1 < PC / CH) {
+                        tmem_ld_async(taddr + (uint32_t)(b * BY + (c + 1) * CH), r[(c + 1) & 1]);
+                    } else {                       // the buffer is read: hand it back
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tempty(b));
+                    }
+#pragma unroll
+                    for (int i = 0; i < CH; i += 4) {
+                        const float4 s4 = *reinterpret_cast<const float4 *>(sc + c * CH + i);
+                        float2 t0 = make_float2(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1]));
+                        float2 t1 = make_float2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
+                        float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
+                        if (XVEC) {
+                            t0 = __fmul2_rn(t0, make_float2(s4.x, s4.y));
+                            t1 = __fmul2_rn(t1, make_float2(s4.z, s4.w));
+                            a0 = __ffma2_rn(t0, sx2, a0);
+                            a1 = __ffma2_rn(t1, sx2, a1);
+                        } else {
+                            a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
+                            a1 = __ffma2_rn(t1, make_float2(s4.z, s4.w), a1);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty(slot));
+                if (++slot == SCALE_SLOTS) { slot = 0; sph ^= 1; }
+                if (++b == 2) { b = 0; bph ^= 1; }
+            }
+            if (!ok || ks > 1) break;
+            if (n < p.N) {
+                const int m0 = ty * BY + half * PC;
+#pragma unroll
+                for (int i = 0; i < PC / 2; ++i) {
+                    if (m0 + 2 * i < p.M) store_c(p, m0 + 2 * i, n, acc[i].x);
+                    if (m0 + 2 * i + 1 < p.M) store_c(p, m0 + 2 * i + 1, n, acc[i].y);
+                }
+            }
+        }
+    }
+
+    if (ks > 1) {
+        // every MMA of this CTA has completed (the promoters saw the last one),
+        // so its stages hold the partial sums now: [column][128 rows of X]
+        float *part = reinterpret_cast<float *>(smem);
+        const int q = warp & 3, half = (warp - 3) >> 2;
+        __syncthreads();                           // (on an early stop: copies have landed)
+        if (warp >= 3) {
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) {
+                part[(half * PC + 2 * i) * BX + q * 32 + lane] = acc[i].x;
+                part[(half * PC + 2 * i + 1) * BX + q * 32 + lane] = acc[i].y;
+            }
+        }
+        cluster_sync_all();
+        if (warp >= 3) {
+            int tx, ty;
+            tile_of(p, group, tx, ty);
+            const int n = tx * BX + q * 32 + lane;
+            const int c1 = BY * (rank + 1) / ks;
+            for (int c = BY * rank / ks + half; c < c1; c += 2) {
+                const int m = ty * BY + c;
+                if (m >= p.M) break;
+                const uint32_t at = smem0 + 4u * (uint32_t)(c * BX + q * 32 + lane);
+                float sum = 0.0f;
+                for (int r = 0; r < ks; ++r) sum = __fadd_rn(sum, load_cluster(peer_addr(at, (uint32_t)r)));
+                if (n < p.N) store_c(p, m, n, sum);
+            }
+        }
+        cluster_sync_all();                        // no CTA leaves while a peer reads its sums
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<false>(tmem, COLS);
+    }
+}
+
+// C = beta * C (no product term)
+__global__ void __launch_bounds__(256) scale_kernel(const Params p) {
+    const int64_t total = (int64_t)p.M * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = i / p.N * p.ldc + i % p.N;
+        const float v = p.beta == 0.0f ? 0.0f : __fmul_rn(p.beta, load_c(p, at));
+        if (p.c_bf16) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
+        else static_cast<float *>(p.C)[at] = v;
+    }
+}
+
+// Rows of bytes to rows that start on 16 bytes (what a TMA map asks for); one
+// operand for blockIdx.y == 0, the other for 1.
+struct CopyJob {
+    const uint8_t *src;
+    uint8_t *dst;
+    int64_t ld_src, ld_dst;
+    int rows, cols;
+};
+__global__ void __launch_bounds__(256) align_rows_kernel(const CopyJob j0, const CopyJob j1) {
+    const CopyJob j = blockIdx.y == 0 ? j0 : j1;
+    const int per_row = (j.cols + 15) / 16;
+    const int64_t total = (int64_t)j.rows * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row;
+        const int c = (int)(i - row * per_row) * 16;
+        const uint8_t *src = j.src + row * j.ld_src + c;
+        uint32_t w[4];
+        if (c >= 4 && c + 20 <= j.cols) {
+            // five aligned words of this row hold the 16 bytes
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 3);
+            const uint32_t *a = reinterpret_cast<const uint32_t *>(src - off);
+            uint32_t v[5];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __ldg(a + k);
+            v[4] = off ? __ldg(a + 4) : 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(v[k], v[k + 1], 8 * off);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (c + 4 * k + b < j.cols) w[k] |= (uint32_t)src[4 * k + b] << (8 * b);
+            }
+        }
+        *reinterpret_cast<uint4 *>(j.dst + row * j.ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+}  // namespace fp8g
+
+// ---------------------------------------------------------------- host side
+int fp8_take_device_error() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, fp8g::g_error, sizeof(v)) != cudaSuccess) return SGEMM_ERR_CUDA;
+    if (v != 0 && cudaMemcpyToSymbol(fp8g::g_error, &zero, sizeof(zero)) != cudaSuccess)
+        return SGEMM_ERR_CUDA;
+    return v == 0 ? SGEMM_OK : (int)v;
+}
+
+// A row-major array of bytes, `rows` x `cols`, in boxes of box_rows x 128 bytes
+// with the 128-byte swizzle; outside reads as zeros.
+static bool byte_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BY, bool XVEC>
+static int launch_fp8(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
+                      int smem, cudaStream_t s, bool dep) {
+    auto kern = fp8g::fp8_gemm_kernel<BY, XVEC>;
+    static uint64_t attr_done = 0;   // bit d: the shared-memory opt-in is set on device d
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8g::SMEM_MAX) !=
+            cudaSuccess)
+            return launch_status();
+        __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(fp8g::THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (p.ksplit > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)p.ksplit;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (dep) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    timing_mark(s, true);
+    count_launch();
+    cudaLaunchKernelEx(&cfg, kern, mx, my, p);
+    timing_mark(s, false);
+    return launch_status();
+}
+
+template <int BY>
+static int launch_fp8(bool xvec, const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p,
+                      int grid, int smem, cudaStream_t s, bool dep) {
+    return xvec ? launch_fp8<BY, true>(mx, my, p, grid, smem, s, dep)
+                : launch_fp8<BY, false>(mx, my, p, grid, smem, s, dep);
+}
+
+static int run_fp8(char ta, char tb, int64_t M, int64_t N, int64_t K, float alpha, const void *A,
+                   int a_type, int64_t lda, const float *SA, int a_group, int64_t ldsa, const void *B,
+                   int b_type, int64_t ldb, const float *SB, int b_group, int64_t ldsb, float beta,
+                   void *C, int c_type, int64_t ldc, cudaStream_t s) {
+    int sms = 0;
+    int st = usable_device(&sms);
+    if (st != SGEMM_OK) return st;
+    fp8g::Params p{};
+    p.C = C; p.ldc = ldc; p.c_bf16 = c_type == SGEMM_TYPE_BF16;
+    p.M = (int)M; p.N = (int)N;
+    p.alpha = alpha; p.beta = beta;
+    if (K == 0 || alpha == 0.0f) {
+        if (beta == 1.0f) return SGEMM_OK;
+        const int64_t blocks = std::min<int64_t>((M * N + 255) / 256, (int64_t)sms * 8);
+        count_launch();
+        fp8g::scale_kernel<<<(unsigned)blocks, 256, 0, s>>>(p);
+        return launch_status();
+    }
+    const bool a_mn = !is_notrans(ta), b_mn = is_notrans(tb);
+    const int64_t a_rows = a_mn ? K : M, a_cols = a_mn ? M : K;
+    const int64_t b_rows = b_mn ? K : N, b_cols = b_mn ? N : K;
+    // an operand that TMA cannot read in place is copied with rows on 16 bytes
+    auto in_place = [](const void *q, int64_t ld, int64_t rows) { return aligned16(q) && (ld % 16 == 0 || rows == 1); };
+    auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
+    const bool copy_a = !in_place(A, lda, a_rows), copy_b = !in_place(B, ldb, b_rows);
+    if (copy_a || copy_b) {
+        const int64_t la = up16(a_cols), lb = up16(b_cols);
+        const size_t bytes_a = copy_a ? ((size_t)a_rows * la + 255) / 256 * 256 : 0;
+        const size_t bytes_b = copy_b ? (size_t)b_rows * lb : 0;
+        void *ws = nullptr;
+        st = workspace(s, bytes_a + bytes_b, &ws);
+        if (st != SGEMM_OK) return st;
+        uint8_t *w = static_cast<uint8_t *>(ws);
+        fp8g::CopyJob j[2];
+        int n = 0;
+        int64_t most = 0;
+        if (copy_a) {
+            j[n++] = fp8g::CopyJob{static_cast<const uint8_t *>(A), w, lda, la, (int)a_rows, (int)a_cols};
+            A = w;
+            lda = la;
+            most = a_rows * (la / 16);
+        }
+        if (copy_b) {
+            j[n++] = fp8g::CopyJob{static_cast<const uint8_t *>(B), w + bytes_a, ldb, lb, (int)b_rows, (int)b_cols};
+            B = w + bytes_a;
+            ldb = lb;
+            most = std::max(most, b_rows * (lb / 16));
+        }
+        const unsigned blocks = (unsigned)std::min<int64_t>((most + 255) / 256, (int64_t)sms * 16);
+        count_launch();
+        fp8g::align_rows_kernel<<<dim3(blocks, (unsigned)n), 256, 0, s>>>(j[0], j[n - 1]);
+        st = launch_status();
+        if (st != SGEMM_OK) return st;
+    }
+    // (a single row may have any leading dimension; its map takes a valid one)
+    if (lda % 16 != 0) lda = up16(lda);
+    if (ldb % 16 != 0) ldb = up16(ldb);
+
+    const Fp8Plan pl = fp8_plan(M, N, K, sms);
+    const bool xvec = b_group == 1;
+    p.SX = SB; p.SY = SA;
+    p.x_mn = b_group == 1 || b_mn ? 1 : ldsb;      // blocks of B stored N x K: row by row
+    p.x_k = b_group == 1 || b_mn ? ldsb : 1;
+    p.y_mn = a_group == 1 || a_mn ? 1 : ldsa;
+    p.y_k = a_group == 1 || a_mn ? ldsa : 1;
+    p.y_shift = a_group == 1 ? 0 : 7;
+    p.x_mnmajor = b_mn; p.y_mnmajor = a_mn;
+    p.tiles_x = (int)((N + fp8g::BX - 1) / fp8g::BX);
+    p.tiles_y = (int)((M + pl.by - 1) / pl.by);
+    p.group_y = 16;
+    p.nkb = (int)fp8::blocks_of(K);
+    p.ksplit = pl.ksplit;
+    p.y_bytes = a_mn ? (pl.by + 127) / 128 * fp8g::X_BYTES : pl.by * fp8g::BK;
+    const int fixed = 1024 + fp8g::SCALE_SLOTS * pl.by * 4 + fp8g::BAR_BYTES;
+    p.stages = std::min(fp8g::MAX_STAGES, (fp8g::SMEM_MAX - fixed) / (fp8g::X_BYTES + p.y_bytes));
+    p.idesc = tc::idesc_8bit(b_type == SGEMM_TYPE_E5M2, a_type == SGEMM_TYPE_E5M2, b_mn, a_mn, fp8g::BX, pl.by);
+    p.wait_ns = tc_wait_limit();
+    CUtensorMap mx, my;
+    if (!byte_map(&mx, B, b_rows, b_cols, ldb, 128) ||
+        !byte_map(&my, A, a_rows, a_cols, lda, a_mn ? 128 : pl.by))
+        return SGEMM_ERR_UNSUPPORTED;
+    const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
+    if (tiles > INT32_MAX / 16) return SGEMM_ERR_UNSUPPORTED;
+    const int grid = p.ksplit > 1 ? (int)tiles * p.ksplit : (int)std::min<int64_t>(tiles, sms);
+    const int smem = fixed + p.stages * (fp8g::X_BYTES + p.y_bytes);
+    const bool dep = copy_a || copy_b;
+    switch (pl.by) {
+    case 16: return launch_fp8<16>(xvec, mx, my, p, grid, smem, s, dep);
+    case 32: return launch_fp8<32>(xvec, mx, my, p, grid, smem, s, dep);
+    case 64: return launch_fp8<64>(xvec, mx, my, p, grid, smem, s, dep);
+    case 128: return launch_fp8<128>(xvec, mx, my, p, grid, smem, s, dep);
+    default: return launch_fp8<256>(xvec, mx, my, p, grid, smem, s, dep);
+    }
+}
+
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+extern "C" int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha,
+                         const void *A, int a_type, int64_t lda, const float *SA, int a_group,
+                         int64_t ldsa, const void *B, int b_type, int64_t ldb, const float *SB,
+                         int b_group, int64_t ldsb, float beta, void *C, int c_type, int64_t ldc,
+                         sgemm_stream_t stream) {
+    const int64_t lim = INT32_MAX - 255;           // tiles are rounded up in int
+    if (!is_notrans(transA) && !is_trans(transA)) return -1;
+    if (!is_notrans(transB) && !is_trans(transB)) return -2;
+    if (M < 0 || M > lim) return -3;
+    if (N < 0 || N > lim) return -4;
+    if (K < 0 || K > lim) return -5;
+    const bool an = is_notrans(transA), bn = is_notrans(transB);
+    const bool need = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    auto scales_row = [&](int group, int64_t mn, int64_t stored_cols) {
+        return std::max<int64_t>(1, group == 1 ? mn : fp8::blocks_of(stored_cols));
+    };
+    if (need && A == nullptr) return -7;
+    if (!fp8::is_code_type(a_type)) return -8;
+    if (lda < std::max<int64_t>(1, an ? K : M)) return -9;
+    if (need && (SA == nullptr || reinterpret_cast<uintptr_t>(SA) % 4 != 0)) return -10;
+    if (a_group != 1 && a_group != fp8::GROUP) return -11;
+    if (ldsa < scales_row(a_group, M, an ? K : M)) return -12;
+    if (need && B == nullptr) return -13;
+    if (!fp8::is_code_type(b_type)) return -14;
+    if (ldb < std::max<int64_t>(1, bn ? N : K)) return -15;
+    if (need && (SB == nullptr || reinterpret_cast<uintptr_t>(SB) % 4 != 0)) return -16;
+    if (b_group != 1 && b_group != fp8::GROUP) return -17;
+    if (ldsb < scales_row(b_group, N, bn ? N : K)) return -18;
+    if (!fp8::is_float_type(c_type)) return -21;
+    if (M > 0 && N > 0 && (C == nullptr || reinterpret_cast<uintptr_t>(C) % (c_type == SGEMM_TYPE_F32 ? 4 : 2) != 0))
+        return -20;
+    if (ldc < std::max<int64_t>(1, N)) return -22;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    try {
+        return run_fp8(transA, transB, M, N, K, alpha, A, a_type, lda, SA, a_group, ldsa, B, b_type, ldb,
+                       SB, b_group, ldsb, beta, C, c_type, ldc, reinterpret_cast<cudaStream_t>(stream));
+    } catch (const std::bad_alloc &) {
+        return SGEMM_ERR_NOMEM;
+    }
+}
+
+extern "C" int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int *out_tile_m,
+                              int *out_tile_n, int *out_ksplit) {
+    if (M < 1 || M > INT32_MAX - 255) return -1;
+    if (N < 1 || N > INT32_MAX - 255) return -2;
+    if (K < 1 || K > INT32_MAX - 255) return -3;
+    if (num_sms <= 0) return -4;
+    const Fp8Plan pl = fp8_plan(M, N, K, num_sms);
+    if (out_tile_m) *out_tile_m = pl.by;
+    if (out_tile_n) *out_tile_n = 128;
+    if (out_ksplit) *out_ksplit = pl.ksplit;
+    return SGEMM_OK;
+}

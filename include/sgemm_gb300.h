@@ -388,7 +388,8 @@ int sgemm_ffma_static_scratch(char transA, char transB, int64_t M, int64_t N, in
 int sgemm_version(void);
 
 /* ------------------------------------------------------------------------
- * 8-bit floating point: quantisation.
+ * 8-bit floating point: quantisation and the matrix product of two quantised
+ * operands.
  *
  * A quantised matrix is two arrays: codes (one byte each, E4M3 or E5M2) and
  * fp32 scales, one for each group of the codes; value = code * scale.  Groups
@@ -434,6 +435,55 @@ typedef enum {
 int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx,
                        int group_rows, int group_cols, void *Q, int q_type, int64_t ldq,
                        float *S, int64_t lds, sgemm_stream_t stream);
+
+/*
+ * sgemm_fp8 - C = alpha * op(A) * op(B) + beta * C with quantised A and B:
+ *
+ *   C(i,j) = alpha * sum_b sA(i,b) sB(b,j) (sum_{k in block b} A(i,k) B(k,j)) + beta * C(i,j)
+ *
+ * over the blocks b of 128 of the sum.  Storage and the two trans flags as
+ * sgemm; A and B hold codes of a_type and b_type (SGEMM_TYPE_E4M3 or
+ * SGEMM_TYPE_E5M2, which may differ), C is SGEMM_TYPE_F32 or SGEMM_TYPE_BF16.
+ *
+ *   a_group  1: one scale for each row of op(A) and block of the sum:
+ *               sA(i,b) = SA[b * ldsa + i], ldsa >= M
+ *          128: one for each 128 x 128 block of A AS STORED:
+ *               SA[(row / 128) * ldsa + col / 128], ldsa >= ceil(columns of A / 128)
+ *   b_group  the same for the columns of op(B): SB[b * ldsb + j], ldsb >= N, or
+ *            the blocks of B as stored
+ *
+ * so what sgemm_fp8_quantize writes is taken as it is: 1 x 128 groups for an
+ * operand whose rows run along the sum (A 'N', B 'T'), 128 x 1 for the
+ * others (A 'T', B 'N'), 128 x 128 for either.  A linear layer y = x W^T and
+ * its gradients dx = dy W, dW = dy^T x are the layouts NT, NN and TN.
+ *
+ * Arithmetic: the products of codes are exact and are added in fp32 on the
+ * tensor cores within a block of 128; sA * sB is rounded once (with b_group 1
+ * instead: the block's sum times sA, then a fused multiply-add by sB);
+ * blocks are added in fp32 in ascending order (or, K split over CTAs of a
+ * cluster, in contiguous ranges added in ascending order: no atomics, the
+ * same result every time).  Then alpha * acc (beta == 0: C not read) or
+ * fma(alpha, acc, beta * c), rounded once to C's type.  NaN and infinite
+ * codes give the IEEE result.
+ *
+ * Operands whose base or leading dimension is not a multiple of 16 bytes are
+ * first copied into the library's workspace (per device and stream, as
+ * sgemm's).  K == 0 or alpha == 0: C = beta * C.  Execution, errors and the
+ * bounded waits as sgemm; needs compute capability 10.3.
+ */
+int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha,
+              const void *A, int a_type, int64_t lda, const float *SA, int a_group, int64_t ldsa,
+              const void *B, int b_type, int64_t ldb, const float *SB, int b_group, int64_t ldsb,
+              float beta, void *C, int c_type, int64_t ldc, sgemm_stream_t stream);
+
+/*
+ * sgemm_fp8_plan - how sgemm_fp8 computes an M x N x K problem on a GPU with
+ * num_sms SMs, without touching one: the tile of C and the CTAs of a cluster
+ * that share a tile's sum.  Any output pointer may be NULL.  Returns SGEMM_OK
+ * or a negative argument index.
+ */
+int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int *out_tile_m, int *out_tile_n,
+                   int *out_ksplit);
 
 #ifdef __cplusplus
 }

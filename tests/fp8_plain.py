@@ -75,3 +75,19 @@ def quantize(x, group, fmt):
     with np.errstate(invalid="ignore", over="ignore"):
         y = (x * spread(inv, rows, cols, gr, gc)).astype(np.float32)
     return encode(y, fmt), s
+
+
+def values(codes, s, fmt, group, k_first):
+    """The values of an operand as stored; `k_first`: its rows run across the sum."""
+    rows, cols = codes.shape
+    shape = (128, 128) if group == 128 else ((128, 1) if k_first else (1, 128))
+    return decode(codes, fmt) * spread(np.asarray(s, np.float64), rows, cols, *shape)
+
+
+def product(a, b, alpha=1.0, beta=0.0, c=None):
+    """alpha a b + beta c in 64 bits, and the sum of the terms' magnitudes (for error bounds)."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        out, size = alpha * (a @ b), abs(alpha) * (np.abs(a) @ np.abs(b))
+        if beta != 0:
+            out, size = out + beta * c, size + np.abs(beta * c)
+    return out, size

@@ -64,3 +64,41 @@ def test_plain_quantize_closed_form():
     assert s.shape == (2, 2) and s[0, 0] == 2.0 and s[1, 1] == np.float32(1.75) / np.float32(448)
     assert s[0, 1] == s[1, 0] == np.float32(2.0 ** -126)
     assert codes[0, 0] == 0x7e and codes[1, 129] == 0xfe and not codes[0, 1:].any()
+
+
+@pytest.mark.parametrize("change,want", [
+    ({0: "X"}, -1), ({1: "Q"}, -2), ({2: -1}, -3), ({3: 2 ** 31}, -4), ({4: -1}, -5), ({6: 0}, -7),
+    ({7: F32}, -8), ({8: 299}, -9), ({9: 0}, -10), ({9: P + 2}, -10), ({10: 64}, -11), ({11: 9}, -12),
+    ({10: 128, 11: 2}, -12), ({12: 0}, -13), ({13: BF16}, -14), ({14: 299}, -15), ({15: 0}, -16),
+    ({16: 2}, -17), ({17: 2}, -18), ({16: 1, 17: 19}, -18), ({19: 0}, -20), ({19: P + 1}, -20),
+    ({20: E4M3}, -21), ({21: 19}, -22), ({0: "T", 8: 9}, -9), ({1: "N", 14: 19}, -15),
+])
+def test_product_refusals(change, want):
+    args = ["N", "T", 10, 20, 300, 1.0, P, E4M3, 300, P, 1, 10, P, E5M2, 300, P, 128, 3, 0.0, P, F32, 20]
+    for i, v in change.items():
+        args[i] = v
+    assert sg.sgemm_fp8(*args) == want
+
+
+def test_product_of_nothing_is_ok():
+    assert sg.sgemm_fp8("N", "T", 0, 20, 300, 1.0, 0, E4M3, 300, 0, 1, 1, 0, E4M3, 300, 0, 128, 3, 0.0, 0,
+                        F32, 20) == 0
+
+
+def test_product_plan_covers_every_shape():
+    rng = np.random.default_rng(0)
+    for _ in range(2000):
+        M, N, K = (int(np.exp(rng.uniform(0, np.log(20000)))) for _ in range(3))
+        st, p = sg.sgemm_fp8_plan(M, N, K)
+        nkb = -(-K // 128)
+        assert st == 0 and p["tile_m"] in (16, 32, 64, 128, 256) and 1 <= p["ksplit"] <= min(8, nkb)
+    for args, want in (((0, 1, 1), -1), ((1, 0, 1), -2), ((1, 1, 0), -3), ((1, 1, 1, 0), -4)):
+        assert sg.sgemm_fp8_plan(*args)[0] == want
+
+
+def test_plain_product_closed_form():
+    ones = np.full((3, 256), fp.encode(np.ones(1), "e4m3")[0])
+    s = np.array([[2.0, 3.0, 4.0], [0.5, 0.25, 1.0]], np.float32)      # two blocks, three rows
+    v = fp.values(ones, s, "e4m3", 1, False)
+    out, size = fp.product(v, np.ones((256, 1)))
+    assert out[:, 0].tolist() == [128 * 2.5, 128 * 3.25, 128 * 5.0] and np.array_equal(out, size)
