@@ -22,6 +22,7 @@ __all__ = [
     "sgemm_timing_read", "sgemm_launch_count", "sgemm_probe_tf32_rate", "gemm",
     "exported_symbols", "TYPE_F32", "TYPE_BF16", "TYPE_E4M3", "TYPE_E5M2",
     "sgemm_fp8_quantize", "fp8_quantize", "sgemm_fp8", "sgemm_fp8_plan", "fp8_gemm",
+    "sgemm_moe", "moe",
 ]
 
 SGEMM_OK = 0
@@ -116,6 +117,9 @@ def _declare(lib):
     lib.sgemm_fp8.restype = i32
     lib.sgemm_fp8_plan.argtypes = [i64, i64, i64, i32, ip, ip, ip]
     lib.sgemm_fp8_plan.restype = i32
+    lib.sgemm_moe.argtypes = [i64, i64, i64, i64, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64,
+                              vp, vp, i64, i64, i32, vp, i64, vp, vp, vp]
+    lib.sgemm_moe.restype = i32
 
 
 def load():
@@ -141,7 +145,7 @@ def exported_symbols(lib=None):
             "sgemm_set_wait_limit", "sgemm_release_workspace", "sgemm_version",
             "sgemm_ffma_static_scratch", "sgemm_timing_enable", "sgemm_timing_read",
             "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize",
-            "sgemm_fp8", "sgemm_fp8_plan"]
+            "sgemm_fp8", "sgemm_fp8_plan", "sgemm_moe"]
 
 
 def _b(t: str) -> bytes:
@@ -419,3 +423,84 @@ def fp8_gemm(A, SA, B, SB, C, transA="N", transB="T", alpha=1.0, beta=0.0, a_gro
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_fp8")
     return C
+
+
+def sgemm_moe(T, D, F, E, topk, x, x_type, ldx, router, logits, gate, s_gate, up, s_up, ld_in,
+              stride_in, down, s_down, ld_down, stride_down, renormalize, y, ldy, indices, weights,
+              stream=None) -> int:
+    """A mixture-of-experts layer for a few tokens; device addresses (int), router 0 = none."""
+    return load().sgemm_moe(T, D, F, E, topk, x, x_type, ldx, router or None, logits, gate, s_gate, up,
+                            s_up, ld_in, stride_in, down, s_down, ld_down, stride_down,
+                            int(renormalize), y, ldy, indices, weights, _stream(stream))
+
+
+def _experts(name, t, E, rows, cols):
+    """(address, row stride, matrix stride) of E matrices of E4M3 codes."""
+    if _type_of(t.dtype) != TYPE_E4M3 or not t.is_cuda or t.shape != (E, rows, cols) or t.stride(2) != 1:
+        raise ValueError(f"{name} must be an {E} x {rows} x {cols} CUDA tensor of float8_e4m3fn codes "
+                         "with unit stride along its last dimension")
+    stride, ld, _ = t.stride()
+    return t.data_ptr(), ld, stride
+
+
+def _packed(name, t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True, y=None, logits=None,
+        indices=None, weights=None, stream=None):
+    """(y, logits, indices, weights): a mixture-of-experts layer for up to 128 tokens.
+
+    x: T x D, float32 or bfloat16.  router: E x D float32, or None with ``logits``
+    (T x E float32) given.  gate and up: E x F x D codes (float8_e4m3fn) with
+    128 x 128 block scales s_gate, s_up (E x ceil(F/128) x ceil(D/128)); down:
+    E x D x F with s_down; rows of codes start on 16 bytes (pad them where D or F
+    is no multiple of 16).  Each token takes its ``topk`` experts of the largest
+    logits with their softmax weights (``renormalize``: divided by their sum);
+    an expert is down (silu(gate x) * (up x)).  y, logits, indices (int32) and
+    weights take buffers to write into.  Asynchronous on ``stream`` (default:
+    torch's current stream on x's device); raises SgemmError on any non-zero
+    status.
+    """
+    import torch
+
+    px, x_type, ldx = _matrix("x", x, (TYPE_F32, TYPE_BF16))
+    T, D = x.shape
+    E, F = gate.shape[:2]
+    device = x.device
+    pg, ld_in, stride_in = _experts("gate", gate, E, F, D)
+    pu, ld_up, stride_up = _experts("up", up, E, F, D)
+    pd, ld_down, stride_down = _experts("down", down, E, D, F)
+    if (ld_up, stride_up) != (ld_in, stride_in):
+        raise ValueError("gate and up must have the same strides")
+    fb, db = (F + 127) // 128, (D + 127) // 128
+    f32 = torch.float32
+    if router is None and logits is None:
+        raise ValueError("give router or logits")
+    pr = _packed("router", router, (E, D), f32) if router is not None else None
+    if logits is None:
+        logits = torch.empty((T, E), device=device, dtype=f32)
+    if y is None:
+        y = torch.empty((T, D), device=device, dtype=x.dtype)
+    elif y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("y must have x's shape and dtype")
+    if indices is None:
+        indices = torch.empty((T, topk), device=device, dtype=torch.int32)
+    if weights is None:
+        weights = torch.empty((T, topk), device=device, dtype=f32)
+    py, _, ldy = _matrix("y", y, (TYPE_F32, TYPE_BF16))
+    for t in (router, logits, gate, s_gate, up, s_up, down, s_down, y, indices, weights):
+        if t is not None and t.device != device:
+            raise ValueError("the operands must be on one device")
+    st = load().sgemm_moe(
+        T, D, F, E, topk, px, x_type, ldx, pr, _packed("logits", logits, (T, E), f32), pg,
+        _packed("s_gate", s_gate, (E, fb, db), f32), pu, _packed("s_up", s_up, (E, fb, db), f32), ld_in,
+        stride_in, pd, _packed("s_down", s_down, (E, db, fb), f32), ld_down, stride_down,
+        int(renormalize), py, ldy, _packed("indices", indices, (T, topk), torch.int32),
+        _packed("weights", weights, (T, topk), f32),
+        _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_moe")
+    return y, logits, indices, weights

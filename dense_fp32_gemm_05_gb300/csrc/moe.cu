@@ -1,0 +1,983 @@
+// A mixture-of-experts layer for a few tokens in one kernel: the router, the
+// top-k choice, the experts' gate, up and down products over 8-bit weights and
+// the weighted sum of the experts' outputs.
+//
+// A few tokens use every weight a few times at most, so the layer is bound by
+// reading the chosen experts' weights once, 3 D F bytes for each.  What the
+// kernel is built for is therefore an HBM stream that never stops:
+//   * weights go from HBM by TMA into shared memory and from there into the
+//     tensor cores (tcgen05 kind::f8f6f4) as they are, 8-bit codes as the
+//     MMA's 128 rows; no instruction converts a weight;
+//   * activations are the MMA's columns.  They are wider than 8 bits, so each
+//     block of 128 of a token is scaled by a power of two (largest value in
+//     [128, 256)) and split into PARTS E4M3 numbers,
+//       x = 2^-e (q_0 + q_1 / 32 + q_2 / 1024 + ...),
+//     q_i the rounding of what the parts before left, times 32^i: each part adds
+//     5 bits.  bf16 takes 2 parts (exact but for values below 2^-14 of the
+//     block's largest, and those to 2^-22 of it), fp32 takes 4 (2^-20 of each
+//     value).  The parts are separate columns of one MMA: it costs the same
+//     (few columns), and the products are exact;
+//   * a block's sums come back from tensor memory, the parts are added and the
+//     block's scales (weights' and token's) applied in fp32 registers;
+//   * the work of a product, (expert, 128 rows, block of 128 k) after block, is
+//     cut into equal contiguous ranges, one for each CTA.  A range's first and
+//     last tile may be shared with the neighbours; partial sums go to a
+//     workspace and are added in ascending order of k: no result depends on
+//     timing.
+//
+// Phases, one CTA per SM, cooperative launch:
+//   0  router logits: tiles of 8 tokens x 8 experts x a slice of D over the CTAs
+//      (fp32 FMAs), then a grid barrier; every CTA then works out the routing
+//      (softmax, top-k, the experts' token lists) for itself;
+//   1  h = silu(gate x) * (up x): tiles of 64 gate rows and the same 64 up rows.
+//      The last CTA to finish a shared tile adds its parts;
+//   2  down h.  Only the warps that split h wait for the grid barrier between 1
+//      and 2: the weights' stream goes on across it;
+//   3  after a third barrier y = sum over a token's experts, all threads.
+//
+// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-5 split activations
+// into the MMA's column operand; 6-9 promotion (128 rows, one per thread).
+// Every wait is bounded: a role that gives up sets the device error word and
+// stops; every CTA still arrives at every grid barrier, so that the counters
+// are whole again when the kernel ends.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "fp8.cuh"
+#include "plan.h"
+#include "ptx_util.cuh"
+#include "tc_gemm.h"
+#include "tc_ptx.cuh"
+
+namespace sgemm_gb300 {
+namespace moe {
+
+using namespace tc;
+
+constexpr int BK = fp8::GROUP;
+constexpr int ROWS = 128;                      // weight rows of a tile (64 gate + 64 up, or 128 down)
+constexpr int A_BYTES = ROWS * BK;
+constexpr int SPLITTERS = 4;                   // warps 2..5
+constexpr int THREADS = 320;
+constexpr int MAX_T = 128, MAX_E = 512, MAX_TOPK = 16;
+constexpr int MAX_SLOTS = MAX_T * MAX_TOPK;
+constexpr int MAX_CHUNKS = 2 * MAX_E;          // (expert, up to NT of its tokens)
+constexpr int LOGIT_SLICES = 16;               // slices of D per tile of logits, at most
+constexpr int SMEM_MAX = 232448;               // shared memory per block, static and dynamic
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+__device__ unsigned int g_error;               // sticky device error word of this path
+
+// NT: tokens of one expert that a tile takes (columns for each part).
+template <int NT>
+struct Cfg {
+    static constexpr int A_STAGES = NT <= 8 ? 10 : NT <= 16 ? 8 : 6;   // 16 KB of weights each
+    static constexpr int B_BYTES = 4 * NT * BK;
+    static constexpr int B_STAGES = NT >= 64 ? 2 : 4;
+    static constexpr uint32_t COLS = 8 * NT;    // two buffers of 4 NT columns
+    static constexpr int EX = NT * 64 > 640 ? NT * 64 : 640;   // floats: up's values for gate's rows; phase 0's sums
+    static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES + EX * 4;
+    static_assert(COLS <= 512, "tensor memory");
+    static_assert(SMEM + 32 * 1024 <= SMEM_MAX, "shared memory (the routing is static)");
+};
+
+struct Params {
+    int T, D, F, E, topk;
+    const void *x;
+    int64_t ldx;
+    int x_vec;                                 // whole-quad loads of x
+    const float *router;
+    float *logits;
+    const float *s_gate, *s_up, *s_down;
+    int renormalize;
+    void *y;
+    int64_t ldy;
+    int32_t *indices;
+    float *weights;
+    int slices;                                // of D in phase 0
+    int ldh;
+    unsigned int *sync;                        // grid barriers 0..2, exits (3)
+    unsigned int *arrivals;                    // one for each tile of phase 1
+    int n_arrivals;
+    float *logit_parts;                        // [slices][T][E]
+    float *h;                                  // [slot][ldh]
+    float *parts;                              // [CTA][first, last tile of its range][token][ROWS]
+    float *out;                                // [slot][D]: down h
+    unsigned long long wait_ns;
+};
+
+// Routing as every CTA holds it.  A slot is t * topk + j.
+struct Routing {
+    float weight[MAX_SLOTS];
+    short expert[MAX_SLOTS];                   // of a slot
+    short rank[MAX_SLOTS];                     // of a slot among its expert's
+    short list[MAX_SLOTS];                     // slots by expert, ascending within one
+    short count[MAX_E], first[MAX_E];          // of an expert in `list`
+    short chunk0[MAX_E];                       // an expert's first chunk
+    short c_expert[MAX_CHUNKS], c_first[MAX_CHUNKS], c_n[MAX_CHUNKS];
+    int chunks;
+};
+
+__device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ bool grid_wait(const unsigned int *counter, unsigned int n, uint64_t limit) {
+    if (load_acquire(counter) >= n) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (load_acquire(counter) < n) {
+        if (global_timer_ns() - t0 > limit) {
+            atomicExch(&g_error, (unsigned)SGEMM_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+__device__ __forceinline__ float4 quad(const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); }
+__device__ __forceinline__ float4 quad(const __nv_bfloat16 *p) {
+    const uint2 t = __ldcg(reinterpret_cast<const uint2 *>(p));
+    return make_float4(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xffff0000u),
+                       __uint_as_float(t.y << 16), __uint_as_float(t.y & 0xffff0000u));
+}
+
+// Elements k .. k+3 of a row of n (zeros past it).
+template <typename T>
+__device__ __forceinline__ float4 load_quad(const T *row, int k, int n, bool vec) {
+    if (vec && k + 3 < n) return quad(row + k);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (k < n) v.x = to_f32(row[k]);
+    if (k + 1 < n) v.y = to_f32(row[k + 1]);
+    if (k + 2 < n) v.z = to_f32(row[k + 2]);
+    if (k + 3 < n) v.w = to_f32(row[k + 3]);
+    return v;
+}
+
+// ------------------------------------------------------------ phase 0: logits
+// One tile of 8 tokens x 8 experts over a slice of D by the whole CTA: each
+// thread has 4 k of each chunk of 128 for all 64 sums, then lanes and warps are
+// added in a fixed order.
+template <typename XT>
+__device__ void logits_tile(const Params &p, int t0, int e0, int slice, float (*red)[64]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int chunks = (p.D + BK - 1) / BK;
+    const int c0 = (int)((int64_t)chunks * slice / p.slices), c1 = (int)((int64_t)chunks * (slice + 1) / p.slices);
+    const XT *x = static_cast<const XT *>(p.x);
+    const bool w_vec = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.router) & 15) == 0;
+    float v[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+    for (int c = c0 + warp; c < c1; c += THREADS / 32) {
+        const int k = c * BK + 4 * lane;
+        float4 w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = e0 + e < p.E ? load_quad(p.router + (int64_t)(e0 + e) * p.D, k, p.D, w_vec)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (t0 + t >= p.T) break;
+            const float4 a = load_quad(x + (int64_t)(t0 + t) * p.ldx, k, p.D, p.x_vec != 0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float s = v[8 * t + e];
+                s = __fmaf_rn(a.x, w[e].x, s);
+                s = __fmaf_rn(a.y, w[e].y, s);
+                s = __fmaf_rn(a.z, w[e].z, s);
+                v[8 * t + e] = __fmaf_rn(a.w, w[e].w, s);
+            }
+        }
+    }
+    // lane l ends with the sums 2 r and 2 r + 1, r = l's bits as the halves were kept
+#pragma unroll
+    for (int half = 32; half >= 2; half /= 2) {
+        const int mask = half / 2;             // lanes: 16, 8, 4, 2, 1
+        const bool up = (lane & mask) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, mask));
+        }
+    }
+    red[warp][2 * lane] = v[0];
+    red[warp][2 * lane + 1] = v[1];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) s = __fadd_rn(s, red[w][threadIdx.x]);
+        const int t = t0 + threadIdx.x / 8, e = e0 + threadIdx.x % 8;
+        if (t < p.T && e < p.E) p.logit_parts[((int64_t)slice * p.T + t) * p.E + e] = s;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------ routing
+// fp32 values in the order of unsigned integers; NaN lowest, -0 as +0
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (v != v) return 0u;
+    const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One token's softmax and top-k by a warp.
+__device__ void route_token(const Params &p, int t, Routing &rt, bool write) {
+    constexpr int PER = MAX_E / 32;
+    const int lane = threadIdx.x & 31;
+    float l[PER];
+    float most = -INFINITY;
+    bool nan = false;
+    const int per = (p.E + 31) / 32;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        l[i] = 0.0f;
+        const int e = 32 * i + lane;
+        if (i >= per || e >= p.E) continue;
+        float s;
+        if (p.router) {
+            const float *src = p.logit_parts + (int64_t)t * p.E + e;
+            s = __ldcg(src);
+            for (int k = 1; k < p.slices; ++k) s = __fadd_rn(s, __ldcg(src + (int64_t)k * p.T * p.E));
+            if (write) p.logits[(int64_t)t * p.E + e] = s;
+        } else {
+            s = p.logits[(int64_t)t * p.E + e];
+        }
+        l[i] = s;
+        nan |= s != s;
+        most = fmaxf(most, s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (__any_sync(0xffffffffu, nan)) most = __uint_as_float(0x7fffffffu);   // every weight is NaN then
+    float sum = 0.0f;
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = i < per && 32 * i + lane < p.E;
+        if (in) sum = __fadd_rn(sum, expf(__fsub_rn(l[i], most)));
+        // keys of what may still be chosen, above 0
+        key[i] = in ? max(order_key(l[i]), 1u) : 0u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    float mine = 0.0f;                          // lane j: the weight of choice j
+    int mine_e = 0;
+    for (int j = 0; j < p.topk; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i < per) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        uint32_t at = 0xffffffffu;              // the lowest index with it
+        float v = 0.0f;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (i < per && key[i] == best) { at = 32 * i + lane; v = l[i]; }
+        const uint32_t e = __reduce_min_sync(0xffffffffu, at);
+        v = __shfl_sync(0xffffffffu, v, (int)(e & 31));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (32 * i + lane == (int)e) key[i] = 0;
+        if (lane == j) {
+            mine = __fdiv_rn(expf(__fsub_rn(v, most)), sum);
+            mine_e = (int)e;
+        }
+    }
+    if (p.renormalize) {
+        float total = 0.0f;
+        for (int j = 0; j < p.topk; ++j) total = __fadd_rn(total, __shfl_sync(0xffffffffu, mine, j));
+        mine = __fdiv_rn(mine, total);
+    }
+    if (lane < p.topk) {
+        const int slot = t * p.topk + lane;
+        rt.weight[slot] = mine;
+        rt.expert[slot] = (short)mine_e;
+        if (write) {
+            p.weights[slot] = mine;
+            p.indices[slot] = mine_e;
+        }
+    }
+}
+
+// The experts' slot lists and chunks of up to NT slots (one warp).
+template <int NT>
+__device__ void route_lists(const Params &p, Routing &rt) {
+    const int lane = threadIdx.x & 31;
+    const int slots = p.T * p.topk;
+    for (int e = lane; e < p.E; e += 32) rt.count[e] = 0;
+    __syncwarp();
+    for (int s0 = 0; s0 < slots; s0 += 32) {
+        const int s = s0 + lane;
+        const int e = s < slots ? rt.expert[s] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int before = e >= 0 ? rt.count[e] : 0;
+        const int r = before + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0) {
+            rt.rank[s] = (short)r;
+            if ((same >> lane) == 1u) rt.count[e] = (short)(r + 1);   // the last of them
+        }
+        __syncwarp();
+    }
+    int slot_base = 0, chunk_base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < p.E ? rt.count[e] : 0;
+        const int c = (n + NT - 1) / NT;
+        int ns = n, cs = c;                     // inclusive prefix sums
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int a = __shfl_up_sync(0xffffffffu, ns, o), b = __shfl_up_sync(0xffffffffu, cs, o);
+            if (lane >= o) { ns += a; cs += b; }
+        }
+        if (e < p.E) {
+            rt.first[e] = (short)(slot_base + ns - n);
+            rt.chunk0[e] = (short)(chunk_base + cs - c);
+            for (int i = 0; i < c; ++i) {
+                const int at = chunk_base + cs - c + i;
+                rt.c_expert[at] = (short)e;
+                rt.c_first[at] = (short)(slot_base + ns - n + i * NT);
+                rt.c_n[at] = (short)min(NT, n - i * NT);
+            }
+        }
+        slot_base += __shfl_sync(0xffffffffu, ns, 31);
+        chunk_base += __shfl_sync(0xffffffffu, cs, 31);
+    }
+    if (lane == 0) rt.chunks = chunk_base;
+    __syncwarp();
+    for (int s = lane; s < slots; s += 32) rt.list[rt.first[rt.expert[s]] + rt.rank[s]] = (short)s;
+}
+
+// ------------------------------------------------------------ work ranges
+// A product's blocks: tile after tile (chunk-major), kb blocks each; CTA c has
+// [c total / n, (c + 1) total / n).
+struct Work {
+    int tiles, kb;                              // tiles per chunk, blocks per tile
+    int64_t total;
+    int n;                                      // CTAs with a range: no range is empty
+    __device__ Work(int chunks, int tiles_, int kb_)
+        : tiles(tiles_), kb(kb_), total((int64_t)chunks * tiles_ * kb_),
+          n((int)max((int64_t)1, min((int64_t)gridDim.x, total))) {}
+    __device__ int64_t begin(int c) const { return c >= n ? total : total * c / n; }
+    __device__ int owner(int64_t it) const { return (int)(((it + 1) * n - 1) / total); }
+    // which of CTA c's two partial sums belongs to tile u
+    __device__ int part_of(int c, int u) const { return begin(c) / kb == u ? 0 : 1; }
+};
+
+// Calls f(tile, first block, end block) for the pieces of this CTA's range;
+// stops when f returns false.
+template <typename Fn>
+__device__ __forceinline__ bool for_pieces(const Work &w, Fn f) {
+    int64_t it = w.begin(blockIdx.x);
+    const int64_t end = w.begin(blockIdx.x + 1);
+    while (it < end) {
+        const int u = (int)(it / w.kb);
+        const int kb0 = (int)(it - (int64_t)u * w.kb);
+        const int kb1 = (int)min((int64_t)w.kb, kb0 + (end - it));
+        if (!f(u, kb0, kb1)) return false;
+        it += kb1 - kb0;
+    }
+    return true;
+}
+
+__device__ __forceinline__ void promoters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// ------------------------------------------------------------ activations
+// A lane's 4 values of a token's block -> its bytes of the column operand, and
+// (lane 0) the block's scale.  Part i of token c is row i * n8 + c: 128 bytes, the
+// 16-byte chunk index flipped by the row's low 3 bits (128-byte swizzle).
+template <int PARTS>
+__device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, int c, int n8, int lane) {
+    const uint32_t hi = max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
+                            max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+    const uint32_t amax = __reduce_max_sync(0xffffffffu, hi);
+    const int e = (int)(amax >> 23);
+    if (e == 255) {
+        // an infinity or NaN makes the token NaN
+        const float q = __uint_as_float(0x7fffffffu);
+        if ((__float_as_uint(v.x) & 0x7fffffffu) >= 0x7f800000u) v.x = q;
+        if ((__float_as_uint(v.y) & 0x7fffffffu) >= 0x7f800000u) v.y = q;
+        if ((__float_as_uint(v.z) & 0x7fffffffu) >= 0x7f800000u) v.z = q;
+        if ((__float_as_uint(v.w) & 0x7fffffffu) >= 0x7f800000u) v.w = q;
+    }
+    // 2^(7 - floor(log2 amax)), within the powers whose reciprocal is a normal number
+    const int ub = min(max(261 - e, 1), 253);
+    const float up = __uint_as_float((uint32_t)ub << 23);
+    if (lane == 0) scale[c] = __uint_as_float((uint32_t)(254 - ub) << 23);
+    float y[4] = {__fmul_rn(v.x, up), __fmul_rn(v.y, up), __fmul_rn(v.z, up), __fmul_rn(v.w, up)};
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const uint32_t q = fp8::codes4<false>(y);
+        const int row = i * n8 + c;
+        const uint32_t at = b + (uint32_t)(row * BK) + ((uint32_t)(((lane >> 2) ^ (row & 7)) << 4) | (uint32_t)(4 * (lane & 3)));
+        asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(q) : "memory");
+        if (i + 1 < PARTS) {
+            uint32_t h01, h23;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"((uint16_t)(q & 0xffffu)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"((uint16_t)(q >> 16)));
+            const float2 d01 = __half22float2(*reinterpret_cast<__half2 *>(&h01));
+            const float2 d23 = __half22float2(*reinterpret_cast<__half2 *>(&h23));
+            // (y - q) * 32: exact
+            y[0] = __fmul_rn(__fsub_rn(y[0], d01.x), 32.0f);
+            y[1] = __fmul_rn(__fsub_rn(y[1], d01.y), 32.0f);
+            y[2] = __fmul_rn(__fsub_rn(y[2], d23.x), 32.0f);
+            y[3] = __fmul_rn(__fsub_rn(y[3], d23.y), 32.0f);
+        }
+    }
+}
+
+// ------------------------------------------------------------ kernel
+template <typename XT, int NT>
+__global__ void __launch_bounds__(THREADS, 1)
+    moe_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
+               const __grid_constant__ CUtensorMap tm_down, const Params p) {
+    using K_ = Cfg<NT>;
+    constexpr int P1 = sizeof(XT) == 2 ? 2 : 4;   // parts of x
+    constexpr int P2 = 4;                         // parts of h
+    constexpr int SB = K_::B_STAGES, A_STAGES = K_::A_STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ Routing rt;
+    __shared__ float b_scale[SB][NT];
+    __shared__ uint64_t bars[2 * A_STAGES + 2 * SB + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ unsigned int s_last;
+    const uint32_t smem0 = smem_u32(smem), bar0 = smem_u32(bars);
+    float *ex = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES + SB * K_::B_BYTES);
+    auto a_at = [&](int s) { return smem0 + (uint32_t)(s * A_BYTES); };
+    auto b_at = [&](int s) { return smem0 + (uint32_t)(A_STAGES * A_BYTES + s * K_::B_BYTES); };
+    auto a_full = [&](int s) { return bar0 + 8u * s; };
+    auto a_empty = [&](int s) { return bar0 + 8u * (A_STAGES + s); };
+    auto b_full = [&](int s) { return bar0 + 8u * (2 * A_STAGES + s); };
+    auto b_empty = [&](int s) { return bar0 + 8u * (2 * A_STAGES + SB + s); };
+    auto t_full = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + b); };
+    auto t_empty = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + 2 + b); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned int G = gridDim.x;
+    const uint64_t lim = p.wait_ns;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < A_STAGES; ++s) {
+            mbar_init(a_full(s), 1);
+            mbar_init(a_empty(s), 1);
+        }
+        for (int s = 0; s < SB; ++s) {
+            mbar_init(b_full(s), SPLITTERS);
+            mbar_init(b_empty(s), 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(t_full(b), 1);
+            mbar_init(t_empty(b), 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&tm_gate);
+        prefetch_map(&tm_up);
+        prefetch_map(&tm_down);
+    }
+    if (warp == 1) tmem_alloc<false>(smem_u32(&tmem_slot), K_::COLS);
+
+    // ---- phase 0: logits, and the shared tiles' arrival counters
+    for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.n_arrivals; i += G * THREADS) p.arrivals[i] = 0;
+    if (p.router) {
+        float(*red)[64] = reinterpret_cast<float(*)[64]>(ex);
+        const int tt = (p.T + 7) / 8, et = (p.E + 7) / 8;
+        for (int i = blockIdx.x; i < tt * et * p.slices; i += G) {
+            const int slice = i % p.slices, tile = i / p.slices;
+            logits_tile<XT>(p, tile / et * 8, tile % et * 8, slice, red);
+        }
+    }
+    bool ok = true;
+    __threadfence();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (threadIdx.x == 0) {
+        atomicAdd(&p.sync[0], 1u);
+        s_last = grid_wait(&p.sync[0], G, lim);
+    }
+    __syncthreads();
+    ok = s_last != 0;
+    if (ok) {
+        for (int t = warp; t < p.T; t += THREADS / 32) route_token(p, t, rt, blockIdx.x == 0);
+        __syncthreads();
+        if (warp == 0) route_lists<NT>(p, rt);
+    } else if (threadIdx.x == 0) {
+        rt.chunks = 0;
+    }
+    __syncthreads();
+    const int kb1 = (p.D + BK - 1) / BK, kb2 = (p.F + BK - 1) / BK;
+    const Work w1(rt.chunks, (p.F + 63) / 64, kb1), w2(rt.chunks, (p.D + ROWS - 1) / ROWS, kb2);
+    ok = ok && rt.chunks > 0;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0 && ok) {
+            int s = 0, filled = 0;
+            uint32_t ph = 1;
+            auto produce = [&](const Work &w, bool second) {
+                return for_pieces(w, [&](int u, int k0, int k1) {
+                    const int e = rt.c_expert[u / w.tiles], tile = u % w.tiles;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!mbar_wait_for(a_empty(s), ph, lim, &g_error)) return false;
+                        mbar_expect_tx(a_full(s), A_BYTES);
+                        if (second) {
+                            tma_load_3d(a_at(s), &tm_down, a_full(s), kb * BK, tile * ROWS, e);
+                        } else {
+                            tma_load_3d(a_at(s), &tm_gate, a_full(s), kb * BK, tile * 64, e);
+                            tma_load_3d(a_at(s) + A_BYTES / 2, &tm_up, a_full(s), kb * BK, tile * 64, e);
+                        }
+                        ++filled;
+                        if (++s == A_STAGES) { s = 0; ph ^= 1; }
+                    }
+                    return true;
+                });
+            };
+            if (produce(w1, false)) produce(w2, true);
+            for (int i = 0; i < min(filled, A_STAGES); ++i) {   // copies in flight land before shared memory goes
+                if (s == 0) { s = A_STAGES; ph ^= 1; }
+                --s;
+                mbar_wait_for(a_full(s), ph ^ 1u, kDrainNs, &g_error);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0 && ok) {
+            int s = 0, bs = 0, b = 0, issued = 0;
+            uint32_t ph = 0, bph = 0, tph = 1;
+            auto multiply = [&](const Work &w, int parts) {
+                return for_pieces(w, [&](int u, int k0, int k1) {
+                    const int n8 = (rt.c_n[u / w.tiles] + 7) / 8 * 8;
+                    const uint32_t idesc = idesc_8bit(0, 0, 0, 0, ROWS, (parts * n8 + 15) / 16 * 16);
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!mbar_wait_for(t_empty(b), tph, lim, &g_error) ||
+                            !mbar_wait_for(b_full(bs), bph, lim, &g_error) ||
+                            !mbar_wait_for(a_full(s), ph, lim, &g_error)) return false;
+                        tc_fence_after();
+                        const uint64_t da = smem_desc_8bit(a_at(s), A_BYTES), db = smem_desc_8bit(b_at(bs), A_BYTES);
+#pragma unroll
+                        for (int i = 0; i < BK / 32; ++i)
+                            umma_8bit<false>(tmem + (uint32_t)(b * 4 * NT), da + i * 2, db + i * 2, idesc, i > 0);
+                        umma_commit(a_empty(s));
+                        umma_commit(t_full(b));
+                        ++issued;
+                        if (++s == A_STAGES) { s = 0; ph ^= 1; }
+                        if (++bs == SB) { bs = 0; bph ^= 1; }
+                        if (++b == 2) { b = 0; tph ^= 1; }
+                    }
+                    return true;
+                });
+            };
+            if (multiply(w1, P1)) multiply(w2, P2);
+            if (issued > 0)                      // MMAs retire before tensor memory is freed
+                mbar_wait_for(t_full((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
+        }
+        __syncwarp();
+    } else if (warp < 2 + SPLITTERS) {
+        // ------------------------------------------------ activations
+        if (ok) {
+            int bs = 0;
+            uint32_t bph = 1;
+            // the pieces' (block, token) pairs of this warp, four loaded ahead
+            auto split = [&](const Work &w, auto *base, auto row_of, int width, int64_t ld, bool vec, auto parts) {
+                constexpr int PARTS = decltype(parts)::value;
+                return for_pieces(w, [&](int u, int k0, int k1) {
+                    const int ch = u / w.tiles, n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
+                    const int mine = warp - 2 < n ? (n - (warp - 2) + SPLITTERS - 1) / SPLITTERS : 0;
+                    constexpr int AHEAD = 4;
+                    float4 next[AHEAD];
+                    int lk = k0, li = 0;        // the next pair to load
+                    auto fetch = [&](float4 &v) {
+                        if (lk < k1) {
+                            const int slot = rt.list[first + warp - 2 + li * SPLITTERS];
+                            v = load_quad(base + (int64_t)row_of(slot) * ld, lk * BK + 4 * lane, width, vec);
+                            if (++li == mine) { li = 0; ++lk; }
+                        }
+                    };
+                    if (mine > 0) {
+#pragma unroll
+                        for (int a = 0; a < AHEAD; ++a) fetch(next[a]);
+                    }
+                    int a = 0;
+                    for (int kb = k0; kb < k1; ++kb) {
+                        bool go = mbar_wait_for(b_empty(bs), bph, lim, &g_error);
+                        if (__any_sync(0xffffffffu, !go)) return false;
+                        for (int i = 0; i < mine; ++i) {
+                            // (a is the warp's count modulo AHEAD; a switch keeps `next` in registers)
+                            float4 v;
+                            switch (a) {
+                            case 0: v = next[0]; fetch(next[0]); break;
+                            case 1: v = next[1]; fetch(next[1]); break;
+                            case 2: v = next[2]; fetch(next[2]); break;
+                            default: v = next[3]; fetch(next[3]); break;
+                            }
+                            a = (a + 1) & (AHEAD - 1);
+                            split_block<PARTS>(v, b_at(bs), b_scale[bs], warp - 2 + i * SPLITTERS, n8, lane);
+                        }
+                        // generic-proxy stores must be visible to the tensor core's reads
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_full(bs));
+                        if (++bs == SB) { bs = 0; bph ^= 1; }
+                    }
+                    return true;
+                });
+            };
+            const int topk = p.topk;
+            bool go = split(w1, static_cast<const XT *>(p.x), [&](int slot) { return slot / topk; }, p.D, p.ldx,
+                            p.x_vec != 0, std::integral_constant<int, P1>{});
+            if (go) {
+                if (lane == 0) go = grid_wait(&p.sync[1], G, lim);   // h is whole
+                if (!__any_sync(0xffffffffu, !go))
+                    split(w2, static_cast<const float *>(p.h), [](int slot) { return slot; }, p.F, p.ldh, true,
+                          std::integral_constant<int, P2>{});
+            }
+        }
+    } else {
+        // ------------------------------------------------ promotion
+        const int q = warp & 3, row = q * 32 + lane;
+        int b = 0, bs = 0;
+        uint32_t tph = 0, bph = 0;
+        // A warp whose wait ran out goes on without waiting or computing, so that
+        // the four warps still meet at every promoters_sync.
+        bool alive = true;
+        auto promote = [&](const Work &w, bool second, auto parts_) {
+            constexpr int PARTS = decltype(parts_)::value;
+            for_pieces(w, [&](int u, int k0, int k1) {
+                const int ch = u / w.tiles, tile = u - ch * w.tiles;
+                const int e = rt.c_expert[ch], n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
+                // this row's weight scales, block after block
+                const float *ws;
+                if (second) {
+                    ws = p.s_down + ((int64_t)e * ((p.D + 127) / 128) + tile) * w.kb;
+                } else {
+                    ws = (row < 64 ? p.s_gate : p.s_up) + ((int64_t)e * ((p.F + 127) / 128) + tile / 2) * w.kb;
+                }
+                float acc[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
+                float ws_next = __ldg(ws + k0);
+                for (int kb = k0; kb < k1; ++kb) {
+                    const float sw = ws_next;
+                    if (kb + 1 < k1) ws_next = __ldg(ws + kb + 1);
+                    if (alive) {
+                        const bool go = mbar_wait_for(t_full(b), tph, lim, &g_error);
+                        alive = !__any_sync(0xffffffffu, !go);
+                    }
+                    if (!alive) break;
+                    tc_fence_after();
+                    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 4 * NT);
+#pragma unroll
+                    for (int i0 = 0; i0 < NT; i0 += 8) {
+                        if (i0 >= n8) break;
+                        uint32_t r[PARTS][8];
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) tmem_ld_async(ta + (uint32_t)(i * n8 + i0), r[i]);
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) tmem_ld_wait(r[i]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float t = __uint_as_float(r[PARTS - 1][j]);
+#pragma unroll
+                            for (int i = PARTS - 2; i >= 0; --i)
+                                t = __fmaf_rn(t, 1.0f / 32.0f, __uint_as_float(r[i][j]));
+                            acc[i0 + j] = __fmaf_rn(t, __fmul_rn(sw, b_scale[bs][i0 + j]), acc[i0 + j]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(t_empty(b));
+                        mbar_arrive(b_empty(bs));   // (the block's MMAs are done too)
+                    }
+                    if (++b == 2) { b = 0; tph ^= 1; }
+                    if (++bs == SB) { bs = 0; bph ^= 1; }
+                }
+                if (k0 == 0 && k1 == w.kb) {
+                    // the whole sum is here
+                    if (second) {
+                        const int d = tile * ROWS + row;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            if (i < n && d < p.D) __stcg(p.out + (int64_t)rt.list[first + i] * p.D + d, acc[i]);
+                    } else {
+                        const int f = tile * 64 + (row & 63);
+                        promoters_sync();       // (the tile before has been read)
+                        if (row >= 64) {
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+                                if (i < n) ex[i * 64 + row - 64] = acc[i];
+                        }
+                        promoters_sync();
+                        if (row < 64 && f < p.F) {
+#pragma unroll
+                            for (int i = 0; i < NT; ++i)
+                                if (i < n) {
+                                    const float g = acc[i];
+                                    const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
+                                    __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, ex[i * 64 + row]));
+                                }
+                        }
+                    }
+                    return true;
+                }
+                // a share of the sum
+                float *dst = p.parts + ((int64_t)blockIdx.x * 2 + w.part_of(blockIdx.x, u)) * NT * ROWS + row;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (i < n) __stcg(dst + i * ROWS, acc[i]);
+                if (second) return true;        // added in the last phase
+                __threadfence();
+                promoters_sync();
+                const int c0 = w.owner((int64_t)u * w.kb), c1 = w.owner((int64_t)(u + 1) * w.kb - 1);
+                if (row == 0) s_last = atomicAdd(&p.arrivals[u], 1u) == (unsigned)(c1 - c0);
+                promoters_sync();
+                if (s_last) {
+                    __threadfence();
+                    const int f = tile * 64 + (row & 63);
+                    for (int i = row >> 6; i < n; i += 2) {
+                        float g = 0.0f, up = 0.0f;
+                        for (int c = c0; c <= c1; ++c) {
+                            const float *src = p.parts + (((int64_t)c * 2 + w.part_of(c, u)) * NT + i) * ROWS + (row & 63);
+                            g = __fadd_rn(g, __ldcg(src));
+                            up = __fadd_rn(up, __ldcg(src + 64));
+                        }
+                        const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
+                        if (f < p.F) __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, up));
+                    }
+                }
+                return true;
+            });
+        };
+        if (ok) promote(w1, false, std::integral_constant<int, P1>{});
+        __threadfence();
+        promoters_sync();
+        if (row == 0) atomicAdd(&p.sync[1], 1u);
+        if (ok) promote(w2, true, std::integral_constant<int, P2>{});
+        __threadfence();
+        promoters_sync();
+        if (row == 0) atomicAdd(&p.sync[2], 1u);
+    }
+    // ---- phase 3: y
+    if (threadIdx.x == THREADS - 1) s_last = grid_wait(&p.sync[2], G, lim);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<false>(tmem, K_::COLS);
+    }
+    if (s_last && ok) {
+        const int64_t total = (int64_t)p.T * p.D;
+        for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)G * THREADS) {
+            const int t = (int)(i / p.D), d = (int)(i - (int64_t)t * p.D);
+            const int tile = d / ROWS;
+            float sum = 0.0f;
+            for (int j = 0; j < p.topk; ++j) {
+                const int slot = t * p.topk + j;
+                const int e = rt.expert[slot], r = rt.rank[slot];
+                const int u = (rt.chunk0[e] + r / NT) * w2.tiles + tile;
+                const int c0 = w2.owner((int64_t)u * w2.kb), c1 = w2.owner((int64_t)(u + 1) * w2.kb - 1);
+                float v;
+                if (c0 == c1) {
+                    v = __ldcg(p.out + (int64_t)slot * p.D + d);
+                } else {
+                    v = 0.0f;
+                    for (int c = c0; c <= c1; ++c)
+                        v = __fadd_rn(v, __ldcg(p.parts + (((int64_t)c * 2 + w2.part_of(c, u)) * NT + r % NT) * ROWS +
+                                                d % ROWS));
+                }
+                sum = __fmaf_rn(rt.weight[slot], v, sum);
+            }
+            XT *y = static_cast<XT *>(p.y) + (int64_t)t * p.ldy + d;
+            if (sizeof(XT) == 2) *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(sum);
+            else *reinterpret_cast<float *>(y) = sum;
+        }
+    }
+    __syncthreads();
+    // the last CTA to leave clears the barriers for the next call
+    if (threadIdx.x == 0 && atomicAdd(&p.sync[3], 1u) == G - 1) {
+        p.sync[0] = p.sync[1] = p.sync[2] = p.sync[3] = 0;
+        __threadfence();
+    }
+}
+
+}  // namespace moe
+
+// ---------------------------------------------------------------- host side
+int moe_take_device_error() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, moe::g_error, sizeof(v)) != cudaSuccess) return SGEMM_ERR_CUDA;
+    if (v != 0 && cudaMemcpyToSymbol(moe::g_error, &zero, sizeof(zero)) != cudaSuccess)
+        return SGEMM_ERR_CUDA;
+    return v == 0 ? SGEMM_OK : (int)v;
+}
+
+// E matrices of rows x cols bytes in boxes of box_rows x 128, 128-byte swizzle.
+static bool experts_map(CUtensorMap *m, const void *base, int64_t E, int64_t rows, int64_t cols, int64_t ld,
+                        int64_t stride, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)E};
+    cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename XT, int NT>
+static int launch_moe(const CUtensorMap *maps, const moe::Params &p, int sms, cudaStream_t s) {
+    auto kern = moe::moe_kernel<XT, NT>;
+    constexpr int smem = moe::Cfg<NT>::SMEM;
+    static uint64_t attr_done = 0;   // bit d: the shared-memory opt-in is set on device d
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!bit || !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return launch_status();
+        __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(moe::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    timing_mark(s, true);
+    count_launch();
+    cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], p);
+    timing_mark(s, false);
+    return launch_status();
+}
+
+template <typename XT>
+static int launch_moe(const CUtensorMap *maps, const moe::Params &p, int nt, int sms, cudaStream_t s) {
+    return nt == 8    ? launch_moe<XT, 8>(maps, p, sms, s)
+           : nt == 16 ? launch_moe<XT, 16>(maps, p, sms, s)
+           : nt == 32 ? launch_moe<XT, 32>(maps, p, sms, s)
+                      : launch_moe<XT, 64>(maps, p, sms, s);
+}
+
+static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, int64_t ld_in, int64_t stride_in,
+                   const void *down, int64_t ld_down, int64_t stride_down, cudaStream_t s) {
+    int sms = 0;
+    int st = usable_device(&sms);
+    if (st != SGEMM_OK) return st;
+    const int64_t T = p.T, D = p.D, F = p.F, E = p.E, slots = T * p.topk;
+    // an expert has at most T tokens: one tile takes them all up to 64
+    const int nt = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const int64_t logit_tiles = ((T + 7) / 8) * ((E + 7) / 8);
+    p.slices = p.router ? (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fp8::blocks_of(D), moe::LOGIT_SLICES),
+                                                                      sms / logit_tiles))
+                        : 1;
+    p.ldh = (int)((F + 3) / 4 * 4);
+    const int64_t chunks = std::min<int64_t>(slots, E * ((T + nt - 1) / nt));
+    const int64_t arrivals = chunks * ((F + 63) / 64);
+    if (arrivals > INT32_MAX || chunks * ((D + 127) / 128) > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
+    p.n_arrivals = (int)arrivals;
+    auto up256 = [](size_t b) { return (b + 255) & ~size_t(255); };
+    // the barriers keep a workspace of their own: they are zero between calls
+    void *sync = nullptr, *ws = nullptr;
+    bool fresh = false;
+    st = workspace(s, 256, &sync, 2, &fresh);
+    if (st != SGEMM_OK) return st;
+    if (fresh && cudaMemsetAsync(sync, 0, 256, s) != cudaSuccess) return launch_status();
+    const size_t b_arr = up256((size_t)arrivals * 4), b_log = up256((size_t)p.slices * T * E * 4),
+                 b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)sms * 2 * nt * moe::ROWS * 4),
+                 b_out = up256((size_t)slots * D * 4);
+    st = workspace(s, b_arr + b_log + b_h + b_parts + b_out, &ws);
+    if (st != SGEMM_OK) return st;
+    char *w = static_cast<char *>(ws);
+    p.sync = static_cast<unsigned int *>(sync);
+    p.arrivals = reinterpret_cast<unsigned int *>(w);
+    p.logit_parts = reinterpret_cast<float *>(w += b_arr);
+    p.h = reinterpret_cast<float *>(w += b_log);
+    p.parts = reinterpret_cast<float *>(w += b_h);
+    p.out = reinterpret_cast<float *>(w += b_parts);
+    p.wait_ns = tc_wait_limit();
+    const int esize = x_type == SGEMM_TYPE_F32 ? 4 : 2;
+    p.x_vec = reinterpret_cast<uintptr_t>(p.x) % (4 * esize) == 0 && p.ldx % 4 == 0;
+    CUtensorMap maps[3];
+    if (!experts_map(&maps[0], gate, E, F, D, ld_in, stride_in, 64) ||
+        !experts_map(&maps[1], up, E, F, D, ld_in, stride_in, 64) ||
+        !experts_map(&maps[2], down, E, D, F, ld_down, stride_down, 128))
+        return SGEMM_ERR_UNSUPPORTED;
+    return x_type == SGEMM_TYPE_F32 ? launch_moe<float>(maps, p, nt, sms, s)
+                                    : launch_moe<__nv_bfloat16>(maps, p, nt, sms, s);
+}
+
+}  // namespace sgemm_gb300
+
+using namespace sgemm_gb300;
+
+extern "C" int sgemm_moe(int64_t T, int64_t D, int64_t F, int64_t E, int64_t topk, const void *x, int x_type,
+                         int64_t ldx, const float *router, float *logits, const void *gate,
+                         const float *s_gate, const void *up, const float *s_up, int64_t ld_in,
+                         int64_t stride_in, const void *down, const float *s_down, int64_t ld_down,
+                         int64_t stride_down, int renormalize, void *y, int64_t ldy, int32_t *indices,
+                         float *weights, sgemm_stream_t stream) {
+    const int64_t most = 1 << 20;                  // widths (tiles and blocks are ints)
+    if (T < 0 || T > moe::MAX_T) return -1;
+    if (D < 1 || D > most) return -2;
+    if (F < 1 || F > most) return -3;
+    if (E < 1 || E > moe::MAX_E) return -4;
+    if (topk < 1 || topk > std::min<int64_t>(E, moe::MAX_TOPK)) return -5;
+    if (!fp8::is_float_type(x_type)) return -7;
+    auto bad = [](const void *q, int align) { return q == nullptr || reinterpret_cast<uintptr_t>(q) % align != 0; };
+    const int esize = x_type == SGEMM_TYPE_F32 ? 4 : 2;
+    if (T > 0 && bad(x, esize)) return -6;
+    if (ldx < D) return -8;
+    if (router != nullptr && bad(router, 4)) return -9;
+    if (T > 0 && bad(logits, 4)) return -10;
+    if (T > 0 && gate == nullptr) return -11;
+    if (T > 0 && bad(s_gate, 4)) return -12;
+    if (T > 0 && up == nullptr) return -13;
+    if (T > 0 && bad(s_up, 4)) return -14;
+    if (ld_in < D) return -15;
+    if (stride_in < F * ld_in) return -16;
+    if (T > 0 && down == nullptr) return -17;
+    if (T > 0 && bad(s_down, 4)) return -18;
+    if (ld_down < F) return -19;
+    if (stride_down < D * ld_down) return -20;
+    if (T > 0 && bad(y, esize)) return -22;
+    if (ldy < D) return -23;
+    if (T > 0 && bad(indices, 4)) return -24;
+    if (T > 0 && bad(weights, 4)) return -25;
+    if (!aligned16(gate) || !aligned16(up) || !aligned16(down) || ld_in % 16 || stride_in % 16 || ld_down % 16 ||
+        stride_down % 16)
+        return SGEMM_ERR_UNSUPPORTED;
+    if (T == 0) return SGEMM_OK;
+    moe::Params p{};
+    p.T = (int)T; p.D = (int)D; p.F = (int)F; p.E = (int)E; p.topk = (int)topk;
+    p.x = x; p.ldx = ldx; p.router = router; p.logits = logits;
+    p.s_gate = s_gate; p.s_up = s_up; p.s_down = s_down;
+    p.renormalize = renormalize;
+    p.y = y; p.ldy = ldy; p.indices = indices; p.weights = weights;
+    try {
+        return run_moe(p, x_type, gate, up, ld_in, stride_in, down, ld_down, stride_down,
+                       reinterpret_cast<cudaStream_t>(stream));
+    } catch (const std::bad_alloc &) {
+        return SGEMM_ERR_NOMEM;
+    }
+}

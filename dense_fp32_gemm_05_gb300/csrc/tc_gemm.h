@@ -49,6 +49,7 @@ int tc_probe_tf32_rate(int reps, double *mac_per_clock);
 // Reads and clears the current device's sticky device error word.
 int tc_take_device_error();
 int fp8_take_device_error();
+int moe_take_device_error();
 
 // Sets the bounded-wait limit (ns; 0 = default).
 void tc_set_wait_limit(uint64_t ns);

@@ -388,8 +388,8 @@ int sgemm_ffma_static_scratch(char transA, char transB, int64_t M, int64_t N, in
 int sgemm_version(void);
 
 /* ------------------------------------------------------------------------
- * 8-bit floating point: quantisation and the matrix product of two quantised
- * operands.
+ * 8-bit floating point: quantisation, the matrix product of two quantised
+ * operands, and a mixture-of-experts layer over quantised weights.
  *
  * A quantised matrix is two arrays: codes (one byte each, E4M3 or E5M2) and
  * fp32 scales, one for each group of the codes; value = code * scale.  Groups
@@ -484,6 +484,47 @@ int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float a
  */
 int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int *out_tile_m, int *out_tile_n,
                    int *out_ksplit);
+
+/*
+ * sgemm_moe - a mixture-of-experts layer for a few tokens (decode), whole:
+ *
+ *   logits(t,e) = sum_d x(t,d) router(e,d)
+ *   p(t,.)      = softmax over the E experts of logits(t,.)
+ *   e_1..e_k    = the topk experts of the largest logits (ties, and NaN as
+ *                 the lowest: the lower index first)
+ *   w(t,j)      = p(t,e_j), with renormalize divided by their sum over j
+ *   h           = silu(gate_e x_t) * (up_e x_t),  silu(v) = v / (1 + exp(-v))
+ *   y(t,.)      = sum_j w(t,j) down_{e_j} h
+ *
+ *   T      tokens, 0 .. 128; D: width, F: experts' inner width, E: experts,
+ *          1 .. 512; topk 1 .. min(E, 16)
+ *   x, y   T x D, SGEMM_TYPE_F32 or SGEMM_TYPE_BF16 (x_type), ldx, ldy >= D
+ *   router E x D fp32 packed, or NULL: then logits is read, not written
+ *   logits T x E fp32 packed
+ *   gate, up  E matrices F x D of E4M3 codes (row stride ld_in >= D, matrix
+ *          stride stride_in >= F * ld_in), scales s_gate, s_up in 128 x 128
+ *          blocks, packed E x ceil(F/128) x ceil(D/128)
+ *   down   E matrices D x F (ld_down >= F, stride_down >= D * ld_down), s_down
+ *          packed E x ceil(D/128) x ceil(F/128)
+ *          (codes start on 16 bytes and all four strides are multiples of 16:
+ *          weights are laid out once; else SGEMM_ERR_UNSUPPORTED)
+ *   indices, weights   T x topk int32 and fp32 packed: e_j and w(t,j) (written)
+ *
+ * One kernel: routing, both expert products and the combination, with the
+ * weights of the chosen experts read once.  Weights never leave 8 bits:
+ * activations are split into E4M3 parts that add up to the activation (bf16:
+ * 2 parts, exact to 2^-21 of the largest of 128; fp32 and h: 4 parts, 2^-20 of
+ * each value), so results have fp32 accuracy.  Every sum is in fp32, in a
+ * fixed order.  Device workspace as sgemm's.  The kernel's CTAs wait for one
+ * another (cooperative launch, bounded waits): SGEMM_ERR_CUDA if the device
+ * cannot hold one CTA per SM at once.
+ */
+int sgemm_moe(int64_t T, int64_t D, int64_t F, int64_t E, int64_t topk, const void *x, int x_type,
+              int64_t ldx, const float *router, float *logits, const void *gate,
+              const float *s_gate, const void *up, const float *s_up, int64_t ld_in,
+              int64_t stride_in, const void *down, const float *s_down, int64_t ld_down,
+              int64_t stride_down, int renormalize, void *y, int64_t ldy, int32_t *indices,
+              float *weights, sgemm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -91,3 +91,26 @@ def product(a, b, alpha=1.0, beta=0.0, c=None):
         if beta != 0:
             out, size = out + beta * c, size + np.abs(beta * c)
     return out, size
+
+
+def moe(x, router, gate, up, down, topk, renormalize, logits=None):
+    """(y, logits, indices, weights) in 64 bits; gate, up, down: E matrices of values."""
+    logits = x @ router.T if logits is None else logits
+    order = np.argsort(-logits, axis=1, kind="stable")[:, :topk]
+    p = np.exp(logits - logits.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    w = np.take_along_axis(p, order, 1)
+    if renormalize:
+        w = w / w.sum(1, keepdims=True)
+    y = np.zeros(x.shape)
+    size = np.zeros(x.shape)                   # what errors of the products are measured against
+    for t in range(x.shape[0]):
+        for j, e in enumerate(order[t]):
+            g, u = gate[e] @ x[t], up[e] @ x[t]
+            with np.errstate(over="ignore"):
+                h = g / (1 + np.exp(-g)) * u
+            y[t] += w[t, j] * (down[e] @ h)
+            gs, us = np.abs(gate[e]) @ np.abs(x[t]), np.abs(up[e]) @ np.abs(x[t])
+            # |dh| <= |silu'| |dg| |u| + |silu| |du|, |silu'| < 1.1
+            size[t] += w[t, j] * (np.abs(down[e]) @ (1.1 * gs * np.abs(u) + np.abs(h / np.where(u == 0, 1, u)) * us + np.abs(h)))
+    return y, logits, order, w, size

@@ -102,3 +102,33 @@ def test_plain_product_closed_form():
     v = fp.values(ones, s, "e4m3", 1, False)
     out, size = fp.product(v, np.ones((256, 1)))
     assert out[:, 0].tolist() == [128 * 2.5, 128 * 3.25, 128 * 5.0] and np.array_equal(out, size)
+
+
+@pytest.mark.parametrize("change,want", [
+    ({0: -1}, -1), ({0: 129}, -1), ({1: 0}, -2), ({2: 0}, -3), ({3: 0}, -4), ({3: 513}, -4), ({4: 0}, -5),
+    ({4: 9}, -5), ({3: 64, 4: 17}, -5), ({5: 0}, -6), ({5: P + 1}, -6), ({6: E4M3}, -7), ({7: 255}, -8),
+    ({8: P + 1}, -9), ({9: 0}, -10), ({10: 0}, -11), ({11: 0}, -12), ({12: 0}, -13), ({13: P + 2}, -14),
+    ({14: 255}, -15), ({15: 128 * 256 - 1}, -16), ({16: 0}, -17), ({17: 0}, -18), ({18: 127}, -19),
+    ({19: 1}, -20), ({21: 0}, -22), ({22: 255}, -23), ({23: 0}, -24), ({24: 0}, -25),
+    ({10: P + 8}, sg.SGEMM_ERR_UNSUPPORTED), ({14: 257, 15: 257 * 128}, sg.SGEMM_ERR_UNSUPPORTED),
+    ({19: 256 * 128 + 8}, sg.SGEMM_ERR_UNSUPPORTED),
+])
+def test_moe_refusals(change, want):
+    args = [4, 256, 128, 8, 2, P, BF16, 256, P, P, P, P, P, P, 256, 256 * 128, P, P, 128, 256 * 128, 1, P, 256, P, P]
+    for i, v in change.items():
+        args[i] = v
+    assert sg.sgemm_moe(*args) == want
+
+
+def test_moe_of_nothing_is_ok():
+    assert sg.sgemm_moe(0, 256, 128, 8, 2, 0, F32, 256, 0, 0, 0, 0, 0, 0, 256, 256 * 128, 0, 0, 128, 256 * 128, 1,
+                        0, 256, 0, 0) == 0
+
+
+def test_plain_moe_closed_form():
+    x = np.array([[2.0, 0.0]])
+    gate, up, down = (np.array([[[a, 0.0]]]) for a in (1.0, 3.0, 0.0))
+    down = np.array([[[5.0], [7.0]]])
+    y, _, idx, w, _ = fp.moe(x, np.ones((1, 2)), gate, up, down, 1, False)
+    h = 2 / (1 + np.exp(-2)) * 6
+    assert np.allclose(y, [[5 * h, 7 * h]]) and w[0, 0] == 1.0 and idx[0, 0] == 0
