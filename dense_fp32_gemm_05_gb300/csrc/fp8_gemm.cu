@@ -78,7 +78,8 @@ struct Params {
     float alpha, beta;
     const float *SX, *SY;                  // scales of B (X) and A (Y)
     int64_t x_mn, x_k, y_mn, y_k;          // strides of the scales along N / M (per group) and per block of k
-    int y_shift;                           // a scale of A for each 1 << y_shift rows
+    int x_shift, y_shift;                  // a scale for each 1 << shift rows
+    int c_vec;                             // quads of C may be accessed whole
     int x_mnmajor, y_mnmajor;              // operand stored across k
     int y_bytes;                           // bytes of Y per stage
     uint32_t idesc;
@@ -103,11 +104,13 @@ __device__ __forceinline__ float load_c(const Params &p, int64_t at) {
                     : static_cast<const float *>(p.C)[at];
 }
 
-// alpha * acc, or fma(alpha, acc, beta * c), rounded once to C's type
-__device__ __forceinline__ void store_c(const Params &p, int m, int n, float acc) {
-    const int64_t at = (int64_t)m * p.ldc + n;
-    const float v = p.beta == 0.0f ? __fmul_rn(p.alpha, acc)
-                                   : __fmaf_rn(p.alpha, acc, __fmul_rn(p.beta, load_c(p, at)));
+// alpha * acc, or fma(alpha, acc, beta * c), to be rounded once to C's type
+__device__ __forceinline__ float epilogue(const Params &p, float acc, float old) {
+    return p.beta == 0.0f ? __fmul_rn(p.alpha, acc) : __fmaf_rn(p.alpha, acc, __fmul_rn(p.beta, old));
+}
+
+__device__ __forceinline__ void store_c(const Params &p, int64_t at, float acc, float old) {
+    const float v = epilogue(p, acc, old);
     if (p.c_bf16) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(v);
     else static_cast<float *>(p.C)[at] = v;
 }
@@ -124,7 +127,8 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
     return v;
 }
 
-// BY: columns of the MMA (rows of C) per tile.  XVEC: B has a scale for each
+// ---------------------------------------------------------------- narrow tiles
+// BY: columns of the MMA (rows of C) per tile, 16 .. 128.  XVEC: B has a scale for each
 // of its rows (else one for the CTA's 128).
 template <int BY, bool XVEC>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -199,7 +203,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     else tma_load_2d(x, &tm_x, full(s), kb * BK, tx * BX);
                     if (p.y_mnmajor) {
                         tma_load_2d(y, &tm_y, full(s), ty * BY, kb * BK);
-                        if (BY > 128) tma_load_2d(y + X_BYTES, &tm_y, full(s), ty * BY + 128, kb * BK);
                     } else {
                         tma_load_2d(y, &tm_y, full(s), kb * BK, ty * BY);
                     }
@@ -354,9 +357,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (n < p.N) {
                 const int m0 = ty * BY + half * PC;
 #pragma unroll
-                for (int i = 0; i < PC / 2; ++i) {
-                    if (m0 + 2 * i < p.M) store_c(p, m0 + 2 * i, n, acc[i].x);
-                    if (m0 + 2 * i + 1 < p.M) store_c(p, m0 + 2 * i + 1, n, acc[i].y);
+                for (int c = 0; c < PC; c += CH) {
+                    // a batch's loads of C are all under way before its first store
+                    float old[CH];
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+                        old[i] = p.beta != 0.0f && m0 + c + i < p.M ? load_c(p, (int64_t)(m0 + c + i) * p.ldc + n) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+                        if (m0 + c + i < p.M) {
+                            const float2 a = acc[(c + i) / 2];
+                            store_c(p, (int64_t)(m0 + c + i) * p.ldc + n, i % 2 ? a.y : a.x, old[i]);
+                        }
                 }
             }
         }
@@ -387,7 +399,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t at = smem0 + 4u * (uint32_t)(c * BX + q * 32 + lane);
                 float sum = 0.0f;
                 for (int r = 0; r < ks; ++r) sum = __fadd_rn(sum, load_cluster(peer_addr(at, (uint32_t)r)));
-                if (n < p.N) store_c(p, m, n, sum);
+                const int64_t to = (int64_t)m * p.ldc + n;
+                if (n < p.N) store_c(p, to, sum, p.beta != 0.0f ? load_c(p, to) : 0.0f);
             }
         }
         cluster_sync_all();                        // no CTA leaves while a peer reads its sums
@@ -398,6 +411,342 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_free<false>(tmem, COLS);
+    }
+}
+
+// ---------------------------------------------------------------- wide tiles
+// 256 x 256 tiles of C on a pair of SMs (cta_group::2): each CTA holds its 128
+// rows of A ("X"), half of the tile's 256 columns of B ("Y") and its 128 rows of
+// the two tensor-memory buffers.  Here the lanes are C's rows: a row's scale is one
+// register, and where B has one scale for its 128 x 128 block the product of the
+// two is one value for each thread and block of k, so that promotion is one
+// multiply-add per value and nothing else.  (With C's columns on the lanes, as
+// in the narrow kernel, every column's scale comes from shared memory for
+// every block, beside the MMAs' own reads: 1.34 against PFLOP/s at 8192^3.)
+// 128 accumulators per promoting thread need more registers than an equal
+// share: the three issuing warps hand theirs over (setmaxnreg).
+// The epilogue turns 32 x 32 blocks around through shared memory.
+constexpr int WT = 256;                        // tile rows and columns
+constexpr int W_THREADS = 384;                 // TMA, MMA, scales, idle, 8 promoters
+constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
+constexpr int W_SLOTS = 6;                     // scale slots
+constexpr int W_STAGE_OUT = 32 * 32 * 4;       // epilogue staging per promoting warp
+
+template <bool YVEC>
+struct Wide {
+    static constexpr int SLOT = YVEC ? WT + BX : WT;   // floats: columns' then rows' scales, or their products
+    static constexpr int FIXED = 1024 + PROMOTERS * W_STAGE_OUT + W_SLOTS * SLOT * 4 + BAR_BYTES;
+    static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
+    static constexpr int SMEM = FIXED + STAGES * W_STAGE;
+    static_assert(STAGES >= 4 && STAGES <= MAX_STAGES, "stages");
+};
+
+// One value of C's row m, columns n .. n + 3, from and to memory.
+__device__ __forceinline__ float4 load_c4(const Params &p, int64_t at, int cols, bool vec) {
+    if (vec && cols >= 4) {
+        if (!p.c_bf16) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p.C) + at);
+        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.C) + at);
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+    }
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (cols > 0) v.x = load_c(p, at);
+    if (cols > 1) v.y = load_c(p, at + 1);
+    if (cols > 2) v.z = load_c(p, at + 2);
+    if (cols > 3) v.w = load_c(p, at + 3);
+    return v;
+}
+__device__ __forceinline__ void store_c4(const Params &p, int64_t at, float4 a, float4 old, int cols, bool vec) {
+    if (vec && cols >= 4) {
+        const float4 v = make_float4(epilogue(p, a.x, old.x), epilogue(p, a.y, old.y), epilogue(p, a.z, old.z),
+                                     epilogue(p, a.w, old.w));
+        if (!p.c_bf16) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = v;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.C) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
+        return;
+    }
+    if (cols > 0) store_c(p, at, a.x, old.x);
+    if (cols > 1) store_c(p, at + 1, a.y, old.y);
+    if (cols > 2) store_c(p, at + 2, a.z, old.z);
+    if (cols > 3) store_c(p, at + 3, a.w, old.w);
+}
+
+// YVEC: B has a scale for each of its rows (else one for each 128 x 128 block).
+template <bool YVEC>
+__global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+                    const Params p) {
+    using K_ = Wide<YVEC>;
+    constexpr int S = K_::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem0 = smem_u32(smem);
+    float *staging = reinterpret_cast<float *>(smem + S * W_STAGE);
+    float *scales = staging + PROMOTERS * W_STAGE_OUT / 4;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + W_SLOTS * K_::SLOT);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4 + 2 * W_SLOTS);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
+    auto tempty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    auto sfull = [&](int s) { return bar0 + 8u * (2 * S + 4 + s); };
+    auto sempty = [&](int s) { return bar0 + 8u * (2 * S + 4 + W_SLOTS + s); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int group = (int)blockIdx.x >> 1, groups = (int)gridDim.x >> 1;
+    const int units = p.tiles_x * p.tiles_y;
+    const uint64_t lim = p.wait_ns;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), 2 * PROMOTERS);   // of both CTAs, on the leader's
+        }
+        for (int s = 0; s < W_SLOTS; ++s) {
+            mbar_init(sfull(s), 1);
+            mbar_init(sempty(s), PROMOTERS);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&tm_x);
+        prefetch_map(&tm_y);
+    }
+    if (warp == 1) tmem_alloc<true>(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    cluster_sync_all();                            // the peer's barriers exist before anything arrives on them
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();                                    // a copy of an operand may precede this kernel
+
+    bool ok = true;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer
+            if (lane == 0) {
+                int s = 0, filled = 0;
+                uint32_t ph = 1;
+                const uint32_t lead_full0 = leader_addr(full(0));
+                for (int u = group; ok && u < units; u += groups) {
+                    int tx, ty;
+                    tile_of(p, u, tx, ty);
+                    const int m = ty * WT + (int)rank * BX, n = tx * WT + (int)rank * BX;
+                    for (int kb = 0; kb < p.nkb; ++kb) {
+                        if (!mbar_wait_for(empty(s), ph, lim, &g_error)) { ok = false; break; }
+                        const uint32_t x = smem0 + (uint32_t)(s * W_STAGE), y = x + X_BYTES;
+                        const uint32_t bar = lead_full0 + 8u * s;
+                        if (rank == 0) mbar_expect_tx(full(s), 2 * W_STAGE);
+                        if (p.x_mnmajor) tma_load_2d_pair(x, &tm_x, bar, m, kb * BK);
+                        else tma_load_2d_pair(x, &tm_x, bar, kb * BK, m);
+                        if (p.y_mnmajor) tma_load_2d_pair(y, &tm_y, bar, n, kb * BK);
+                        else tma_load_2d_pair(y, &tm_y, bar, kb * BK, n);
+                        ++filled;
+                        if (++s == S) { s = 0; ph ^= 1; }
+                    }
+                }
+                // copies in flight land (both CTAs', counted here) before shared memory goes
+                for (int i = 0; rank == 0 && i < min(filled, S); ++i) {
+                    if (s == 0) { s = S; ph ^= 1; }
+                    --s;
+                    mbar_wait_for<true>(full(s), ph ^ 1u, kDrainNs, &g_error);
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer (the leader's)
+            if (lane == 0 && rank == 0) {
+                int s = 0, b = 0, issued = 0;
+                uint32_t ph = 0, bph = 1;
+                const uint32_t x_step = p.x_mnmajor ? 4096u >> 4 : 32u >> 4;
+                const uint32_t y_step = p.y_mnmajor ? 4096u >> 4 : 32u >> 4;
+                for (int u = group; ok && u < units; u += groups) {
+                    for (int kb = 0; kb < p.nkb; ++kb) {
+                        if (!mbar_wait_for<true>(tempty(b), bph, lim, &g_error) ||
+                            !mbar_wait_for<true>(full(s), ph, lim, &g_error)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t x = smem0 + (uint32_t)(s * W_STAGE), y = x + X_BYTES;
+                        const uint64_t dx = smem_desc_8bit(x, X_BYTES), dy = smem_desc_8bit(y, X_BYTES);
+                        const uint32_t d = tmem + (uint32_t)(b * WT);
+#pragma unroll
+                        for (int i = 0; i < BK / 32; ++i)
+                            umma_8bit<true>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
+                        umma_commit_pair(empty(s));
+                        umma_commit_pair(tfull(b));
+                        ++issued;
+                        if (++s == S) { s = 0; ph ^= 1; }
+                        if (++b == 2) { b = 0; bph ^= 1; }
+                    }
+                }
+                if (issued > 0)                    // MMAs retire before tensor memory is freed
+                    mbar_wait_for(tfull((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------ scales
+            constexpr int J = K_::SLOT / 32, AHEAD = 2;
+            int slot = 0;
+            uint32_t ph = 1;
+            for (int u = group; ok && u < units; u += groups) {
+                int tx, ty;
+                tile_of(p, u, tx, ty);
+                const int m0 = ty * WT + (int)rank * BX, n0 = tx * WT;
+                auto row_scale = [&](int i, int kb) {     // A's, of this CTA's row i
+                    const int m = min(m0 + i, p.M - 1);
+                    return __ldg(p.SX + (int64_t)(m >> p.x_shift) * p.x_mn + (int64_t)kb * p.x_k);
+                };
+                // (the last block of columns may lie past N: any valid scale will do)
+                auto block_scale = [&](int h, int kb) {
+                    const int n = min(n0 + h * BX, p.N - 1);
+                    return __ldg(p.SY + (int64_t)(n >> 7) * p.y_mn + (int64_t)kb * p.y_k);
+                };
+                float v[AHEAD][J];
+                float c[AHEAD][2];
+                auto fetch = [&](int kb) {
+#pragma unroll
+                    for (int a = 0; a < AHEAD; ++a) {
+                        if (kb + a >= p.nkb) break;
+                        if (YVEC) {
+#pragma unroll
+                            for (int j = 0; j < WT / 32; ++j) {
+                                const int n = min(n0 + 32 * j + lane, p.N - 1);
+                                v[a][j] = __ldg(p.SY + (int64_t)n * p.y_mn + (int64_t)(kb + a) * p.y_k);
+                            }
+#pragma unroll
+                            for (int j = 0; j < BX / 32; ++j) v[a][WT / 32 + j < J ? WT / 32 + j : 0] = row_scale(32 * j + lane, kb + a);
+                        } else {
+                            c[a][0] = block_scale(0, kb + a);
+                            c[a][1] = block_scale(1, kb + a);
+#pragma unroll
+                            for (int j = 0; j < BX / 32; ++j) v[a][j] = row_scale(32 * j + lane, kb + a);
+                        }
+                    }
+                };
+                fetch(0);
+                for (int kb = 0; ok && kb < p.nkb; kb += AHEAD) {
+                    float t[AHEAD][J];
+#pragma unroll
+                    for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            t[a][j] = YVEC ? v[a][j] : __fmul_rn(v[a][j % (BX / 32)], c[a][j / (BX / 32)]);
+                    fetch(kb + AHEAD);
+#pragma unroll
+                    for (int a = 0; a < AHEAD; ++a) {
+                        if (kb + a >= p.nkb) break;
+                        if (!mbar_wait_for(sempty(slot), ph, lim, &g_error)) { ok = false; break; }
+#pragma unroll
+                        for (int j = 0; j < J; ++j) scales[slot * K_::SLOT + 32 * j + lane] = t[a][j];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sfull(slot));
+                        if (++slot == W_SLOTS) { slot = 0; ph ^= 1; }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ promotion and epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        constexpr int PC = WT / 2, CH = 32;
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
+        const uint32_t lead_tempty0 = leader_addr(tempty(0));
+        float *stg = staging + (warp - 4) * (W_STAGE_OUT / 4);
+        int b = 0, slot = 0;
+        uint32_t bph = 0, sph = 0;
+        for (int u = group; u < units; u += groups) {
+            int tx, ty;
+            tile_of(p, u, tx, ty);
+            float2 acc[PC / 2];
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                ok = mbar_wait_for(sfull(slot), sph, lim, &g_error);
+                const float *sc = scales + slot * K_::SLOT;
+                const float s = YVEC ? sc[WT + q * 32 + lane] : sc[half * BX + q * 32 + lane];
+                const float2 s2 = make_float2(s, s);
+                ok = ok && mbar_wait_for(tfull(b), bph, lim, &g_error);
+                if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t r[2][CH];
+                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+#pragma unroll
+                for (int c = 0; c < PC / CH; ++c) {
+                    tmem_ld_wait(r[c & 1]);
+                    if (c + 1 < PC / CH) {
+                        tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) & 1]);
+                    } else {                       // the buffer is read: hand it back
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) remote_arrive_relaxed(lead_tempty0 + 8u * b);
+                    }
+#pragma unroll
+                    for (int i = 0; i < CH; i += 4) {
+                        float2 t0 = make_float2(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1]));
+                        float2 t1 = make_float2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
+                        float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
+                        if (YVEC) {
+                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + half * PC + c * CH + i);
+                            t0 = __fmul2_rn(t0, s2);
+                            t1 = __fmul2_rn(t1, s2);
+                            a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
+                            a1 = __ffma2_rn(t1, make_float2(s4.z, s4.w), a1);
+                        } else {
+                            a0 = __ffma2_rn(t0, s2, a0);
+                            a1 = __ffma2_rn(t1, s2, a1);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty(slot));
+                if (++slot == W_SLOTS) { slot = 0; sph ^= 1; }
+                if (++b == 2) { b = 0; bph ^= 1; }
+            }
+            if (!ok) break;
+            // 32 x 32 blocks: lane = row in, 4 rows x 8 quads of columns out; the
+            // 16-byte chunk index is flipped by the row's low 3 bits
+            const int m0 = ty * WT + (int)rank * BX + q * 32, n0 = tx * WT + half * PC;
+#pragma unroll
+            for (int c = 0; c < PC / CH; ++c) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i) {
+                    const float2 a0 = acc[(c * CH + 4 * i) / 2], a1 = acc[(c * CH + 4 * i) / 2 + 1];
+                    *reinterpret_cast<float4 *>(stg + lane * 32 + ((i ^ (lane & 7)) << 2)) =
+                        make_float4(a0.x, a0.y, a1.x, a1.y);
+                }
+                __syncwarp();
+                const int n = n0 + c * CH + 4 * (lane & 7), cols = p.N - n;
+                float4 old[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int m = m0 + 4 * i + (lane >> 3);
+                    old[i] = p.beta != 0.0f && m < p.M ? load_c4(p, (int64_t)m * p.ldc + n, cols, p.c_vec != 0)
+                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3), m = m0 + r;
+                    const float4 v = *reinterpret_cast<const float4 *>(stg + r * 32 + (((lane & 7) ^ (r & 7)) << 2));
+                    if (m < p.M) store_c4(p, (int64_t)m * p.ldc + n, v, old[i], cols, p.c_vec != 0);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();                            // no CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free<true>(tmem, 512);
     }
 }
 
@@ -477,30 +826,30 @@ static bool byte_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BY, bool XVEC>
-static int launch_fp8(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
-                      int smem, cudaStream_t s, bool dep) {
-    auto kern = fp8g::fp8_gemm_kernel<BY, XVEC>;
-    static uint64_t attr_done = 0;   // bit d: the shared-memory opt-in is set on device d
+// One launch, with the shared-memory opt-in made once on each device (bit d of `done`).
+template <typename Kern>
+static int launch_kernel(Kern kern, uint64_t &done, const CUtensorMap &mx, const CUtensorMap &my,
+                         const fp8g::Params &p, int grid, int threads, int smem, int cluster, cudaStream_t s,
+                         bool dep) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-    if (!bit || !(__atomic_load_n(&attr_done, __ATOMIC_ACQUIRE) & bit)) {
+    if (!bit || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & bit)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fp8g::SMEM_MAX) !=
             cudaSuccess)
             return launch_status();
-        __atomic_fetch_or(&attr_done, bit, __ATOMIC_RELEASE);
+        __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(fp8g::THREADS);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (p.ksplit > 1) {
+    if (cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)p.ksplit;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
@@ -515,6 +864,22 @@ static int launch_fp8(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::
     cudaLaunchKernelEx(&cfg, kern, mx, my, p);
     timing_mark(s, false);
     return launch_status();
+}
+
+template <int BY, bool XVEC>
+static int launch_fp8(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
+                      int smem, cudaStream_t s, bool dep) {
+    static uint64_t done = 0;
+    return launch_kernel(fp8g::fp8_gemm_kernel<BY, XVEC>, done, mx, my, p, grid, fp8g::THREADS, smem, p.ksplit,
+                         s, dep);
+}
+
+template <bool YVEC>
+static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
+                       cudaStream_t s, bool dep) {
+    static uint64_t done = 0;
+    return launch_kernel(fp8g::fp8_wide_kernel<YVEC>, done, mx, my, p, grid, fp8g::W_THREADS,
+                         fp8g::Wide<YVEC>::SMEM, 1, s, dep);
 }
 
 template <int BY>
@@ -583,39 +948,51 @@ static int run_fp8(char ta, char tb, int64_t M, int64_t N, int64_t K, float alph
     if (ldb % 16 != 0) ldb = up16(ldb);
 
     const Fp8Plan pl = fp8_plan(M, N, K, sms);
-    const bool xvec = b_group == 1;
-    p.SX = SB; p.SY = SA;
-    p.x_mn = b_group == 1 || b_mn ? 1 : ldsb;      // blocks of B stored N x K: row by row
-    p.x_k = b_group == 1 || b_mn ? ldsb : 1;
-    p.y_mn = a_group == 1 || a_mn ? 1 : ldsa;
-    p.y_k = a_group == 1 || a_mn ? ldsa : 1;
-    p.y_shift = a_group == 1 ? 0 : 7;
-    p.x_mnmajor = b_mn; p.y_mnmajor = a_mn;
-    p.tiles_x = (int)((N + fp8g::BX - 1) / fp8g::BX);
-    p.tiles_y = (int)((M + pl.by - 1) / pl.by);
-    p.group_y = 16;
+    const bool dep = copy_a || copy_b;
+    // scales: strides along M or N and along the sum, for each operand
+    const int64_t a_mn_stride = a_group == 1 || a_mn ? 1 : ldsa, a_k_stride = a_group == 1 || a_mn ? ldsa : 1;
+    const int64_t b_mn_stride = b_group == 1 || b_mn ? 1 : ldsb, b_k_stride = b_group == 1 || b_mn ? ldsb : 1;
+    const int a_shift = a_group == 1 ? 0 : 7, b_shift = b_group == 1 ? 0 : 7;
     p.nkb = (int)fp8::blocks_of(K);
+    p.c_vec = reinterpret_cast<uintptr_t>(C) % (p.c_bf16 ? 8 : 16) == 0 && ldc % 4 == 0;
     p.ksplit = pl.ksplit;
-    p.y_bytes = a_mn ? (pl.by + 127) / 128 * fp8g::X_BYTES : pl.by * fp8g::BK;
+    p.wait_ns = tc_wait_limit();
+    const int a5 = a_type == SGEMM_TYPE_E5M2, b5 = b_type == SGEMM_TYPE_E5M2;
+    const int64_t tiles = ((N + pl.bx - 1) / pl.bx) * ((M + pl.by - 1) / pl.by);
+    if (tiles > INT32_MAX / 16) return SGEMM_ERR_UNSUPPORTED;
+    p.tiles_x = (int)((N + pl.bx - 1) / pl.bx);
+    p.tiles_y = (int)((M + pl.by - 1) / pl.by);
+    CUtensorMap mx, my;
+    if (pl.bx == fp8g::WT) {
+        // the wide kernel: X is A, Y is B
+        p.SX = SA; p.x_mn = a_mn_stride; p.x_k = a_k_stride; p.x_shift = a_shift; p.x_mnmajor = a_mn;
+        p.SY = SB; p.y_mn = b_mn_stride; p.y_k = b_k_stride; p.y_shift = b_shift; p.y_mnmajor = b_mn;
+        p.group_y = 8;
+        p.idesc = tc::idesc_8bit(a5, b5, a_mn, b_mn, fp8g::WT, fp8g::WT);
+        if (!byte_map(&mx, A, a_rows, a_cols, lda, 128) || !byte_map(&my, B, b_rows, b_cols, ldb, 128))
+            return SGEMM_ERR_UNSUPPORTED;
+        const int grid = 2 * (int)std::min<int64_t>(tiles, std::max(sms / 2, 1));
+        return b_group == 1 ? launch_wide<true>(mx, my, p, grid, s, dep)
+                            : launch_wide<false>(mx, my, p, grid, s, dep);
+    }
+    // the narrow kernel: X is B, Y is A
+    p.SX = SB; p.x_mn = b_mn_stride; p.x_k = b_k_stride; p.x_shift = b_shift; p.x_mnmajor = b_mn;
+    p.SY = SA; p.y_mn = a_mn_stride; p.y_k = a_k_stride; p.y_shift = a_shift; p.y_mnmajor = a_mn;
+    p.group_y = 16;
+    p.y_bytes = a_mn ? fp8g::X_BYTES : pl.by * fp8g::BK;
     const int fixed = 1024 + fp8g::SCALE_SLOTS * pl.by * 4 + fp8g::BAR_BYTES;
     p.stages = std::min(fp8g::MAX_STAGES, (fp8g::SMEM_MAX - fixed) / (fp8g::X_BYTES + p.y_bytes));
-    p.idesc = tc::idesc_8bit(b_type == SGEMM_TYPE_E5M2, a_type == SGEMM_TYPE_E5M2, b_mn, a_mn, fp8g::BX, pl.by);
-    p.wait_ns = tc_wait_limit();
-    CUtensorMap mx, my;
-    if (!byte_map(&mx, B, b_rows, b_cols, ldb, 128) ||
-        !byte_map(&my, A, a_rows, a_cols, lda, a_mn ? 128 : pl.by))
+    p.idesc = tc::idesc_8bit(b5, a5, b_mn, a_mn, fp8g::BX, pl.by);
+    if (!byte_map(&mx, B, b_rows, b_cols, ldb, 128) || !byte_map(&my, A, a_rows, a_cols, lda, a_mn ? 128 : pl.by))
         return SGEMM_ERR_UNSUPPORTED;
-    const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
-    if (tiles > INT32_MAX / 16) return SGEMM_ERR_UNSUPPORTED;
     const int grid = p.ksplit > 1 ? (int)tiles * p.ksplit : (int)std::min<int64_t>(tiles, sms);
     const int smem = fixed + p.stages * (fp8g::X_BYTES + p.y_bytes);
-    const bool dep = copy_a || copy_b;
+    const bool xvec = b_group == 1;
     switch (pl.by) {
     case 16: return launch_fp8<16>(xvec, mx, my, p, grid, smem, s, dep);
     case 32: return launch_fp8<32>(xvec, mx, my, p, grid, smem, s, dep);
     case 64: return launch_fp8<64>(xvec, mx, my, p, grid, smem, s, dep);
-    case 128: return launch_fp8<128>(xvec, mx, my, p, grid, smem, s, dep);
-    default: return launch_fp8<256>(xvec, mx, my, p, grid, smem, s, dep);
+    default: return launch_fp8<128>(xvec, mx, my, p, grid, smem, s, dep);
     }
 }
 
@@ -672,7 +1049,7 @@ extern "C" int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int 
     if (num_sms <= 0) return -4;
     const Fp8Plan pl = fp8_plan(M, N, K, num_sms);
     if (out_tile_m) *out_tile_m = pl.by;
-    if (out_tile_n) *out_tile_n = 128;
+    if (out_tile_n) *out_tile_n = pl.bx;
     if (out_ksplit) *out_ksplit = pl.ksplit;
     return SGEMM_OK;
 }
