@@ -434,7 +434,7 @@ constexpr int W_STAGE_OUT = 32 * 32 * 4;       // epilogue staging per promoting
 
 template <bool YVEC>
 struct Wide {
-    static constexpr int SLOT = YVEC ? WT + BX : WT;   // floats: columns' then rows' scales, or their products
+    static constexpr int SLOT = BX + (YVEC ? WT : 32);   // floats: rows' scales, then columns' (or two blocks')
     static constexpr int FIXED = 1024 + PROMOTERS * W_STAGE_OUT + W_SLOTS * SLOT * 4 + BAR_BYTES;
     static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
     static constexpr int SMEM = FIXED + STAGES * W_STAGE;
@@ -473,6 +473,54 @@ __device__ __forceinline__ void store_c4(const Params &p, int64_t at, float4 a, 
     if (cols > 1) store_c(p, at + 1, a.y, old.y);
     if (cols > 2) store_c(p, at + 2, a.z, old.z);
     if (cols > 3) store_c(p, at + 3, a.w, old.w);
+}
+
+// The scale warp: for each block of k the CTA's 128 rows' scales and the columns'
+// (256, or one for each half of them) into a slot, copied asynchronously so that
+// W_SLOTS blocks are under way at once and no register waits for memory.  Scales of
+// single rows or columns are neighbours in memory.  Rows and columns past the
+// matrix take its last scale: any valid one will do.
+template <bool YVEC>
+__device__ __forceinline__ void scale_role(const Params &p, uint32_t rank, int group, int groups, float *scales,
+                                           uint32_t sfull0, uint32_t sempty0) {
+    constexpr int JX = BX / 32, JY = YVEC ? WT / 32 : 1;
+    const int lane = threadIdx.x & 31, units = p.tiles_x * p.tiles_y;
+    const uint32_t to = smem_u32(scales) + 4u * (uint32_t)lane;
+    int slot = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int u = group; ok && u < units; u += groups) {
+        int tx, ty;
+        tile_of(p, u, tx, ty);
+        const int x0 = min(ty * WT + (int)rank * BX, p.M - 1), y0 = min(tx * WT, p.N - 1);
+        const float *sx = p.SX + (int64_t)(x0 >> p.x_shift) * p.x_mn;
+        const float *sy = p.SY + (int64_t)(y0 >> p.y_shift) * p.y_mn;
+        int ox[JX], oy[JY];
+#pragma unroll
+        for (int j = 0; j < JX; ++j) ox[j] = p.x_shift ? 0 : min(32 * j + lane, p.M - 1 - x0);
+#pragma unroll
+        for (int j = 0; j < JY; ++j) oy[j] = min(32 * j + lane, p.N - 1 - y0);
+        // (one scale of B per block: lane 1 takes the second block's, if there is one)
+        if (!YVEC && lane == 1 && y0 + BX < p.N) sy += p.y_mn;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+            const bool go = mbar_wait_for(sempty0 + 8u * slot, ph, p.wait_ns, &g_error);
+            if (__any_sync(0xffffffffu, !go)) { ok = false; break; }
+            const uint32_t at = to + 4u * (uint32_t)(slot * Wide<YVEC>::SLOT);
+#pragma unroll
+            for (int j = 0; j < JX; ++j) cp_async_4(at + 128u * j, sx + ox[j], 4);
+            if (YVEC) {
+#pragma unroll
+                for (int j = 0; j < JY; ++j) cp_async_4(at + 4u * BX + 128u * j, sy + oy[j], 4);
+            } else if (lane < 2) {
+                cp_async_4(at + 4u * BX, sy, 4);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull0 + 8u * slot) : "memory");
+            sx += p.x_k;
+            sy += p.y_k;
+            if (++slot == W_SLOTS) { slot = 0; ph ^= 1; }
+        }
+    }
+    cp_async_wait_all();
 }
 
 // YVEC: B has a scale for each of its rows (else one for each 128 x 128 block).
@@ -514,7 +562,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(tempty(b), 2 * PROMOTERS);   // of both CTAs, on the leader's
         }
         for (int s = 0; s < W_SLOTS; ++s) {
-            mbar_init(sfull(s), 1);
+            mbar_init(sfull(s), 32);               // each lane's copies
             mbar_init(sempty(s), PROMOTERS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -530,7 +578,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
 
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             // ------------------------------------------------ TMA producer
             if (lane == 0) {
@@ -590,71 +638,12 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                     mbar_wait_for(tfull((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
             }
         } else if (warp == 2) {
-            // ------------------------------------------------ scales
-            constexpr int J = K_::SLOT / 32, AHEAD = 2;
-            int slot = 0;
-            uint32_t ph = 1;
-            for (int u = group; ok && u < units; u += groups) {
-                int tx, ty;
-                tile_of(p, u, tx, ty);
-                const int m0 = ty * WT + (int)rank * BX, n0 = tx * WT;
-                auto row_scale = [&](int i, int kb) {     // A's, of this CTA's row i
-                    const int m = min(m0 + i, p.M - 1);
-                    return __ldg(p.SX + (int64_t)(m >> p.x_shift) * p.x_mn + (int64_t)kb * p.x_k);
-                };
-                // (the last block of columns may lie past N: any valid scale will do)
-                auto block_scale = [&](int h, int kb) {
-                    const int n = min(n0 + h * BX, p.N - 1);
-                    return __ldg(p.SY + (int64_t)(n >> 7) * p.y_mn + (int64_t)kb * p.y_k);
-                };
-                float v[AHEAD][J];
-                float c[AHEAD][2];
-                auto fetch = [&](int kb) {
-#pragma unroll
-                    for (int a = 0; a < AHEAD; ++a) {
-                        if (kb + a >= p.nkb) break;
-                        if (YVEC) {
-#pragma unroll
-                            for (int j = 0; j < WT / 32; ++j) {
-                                const int n = min(n0 + 32 * j + lane, p.N - 1);
-                                v[a][j] = __ldg(p.SY + (int64_t)n * p.y_mn + (int64_t)(kb + a) * p.y_k);
-                            }
-#pragma unroll
-                            for (int j = 0; j < BX / 32; ++j) v[a][WT / 32 + j < J ? WT / 32 + j : 0] = row_scale(32 * j + lane, kb + a);
-                        } else {
-                            c[a][0] = block_scale(0, kb + a);
-                            c[a][1] = block_scale(1, kb + a);
-#pragma unroll
-                            for (int j = 0; j < BX / 32; ++j) v[a][j] = row_scale(32 * j + lane, kb + a);
-                        }
-                    }
-                };
-                fetch(0);
-                for (int kb = 0; ok && kb < p.nkb; kb += AHEAD) {
-                    float t[AHEAD][J];
-#pragma unroll
-                    for (int a = 0; a < AHEAD; ++a)
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            t[a][j] = YVEC ? v[a][j] : __fmul_rn(v[a][j % (BX / 32)], c[a][j / (BX / 32)]);
-                    fetch(kb + AHEAD);
-#pragma unroll
-                    for (int a = 0; a < AHEAD; ++a) {
-                        if (kb + a >= p.nkb) break;
-                        if (!mbar_wait_for(sempty(slot), ph, lim, &g_error)) { ok = false; break; }
-#pragma unroll
-                        for (int j = 0; j < J; ++j) scales[slot * K_::SLOT + 32 * j + lane] = t[a][j];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sfull(slot));
-                        if (++slot == W_SLOTS) { slot = 0; ph ^= 1; }
-                    }
-                }
-            }
+            scale_role<YVEC>(p, rank, group, groups, scales, sfull(0), sempty(0));
         }
         __syncwarp();
     } else {
         // ------------------------------------------------ promotion and epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         constexpr int PC = WT / 2, CH = 32;
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
@@ -671,7 +660,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
             for (int kb = 0; kb < p.nkb; ++kb) {
                 ok = mbar_wait_for(sfull(slot), sph, lim, &g_error);
                 const float *sc = scales + slot * K_::SLOT;
-                const float s = YVEC ? sc[WT + q * 32 + lane] : sc[half * BX + q * 32 + lane];
+                float s = sc[q * 32 + lane];
+                if (!YVEC) s = __fmul_rn(s, sc[BX + half]);
                 const float2 s2 = make_float2(s, s);
                 ok = ok && mbar_wait_for(tfull(b), bph, lim, &g_error);
                 if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
@@ -694,7 +684,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                         float2 t1 = make_float2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
                         float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
                         if (YVEC) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + half * PC + c * CH + i);
+                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + BX + half * PC + c * CH + i);
                             t0 = __fmul2_rn(t0, s2);
                             t1 = __fmul2_rn(t1, s2);
                             a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
