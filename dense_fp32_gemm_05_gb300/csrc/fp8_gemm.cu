@@ -89,6 +89,11 @@ struct Params {
     unsigned long long wait_ns;
 };
 
+// Bounded wait by a converged warp: true when every lane's was.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, limit, &g_error));
+}
+
 // Tile u of the grouped raster: group_y tile rows of C at a time, so that the
 // tiles in flight share operand panels in L2.
 __device__ __forceinline__ void tile_of(const Params &p, int u, int &tx, int &ty) {
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto sfull = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + 4 + s); };
     auto sempty = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + 4 + SCALE_SLOTS + s); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int ks = p.ksplit;
     const int rank = ks > 1 ? (int)cluster_rank() : 0;
     const int group = (int)blockIdx.x / ks, groups = (int)gridDim.x / ks;
@@ -189,22 +194,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
+        {
             int s = 0, filled = 0;
             uint32_t ph = 1;                       // an empty stage's first wait passes
             for (int u = group; ok && u < units; u += groups) {
                 int tx, ty;
                 tile_of(p, u, tx, ty);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_for(empty(s), ph, lim, &g_error)) { ok = false; break; }
+                    if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
                     const uint32_t x = smem0 + (uint32_t)(s * stage_bytes), y = x + X_BYTES;
-                    mbar_expect_tx(full(s), (uint32_t)stage_bytes);
-                    if (p.x_mnmajor) tma_load_2d(x, &tm_x, full(s), tx * BX, kb * BK);
-                    else tma_load_2d(x, &tm_x, full(s), kb * BK, tx * BX);
-                    if (p.y_mnmajor) {
-                        tma_load_2d(y, &tm_y, full(s), ty * BY, kb * BK);
-                    } else {
-                        tma_load_2d(y, &tm_y, full(s), kb * BK, ty * BY);
+                    const int k = kb * BK, n = tx * BX, m = ty * BY;
+                    if (elect_one()) {
+                        mbar_expect_tx(full(s), (uint32_t)stage_bytes);
+                        tma_load_2d(x, &tm_x, full(s), p.x_mnmajor ? n : k, p.x_mnmajor ? k : n);
+                        tma_load_2d(y, &tm_y, full(s), p.y_mnmajor ? m : k, p.y_mnmajor ? k : m);
                     }
                     ++filled;
                     if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -221,24 +224,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
             int s = 0, b = 0, issued = 0;
             uint32_t ph = 0, bph = 1;
             const uint32_t x_step = p.x_mnmajor ? 4096u >> 4 : 32u >> 4;
             const uint32_t y_step = p.y_mnmajor ? 4096u >> 4 : 32u >> 4;
             for (int u = group; ok && u < units; u += groups) {
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait_for(tempty(b), bph, lim, &g_error) ||
-                        !mbar_wait_for(full(s), ph, lim, &g_error)) { ok = false; break; }
+                    if (!warp_wait(full(s), ph, lim) || !warp_wait(tempty(b), bph, lim)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t x = smem0 + (uint32_t)(s * stage_bytes), y = x + X_BYTES;
                     const uint64_t dx = smem_desc_8bit(x, X_BYTES), dy = smem_desc_8bit(y, X_BYTES);
                     const uint32_t d = tmem + (uint32_t)(b * BY);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < BK / 32; ++i)
-                        umma_8bit<false>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
-                    umma_commit(empty(s));
-                    umma_commit(tfull(b));
+                        for (int i = 0; i < BK / 32; ++i)
+                            umma_8bit<false>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
+                        umma_commit(empty(s));
+                        umma_commit(tfull(b));
+                    }
                     ++issued;
                     if (++s == p.stages) { s = 0; ph ^= 1; }
                     if (++b == 2) { b = 0; bph ^= 1; }
@@ -427,15 +431,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 // share: the three issuing warps hand theirs over (setmaxnreg).
 // The epilogue turns 32 x 32 blocks around through shared memory.
 constexpr int WT = 256;                        // tile rows and columns
-constexpr int W_THREADS = 384;                 // TMA, MMA, scales, idle, 8 promoters
+constexpr int W_THREADS = 384;                 // TMA, MMA, 2 idle (a warpgroup), 8 promoters
 constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
-constexpr int W_SLOTS = 6;                     // scale slots
 constexpr int W_STAGE_OUT = 32 * 32 * 4;       // epilogue staging per promoting warp
 
 template <bool YVEC>
 struct Wide {
-    static constexpr int SLOT = BX + (YVEC ? WT : 32);   // floats: rows' scales, then columns' (or two blocks')
-    static constexpr int FIXED = 1024 + PROMOTERS * W_STAGE_OUT + W_SLOTS * SLOT * 4 + BAR_BYTES;
+    // YVEC: the scales of a promoting warp's 128 columns, in a ring of its own
+    static constexpr int SLOTS = YVEC ? 6 : 0;
+    static constexpr int RING = SLOTS * (WT / 2);          // floats
+    static constexpr int FIXED = 1024 + PROMOTERS * (W_STAGE_OUT + RING * 4) + BAR_BYTES;
     static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
     static constexpr int SMEM = FIXED + STAGES * W_STAGE;
     static_assert(STAGES >= 4 && STAGES <= MAX_STAGES, "stages");
@@ -475,54 +480,6 @@ __device__ __forceinline__ void store_c4(const Params &p, int64_t at, float4 a, 
     if (cols > 3) store_c(p, at + 3, a.w, old.w);
 }
 
-// The scale warp: for each block of k the CTA's 128 rows' scales and the columns'
-// (256, or one for each half of them) into a slot, copied asynchronously so that
-// W_SLOTS blocks are under way at once and no register waits for memory.  Scales of
-// single rows or columns are neighbours in memory.  Rows and columns past the
-// matrix take its last scale: any valid one will do.
-template <bool YVEC>
-__device__ __forceinline__ void scale_role(const Params &p, uint32_t rank, int group, int groups, float *scales,
-                                           uint32_t sfull0, uint32_t sempty0) {
-    constexpr int JX = BX / 32, JY = YVEC ? WT / 32 : 1;
-    const int lane = threadIdx.x & 31, units = p.tiles_x * p.tiles_y;
-    const uint32_t to = smem_u32(scales) + 4u * (uint32_t)lane;
-    int slot = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-    for (int u = group; ok && u < units; u += groups) {
-        int tx, ty;
-        tile_of(p, u, tx, ty);
-        const int x0 = min(ty * WT + (int)rank * BX, p.M - 1), y0 = min(tx * WT, p.N - 1);
-        const float *sx = p.SX + (int64_t)(x0 >> p.x_shift) * p.x_mn;
-        const float *sy = p.SY + (int64_t)(y0 >> p.y_shift) * p.y_mn;
-        int ox[JX], oy[JY];
-#pragma unroll
-        for (int j = 0; j < JX; ++j) ox[j] = p.x_shift ? 0 : min(32 * j + lane, p.M - 1 - x0);
-#pragma unroll
-        for (int j = 0; j < JY; ++j) oy[j] = min(32 * j + lane, p.N - 1 - y0);
-        // (one scale of B per block: lane 1 takes the second block's, if there is one)
-        if (!YVEC && lane == 1 && y0 + BX < p.N) sy += p.y_mn;
-        for (int kb = 0; kb < p.nkb; ++kb) {
-            const bool go = mbar_wait_for(sempty0 + 8u * slot, ph, p.wait_ns, &g_error);
-            if (__any_sync(0xffffffffu, !go)) { ok = false; break; }
-            const uint32_t at = to + 4u * (uint32_t)(slot * Wide<YVEC>::SLOT);
-#pragma unroll
-            for (int j = 0; j < JX; ++j) cp_async_4(at + 128u * j, sx + ox[j], 4);
-            if (YVEC) {
-#pragma unroll
-                for (int j = 0; j < JY; ++j) cp_async_4(at + 4u * BX + 128u * j, sy + oy[j], 4);
-            } else if (lane < 2) {
-                cp_async_4(at + 4u * BX, sy, 4);
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull0 + 8u * slot) : "memory");
-            sx += p.x_k;
-            sy += p.y_k;
-            if (++slot == W_SLOTS) { slot = 0; ph ^= 1; }
-        }
-    }
-    cp_async_wait_all();
-}
-
 // YVEC: B has a scale for each of its rows (else one for each 128 x 128 block).
 template <bool YVEC>
 __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
@@ -536,17 +493,15 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
     const uint32_t smem0 = smem_u32(smem);
     float *staging = reinterpret_cast<float *>(smem + S * W_STAGE);
     float *scales = staging + PROMOTERS * W_STAGE_OUT / 4;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + W_SLOTS * K_::SLOT);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4 + 2 * W_SLOTS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + PROMOTERS * K_::RING);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
     auto tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
     auto tempty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
-    auto sfull = [&](int s) { return bar0 + 8u * (2 * S + 4 + s); };
-    auto sempty = [&](int s) { return bar0 + 8u * (2 * S + 4 + W_SLOTS + s); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int group = (int)blockIdx.x >> 1, groups = (int)gridDim.x >> 1;
     const int units = p.tiles_x * p.tiles_y;
@@ -561,10 +516,6 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
             mbar_init(tfull(b), 1);
             mbar_init(tempty(b), 2 * PROMOTERS);   // of both CTAs, on the leader's
         }
-        for (int s = 0; s < W_SLOTS; ++s) {
-            mbar_init(sfull(s), 32);               // each lane's copies
-            mbar_init(sempty(s), PROMOTERS);
-        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&tm_x);
         prefetch_map(&tm_y);
@@ -578,10 +529,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
 
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             // ------------------------------------------------ TMA producer
-            if (lane == 0) {
+            {
                 int s = 0, filled = 0;
                 uint32_t ph = 1;
                 const uint32_t lead_full0 = leader_addr(full(0));
@@ -590,14 +541,15 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                     tile_of(p, u, tx, ty);
                     const int m = ty * WT + (int)rank * BX, n = tx * WT + (int)rank * BX;
                     for (int kb = 0; kb < p.nkb; ++kb) {
-                        if (!mbar_wait_for(empty(s), ph, lim, &g_error)) { ok = false; break; }
+                        if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
                         const uint32_t x = smem0 + (uint32_t)(s * W_STAGE), y = x + X_BYTES;
                         const uint32_t bar = lead_full0 + 8u * s;
-                        if (rank == 0) mbar_expect_tx(full(s), 2 * W_STAGE);
-                        if (p.x_mnmajor) tma_load_2d_pair(x, &tm_x, bar, m, kb * BK);
-                        else tma_load_2d_pair(x, &tm_x, bar, kb * BK, m);
-                        if (p.y_mnmajor) tma_load_2d_pair(y, &tm_y, bar, n, kb * BK);
-                        else tma_load_2d_pair(y, &tm_y, bar, kb * BK, n);
+                        const int k = kb * BK;
+                        if (elect_one()) {
+                            if (rank == 0) mbar_expect_tx(full(s), 2 * W_STAGE);
+                            tma_load_2d_pair(x, &tm_x, bar, p.x_mnmajor ? m : k, p.x_mnmajor ? k : m);
+                            tma_load_2d_pair(y, &tm_y, bar, p.y_mnmajor ? n : k, p.y_mnmajor ? k : n);
+                        }
                         ++filled;
                         if (++s == S) { s = 0; ph ^= 1; }
                     }
@@ -606,29 +558,30 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                 for (int i = 0; rank == 0 && i < min(filled, S); ++i) {
                     if (s == 0) { s = S; ph ^= 1; }
                     --s;
-                    mbar_wait_for<true>(full(s), ph ^ 1u, kDrainNs, &g_error);
+                    mbar_wait_for(full(s), ph ^ 1u, kDrainNs, &g_error);
                 }
             }
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer (the leader's)
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 int s = 0, b = 0, issued = 0;
                 uint32_t ph = 0, bph = 1;
                 const uint32_t x_step = p.x_mnmajor ? 4096u >> 4 : 32u >> 4;
                 const uint32_t y_step = p.y_mnmajor ? 4096u >> 4 : 32u >> 4;
                 for (int u = group; ok && u < units; u += groups) {
                     for (int kb = 0; kb < p.nkb; ++kb) {
-                        if (!mbar_wait_for<true>(tempty(b), bph, lim, &g_error) ||
-                            !mbar_wait_for<true>(full(s), ph, lim, &g_error)) { ok = false; break; }
+                        if (!warp_wait(full(s), ph, lim) || !warp_wait(tempty(b), bph, lim)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t x = smem0 + (uint32_t)(s * W_STAGE), y = x + X_BYTES;
                         const uint64_t dx = smem_desc_8bit(x, X_BYTES), dy = smem_desc_8bit(y, X_BYTES);
                         const uint32_t d = tmem + (uint32_t)(b * WT);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < BK / 32; ++i)
-                            umma_8bit<true>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
-                        umma_commit_pair(empty(s));
-                        umma_commit_pair(tfull(b));
+                            for (int i = 0; i < BK / 32; ++i)
+                                umma_8bit<true>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
+                            umma_commit_pair(empty(s));
+                            umma_commit_pair(tfull(b));
+                        }
                         ++issued;
                         if (++s == S) { s = 0; ph ^= 1; }
                         if (++b == 2) { b = 0; bph ^= 1; }
@@ -637,46 +590,113 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (issued > 0)                    // MMAs retire before tensor memory is freed
                     mbar_wait_for(tfull((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
             }
-        } else if (warp == 2) {
-            scale_role<YVEC>(p, rank, group, groups, scales, sfull(0), sempty(0));
         }
         __syncwarp();
     } else {
         // ------------------------------------------------ promotion and epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        constexpr int PC = WT / 2, CH = 32;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        constexpr int PC = WT / 2, CH = 32, NC = PC / CH;
+        constexpr int BATCH = YVEC ? 2 : 4;        // blocks whose scales are fetched together
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
         const uint32_t lead_tempty0 = leader_addr(tempty(0));
         float *stg = staging + (warp - 4) * (W_STAGE_OUT / 4);
+        const float *ring = scales + (warp - 4) * K_::RING;
+
+        // Scales are fetched a batch ahead, across tiles: what a block of k costs
+        // beside reading and adding its sums is what bounds this role, so nothing
+        // here waits for memory.  The row's (and the columns' block's) go to
+        // registers, single columns' to the warp's ring (asynchronous copies
+        // complete in order: no barrier).  Rows and columns past the matrix take its
+        // last scale: any valid one will do.
+        int fu = group, fkb = 0, fslot = 0;        // the batch to fetch next
+        const float *fx = nullptr, *fy = nullptr;
+        int fo[YVEC ? 4 : 1];
+        float nx[BATCH], ny[BATCH];
+        auto fetch = [&]() {
+            if (fu < units) {
+                if (fkb == 0) {
+                    int tx, ty;
+                    tile_of(p, fu, tx, ty);
+                    const int m = min(ty * WT + (int)rank * BX + q * 32 + lane, p.M - 1);
+                    const int n = min(tx * WT + half * PC, p.N - 1);
+                    fx = p.SX + (int64_t)(m >> p.x_shift) * p.x_mn;
+                    fy = p.SY + (int64_t)(n >> p.y_shift) * p.y_mn;
+                    if (YVEC)                      // scales of single columns are neighbours
+#pragma unroll
+                        for (int j = 0; j < (YVEC ? 4 : 1); ++j) fo[j] = min(32 * j + lane, p.N - 1 - n);
+                }
+#pragma unroll
+                for (int a = 0; a < BATCH; ++a) {
+                    if (fkb + a < p.nkb) {
+                        nx[a] = __ldg(fx);
+                        if (!YVEC) ny[a] = __ldg(fy);
+                        if (YVEC) {
+                            const uint32_t to = smem_u32(ring + (fslot + a) * PC) + 4u * (uint32_t)lane;
+#pragma unroll
+                            for (int j = 0; j < (YVEC ? 4 : 1); ++j) cp_async_4(to + 128u * j, fy + fo[j], 4);
+                        }
+                        fx += p.x_k;
+                        fy += p.y_k;
+                    }
+                }
+                fkb += BATCH;
+                if (fkb >= p.nkb) { fkb = 0; fu += groups; }
+                if (YVEC && (fslot += BATCH) == K_::SLOTS) fslot = 0;
+            }
+            if (YVEC) cp_async_commit();
+        };
+        fetch();
+
         int b = 0, slot = 0;
-        uint32_t bph = 0, sph = 0;
-        for (int u = group; u < units; u += groups) {
+        uint32_t bph = 0;
+        uint32_t r[2][CH];
+        // waits for the next buffer and starts reading it
+        auto next_buffer = [&]() {
+            ok = warp_wait(tfull(b), bph, lim);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+            }
+        };
+        for (int u = group; ok && u < units; u += groups) {
             int tx, ty;
             tile_of(p, u, tx, ty);
             float2 acc[PC / 2];
 #pragma unroll
             for (int i = 0; i < PC / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            float sv[BATCH];
+            // (no tensor-memory read is under way across the epilogue: its registers could be moved)
+            next_buffer();
+            if (!ok) break;
             for (int kb = 0; kb < p.nkb; ++kb) {
-                ok = mbar_wait_for(sfull(slot), sph, lim, &g_error);
-                const float *sc = scales + slot * K_::SLOT;
-                float s = sc[q * 32 + lane];
-                if (!YVEC) s = __fmul_rn(s, sc[BX + half]);
-                const float2 s2 = make_float2(s, s);
-                ok = ok && mbar_wait_for(tfull(b), bph, lim, &g_error);
-                if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
-                tc_fence_after();
-                uint32_t r[2][CH];
-                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+                if (kb % BATCH == 0) {
 #pragma unroll
-                for (int c = 0; c < PC / CH; ++c) {
+                    for (int a = 0; a < BATCH; ++a) sv[a] = YVEC ? nx[a] : __fmul_rn(nx[a], ny[a]);
+                    fetch();
+                    if (YVEC) {
+                        cp_async_wait_group<1>();  // all but the batch just begun
+                        __syncwarp();
+                    }
+                }
+                const float2 s2 = make_float2(sv[0], sv[0]);
+#pragma unroll
+                for (int a = 0; a + 1 < BATCH; ++a) sv[a] = sv[a + 1];
+                const float *sc = ring + slot * PC;
+                if (YVEC && ++slot == K_::SLOTS) slot = 0;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
                     tmem_ld_wait(r[c & 1]);
-                    if (c + 1 < PC / CH) {
+                    if (c + 1 < NC) {
                         tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) & 1]);
-                    } else {                       // the buffer is read: hand it back
+                    } else {
+                        // the buffer is read: hand it back, and start on the next one
+                        // while this chunk is added
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) remote_arrive_relaxed(lead_tempty0 + 8u * b);
+                        if (++b == 2) { b = 0; bph ^= 1; }
+                        if (kb + 1 < p.nkb) next_buffer();
                     }
 #pragma unroll
                     for (int i = 0; i < CH; i += 4) {
@@ -684,7 +704,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                         float2 t1 = make_float2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
                         float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
                         if (YVEC) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + BX + half * PC + c * CH + i);
+                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + c * CH + i);
                             t0 = __fmul2_rn(t0, s2);
                             t1 = __fmul2_rn(t1, s2);
                             a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
@@ -695,12 +715,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sempty(slot));
-                if (++slot == W_SLOTS) { slot = 0; sph ^= 1; }
-                if (++b == 2) { b = 0; bph ^= 1; }
+                if (!ok) break;
             }
             if (!ok) break;
+            // a tile ends within a batch: the ring's place of the next one
+            if (YVEC && p.nkb % BATCH != 0 && (slot += BATCH - p.nkb % BATCH) >= K_::SLOTS) slot -= K_::SLOTS;
             // 32 x 32 blocks: lane = row in, 4 rows x 8 quads of columns out; the
             // 16-byte chunk index is flipped by the row's low 3 bits
             const int m0 = ty * WT + (int)rank * BX + q * 32, n0 = tx * WT + half * PC;
@@ -730,6 +749,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                 }
             }
         }
+        if (YVEC) cp_async_wait_all();
     }
 
     tc_fence_before();

@@ -298,19 +298,18 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
 
 // As mbar_wait of the kernels, with the error word given: waits for the phase
 // of `parity`, at most limit_ns; false (and `error` set) when that passes first.
-template <bool CLUSTER = false>
+// A limit below a microsecond (the timer may be no finer) allows one test and no
+// wait.
 __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                               unsigned int *error) {
-    auto ready = [&] { return CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); };
-    if (ready()) return true;
+    if (mbar_test(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (ready()) return true;
-        if (global_timer_ns() - t0 > limit_ns) {
-            atomicExch(error, (unsigned)SGEMM_ERR_TIMEOUT);
-            return false;
-        }
+    while (limit_ns >= 1000) {
+        if (mbar_try(bar, parity)) return true;
+        if (global_timer_ns() - t0 > limit_ns) break;
     }
+    atomicExch(error, (unsigned)SGEMM_ERR_TIMEOUT);
+    return false;
 }
 
 // Hand-back of a TMEM buffer to the pair's leader, once for each k-block:
@@ -319,6 +318,25 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
 __device__ __forceinline__ void remote_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
                  :: "r"(cluster_addr) : "memory");
+}
+
+// One lane of a converged warp (the same one every time).  Roles that issue MMAs
+// or TMA loads run with the whole warp and elect a lane for the instruction itself:
+// descriptors and addresses then stay in uniform registers.  Under "if (lane ==
+// 0)" each operand is moved there first; 4 MMAs and 2 commits took ~400 clocks
+// to issue that way, whatever their size.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok));
+    return ok != 0;
+}
+
+// The warp's index, known to be the same in all its lanes.
+__device__ __forceinline__ int warp_index() {
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 }
 
 }  // namespace tc
