@@ -26,7 +26,7 @@
 //     timing.
 //
 // Phases, one CTA per SM, cooperative launch:
-//   0  router logits: tiles of 8 tokens x 8 experts x a slice of D over the CTAs
+//   0  router logits: tiles of 8 tokens x 4 experts x a slice of D over the CTAs
 //      (fp32 FMAs), then a grid barrier; every CTA then works out the routing
 //      (softmax, top-k, the experts' token lists) for itself;
 //   1  h = silu(gate x) * (up x): tiles of 64 gate rows and the same 64 up rows.
@@ -35,8 +35,8 @@
 //      and 2: the weights' stream goes on across it;
 //   3  after a third barrier y = sum over a token's experts, all threads.
 //
-// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-5 split activations
-// into the MMA's column operand; 6-9 promotion (128 rows, one per thread).
+// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-11 split activations
+// into the MMA's column operand; 12-15 promotion (128 rows, one per thread).
 // Every wait is bounded: a role that gives up sets the device error word and
 // stops; every CTA still arrives at every grid barrier, so that the counters
 // are whole again when the kernel ends.
@@ -63,8 +63,9 @@ using namespace tc;
 constexpr int BK = fp8::GROUP;
 constexpr int ROWS = 128;                      // weight rows of a tile (64 gate + 64 up, or 128 down)
 constexpr int A_BYTES = ROWS * BK;
-constexpr int SPLITTERS = 4;                   // warps 2..5
-constexpr int THREADS = 320;
+constexpr int SPLITTERS = 10;                  // warps 2..11
+constexpr int PROMOTER0 = 2 + SPLITTERS;       // the first of the 4 promoting warps
+constexpr int THREADS = 32 * (PROMOTER0 + 4);
 constexpr int MAX_T = 128, MAX_E = 512, MAX_TOPK = 16;
 constexpr int MAX_SLOTS = MAX_T * MAX_TOPK;
 constexpr int MAX_CHUNKS = 2 * MAX_E;          // (expert, up to NT of its tokens)
@@ -77,9 +78,9 @@ __device__ unsigned int g_error;               // sticky device error word of th
 // NT: tokens of one expert that a tile takes (columns for each part).
 template <int NT>
 struct Cfg {
-    static constexpr int A_STAGES = NT <= 8 ? 10 : NT <= 16 ? 8 : 6;   // 16 KB of weights each
+    static constexpr int A_STAGES = NT <= 8 ? 9 : NT <= 16 ? 7 : 6;   // 16 KB of weights each
     static constexpr int B_BYTES = 4 * NT * BK;
-    static constexpr int B_STAGES = NT >= 64 ? 2 : 4;
+    static constexpr int B_STAGES = NT >= 64 ? 2 : NT >= 32 ? 4 : 8;
     static constexpr uint32_t COLS = 8 * NT;    // two buffers of 4 NT columns
     static constexpr int EX = NT * 64 > 640 ? NT * 64 : 640;   // floats: up's values for gate's rows; phase 0's sums
     static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES + EX * 4;
@@ -142,6 +143,11 @@ __device__ __forceinline__ bool grid_wait(const unsigned int *counter, unsigned 
     return true;
 }
 
+// Bounded wait by a converged warp: true when every lane's was.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, limit, &g_error));
+}
+
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -166,24 +172,24 @@ __device__ __forceinline__ float4 load_quad(const T *row, int k, int n, bool vec
 }
 
 // ------------------------------------------------------------ phase 0: logits
-// One tile of 8 tokens x 8 experts over a slice of D by the whole CTA: each
-// thread has 4 k of each chunk of 128 for all 64 sums, then lanes and warps are
+// One tile of 8 tokens x 4 experts over a slice of D by the whole CTA: each
+// thread has 4 k of each chunk of 128 for all 32 sums, then lanes and warps are
 // added in a fixed order.
 template <typename XT>
-__device__ void logits_tile(const Params &p, int t0, int e0, int slice, float (*red)[64]) {
+__device__ void logits_tile(const Params &p, int t0, int e0, int slice, float (*red)[32]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunks = (p.D + BK - 1) / BK;
     const int c0 = (int)((int64_t)chunks * slice / p.slices), c1 = (int)((int64_t)chunks * (slice + 1) / p.slices);
     const XT *x = static_cast<const XT *>(p.x);
     const bool w_vec = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.router) & 15) == 0;
-    float v[64];
+    float v[32];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
     for (int c = c0 + warp; c < c1; c += THREADS / 32) {
         const int k = c * BK + 4 * lane;
-        float4 w[8];
+        float4 w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 4; ++e)
             w[e] = e0 + e < p.E ? load_quad(p.router + (int64_t)(e0 + e) * p.D, k, p.D, w_vec)
                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -191,34 +197,32 @@ __device__ void logits_tile(const Params &p, int t0, int e0, int slice, float (*
             if (t0 + t >= p.T) break;
             const float4 a = load_quad(x + (int64_t)(t0 + t) * p.ldx, k, p.D, p.x_vec != 0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = v[8 * t + e];
+            for (int e = 0; e < 4; ++e) {
+                float s = v[4 * t + e];
                 s = __fmaf_rn(a.x, w[e].x, s);
                 s = __fmaf_rn(a.y, w[e].y, s);
                 s = __fmaf_rn(a.z, w[e].z, s);
-                v[8 * t + e] = __fmaf_rn(a.w, w[e].w, s);
+                v[4 * t + e] = __fmaf_rn(a.w, w[e].w, s);
             }
         }
     }
-    // lane l ends with the sums 2 r and 2 r + 1, r = l's bits as the halves were kept
+    // lane l ends with sum l: each step keeps the half that the lane's bit names
 #pragma unroll
-    for (int half = 32; half >= 2; half /= 2) {
-        const int mask = half / 2;             // lanes: 16, 8, 4, 2, 1
-        const bool up = (lane & mask) != 0;
+    for (int half = 16; half >= 1; half /= 2) {
+        const bool up = (lane & half) != 0;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, mask));
+            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, half));
         }
     }
-    red[warp][2 * lane] = v[0];
-    red[warp][2 * lane + 1] = v[1];
+    red[warp][lane] = v[0];
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (threadIdx.x < 32) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) s = __fadd_rn(s, red[w][threadIdx.x]);
-        const int t = t0 + threadIdx.x / 8, e = e0 + threadIdx.x % 8;
+        const int t = t0 + threadIdx.x / 4, e = e0 + threadIdx.x % 4;
         if (t < p.T && e < p.E) p.logit_parts[((int64_t)slice * p.T + t) * p.E + e] = s;
     }
     __syncthreads();
@@ -395,14 +399,20 @@ __device__ __forceinline__ bool for_pieces(const Work &w, Fn f) {
 __device__ __forceinline__ void promoters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // ------------------------------------------------------------ activations
+// The larger of two magnitudes; NaN (as bits above every number) if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A lane's 4 values of a token's block -> its bytes of the column operand, and
 // (lane 0) the block's scale.  Part i of token c is row i * n8 + c: 128 bytes, the
 // 16-byte chunk index flipped by the row's low 3 bits (128-byte swizzle).
 template <int PARTS>
 __device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, int c, int n8, int lane) {
-    const uint32_t hi = max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
-                            max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
-    const uint32_t amax = __reduce_max_sync(0xffffffffu, hi);
+    const float hi = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
+    const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
     const int e = (int)(amax >> 23);
     if (e == 255) {
         // an infinity or NaN makes the token NaN
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                const __grid_constant__ CUtensorMap tm_down, const Params p) {
     using K_ = Cfg<NT>;
     constexpr int P1 = sizeof(XT) == 2 ? 2 : 4;   // parts of x
-    constexpr int P2 = 4;                         // parts of h
+    constexpr int P2 = sizeof(XT) == 2 ? 3 : 4;   // parts of h (bf16 y: 2^-15 of a value, 1/64 of y's rounding)
     constexpr int SB = K_::B_STAGES, A_STAGES = K_::A_STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -466,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto t_full = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + b); };
     auto t_empty = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + 2 + b); };
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const unsigned int G = gridDim.x;
     const uint64_t lim = p.wait_ns;
 
@@ -493,11 +503,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- phase 0: logits, and the shared tiles' arrival counters
     for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.n_arrivals; i += G * THREADS) p.arrivals[i] = 0;
     if (p.router) {
-        float(*red)[64] = reinterpret_cast<float(*)[64]>(ex);
-        const int tt = (p.T + 7) / 8, et = (p.E + 7) / 8;
+        float(*red)[32] = reinterpret_cast<float(*)[32]>(ex);
+        const int tt = (p.T + 7) / 8, et = (p.E + 3) / 4;
         for (int i = blockIdx.x; i < tt * et * p.slices; i += G) {
             const int slice = i % p.slices, tile = i / p.slices;
-            logits_tile<XT>(p, tile / et * 8, tile % et * 8, slice, red);
+            logits_tile<XT>(p, tile / et * 8, tile % et * 4, slice, red);
         }
     }
     bool ok = true;
@@ -526,20 +536,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0 && ok) {
+        if (ok) {
             int s = 0, filled = 0;
             uint32_t ph = 1;
             auto produce = [&](const Work &w, bool second) {
                 return for_pieces(w, [&](int u, int k0, int k1) {
                     const int e = rt.c_expert[u / w.tiles], tile = u % w.tiles;
                     for (int kb = k0; kb < k1; ++kb) {
-                        if (!mbar_wait_for(a_empty(s), ph, lim, &g_error)) return false;
-                        mbar_expect_tx(a_full(s), A_BYTES);
-                        if (second) {
-                            tma_load_3d(a_at(s), &tm_down, a_full(s), kb * BK, tile * ROWS, e);
-                        } else {
-                            tma_load_3d(a_at(s), &tm_gate, a_full(s), kb * BK, tile * 64, e);
-                            tma_load_3d(a_at(s) + A_BYTES / 2, &tm_up, a_full(s), kb * BK, tile * 64, e);
+                        if (!warp_wait(a_empty(s), ph, lim)) return false;
+                        if (elect_one()) {
+                            mbar_expect_tx(a_full(s), A_BYTES);
+                            if (second) {
+                                tma_load_3d(a_at(s), &tm_down, a_full(s), kb * BK, tile * ROWS, e);
+                            } else {
+                                tma_load_3d(a_at(s), &tm_gate, a_full(s), kb * BK, tile * 64, e);
+                                tma_load_3d(a_at(s) + A_BYTES / 2, &tm_up, a_full(s), kb * BK, tile * 64, e);
+                            }
                         }
                         ++filled;
                         if (++s == A_STAGES) { s = 0; ph ^= 1; }
@@ -557,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0 && ok) {
+        if (ok) {
             int s = 0, bs = 0, b = 0, issued = 0;
             uint32_t ph = 0, bph = 0, tph = 1;
             auto multiply = [&](const Work &w, int parts) {
@@ -565,16 +577,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int n8 = (rt.c_n[u / w.tiles] + 7) / 8 * 8;
                     const uint32_t idesc = idesc_8bit(0, 0, 0, 0, ROWS, (parts * n8 + 15) / 16 * 16);
                     for (int kb = k0; kb < k1; ++kb) {
-                        if (!mbar_wait_for(t_empty(b), tph, lim, &g_error) ||
-                            !mbar_wait_for(b_full(bs), bph, lim, &g_error) ||
-                            !mbar_wait_for(a_full(s), ph, lim, &g_error)) return false;
+                        if (!warp_wait(t_empty(b), tph, lim) || !warp_wait(a_full(s), ph, lim) ||
+                            !warp_wait(b_full(bs), bph, lim)) return false;
                         tc_fence_after();
                         const uint64_t da = smem_desc_8bit(a_at(s), A_BYTES), db = smem_desc_8bit(b_at(bs), A_BYTES);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < BK / 32; ++i)
-                            umma_8bit<false>(tmem + (uint32_t)(b * 4 * NT), da + i * 2, db + i * 2, idesc, i > 0);
-                        umma_commit(a_empty(s));
-                        umma_commit(t_full(b));
+                            for (int i = 0; i < BK / 32; ++i)
+                                umma_8bit<false>(tmem + (uint32_t)(b * 4 * NT), da + i * 2, db + i * 2, idesc, i > 0);
+                            umma_commit(a_empty(s));
+                            umma_commit(t_full(b));
+                        }
                         ++issued;
                         if (++s == A_STAGES) { s = 0; ph ^= 1; }
                         if (++bs == SB) { bs = 0; bph ^= 1; }
@@ -588,50 +601,52 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait_for(t_full((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
         }
         __syncwarp();
-    } else if (warp < 2 + SPLITTERS) {
+    } else if (warp < PROMOTER0) {
         // ------------------------------------------------ activations
         if (ok) {
+            // The (block, token) pairs of a piece go round the warps, so that several
+            // blocks are under way when an expert has few tokens.  Every warp still
+            // waits for every block's stage and arrives on it: a parity tells
+            // neighbouring uses of a stage apart and no more.
+            const int me = warp - 2;
             int bs = 0;
             uint32_t bph = 1;
-            // the pieces' (block, token) pairs of this warp, four loaded ahead
             auto split = [&](const Work &w, auto *base, auto row_of, int width, int64_t ld, bool vec, auto parts) {
                 constexpr int PARTS = decltype(parts)::value;
                 return for_pieces(w, [&](int u, int k0, int k1) {
                     const int ch = u / w.tiles, n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
-                    const int mine = warp - 2 < n ? (n - (warp - 2) + SPLITTERS - 1) / SPLITTERS : 0;
-                    constexpr int AHEAD = 4;
-                    float4 next[AHEAD];
-                    int lk = k0, li = 0;        // the next pair to load
-                    auto fetch = [&](float4 &v) {
-                        if (lk < k1) {
-                            const int slot = rt.list[first + warp - 2 + li * SPLITTERS];
-                            v = load_quad(base + (int64_t)row_of(slot) * ld, lk * BK + 4 * lane, width, vec);
-                            if (++li == mine) { li = 0; ++lk; }
-                        }
+                    const int dk = SPLITTERS / n, di = SPLITTERS - dk * n;
+                    int ik = k0 + me / n, i = me - me / n * n;     // this warp's next pair
+                    int fk = ik, fi = i;                           // its next pair to load
+                    auto advance = [&](int &k, int &c) {
+                        k += dk;
+                        c += di;
+                        if (c >= n) { c -= n; ++k; }
                     };
-                    if (mine > 0) {
-#pragma unroll
-                        for (int a = 0; a < AHEAD; ++a) fetch(next[a]);
-                    }
-                    int a = 0;
-                    for (int kb = k0; kb < k1; ++kb) {
-                        bool go = mbar_wait_for(b_empty(bs), bph, lim, &g_error);
-                        if (__any_sync(0xffffffffu, !go)) return false;
-                        for (int i = 0; i < mine; ++i) {
-                            // (a is the warp's count modulo AHEAD; a switch keeps `next` in registers)
-                            float4 v;
-                            switch (a) {
-                            case 0: v = next[0]; fetch(next[0]); break;
-                            case 1: v = next[1]; fetch(next[1]); break;
-                            case 2: v = next[2]; fetch(next[2]); break;
-                            default: v = next[3]; fetch(next[3]); break;
-                            }
-                            a = (a + 1) & (AHEAD - 1);
-                            split_block<PARTS>(v, b_at(bs), b_scale[bs], warp - 2 + i * SPLITTERS, n8, lane);
+                    auto fetch = [&]() {
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (fk < k1) {
+                            const int slot = rt.list[first + fi];
+                            v = load_quad(base + (int64_t)row_of(slot) * ld, fk * BK + 4 * lane, width, vec);
+                            advance(fk, fi);
                         }
-                        // generic-proxy stores must be visible to the tensor core's reads
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                        return v;
+                    };
+                    float4 v0 = fetch(), v1 = fetch();
+                    for (int kb = k0; kb < k1; ++kb) {
+                        if (!warp_wait(b_empty(bs), bph, lim)) return false;
+                        if (ik == kb) {
+                            do {
+                                const float4 v = v0;
+                                v0 = v1;
+                                v1 = fetch();
+                                split_block<PARTS>(v, b_at(bs), b_scale[bs], i, n8, lane);
+                                advance(ik, i);
+                            } while (ik == kb);
+                            // generic-proxy stores must be visible to the tensor core's reads
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
                         if (lane == 0) mbar_arrive(b_full(bs));
                         if (++bs == SB) { bs = 0; bph ^= 1; }
                     }
@@ -675,10 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int kb = k0; kb < k1; ++kb) {
                     const float sw = ws_next;
                     if (kb + 1 < k1) ws_next = __ldg(ws + kb + 1);
-                    if (alive) {
-                        const bool go = mbar_wait_for(t_full(b), tph, lim, &g_error);
-                        alive = !__any_sync(0xffffffffu, !go);
-                    }
+                    alive = alive && warp_wait(t_full(b), tph, lim);
                     if (!alive) break;
                     tc_fence_after();
                     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 4 * NT);
@@ -887,7 +899,7 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     const int64_t T = p.T, D = p.D, F = p.F, E = p.E, slots = T * p.topk;
     // an expert has at most T tokens: one tile takes them all up to 64
     const int nt = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
-    const int64_t logit_tiles = ((T + 7) / 8) * ((E + 7) / 8);
+    const int64_t logit_tiles = ((T + 7) / 8) * ((E + 3) / 4);
     p.slices = p.router ? (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fp8::blocks_of(D), moe::LOGIT_SLICES),
                                                                       sms / logit_tiles))
                         : 1;
