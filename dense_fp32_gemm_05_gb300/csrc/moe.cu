@@ -69,7 +69,7 @@ constexpr int THREADS = 32 * (PROMOTER0 + 4);
 constexpr int MAX_T = 128, MAX_E = 512, MAX_TOPK = 16;
 constexpr int MAX_SLOTS = MAX_T * MAX_TOPK;
 constexpr int MAX_CHUNKS = 2 * MAX_E;          // (expert, up to NT of its tokens)
-constexpr int LOGIT_SLICES = 16;               // slices of D per tile of logits, at most
+constexpr int LOGIT_SLICES = 8;                // slices of D per tile of logits, at most
 constexpr int SMEM_MAX = 232448;               // shared memory per block, static and dynamic
 constexpr uint64_t kDrainNs = 1000000000ull;
 
@@ -252,8 +252,14 @@ __device__ void route_token(const Params &p, int t, Routing &rt, bool write) {
         float s;
         if (p.router) {
             const float *src = p.logit_parts + (int64_t)t * p.E + e;
-            s = __ldcg(src);
-            for (int k = 1; k < p.slices; ++k) s = __fadd_rn(s, __ldcg(src + (int64_t)k * p.T * p.E));
+            float part[LOGIT_SLICES];           // (all loads under way before the first addition)
+#pragma unroll
+            for (int k = 0; k < LOGIT_SLICES; ++k)
+                part[k] = k < p.slices ? __ldcg(src + (int64_t)k * p.T * p.E) : 0.0f;
+            s = part[0];
+#pragma unroll
+            for (int k = 1; k < LOGIT_SLICES; ++k)
+                if (k < p.slices) s = __fadd_rn(s, part[k]);
             if (write) p.logits[(int64_t)t * p.E + e] = s;
         } else {
             s = p.logits[(int64_t)t * p.E + e];
@@ -365,31 +371,57 @@ __device__ void route_lists(const Params &p, Routing &rt) {
 }
 
 // ------------------------------------------------------------ work ranges
-// A product's blocks: tile after tile (chunk-major), kb blocks each; CTA c has
-// [c total / n, (c + 1) total / n).
+// A product's blocks: tile after tile (chunk-major), kb blocks each, in equal
+// contiguous ranges (the first `more` are one block longer).
 struct Work {
     int tiles, kb;                              // tiles per chunk, blocks per tile
-    int64_t total;
-    int n;                                      // CTAs with a range: no range is empty
+    int total;
+    int n;                                      // CTAs with a range: none of these is empty
+    int each, more;
     __device__ Work(int chunks, int tiles_, int kb_)
-        : tiles(tiles_), kb(kb_), total((int64_t)chunks * tiles_ * kb_),
-          n((int)max((int64_t)1, min((int64_t)gridDim.x, total))) {}
-    __device__ int64_t begin(int c) const { return c >= n ? total : total * c / n; }
-    __device__ int owner(int64_t it) const { return (int)(((it + 1) * n - 1) / total); }
-    // which of CTA c's two partial sums belongs to tile u
-    __device__ int part_of(int c, int u) const { return begin(c) / kb == u ? 0 : 1; }
+        : tiles(tiles_), kb(kb_), total(chunks * tiles_ * kb_), n(max(1, min((int)gridDim.x, total))),
+          each(total / n), more(total - each * n) {}
+    __device__ int begin(int c) const { return c >= n ? total : c * each + min(c, more); }
+    __device__ int owner(int it) const {
+        const int longer = more * (each + 1);
+        return it < longer ? it / (each + 1) : more + (it - longer) / each;
+    }
+};
+
+// A tile's partial sums: CTAs c0 .. c1 hold them, c0 in the place `part0` of its
+// two (a range that begins at or inside the tile: the first), the others in the
+// first of theirs.
+struct Parts {
+    int c0, c1, part0;
+    __device__ Parts(const Work &w, int u)
+        : c0(w.owner(u * w.kb)), c1(w.owner((u + 1) * w.kb - 1)), part0(w.begin(c0) >= u * w.kb ? 0 : 1) {}
+    // the sum of value `at` of each, four loads at a time, in ascending order of k
+    __device__ float sum(const float *parts, int64_t size, int at) const {
+        const float *src = parts + at;
+        float s = 0.0f;
+        for (int c = c0; c <= c1; c += 4) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = c + i <= c1 ? __ldcg(src + (2 * (int64_t)(c + i) + (c + i == c0 ? part0 : 0)) * size) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i <= c1) s = __fadd_rn(s, v[i]);
+        }
+        return s;
+    }
 };
 
 // Calls f(tile, first block, end block) for the pieces of this CTA's range;
 // stops when f returns false.
 template <typename Fn>
 __device__ __forceinline__ bool for_pieces(const Work &w, Fn f) {
-    int64_t it = w.begin(blockIdx.x);
-    const int64_t end = w.begin(blockIdx.x + 1);
+    int it = w.begin(blockIdx.x);
+    const int end = w.begin(blockIdx.x + 1);
     while (it < end) {
-        const int u = (int)(it / w.kb);
-        const int kb0 = (int)(it - (int64_t)u * w.kb);
-        const int kb1 = (int)min((int64_t)w.kb, kb0 + (end - it));
+        const int u = it / w.kb;
+        const int kb0 = it - u * w.kb;
+        const int kb1 = min(w.kb, kb0 + (end - it));
         if (!f(u, kb0, kb1)) return false;
         it += kb1 - kb0;
     }
@@ -749,26 +781,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return true;
                 }
                 // a share of the sum
-                float *dst = p.parts + ((int64_t)blockIdx.x * 2 + w.part_of(blockIdx.x, u)) * NT * ROWS + row;
+                const Parts pt(w, u);
+                float *dst = p.parts + ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == pt.c0 ? pt.part0 : 0)) * NT * ROWS + row;
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
                     if (i < n) __stcg(dst + i * ROWS, acc[i]);
                 if (second) return true;        // added in the last phase
                 __threadfence();
                 promoters_sync();
-                const int c0 = w.owner((int64_t)u * w.kb), c1 = w.owner((int64_t)(u + 1) * w.kb - 1);
-                if (row == 0) s_last = atomicAdd(&p.arrivals[u], 1u) == (unsigned)(c1 - c0);
+                if (row == 0) s_last = atomicAdd(&p.arrivals[u], 1u) == (unsigned)(pt.c1 - pt.c0);
                 promoters_sync();
                 if (s_last) {
                     __threadfence();
                     const int f = tile * 64 + (row & 63);
+#pragma unroll 2
                     for (int i = row >> 6; i < n; i += 2) {
-                        float g = 0.0f, up = 0.0f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const float *src = p.parts + (((int64_t)c * 2 + w.part_of(c, u)) * NT + i) * ROWS + (row & 63);
-                            g = __fadd_rn(g, __ldcg(src));
-                            up = __fadd_rn(up, __ldcg(src + 64));
-                        }
+                        const float g = pt.sum(p.parts, NT * ROWS, i * ROWS + (row & 63));
+                        const float up = pt.sum(p.parts, NT * ROWS, i * ROWS + 64 + (row & 63));
                         const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
                         if (f < p.F) __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, up));
                     }
@@ -794,30 +823,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_free<false>(tmem, K_::COLS);
     }
     if (s_last && ok) {
-        const int64_t total = (int64_t)p.T * p.D;
-        for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)G * THREADS) {
-            const int t = (int)(i / p.D), d = (int)(i - (int64_t)t * p.D);
+        // 32 columns of a token per warp, neighbouring tasks on different CTAs
+        const int across = (p.D + 31) / 32;
+        for (int task = warp * (int)G + blockIdx.x; task < p.T * across; task += (THREADS / 32) * G) {
+            const int t = task / across, d = (task - t * across) * 32 + lane;
             const int tile = d / ROWS;
             float sum = 0.0f;
+#pragma unroll 4
             for (int j = 0; j < p.topk; ++j) {
                 const int slot = t * p.topk + j;
                 const int e = rt.expert[slot], r = rt.rank[slot];
                 const int u = (rt.chunk0[e] + r / NT) * w2.tiles + tile;
-                const int c0 = w2.owner((int64_t)u * w2.kb), c1 = w2.owner((int64_t)(u + 1) * w2.kb - 1);
-                float v;
-                if (c0 == c1) {
-                    v = __ldcg(p.out + (int64_t)slot * p.D + d);
-                } else {
-                    v = 0.0f;
-                    for (int c = c0; c <= c1; ++c)
-                        v = __fadd_rn(v, __ldcg(p.parts + (((int64_t)c * 2 + w2.part_of(c, u)) * NT + r % NT) * ROWS +
-                                                d % ROWS));
-                }
+                const Parts pt(w2, u);
+                float v = 0.0f;
+                if (d < p.D)
+                    v = pt.c0 == pt.c1 ? __ldcg(p.out + (int64_t)slot * p.D + d)
+                                       : pt.sum(p.parts, NT * ROWS, r % NT * ROWS + d % ROWS);
                 sum = __fmaf_rn(rt.weight[slot], v, sum);
             }
-            XT *y = static_cast<XT *>(p.y) + (int64_t)t * p.ldy + d;
-            if (sizeof(XT) == 2) *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(sum);
-            else *reinterpret_cast<float *>(y) = sum;
+            if (d < p.D) {
+                XT *y = static_cast<XT *>(p.y) + (int64_t)t * p.ldy + d;
+                if (sizeof(XT) == 2) *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(sum);
+                else *reinterpret_cast<float *>(y) = sum;
+            }
         }
     }
     __syncthreads();
@@ -906,7 +934,8 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     p.ldh = (int)((F + 3) / 4 * 4);
     const int64_t chunks = std::min<int64_t>(slots, E * ((T + nt - 1) / nt));
     const int64_t arrivals = chunks * ((F + 63) / 64);
-    if (arrivals > INT32_MAX || chunks * ((D + 127) / 128) > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
+    // blocks of 128 k and tasks are counted in int
+    if (arrivals * fp8::blocks_of(D) > INT32_MAX || T * D > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
     p.n_arrivals = (int)arrivals;
     auto up256 = [](size_t b) { return (b + 255) & ~size_t(255); };
     // the barriers keep a workspace of their own: they are zero between calls
