@@ -30,7 +30,7 @@
 //      (fp32 FMAs), then a grid barrier; every CTA then works out the routing
 //      (softmax, top-k, the experts' token lists) for itself;
 //   1  h = silu(gate x) * (up x): tiles of 64 gate rows and the same 64 up rows.
-//      The last CTA to finish a shared tile adds its parts;
+//      The last CTA to finish a shared tile adds its parts, here and in 2;
 //   2  down h.  Only the warps that split h wait for the grid barrier between 1
 //      and 2: the weights' stream goes on across it;
 //   3  after a third barrier y = sum over a token's experts, all threads.
@@ -85,6 +85,7 @@ struct Cfg {
     static constexpr int EX = NT * 64 > 640 ? NT * 64 : 640;   // floats: up's values for gate's rows; phase 0's sums
     static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES + EX * 4;
     static_assert(COLS <= 512, "tensor memory");
+    static_assert(B_STAGES * B_BYTES >= THREADS / 32 * MAX_E * 4, "a row of logits for each warp");
     static_assert(SMEM + 32 * 1024 <= SMEM_MAX, "shared memory (the routing is static)");
 };
 
@@ -104,7 +105,7 @@ struct Params {
     int slices;                                // of D in phase 0
     int ldh;
     unsigned int *sync;                        // grid barriers 0..2, exits (3)
-    unsigned int *arrivals;                    // one for each tile of phase 1
+    unsigned int *arrivals;                    // one for each tile of phase 1, then of phase 2
     int n_arrivals;
     float *logit_parts;                        // [slices][T][E]
     float *h;                                  // [slot][ldh]
@@ -236,19 +237,15 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One token's softmax and top-k by a warp.
-__device__ void route_token(const Params &p, int t, Routing &rt, bool write) {
-    constexpr int PER = MAX_E / 32;
+// One token's softmax and top-k by a warp; `buf`: E floats of its own.  Loops are
+// not unrolled: every launch runs this code once, from a cold instruction cache.
+__device__ void route_token(const Params &p, int t, Routing &rt, float *buf, bool write) {
+    constexpr uint32_t TAKEN = 0xffffffffu;     // a NaN that no sum yields marks an expert taken
     const int lane = threadIdx.x & 31;
-    float l[PER];
     float most = -INFINITY;
     bool nan = false;
-    const int per = (p.E + 31) / 32;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        l[i] = 0.0f;
-        const int e = 32 * i + lane;
-        if (i >= per || e >= p.E) continue;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) {
         float s;
         if (p.router) {
             const float *src = p.logit_parts + (int64_t)t * p.E + e;
@@ -264,49 +261,46 @@ __device__ void route_token(const Params &p, int t, Routing &rt, bool write) {
         } else {
             s = p.logits[(int64_t)t * p.E + e];
         }
-        l[i] = s;
-        nan |= s != s;
+        if (s != s) {
+            nan = true;
+            s = __uint_as_float(0x7fffffffu);
+        }
+        buf[e] = s;
         most = fmaxf(most, s);
     }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (__any_sync(0xffffffffu, nan)) most = __uint_as_float(0x7fffffffu);   // every weight is NaN then
     float sum = 0.0f;
-    uint32_t key[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool in = i < per && 32 * i + lane < p.E;
-        if (in) sum = __fadd_rn(sum, expf(__fsub_rn(l[i], most)));
-        // keys of what may still be chosen, above 0
-        key[i] = in ? max(order_key(l[i]), 1u) : 0u;
-    }
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, expf(__fsub_rn(buf[e], most)));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-    float mine = 0.0f;                          // lane j: the weight of choice j
+    float mine = 0.0f;                          // lane j: choice j's logit, then its weight
     int mine_e = 0;
+#pragma unroll 1
     for (int j = 0; j < p.topk; ++j) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (i < per) best = max(best, key[i]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        uint32_t at = 0xffffffffu;              // the lowest index with it
-        float v = 0.0f;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (i < per && key[i] == best) { at = 32 * i + lane; v = l[i]; }
-        const uint32_t e = __reduce_min_sync(0xffffffffu, at);
-        v = __shfl_sync(0xffffffffu, v, (int)(e & 31));
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (32 * i + lane == (int)e) key[i] = 0;
-        if (lane == j) {
-            mine = __fdiv_rn(expf(__fsub_rn(v, most)), sum);
-            mine_e = (int)e;
+        uint32_t best = 0, at = 0xffffffffu;    // this lane's largest key and its lowest index
+#pragma unroll 1
+        for (int e = lane; e < p.E; e += 32) {
+            const float v = buf[e];
+            const uint32_t key = __float_as_uint(v) == TAKEN ? 0u : max(order_key(v), 1u);
+            if (key > best) { best = key; at = (uint32_t)e; }
         }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? at : 0xffffffffu);
+        if (lane == j) {
+            mine = buf[e];
+            mine_e = e;
+        }
+        __syncwarp();
+        if ((e & 31) == lane) buf[e] = __uint_as_float(TAKEN);
+        __syncwarp();
     }
+    mine = __fdiv_rn(expf(__fsub_rn(mine, most)), sum);
     if (p.renormalize) {
         float total = 0.0f;
+#pragma unroll 1
         for (int j = 0; j < p.topk; ++j) total = __fadd_rn(total, __shfl_sync(0xffffffffu, mine, j));
         mine = __fdiv_rn(mine, total);
     }
@@ -555,7 +549,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     ok = s_last != 0;
     if (ok) {
-        for (int t = warp; t < p.T; t += THREADS / 32) route_token(p, t, rt, blockIdx.x == 0);
+        float *buf = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES) + warp * MAX_E;   // (where activations go later)
+        for (int t = warp; t < p.T; t += THREADS / 32) route_token(p, t, rt, buf, blockIdx.x == 0);
         __syncthreads();
         if (warp == 0) route_lists<NT>(p, rt);
     } else if (threadIdx.x == 0) {
@@ -786,20 +781,27 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
                     if (i < n) __stcg(dst + i * ROWS, acc[i]);
-                if (second) return true;        // added in the last phase
                 __threadfence();
                 promoters_sync();
-                if (row == 0) s_last = atomicAdd(&p.arrivals[u], 1u) == (unsigned)(pt.c1 - pt.c0);
+                if (row == 0)
+                    s_last = atomicAdd(&p.arrivals[second ? w1.tiles * rt.chunks + u : u], 1u) == (unsigned)(pt.c1 - pt.c0);
                 promoters_sync();
                 if (s_last) {
                     __threadfence();
-                    const int f = tile * 64 + (row & 63);
-#pragma unroll 2
-                    for (int i = row >> 6; i < n; i += 2) {
-                        const float g = pt.sum(p.parts, NT * ROWS, i * ROWS + (row & 63));
-                        const float up = pt.sum(p.parts, NT * ROWS, i * ROWS + 64 + (row & 63));
-                        const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
-                        if (f < p.F) __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, up));
+                    if (second) {
+                        const int d = tile * ROWS + row;
+                        for (int i = 0; i < n; ++i) {
+                            const float v = pt.sum(p.parts, NT * ROWS, i * ROWS + row);
+                            if (d < p.D) __stcg(p.out + (int64_t)rt.list[first + i] * p.D + d, v);
+                        }
+                    } else {
+                        const int f = tile * 64 + (row & 63);
+                        for (int i = row >> 6; i < n; i += 2) {
+                            const float g = pt.sum(p.parts, NT * ROWS, i * ROWS + (row & 63));
+                            const float up = pt.sum(p.parts, NT * ROWS, i * ROWS + 64 + (row & 63));
+                            const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
+                            if (f < p.F) __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, up));
+                        }
                     }
                 }
                 return true;
@@ -827,20 +829,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int across = (p.D + 31) / 32;
         for (int task = warp * (int)G + blockIdx.x; task < p.T * across; task += (THREADS / 32) * G) {
             const int t = task / across, d = (task - t * across) * 32 + lane;
-            const int tile = d / ROWS;
+            const float *src = p.out + (int64_t)t * p.topk * p.D + min(d, p.D - 1);
             float sum = 0.0f;
 #pragma unroll 4
-            for (int j = 0; j < p.topk; ++j) {
-                const int slot = t * p.topk + j;
-                const int e = rt.expert[slot], r = rt.rank[slot];
-                const int u = (rt.chunk0[e] + r / NT) * w2.tiles + tile;
-                const Parts pt(w2, u);
-                float v = 0.0f;
-                if (d < p.D)
-                    v = pt.c0 == pt.c1 ? __ldcg(p.out + (int64_t)slot * p.D + d)
-                                       : pt.sum(p.parts, NT * ROWS, r % NT * ROWS + d % ROWS);
-                sum = __fmaf_rn(rt.weight[slot], v, sum);
-            }
+            for (int j = 0; j < p.topk; ++j)
+                sum = __fmaf_rn(rt.weight[t * p.topk + j], __ldcg(src + (int64_t)j * p.D), sum);
             if (d < p.D) {
                 XT *y = static_cast<XT *>(p.y) + (int64_t)t * p.ldy + d;
                 if (sizeof(XT) == 2) *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(sum);
@@ -925,17 +918,20 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     int st = usable_device(&sms);
     if (st != SGEMM_OK) return st;
     const int64_t T = p.T, D = p.D, F = p.F, E = p.E, slots = T * p.topk;
-    // an expert has at most T tokens: one tile takes them all up to 64
-    const int nt = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    // Columns for twice the tokens that an expert has on average; one with more is
+    // taken in several chunks, each of which reads its weights again.  Fewer columns
+    // leave room for more stages: T = 64, 8 tokens an expert, 145 us with 64 columns.
+    const int64_t want = std::min<int64_t>(T, (2 * slots + E - 1) / E);
+    const int nt = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
     const int64_t logit_tiles = ((T + 7) / 8) * ((E + 3) / 4);
     p.slices = p.router ? (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fp8::blocks_of(D), moe::LOGIT_SLICES),
                                                                       sms / logit_tiles))
                         : 1;
     p.ldh = (int)((F + 3) / 4 * 4);
-    const int64_t chunks = std::min<int64_t>(slots, E * ((T + nt - 1) / nt));
-    const int64_t arrivals = chunks * ((F + 63) / 64);
+    const int64_t chunks = std::min<int64_t>(slots, std::min(E, slots) + slots / nt);   // at most
+    const int64_t arrivals = chunks * ((F + 63) / 64 + (D + 127) / 128);
     // blocks of 128 k and tasks are counted in int
-    if (arrivals * fp8::blocks_of(D) > INT32_MAX || T * D > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
+    if (arrivals * fp8::blocks_of(std::max(D, F)) > INT32_MAX || T * D > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
     p.n_arrivals = (int)arrivals;
     auto up256 = [](size_t b) { return (b + 255) & ~size_t(255); };
     // the barriers keep a workspace of their own: they are zero between calls
