@@ -26,17 +26,19 @@
 //     timing.
 //
 // Phases, one CTA per SM, cooperative launch:
-//   0  router logits: tiles of 8 tokens x 4 experts x a slice of D over the CTAs
-//      (fp32 FMAs), then a grid barrier; every CTA then works out the routing
-//      (softmax, top-k, the experts' token lists) for itself;
+//   0  router logits: 4 tokens x 2 experts x a slice of D for each warp of the grid
+//      (fp32 FMAs); after a grid barrier softmax and top-k, a token each on
+//      different CTAs; after another every CTA lists the experts' tokens for itself;
 //   1  h = silu(gate x) * (up x): tiles of 64 gate rows and the same 64 up rows.
 //      The last CTA to finish a shared tile adds its parts, here and in 2;
-//   2  down h.  Only the warps that split h wait for the grid barrier between 1
-//      and 2: the weights' stream goes on across it;
-//   3  after a third barrier y = sum over a token's experts, all threads.
+//   2  down h.  Only the warps that split h wait, for all tiles of the chunk's h:
+//      the weights' stream goes on meanwhile, and a CTA waits for the few that
+//      had the same experts, not for the slowest;
+//   3  after a last grid barrier y = sum over a token's experts, all threads.
 //
-// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-11 split activations
-// into the MMA's column operand; 12-15 promotion (128 rows, one per thread).
+// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-10 split activations
+// into the MMA's column operand; 11 publishes finished tiles; 12-15 promotion (128
+// rows, one per thread).
 // Every wait is bounded: a role that gives up sets the device error word and
 // stops; every CTA still arrives at every grid barrier, so that the counters
 // are whole again when the kernel ends.
@@ -63,13 +65,14 @@ using namespace tc;
 constexpr int BK = fp8::GROUP;
 constexpr int ROWS = 128;                      // weight rows of a tile (64 gate + 64 up, or 128 down)
 constexpr int A_BYTES = ROWS * BK;
-constexpr int SPLITTERS = 10;                  // warps 2..11
-constexpr int PROMOTER0 = 2 + SPLITTERS;       // the first of the 4 promoting warps
+constexpr int SPLITTERS = 9;                   // warps 2..10
+constexpr int FINISHER = 2 + SPLITTERS;        // warp 11
+constexpr int PROMOTER0 = FINISHER + 1;        // the first of the 4 promoting warps (a multiple of 4)
 constexpr int THREADS = 32 * (PROMOTER0 + 4);
 constexpr int MAX_T = 128, MAX_E = 512, MAX_TOPK = 16;
 constexpr int MAX_SLOTS = MAX_T * MAX_TOPK;
 constexpr int MAX_CHUNKS = 2 * MAX_E;          // (expert, up to NT of its tokens)
-constexpr int LOGIT_SLICES = 8;                // slices of D per tile of logits, at most
+constexpr int LOGIT_SLICES = 32;               // slices of D for a group of logits, at most
 constexpr int SMEM_MAX = 232448;               // shared memory per block, static and dynamic
 constexpr uint64_t kDrainNs = 1000000000ull;
 
@@ -82,10 +85,9 @@ struct Cfg {
     static constexpr int B_BYTES = 4 * NT * BK;
     static constexpr int B_STAGES = NT >= 64 ? 2 : NT >= 32 ? 4 : 8;
     static constexpr uint32_t COLS = 8 * NT;    // two buffers of 4 NT columns
-    static constexpr int EX = NT * 64 > 640 ? NT * 64 : 640;   // floats: up's values for gate's rows; phase 0's sums
-    static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES + EX * 4;
+    static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES;
     static_assert(COLS <= 512, "tensor memory");
-    static_assert(B_STAGES * B_BYTES >= THREADS / 32 * MAX_E * 4, "a row of logits for each warp");
+    static_assert(B_STAGES * B_BYTES >= (2 * MAX_E + MAX_TOPK) * 4, "a row of logits, a token's choices");
     static_assert(SMEM + 32 * 1024 <= SMEM_MAX, "shared memory (the routing is static)");
 };
 
@@ -103,25 +105,25 @@ struct Params {
     int32_t *indices;
     float *weights;
     int slices;                                // of D in phase 0
-    int ldh;
-    unsigned int *sync;                        // grid barriers 0..2, exits (3)
-    unsigned int *arrivals;                    // one for each tile of phase 1, then of phase 2
+    int ldh, ldo;                              // multiples of 4
+    unsigned int *sync;                        // grid barriers 0 .. 2, exits (3)
+    // counters: CTAs done with a tile (phase 1's tiles, then phase 2's), then tiles of h done in a chunk
+    unsigned int *arrivals;
     int n_arrivals;
     float *logit_parts;                        // [slices][T][E]
     float *h;                                  // [slot][ldh]
-    float *parts;                              // [CTA][first, last tile of its range][token][ROWS]
-    float *out;                                // [slot][D]: down h
+    float *parts;                              // [phase][CTA][first, last tile of its range][token][ROWS]
+    float *out;                                // [slot][ldo]: down h
     unsigned long long wait_ns;
 };
 
 // Routing as every CTA holds it.  A slot is t * topk + j.
 struct Routing {
-    float weight[MAX_SLOTS];
     short expert[MAX_SLOTS];                   // of a slot
     short rank[MAX_SLOTS];                     // of a slot among its expert's
     short list[MAX_SLOTS];                     // slots by expert, ascending within one
-    short count[MAX_E], first[MAX_E];          // of an expert in `list`
-    short chunk0[MAX_E];                       // an expert's first chunk
+    int count[MAX_E];                          // an expert's slots
+    short first[MAX_E];                        // its first in `list`
     short c_expert[MAX_CHUNKS], c_first[MAX_CHUNKS], c_n[MAX_CHUNKS];
     int chunks;
 };
@@ -129,6 +131,17 @@ struct Routing {
 __device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
     unsigned int v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Counter updates by one thread after a barrier of the threads whose writes they
+// publish: release and acquire are cumulative, so no other thread needs a fence.
+__device__ __forceinline__ void add_release(unsigned int *p) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" :: "l"(p) : "memory");
+}
+__device__ __forceinline__ unsigned int add_acq_rel(unsigned int *p) {
+    unsigned int v;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
 
@@ -160,10 +173,10 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p) {
                        __uint_as_float(t.y << 16), __uint_as_float(t.y & 0xffff0000u));
 }
 
-// Elements k .. k+3 of a row of n (zeros past it).
+// Elements k .. k+3 of a row of n (zeros past it).  The element path is a call, so
+// that the code around it stays short: each launch fetches it anew.
 template <typename T>
-__device__ __forceinline__ float4 load_quad(const T *row, int k, int n, bool vec) {
-    if (vec && k + 3 < n) return quad(row + k);
+__device__ __noinline__ float4 load_elements(const T *row, int k, int n) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (k < n) v.x = to_f32(row[k]);
     if (k + 1 < n) v.y = to_f32(row[k + 1]);
@@ -171,62 +184,57 @@ __device__ __forceinline__ float4 load_quad(const T *row, int k, int n, bool vec
     if (k + 3 < n) v.w = to_f32(row[k + 3]);
     return v;
 }
+template <typename T>
+__device__ __forceinline__ float4 load_quad(const T *row, int k, int n, bool vec) {
+    if (vec && k + 3 < n) return quad(row + k);
+    return load_elements(row, k, n);
+}
 
 // ------------------------------------------------------------ phase 0: logits
-// One tile of 8 tokens x 4 experts over a slice of D by the whole CTA: each
-// thread has 4 k of each chunk of 128 for all 32 sums, then lanes and warps are
-// added in a fixed order.
+// One warp: 4 tokens x 2 experts over a slice of D; each lane has 4 k of each chunk
+// of 128, then the lanes are added in a fixed order.  Rows past the last token or
+// expert repeat it; their sums are not stored.
+constexpr int LOGIT_T = 4, LOGIT_E = 2;
 template <typename XT>
-__device__ void logits_tile(const Params &p, int t0, int e0, int slice, float (*red)[32]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ void logits_task(const Params &p, int t0, int e0, int slice) {
+    const int lane = threadIdx.x & 31;
     const int chunks = (p.D + BK - 1) / BK;
-    const int c0 = (int)((int64_t)chunks * slice / p.slices), c1 = (int)((int64_t)chunks * (slice + 1) / p.slices);
+    const int c0 = chunks * slice / p.slices, c1 = chunks * (slice + 1) / p.slices;
     const XT *x = static_cast<const XT *>(p.x);
     const bool w_vec = p.D % 4 == 0 && (reinterpret_cast<uintptr_t>(p.router) & 15) == 0;
-    float v[32];
+    float v[LOGIT_T * LOGIT_E];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    for (int c = c0 + warp; c < c1; c += THREADS / 32) {
+    for (int i = 0; i < LOGIT_T * LOGIT_E; ++i) v[i] = 0.0f;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
         const int k = c * BK + 4 * lane;
-        float4 w[4];
+        float4 w[LOGIT_E], a[LOGIT_T];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = e0 + e < p.E ? load_quad(p.router + (int64_t)(e0 + e) * p.D, k, p.D, w_vec)
-                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int e = 0; e < LOGIT_E; ++e) w[e] = load_quad(p.router + (int64_t)min(e0 + e, p.E - 1) * p.D, k, p.D, w_vec);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (t0 + t >= p.T) break;
-            const float4 a = load_quad(x + (int64_t)(t0 + t) * p.ldx, k, p.D, p.x_vec != 0);
+        for (int t = 0; t < LOGIT_T; ++t) a[t] = load_quad(x + (int64_t)min(t0 + t, p.T - 1) * p.ldx, k, p.D, p.x_vec != 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float s = v[4 * t + e];
-                s = __fmaf_rn(a.x, w[e].x, s);
-                s = __fmaf_rn(a.y, w[e].y, s);
-                s = __fmaf_rn(a.z, w[e].z, s);
-                v[4 * t + e] = __fmaf_rn(a.w, w[e].w, s);
+        for (int t = 0; t < LOGIT_T; ++t)
+#pragma unroll
+            for (int e = 0; e < LOGIT_E; ++e) {
+                float &s = v[LOGIT_E * t + e];
+                s = __fmaf_rn(a[t].w, w[e].w, __fmaf_rn(a[t].z, w[e].z, __fmaf_rn(a[t].y, w[e].y, __fmaf_rn(a[t].x, w[e].x, s))));
             }
-        }
     }
-    // lane l ends with sum l: each step keeps the half that the lane's bit names
+    // lane l ends with sum l / 4: three steps keep the half that a bit of the lane names
 #pragma unroll
-    for (int half = 16; half >= 1; half /= 2) {
-        const bool up = (lane & half) != 0;
+    for (int half = 4; half >= 1; half /= 2) {
+        const bool up = (lane & 4 * half) != 0;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, half));
+            v[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, 4 * half));
         }
     }
-    red[warp][lane] = v[0];
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) s = __fadd_rn(s, red[w][threadIdx.x]);
-        const int t = t0 + threadIdx.x / 4, e = e0 + threadIdx.x % 4;
-        if (t < p.T && e < p.E) p.logit_parts[((int64_t)slice * p.T + t) * p.E + e] = s;
-    }
-    __syncthreads();
+    v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+    v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+    const int t = t0 + lane / 4 / LOGIT_E, e = e0 + lane / 4 % LOGIT_E;
+    if (lane % 4 == 0 && t < p.T && e < p.E) p.logit_parts[((int64_t)slice * p.T + t) * p.E + e] = v[0];
 }
 
 // ------------------------------------------------------------ routing
@@ -237,30 +245,42 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One token's softmax and top-k by a warp; `buf`: E floats of its own.  Loops are
-// not unrolled: every launch runs this code once, from a cold instruction cache.
-__device__ void route_token(const Params &p, int t, Routing &rt, float *buf, bool write) {
+// A token's logits from their parts, by the whole CTA: 8 lanes for each expert.
+__device__ void token_logits(const Params &p, int t, float *buf) {
+    const int n = 8 * p.E, kg = threadIdx.x & 7;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < (n + 31) / 32 * 32; i += THREADS) {
+        const int e = min(i >> 3, p.E - 1);
+        const float *src = p.logit_parts + (int64_t)t * p.E + e;
+        float part[LOGIT_SLICES / 8];           // (loads under way together)
+#pragma unroll
+        for (int k = 0; k < LOGIT_SLICES / 8; ++k) {
+            const int slice = kg * (LOGIT_SLICES / 8) + k;
+            part[k] = slice < p.slices ? __ldcg(src + (int64_t)slice * p.T * p.E) : 0.0f;
+        }
+        float s = part[0];
+#pragma unroll
+        for (int k = 1; k < LOGIT_SLICES / 8; ++k) s = __fadd_rn(s, part[k]);
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+        if (kg == 0 && i < n) {
+            buf[e] = s;
+            p.logits[(int64_t)t * p.E + e] = s;
+        }
+    }
+}
+
+// One token's softmax and top-k by a warp; `buf`: its logits and room for 2 MAX_E
+// floats in all, `chosen`: topk ints.  Loops are not unrolled: every launch runs
+// this code once, from a cold instruction cache.
+__device__ void route_token(const Params &p, int t, float *buf, int *chosen) {
     constexpr uint32_t TAKEN = 0xffffffffu;     // a NaN that no sum yields marks an expert taken
     const int lane = threadIdx.x & 31;
     float most = -INFINITY;
     bool nan = false;
 #pragma unroll 1
     for (int e = lane; e < p.E; e += 32) {
-        float s;
-        if (p.router) {
-            const float *src = p.logit_parts + (int64_t)t * p.E + e;
-            float part[LOGIT_SLICES];           // (all loads under way before the first addition)
-#pragma unroll
-            for (int k = 0; k < LOGIT_SLICES; ++k)
-                part[k] = k < p.slices ? __ldcg(src + (int64_t)k * p.T * p.E) : 0.0f;
-            s = part[0];
-#pragma unroll
-            for (int k = 1; k < LOGIT_SLICES; ++k)
-                if (k < p.slices) s = __fadd_rn(s, part[k]);
-            if (write) p.logits[(int64_t)t * p.E + e] = s;
-        } else {
-            s = p.logits[(int64_t)t * p.E + e];
-        }
+        float s = p.router ? buf[e] : p.logits[(int64_t)t * p.E + e];
         if (s != s) {
             nan = true;
             s = __uint_as_float(0x7fffffffu);
@@ -276,26 +296,52 @@ __device__ void route_token(const Params &p, int t, Routing &rt, float *buf, boo
     for (int e = lane; e < p.E; e += 32) sum = __fadd_rn(sum, expf(__fsub_rn(buf[e], most)));
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-    float mine = 0.0f;                          // lane j: choice j's logit, then its weight
+    float mine = 0.0f;                          // lane j: choice j's weight
     int mine_e = 0;
+    __syncwarp();
+    if (p.E <= 4 * 32) {
+        // each expert's rank: how many come before it.  No round waits for the one
+        // before; the work grows as E^2 / 32, so that many experts take rounds.
+        uint32_t *keys = reinterpret_cast<uint32_t *>(buf + MAX_E);
+        const int padded = (p.E + 3) / 4 * 4;
 #pragma unroll 1
-    for (int j = 0; j < p.topk; ++j) {
-        uint32_t best = 0, at = 0xffffffffu;    // this lane's largest key and its lowest index
+        for (int e = lane; e < padded; e += 32) keys[e] = e < p.E ? order_key(buf[e]) : 0u;   // (0 comes last)
+        __syncwarp();
 #pragma unroll 1
         for (int e = lane; e < p.E; e += 32) {
-            const float v = buf[e];
-            const uint32_t key = __float_as_uint(v) == TAKEN ? 0u : max(order_key(v), 1u);
-            if (key > best) { best = key; at = (uint32_t)e; }
-        }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? at : 0xffffffffu);
-        if (lane == j) {
-            mine = buf[e];
-            mine_e = e;
+            const uint32_t key = keys[e];
+            int rank = 0;
+#pragma unroll 4
+            for (int o = 0; o < padded; o += 4) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(keys + o);
+                rank += (k.x > key || (k.x == key && o < e)) + (k.y > key || (k.y == key && o + 1 < e)) +
+                        (k.z > key || (k.z == key && o + 2 < e)) + (k.w > key || (k.w == key && o + 3 < e));
+            }
+            if (rank < p.topk) chosen[rank] = e;
         }
         __syncwarp();
-        if ((e & 31) == lane) buf[e] = __uint_as_float(TAKEN);
-        __syncwarp();
+        if (lane < p.topk) mine_e = chosen[lane];
+        mine = buf[mine_e];
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < p.topk; ++j) {
+            uint32_t best = 0, at = 0xffffffffu;    // this lane's largest key and its lowest index
+#pragma unroll 1
+            for (int e = lane; e < p.E; e += 32) {
+                const float v = buf[e];
+                const uint32_t key = __float_as_uint(v) == TAKEN ? 0u : max(order_key(v), 1u);
+                if (key > best) { best = key; at = (uint32_t)e; }
+            }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? at : 0xffffffffu);
+            if (lane == j) {
+                mine = buf[e];
+                mine_e = e;
+            }
+            __syncwarp();
+            if ((e & 31) == lane) buf[e] = __uint_as_float(TAKEN);
+            __syncwarp();
+        }
     }
     mine = __fdiv_rn(expf(__fsub_rn(mine, most)), sum);
     if (p.renormalize) {
@@ -305,63 +351,66 @@ __device__ void route_token(const Params &p, int t, Routing &rt, float *buf, boo
         mine = __fdiv_rn(mine, total);
     }
     if (lane < p.topk) {
-        const int slot = t * p.topk + lane;
-        rt.weight[slot] = mine;
-        rt.expert[slot] = (short)mine_e;
-        if (write) {
-            p.weights[slot] = mine;
-            p.indices[slot] = mine_e;
-        }
+        p.weights[t * p.topk + lane] = mine;
+        p.indices[t * p.topk + lane] = mine_e;
     }
 }
 
-// The experts' slot lists and chunks of up to NT slots (one warp).
+// The experts' slot lists and their chunks of up to NT slots, by the whole CTA from
+// the experts that the tokens chose.
 template <int NT>
 __device__ void route_lists(const Params &p, Routing &rt) {
-    const int lane = threadIdx.x & 31;
-    const int slots = p.T * p.topk;
-    for (int e = lane; e < p.E; e += 32) rt.count[e] = 0;
-    __syncwarp();
-    for (int s0 = 0; s0 < slots; s0 += 32) {
-        const int s = s0 + lane;
-        const int e = s < slots ? rt.expert[s] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const int before = e >= 0 ? rt.count[e] : 0;
-        const int r = before + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0) {
-            rt.rank[s] = (short)r;
-            if ((same >> lane) == 1u) rt.count[e] = (short)(r + 1);   // the last of them
-        }
-        __syncwarp();
+    const int lane = threadIdx.x & 31, slots = p.T * p.topk;
+    for (int s = threadIdx.x; s < slots; s += THREADS) {
+        // (an index out of range is left by a router that gave up: its error is reported)
+        rt.expert[s] = (short)min((unsigned)__ldcg(p.indices + s), (unsigned)(p.E - 1));
     }
-    int slot_base = 0, chunk_base = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const int n = e < p.E ? rt.count[e] : 0;
-        const int c = (n + NT - 1) / NT;
-        int ns = n, cs = c;                     // inclusive prefix sums
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int a = __shfl_up_sync(0xffffffffu, ns, o), b = __shfl_up_sync(0xffffffffu, cs, o);
-            if (lane >= o) { ns += a; cs += b; }
-        }
-        if (e < p.E) {
-            rt.first[e] = (short)(slot_base + ns - n);
-            rt.chunk0[e] = (short)(chunk_base + cs - c);
-            for (int i = 0; i < c; ++i) {
-                const int at = chunk_base + cs - c + i;
-                rt.c_expert[at] = (short)e;
-                rt.c_first[at] = (short)(slot_base + ns - n + i * NT);
-                rt.c_n[at] = (short)min(NT, n - i * NT);
+    for (int e = threadIdx.x; e < p.E; e += THREADS) rt.count[e] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // a slot's place among its expert's, 32 slots at a time
+#pragma unroll 1
+        for (int s0 = 0; s0 < slots; s0 += 32) {
+            const int s = s0 + lane;
+            const int e = s < slots ? rt.expert[s] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int r = (e >= 0 ? rt.count[e] : 0) + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e >= 0) {
+                rt.rank[s] = (short)r;
+                if ((same >> lane) == 1u) rt.count[e] = r + 1;   // the last of them
             }
+            __syncwarp();
         }
-        slot_base += __shfl_sync(0xffffffffu, ns, 31);
-        chunk_base += __shfl_sync(0xffffffffu, cs, 31);
+        int slot_base = 0, chunk_base = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < p.E ? rt.count[e] : 0;
+            const int c = (n + NT - 1) / NT;
+            int ns = n, cs = c;                 // inclusive prefix sums
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int a = __shfl_up_sync(0xffffffffu, ns, o), b = __shfl_up_sync(0xffffffffu, cs, o);
+                if (lane >= o) { ns += a; cs += b; }
+            }
+            if (e < p.E) {
+                rt.first[e] = (short)(slot_base + ns - n);
+#pragma unroll 1
+                for (int i = 0; i < c; ++i) {
+                    const int at = chunk_base + cs - c + i;
+                    rt.c_expert[at] = (short)e;
+                    rt.c_first[at] = (short)(slot_base + ns - n + i * NT);
+                    rt.c_n[at] = (short)min(NT, n - i * NT);
+                }
+            }
+            slot_base += __shfl_sync(0xffffffffu, ns, 31);
+            chunk_base += __shfl_sync(0xffffffffu, cs, 31);
+        }
+        if (lane == 0) rt.chunks = chunk_base;
     }
-    if (lane == 0) rt.chunks = chunk_base;
-    __syncwarp();
-    for (int s = lane; s < slots; s += 32) rt.list[rt.first[rt.expert[s]] + rt.rank[s]] = (short)s;
+    __syncthreads();
+    for (int s = threadIdx.x; s < slots; s += THREADS) rt.list[rt.first[rt.expert[s]] + rt.rank[s]] = (short)s;
 }
 
 // ------------------------------------------------------------ work ranges
@@ -389,20 +438,22 @@ struct Parts {
     int c0, c1, part0;
     __device__ Parts(const Work &w, int u)
         : c0(w.owner(u * w.kb)), c1(w.owner((u + 1) * w.kb - 1)), part0(w.begin(c0) >= u * w.kb ? 0 : 1) {}
-    // the sum of value `at` of each, four loads at a time, in ascending order of k
-    __device__ float sum(const float *parts, int64_t size, int at) const {
-        const float *src = parts + at;
-        float s = 0.0f;
-        for (int c = c0; c <= c1; c += 4) {
-            float v[4];
+    // values `at` .. + 3 of tokens c .. c + 7 (those below n), in ascending order of k
+    __device__ void sum8(const float *parts, int64_t size, int at, int c, int n, float4 (&s)[8]) const {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = c + i <= c1 ? __ldcg(src + (2 * (int64_t)(c + i) + (c + i == c0 ? part0 : 0)) * size) : 0.0f;
+        for (int i = 0; i < 8; ++i) s[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int cta = c0; cta <= c1; ++cta) {
+            const float *src = parts + (2 * (int64_t)cta + (cta == c0 ? part0 : 0)) * size + c * ROWS + at;
+            float4 v[8];                        // (loads under way together)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c + i <= c1) s = __fadd_rn(s, v[i]);
+            for (int i = 0; i < 8; ++i)
+                v[i] = c + i < n ? __ldcg(reinterpret_cast<const float4 *>(src + i * ROWS)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] = make_float4(__fadd_rn(s[i].x, v[i].x), __fadd_rn(s[i].y, v[i].y), __fadd_rn(s[i].z, v[i].z),
+                                   __fadd_rn(s[i].w, v[i].w));
         }
-        return s;
     }
 };
 
@@ -422,7 +473,9 @@ __device__ __forceinline__ bool for_pieces(const Work &w, Fn f) {
     return true;
 }
 
-__device__ __forceinline__ void promoters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ float gated(float g, float up) {
+    return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
+}
 
 // ------------------------------------------------------------ activations
 // The larger of two magnitudes; NaN (as bits above every number) if either is.
@@ -488,11 +541,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Routing rt;
     __shared__ float b_scale[SB][NT];
-    __shared__ uint64_t bars[2 * A_STAGES + 2 * SB + 4];
+    __shared__ uint64_t bars[2 * A_STAGES + 2 * SB + 6];
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned int s_last;
     const uint32_t smem0 = smem_u32(smem), bar0 = smem_u32(bars);
-    float *ex = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES + SB * K_::B_BYTES);
     auto a_at = [&](int s) { return smem0 + (uint32_t)(s * A_BYTES); };
     auto b_at = [&](int s) { return smem0 + (uint32_t)(A_STAGES * A_BYTES + s * K_::B_BYTES); };
     auto a_full = [&](int s) { return bar0 + 8u * s; };
@@ -501,6 +553,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto b_empty = [&](int s) { return bar0 + 8u * (2 * A_STAGES + SB + s); };
     auto t_full = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + b); };
     auto t_empty = [&](int b) { return bar0 + 8u * (2 * A_STAGES + 2 * SB + 2 + b); };
+    const uint32_t tile_left = bar0 + 8u * (2 * A_STAGES + 2 * SB + 4), tile_taken = tile_left + 8u;
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const unsigned int G = gridDim.x;
@@ -519,6 +572,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(t_full(b), 1);
             mbar_init(t_empty(b), 4);
         }
+        mbar_init(tile_left, 4);
+        mbar_init(tile_taken, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&tm_gate);
         prefetch_map(&tm_up);
@@ -529,37 +584,47 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- phase 0: logits, and the shared tiles' arrival counters
     for (int i = blockIdx.x * THREADS + threadIdx.x; i < p.n_arrivals; i += G * THREADS) p.arrivals[i] = 0;
     if (p.router) {
-        float(*red)[32] = reinterpret_cast<float(*)[32]>(ex);
-        const int tt = (p.T + 7) / 8, et = (p.E + 3) / 4;
-        for (int i = blockIdx.x; i < tt * et * p.slices; i += G) {
+        const int tt = (p.T + LOGIT_T - 1) / LOGIT_T, et = (p.E + LOGIT_E - 1) / LOGIT_E;
+        for (int i = warp * (int)G + blockIdx.x; i < tt * et * p.slices; i += (THREADS / 32) * G) {
             const int slice = i % p.slices, tile = i / p.slices;
-            logits_tile<XT>(p, tile / et * 8, tile % et * 4, slice, red);
+            logits_task<XT>(p, tile / et * LOGIT_T, tile % et * LOGIT_E, slice);
         }
     }
     bool ok = true;
-    __threadfence();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     if (threadIdx.x == 0) {
-        atomicAdd(&p.sync[0], 1u);
+        add_release(&p.sync[0]);
         s_last = grid_wait(&p.sync[0], G, lim);
     }
     __syncthreads();
     ok = s_last != 0;
-    if (ok) {
-        float *buf = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES) + warp * MAX_E;   // (where activations go later)
-        for (int t = warp; t < p.T; t += THREADS / 32) route_token(p, t, rt, buf, blockIdx.x == 0);
+    // each token is routed by one CTA, the result read by all after another barrier
+    // (every CTA routing every token: 36 us of T = 64's 115)
+    for (int t = blockIdx.x; ok && t < p.T; t += G) {
+        float *buf = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES);   // (where activations go later)
+        if (p.router) token_logits(p, t, buf);
         __syncthreads();
-        if (warp == 0) route_lists<NT>(p, rt);
-    } else if (threadIdx.x == 0) {
-        rt.chunks = 0;
+        if (warp == 0) route_token(p, t, buf, reinterpret_cast<int *>(buf + 2 * MAX_E));
+        __syncthreads();
     }
+    if (threadIdx.x == 0) {
+        add_release(&p.sync[1]);
+        s_last = ok && grid_wait(&p.sync[1], G, lim);
+    }
+    __syncthreads();
+    ok = s_last != 0;
+    if (ok) route_lists<NT>(p, rt);
+    else if (threadIdx.x == 0) rt.chunks = 0;
     __syncthreads();
     const int kb1 = (p.D + BK - 1) / BK, kb2 = (p.F + BK - 1) / BK;
     const Work w1(rt.chunks, (p.F + 63) / 64, kb1), w2(rt.chunks, (p.D + ROWS - 1) / ROWS, kb2);
     ok = ok && rt.chunks > 0;
+    // (a CTA may be in phase 2 while another still adds phase 1's parts)
+    const int64_t phase_parts = (int64_t)G * 2 * NT * ROWS;
+    unsigned int *done = p.arrivals + rt.chunks * (w1.tiles + w2.tiles);   // tiles of h done, by chunk
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -576,8 +641,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (second) {
                                 tma_load_3d(a_at(s), &tm_down, a_full(s), kb * BK, tile * ROWS, e);
                             } else {
-                                tma_load_3d(a_at(s), &tm_gate, a_full(s), kb * BK, tile * 64, e);
-                                tma_load_3d(a_at(s) + A_BYTES / 2, &tm_up, a_full(s), kb * BK, tile * 64, e);
+                                // 16 rows of gate and the same 16 of up for each promoting warp
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    tma_load_3d(a_at(s) + i * 32 * BK, &tm_gate, a_full(s), kb * BK, tile * 64 + 16 * i, e);
+                                    tma_load_3d(a_at(s) + (i * 32 + 16) * BK, &tm_up, a_full(s), kb * BK, tile * 64 + 16 * i, e);
+                                }
                             }
                         }
                         ++filled;
@@ -628,7 +697,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait_for(t_full((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
         }
         __syncwarp();
-    } else if (warp < PROMOTER0) {
+    } else if (warp < FINISHER) {
         // ------------------------------------------------ activations
         if (ok) {
             // The (block, token) pairs of a piece go round the warps, so that several
@@ -638,10 +707,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int me = warp - 2;
             int bs = 0;
             uint32_t bph = 1;
-            auto split = [&](const Work &w, auto *base, auto row_of, int width, int64_t ld, bool vec, auto parts) {
+            auto split = [&](const Work &w, bool second, auto *base, auto row_of, int width, int64_t ld, bool vec, auto parts) {
                 constexpr int PARTS = decltype(parts)::value;
                 return for_pieces(w, [&](int u, int k0, int k1) {
                     const int ch = u / w.tiles, n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
+                    if (second) {                  // the chunk's h is whole?
+                        bool go = true;
+                        if (lane == 0) go = grid_wait(done + ch, (unsigned)w1.tiles, lim);
+                        if (!__all_sync(0xffffffffu, go)) return false;
+                    }
                     const int dk = SPLITTERS / n, di = SPLITTERS - dk * n;
                     int ik = k0 + me / n, i = me - me / n * n;     // this warp's next pair
                     int fk = ik, fi = i;                           // its next pair to load
@@ -681,26 +755,78 @@ __global__ void __launch_bounds__(THREADS, 1)
                 });
             };
             const int topk = p.topk;
-            bool go = split(w1, static_cast<const XT *>(p.x), [&](int slot) { return slot / topk; }, p.D, p.ldx,
-                            p.x_vec != 0, std::integral_constant<int, P1>{});
-            if (go) {
-                if (lane == 0) go = grid_wait(&p.sync[1], G, lim);   // h is whole
-                if (!__any_sync(0xffffffffu, !go))
-                    split(w2, static_cast<const float *>(p.h), [](int slot) { return slot; }, p.F, p.ldh, true,
-                          std::integral_constant<int, P2>{});
-            }
+            if (split(w1, false, static_cast<const XT *>(p.x), [&](int slot) { return slot / topk; }, p.D, p.ldx,
+                      p.x_vec != 0, std::integral_constant<int, P1>{}))
+                split(w2, true, static_cast<const float *>(p.h), [](int slot) { return slot; }, p.F, p.ldh, true,
+                      std::integral_constant<int, P2>{});
         }
+    } else if (warp == FINISHER) {
+        // ------------------------------------------------ finished tiles
+        // What a tile's end needs beyond its sums waits for memory: publishing h,
+        // counting the CTAs done with a shared tile, adding its parts.  This warp does
+        // that while the promoters go on with the next tile.
+        if (ok) {
+            uint32_t ph = 0;
+            auto finish = [&](const Work &w, bool second) {
+                return for_pieces(w, [&](int u, int k0, int k1) {
+                    if (!warp_wait(tile_left, ph, lim)) return false;
+                    if (lane == 0) mbar_arrive(tile_taken);
+                    ph ^= 1;
+                    const int ch = u / w.tiles, tile = u - ch * w.tiles;
+                    bool publish = !second;
+                    if (k0 != 0 || k1 != w.kb) {
+                        const Parts pt(w, u);
+                        const float *parts = p.parts + (second ? phase_parts : 0);
+                        bool last = false;
+                        if (lane == 0)
+                            last = add_acq_rel(&p.arrivals[second ? w1.tiles * rt.chunks + u : u]) == (unsigned)(pt.c1 - pt.c0);
+                        last = __any_sync(0xffffffffu, last);
+                        __syncwarp();
+                        publish = publish && last;
+                        if (last) {
+                            const int n = rt.c_n[ch], first = rt.c_first[ch];
+                            // 4 neighbouring rows for each lane
+                            const int r0 = 4 * lane, f = tile * 64 + (r0 >> 5) * 16 + (r0 & 15);
+#pragma unroll 1
+                            for (int c = 0; c < n; c += 8) {
+                                float4 s[8];
+                                pt.sum8(parts, NT * ROWS, r0, c, n, s);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    if (c + i >= n) break;
+                                    const int slot = rt.list[first + c + i];
+                                    if (second) {
+                                        if (tile * ROWS + r0 < p.ldo)
+                                            __stcg(reinterpret_cast<float4 *>(p.out + (int64_t)slot * p.ldo + tile * ROWS + r0), s[i]);
+                                    } else {
+                                        // up's rows are 16 after gate's: four lanes on
+                                        const float4 up = make_float4(__shfl_xor_sync(0xffffffffu, s[i].x, 4), __shfl_xor_sync(0xffffffffu, s[i].y, 4),
+                                                                      __shfl_xor_sync(0xffffffffu, s[i].z, 4), __shfl_xor_sync(0xffffffffu, s[i].w, 4));
+                                        if ((lane & 4) == 0 && f < p.ldh)
+                                            __stcg(reinterpret_cast<float4 *>(p.h + (int64_t)slot * p.ldh + f),
+                                                   make_float4(gated(s[i].x, up.x), gated(s[i].y, up.y), gated(s[i].z, up.z), gated(s[i].w, up.w)));
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (publish && lane == 0) add_release(done + ch);
+                    return true;
+                });
+            };
+            if (finish(w1, false)) finish(w2, true);
+        }
+        __syncwarp();
+        if (lane == 0) add_release(&p.sync[2]);
     } else {
         // ------------------------------------------------ promotion
         const int q = warp & 3, row = q * 32 + lane;
         int b = 0, bs = 0;
-        uint32_t tph = 0, bph = 0;
-        // A warp whose wait ran out goes on without waiting or computing, so that
-        // the four warps still meet at every promoters_sync.
-        bool alive = true;
+        uint32_t tph = 0, fph = 1;
         auto promote = [&](const Work &w, bool second, auto parts_) {
             constexpr int PARTS = decltype(parts_)::value;
-            for_pieces(w, [&](int u, int k0, int k1) {
+            return for_pieces(w, [&](int u, int k0, int k1) {
                 const int ch = u / w.tiles, tile = u - ch * w.tiles;
                 const int e = rt.c_expert[ch], n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
                 // this row's weight scales, block after block
@@ -708,7 +834,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (second) {
                     ws = p.s_down + ((int64_t)e * ((p.D + 127) / 128) + tile) * w.kb;
                 } else {
-                    ws = (row < 64 ? p.s_gate : p.s_up) + ((int64_t)e * ((p.F + 127) / 128) + tile / 2) * w.kb;
+                    ws = (lane < 16 ? p.s_gate : p.s_up) + ((int64_t)e * ((p.F + 127) / 128) + tile / 2) * w.kb;
                 }
                 float acc[NT];
 #pragma unroll
@@ -717,18 +843,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int kb = k0; kb < k1; ++kb) {
                     const float sw = ws_next;
                     if (kb + 1 < k1) ws_next = __ldg(ws + kb + 1);
-                    alive = alive && warp_wait(t_full(b), tph, lim);
-                    if (!alive) break;
+                    if (!warp_wait(t_full(b), tph, lim)) return false;
                     tc_fence_after();
                     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 4 * NT);
 #pragma unroll
                     for (int i0 = 0; i0 < NT; i0 += 8) {
                         if (i0 >= n8) break;
                         uint32_t r[PARTS][8];
-#pragma unroll
-                        for (int i = 0; i < PARTS; ++i) tmem_ld_async(ta + (uint32_t)(i * n8 + i0), r[i]);
-#pragma unroll
-                        for (int i = 0; i < PARTS; ++i) tmem_ld_wait(r[i]);
+                        tmem_ld_parts(ta + (uint32_t)i0, (uint32_t)n8, r);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float t = __uint_as_float(r[PARTS - 1][j]);
@@ -745,76 +867,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mbar_arrive(b_empty(bs));   // (the block's MMAs are done too)
                     }
                     if (++b == 2) { b = 0; tph ^= 1; }
-                    if (++bs == SB) { bs = 0; bph ^= 1; }
+                    if (++bs == SB) bs = 0;
                 }
-                if (k0 == 0 && k1 == w.kb) {
-                    // the whole sum is here
-                    if (second) {
-                        const int d = tile * ROWS + row;
+                if (k0 != 0 || k1 != w.kb) {
+                    // a share of the sum
+                    const Parts pt(w, u);
+                    float *dst = p.parts + (second ? phase_parts : 0) + ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == pt.c0 ? pt.part0 : 0)) * NT * ROWS + row;
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
-                            if (i < n && d < p.D) __stcg(p.out + (int64_t)rt.list[first + i] * p.D + d, acc[i]);
-                    } else {
-                        const int f = tile * 64 + (row & 63);
-                        promoters_sync();       // (the tile before has been read)
-                        if (row >= 64) {
+                    for (int i = 0; i < NT; ++i)
+                        if (i < n) __stcg(dst + i * ROWS, acc[i]);
+                } else if (second) {
+                    const int d = tile * ROWS + row;
 #pragma unroll
-                            for (int i = 0; i < NT; ++i)
-                                if (i < n) ex[i * 64 + row - 64] = acc[i];
-                        }
-                        promoters_sync();
-                        if (row < 64 && f < p.F) {
+                    for (int i = 0; i < NT; ++i)
+                        if (i < n && d < p.D) __stcg(p.out + (int64_t)rt.list[first + i] * p.ldo + d, acc[i]);
+                } else {
+                    // gate in the lower 16 lanes, up in the upper ones: the lower take the
+                    // even tokens, the upper the odd ones
+                    const int f = tile * 64 + q * 16 + (lane & 15);
 #pragma unroll
-                            for (int i = 0; i < NT; ++i)
-                                if (i < n) {
-                                    const float g = acc[i];
-                                    const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
-                                    __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, ex[i * 64 + row]));
-                                }
-                        }
-                    }
-                    return true;
-                }
-                // a share of the sum
-                const Parts pt(w, u);
-                float *dst = p.parts + ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == pt.c0 ? pt.part0 : 0)) * NT * ROWS + row;
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    if (i < n) __stcg(dst + i * ROWS, acc[i]);
-                __threadfence();
-                promoters_sync();
-                if (row == 0)
-                    s_last = atomicAdd(&p.arrivals[second ? w1.tiles * rt.chunks + u : u], 1u) == (unsigned)(pt.c1 - pt.c0);
-                promoters_sync();
-                if (s_last) {
-                    __threadfence();
-                    if (second) {
-                        const int d = tile * ROWS + row;
-                        for (int i = 0; i < n; ++i) {
-                            const float v = pt.sum(p.parts, NT * ROWS, i * ROWS + row);
-                            if (d < p.D) __stcg(p.out + (int64_t)rt.list[first + i] * p.D + d, v);
-                        }
-                    } else {
-                        const int f = tile * 64 + (row & 63);
-                        for (int i = row >> 6; i < n; i += 2) {
-                            const float g = pt.sum(p.parts, NT * ROWS, i * ROWS + (row & 63));
-                            const float up = pt.sum(p.parts, NT * ROWS, i * ROWS + 64 + (row & 63));
-                            const float sl = __fdiv_rn(g, __fadd_rn(1.0f, expf(-g)));
-                            if (f < p.F) __stcg(p.h + (int64_t)rt.list[first + i] * p.ldh + f, __fmul_rn(sl, up));
-                        }
+                    for (int i = 0; i < NT; i += 2) {
+                        if (i >= n) break;
+                        const bool low = lane < 16;
+                        const float other = __shfl_xor_sync(0xffffffffu, low ? acc[i + 1] : acc[i], 16);
+                        const int c = low ? i : i + 1;
+                        if (c < n && f < p.F)
+                            __stcg(p.h + (int64_t)rt.list[first + c] * p.ldh + f,
+                                   gated(low ? acc[i] : other, low ? other : acc[i + 1]));
                     }
                 }
+                // the finisher has taken the tile before; this one is its now
+                if (!warp_wait(tile_taken, fph, lim)) return false;
+                fph ^= 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tile_left);
                 return true;
             });
         };
-        if (ok) promote(w1, false, std::integral_constant<int, P1>{});
-        __threadfence();
-        promoters_sync();
-        if (row == 0) atomicAdd(&p.sync[1], 1u);
-        if (ok) promote(w2, true, std::integral_constant<int, P2>{});
-        __threadfence();
-        promoters_sync();
-        if (row == 0) atomicAdd(&p.sync[2], 1u);
+        if (ok && promote(w1, false, std::integral_constant<int, P1>{}))
+            promote(w2, true, std::integral_constant<int, P2>{});
     }
     // ---- phase 3: y
     if (threadIdx.x == THREADS - 1) s_last = grid_wait(&p.sync[2], G, lim);
@@ -829,11 +920,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int across = (p.D + 31) / 32;
         for (int task = warp * (int)G + blockIdx.x; task < p.T * across; task += (THREADS / 32) * G) {
             const int t = task / across, d = (task - t * across) * 32 + lane;
-            const float *src = p.out + (int64_t)t * p.topk * p.D + min(d, p.D - 1);
+            const float *src = p.out + (int64_t)t * p.topk * p.ldo + min(d, p.D - 1);
             float sum = 0.0f;
 #pragma unroll 4
             for (int j = 0; j < p.topk; ++j)
-                sum = __fmaf_rn(rt.weight[t * p.topk + j], __ldcg(src + (int64_t)j * p.D), sum);
+                sum = __fmaf_rn(__ldcg(p.weights + t * p.topk + j), __ldcg(src + (int64_t)j * p.ldo), sum);
             if (d < p.D) {
                 XT *y = static_cast<XT *>(p.y) + (int64_t)t * p.ldy + d;
                 if (sizeof(XT) == 2) *reinterpret_cast<__nv_bfloat16 *>(y) = __float2bfloat16_rn(sum);
@@ -843,10 +934,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncthreads();
     // the last CTA to leave clears the barriers for the next call
-    if (threadIdx.x == 0 && atomicAdd(&p.sync[3], 1u) == G - 1) {
+    if (threadIdx.x == 0 && add_acq_rel(&p.sync[3]) == G - 1)
         p.sync[0] = p.sync[1] = p.sync[2] = p.sync[3] = 0;
-        __threadfence();
-    }
 }
 
 }  // namespace moe
@@ -923,13 +1012,14 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     // leave room for more stages: T = 64, 8 tokens an expert, 145 us with 64 columns.
     const int64_t want = std::min<int64_t>(T, (2 * slots + E - 1) / E);
     const int nt = want <= 8 ? 8 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
-    const int64_t logit_tiles = ((T + 7) / 8) * ((E + 3) / 4);
+    const int64_t logit_tasks = ((T + moe::LOGIT_T - 1) / moe::LOGIT_T) * ((E + moe::LOGIT_E - 1) / moe::LOGIT_E);   // a warp each
     p.slices = p.router ? (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fp8::blocks_of(D), moe::LOGIT_SLICES),
-                                                                      sms / logit_tiles))
+                                                                      sms * (moe::THREADS / 32) / logit_tasks))
                         : 1;
     p.ldh = (int)((F + 3) / 4 * 4);
+    p.ldo = (int)((D + 3) / 4 * 4);
     const int64_t chunks = std::min<int64_t>(slots, std::min(E, slots) + slots / nt);   // at most
-    const int64_t arrivals = chunks * ((F + 63) / 64 + (D + 127) / 128);
+    const int64_t arrivals = chunks * ((F + 63) / 64 + (D + 127) / 128 + 1);
     // blocks of 128 k and tasks are counted in int
     if (arrivals * fp8::blocks_of(std::max(D, F)) > INT32_MAX || T * D > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
     p.n_arrivals = (int)arrivals;
@@ -941,8 +1031,8 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     if (st != SGEMM_OK) return st;
     if (fresh && cudaMemsetAsync(sync, 0, 256, s) != cudaSuccess) return launch_status();
     const size_t b_arr = up256((size_t)arrivals * 4), b_log = up256((size_t)p.slices * T * E * 4),
-                 b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)sms * 2 * nt * moe::ROWS * 4),
-                 b_out = up256((size_t)slots * D * 4);
+                 b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)2 * sms * 2 * nt * moe::ROWS * 4),
+                 b_out = up256((size_t)slots * p.ldo * 4);
     st = workspace(s, b_arr + b_log + b_h + b_parts + b_out, &ws);
     if (st != SGEMM_OK) return st;
     char *w = static_cast<char *>(ws);
@@ -956,8 +1046,8 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     const int esize = x_type == SGEMM_TYPE_F32 ? 4 : 2;
     p.x_vec = reinterpret_cast<uintptr_t>(p.x) % (4 * esize) == 0 && p.ldx % 4 == 0;
     CUtensorMap maps[3];
-    if (!experts_map(&maps[0], gate, E, F, D, ld_in, stride_in, 64) ||
-        !experts_map(&maps[1], up, E, F, D, ld_in, stride_in, 64) ||
+    if (!experts_map(&maps[0], gate, E, F, D, ld_in, stride_in, 16) ||
+        !experts_map(&maps[1], up, E, F, D, ld_in, stride_in, 16) ||
         !experts_map(&maps[2], down, E, D, F, ld_down, stride_down, 128))
         return SGEMM_ERR_UNSUPPORTED;
     return x_type == SGEMM_TYPE_F32 ? launch_moe<float>(maps, p, nt, sms, s)

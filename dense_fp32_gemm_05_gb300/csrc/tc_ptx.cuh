@@ -238,6 +238,52 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                  :: "memory");
 }
 
+// 32 lanes x 8 columns at each of several places `step` columns apart, complete when
+// it returns: one statement, so that no register can be moved while a read is
+// under way.
+__device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uint32_t (&r)[2][8]) {
+    asm volatile("{\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;\n\t}"
+                 : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]),
+                   "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
+                   "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
+                   "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7])
+                 : "r"(taddr), "r"(taddr + 1 * step) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uint32_t (&r)[3][8]) {
+    asm volatile("{\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;\n\t}"
+                 : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]),
+                   "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
+                   "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
+                   "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]),
+                   "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
+                   "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7])
+                 : "r"(taddr), "r"(taddr + 1 * step), "r"(taddr + 2 * step) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uint32_t (&r)[4][8]) {
+    asm volatile("{\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;\n\t}"
+                 : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]),
+                   "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
+                   "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
+                   "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]),
+                   "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
+                   "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7]),
+                   "=r"(r[3][0]), "=r"(r[3][1]), "=r"(r[3][2]), "=r"(r[3][3]),
+                   "=r"(r[3][4]), "=r"(r[3][5]), "=r"(r[3][6]), "=r"(r[3][7])
+                 : "r"(taddr), "r"(taddr + 1 * step), "r"(taddr + 2 * step), "r"(taddr + 3 * step) : "memory");
+}
+
 // Shared-memory matrix descriptors of 8-bit operands, tiles of 128-byte rows
 // with the 128-byte swizzle.  K-major: a row is 128 k of one m (or n), 8-row
 // atoms 1024 bytes apart; the next 32 k are 32 bytes on.  MN-major: a row is
