@@ -125,6 +125,8 @@ def _declare(lib):
 def load():
     """Loads the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -295,34 +297,49 @@ def gemm(A, B, C, transA="N", transB="N", alpha=1.0, beta=0.0, path=PATH_AUTO, s
     return C
 
 
-_types = None
+_types = {}
 
 
 def _type_of(dtype):
     """The library's type code of a torch dtype (None: not one of its types)."""
-    global _types
-    if _types is None:
+    if not _types:
         import torch
-        _types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
-                  torch.float8_e4m3fn: TYPE_E4M3, torch.float8_e5m2: TYPE_E5M2}
+        _types.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
+                       torch.float8_e4m3fn: TYPE_E4M3, torch.float8_e5m2: TYPE_E5M2})
     return _types.get(dtype)
 
 
-def _matrix(name, t, types):
-    """(address, type, leading dimension) of a 2-D row-major CUDA tensor."""
-    code = _type_of(t.dtype)
-    if code not in types or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of a type the call takes")
+_FLOATS, _CODES, _SCALES = (TYPE_F32, TYPE_BF16), (TYPE_E4M3, TYPE_E5M2), (TYPE_F32,)
+
+
+def _matrix(name, t, types, device=None):
+    """(address, type, leading dimension, rows, columns) of a 2-D row-major CUDA
+    tensor on `device` (an index).  Small calls take as long as this takes."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
     ld, unit = t.stride()
-    if cols > 1 and unit != 1:
-        raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.data_ptr(), code, (ld if rows > 1 and ld > cols else max(cols, 1))
+    code = _types.get(t.dtype) if _types else _type_of(t.dtype)
+    if code not in types or not t.is_cuda or (unit != 1 and cols > 1):
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of a type the call takes, with unit "
+                         "stride along its last dimension")
+    if device is not None and t.get_device() != device:
+        raise ValueError("the operands must be on one device")
+    return t.data_ptr(), code, (ld if rows > 1 and ld > cols else cols or 1), rows, cols
+
+
+_raw_stream = None
 
 
 def _current_stream(device):
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    """torch's current stream on a device (an index) as an address."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # (the public current_stream() builds an object: 2 us on a Grace core)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device)
 
 
 def sgemm_fp8_quantize(rows, cols, X, x_type, ldx, group_rows, group_cols, Q, q_type, ldq, S, lds,
@@ -342,28 +359,25 @@ def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
     buffers to write into.  Asynchronous on ``stream`` (default: torch's current
     stream on X's device); raises SgemmError on any non-zero status.
     """
-    import torch
-
-    px, tx, ldx = _matrix("X", X, (TYPE_F32, TYPE_BF16))
-    rows, cols = X.shape
+    device = X.get_device()
+    px, tx, ldx, rows, cols = _matrix("X", X, _FLOATS)
     gr, gc = group
     if Q is None:
+        import torch
         Q = torch.empty((rows, cols), device=X.device, dtype=dtype or torch.float8_e4m3fn)
-    elif Q.shape != X.shape or (dtype is not None and dtype != Q.dtype):
-        raise ValueError("Q must have X's shape and the given dtype")
-    pq, tq, ldq = _matrix("Q", Q, (TYPE_E4M3, TYPE_E5M2))
-    row_blocks, col_blocks = (rows + 127) // 128, (cols + 127) // 128
-    shape = ((col_blocks, rows) if gr == 1 else
-             (row_blocks, cols) if gc == 1 else (row_blocks, col_blocks))
+    elif dtype is not None and dtype != Q.dtype:
+        raise ValueError("Q is not of the given dtype")
+    pq, tq, ldq, q_rows, q_cols = _matrix("Q", Q, _CODES, device)
+    s_rows, s_cols = (((cols + 127) // 128, rows) if gr == 1 else
+                      ((rows + 127) // 128, cols if gc == 1 else (cols + 127) // 128))
     if S is None:
-        S = torch.empty(shape, device=X.device, dtype=torch.float32)
-    elif S.shape != shape:
-        raise ValueError(f"S must have shape {shape}")
-    ps, _, lds = _matrix("S", S, (TYPE_F32,))
-    if Q.device != X.device or S.device != X.device:
-        raise ValueError("X, Q and S must be on one device")
+        import torch
+        S = torch.empty((s_rows, s_cols), device=X.device, dtype=torch.float32)
+    ps, _, lds, have_rows, have_cols = _matrix("S", S, _SCALES, device)
+    if q_rows != rows or q_cols != cols or have_rows != s_rows or have_cols != s_cols:
+        raise ValueError(f"Q must have X's shape and S the shape ({s_rows}, {s_cols})")
     st = load().sgemm_fp8_quantize(rows, cols, px, tx, ldx, gr, gc, pq, tq, ldq, ps, lds,
-                                   _current_stream(X.device) if stream is None else _stream(stream))
+                                   _current_stream(device) if stream is None else _stream(stream))
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_fp8_quantize")
     return Q, S
@@ -396,28 +410,25 @@ def fp8_gemm(A, SA, B, SB, C, transA="N", transB="T", alpha=1.0, beta=0.0, a_gro
     Asynchronous on ``stream`` (default: torch's current stream on C's device);
     raises SgemmError on any non-zero status.
     """
-    pa, a_type, lda = _matrix("A", A, (TYPE_E4M3, TYPE_E5M2))
-    pb, b_type, ldb = _matrix("B", B, (TYPE_E4M3, TYPE_E5M2))
-    pc, c_type, ldc = _matrix("C", C, (TYPE_F32, TYPE_BF16))
-    psa, _, ldsa = _matrix("SA", SA, (TYPE_F32,))
-    psb, _, ldsb = _matrix("SB", SB, (TYPE_F32,))
-    ta, tb = transA.upper(), transB.upper()
-    M, N = C.shape
-    K = A.shape[1] if ta == "N" else A.shape[0]
-    kb = (K + 127) // 128
-    if A.shape != ((M, K) if ta == "N" else (K, M)) or B.shape != ((K, N) if tb == "N" else (N, K)):
+    device = C.get_device()
+    pa, a_type, lda, a_rows, a_cols = _matrix("A", A, _CODES, device)
+    pb, b_type, ldb, b_rows, b_cols = _matrix("B", B, _CODES, device)
+    pc, c_type, ldc, M, N = _matrix("C", C, _FLOATS)
+    psa, _, ldsa, sa_rows, sa_cols = _matrix("SA", SA, _SCALES, device)
+    psb, _, ldsb, sb_rows, sb_cols = _matrix("SB", SB, _SCALES, device)
+    a_trans, b_trans = transA in "TtCc", transB in "TtCc"
+    K, a_m = (a_rows, a_cols) if a_trans else (a_cols, a_rows)
+    b_n, b_k = (b_rows, b_cols) if b_trans else (b_cols, b_rows)
+    if a_m != M or b_n != N or b_k != K:
         raise ValueError("the shapes of A, B and C do not fit together")
-
-    def blocks(t):
-        return ((t.shape[0] + 127) // 128, (t.shape[1] + 127) // 128)
-
-    if SA.shape != ((kb, M) if a_group == 1 else blocks(A)) or \
-            SB.shape != ((kb, N) if b_group == 1 else blocks(B)):
-        raise ValueError("the scales' shapes do not fit the operands and their groups")
-    device = C.device
-    if not (A.device == B.device == SA.device == SB.device == device):
-        raise ValueError("the operands must be on one device")
-    st = load().sgemm_fp8(ta.encode(), tb.encode(), M, N, K, alpha, pa, a_type, lda, psa, a_group, ldsa,
+    kb = (K + 127) // 128
+    if ((sa_rows != kb or sa_cols != M) if a_group == 1 else
+            (sa_rows != (a_rows + 127) // 128 or sa_cols != (a_cols + 127) // 128)):
+        raise ValueError("SA's shape does not fit A and its groups")
+    if ((sb_rows != kb or sb_cols != N) if b_group == 1 else
+            (sb_rows != (b_rows + 127) // 128 or sb_cols != (b_cols + 127) // 128)):
+        raise ValueError("SB's shape does not fit B and its groups")
+    st = load().sgemm_fp8(_b(transA), _b(transB), M, N, K, alpha, pa, a_type, lda, psa, a_group, ldsa,
                           pb, b_type, ldb, psb, b_group, ldsb, beta, pc, c_type, ldc,
                           _current_stream(device) if stream is None else _stream(stream))
     if st != SGEMM_OK:
@@ -434,18 +445,21 @@ def sgemm_moe(T, D, F, E, topk, x, x_type, ldx, router, logits, gate, s_gate, up
                             int(renormalize), y, ldy, indices, weights, _stream(stream))
 
 
-def _experts(name, t, E, rows, cols):
-    """(address, row stride, matrix stride) of E matrices of E4M3 codes."""
-    if _type_of(t.dtype) != TYPE_E4M3 or not t.is_cuda or t.shape != (E, rows, cols) or t.stride(2) != 1:
-        raise ValueError(f"{name} must be an {E} x {rows} x {cols} CUDA tensor of float8_e4m3fn codes "
-                         "with unit stride along its last dimension")
-    stride, ld, _ = t.stride()
+def _experts(name, t, shape, device):
+    """(address, row stride, matrix stride) of matrices of E4M3 codes."""
+    if t.shape != shape or _type_of(t.dtype) != TYPE_E4M3 or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor of float8_e4m3fn codes of shape {shape} "
+                         "on the operands' device")
+    stride, ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
     return t.data_ptr(), ld, stride
 
 
-def _packed(name, t, shape, dtype):
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
+def _packed(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} on the "
+                         "operands' device")
     return t.data_ptr()
 
 
@@ -466,40 +480,38 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     """
     import torch
 
-    px, x_type, ldx = _matrix("x", x, (TYPE_F32, TYPE_BF16))
-    T, D = x.shape
-    E, F = gate.shape[:2]
-    device = x.device
-    pg, ld_in, stride_in = _experts("gate", gate, E, F, D)
-    pu, ld_up, stride_up = _experts("up", up, E, F, D)
-    pd, ld_down, stride_down = _experts("down", down, E, D, F)
-    if (ld_up, stride_up) != (ld_in, stride_in):
+    f32, i32 = torch.float32, torch.int32
+    device = x.get_device()
+    px, x_type, ldx, T, D = _matrix("x", x, _FLOATS)
+    E, F, _ = gate.shape
+    inner, outer = (E, F, D), (E, D, F)
+    pg, ld_in, stride_in = _experts("gate", gate, inner, device)
+    pu, ld_up, stride_up = _experts("up", up, inner, device)
+    pd, ld_down, stride_down = _experts("down", down, outer, device)
+    if ld_up != ld_in or stride_up != stride_in:
         raise ValueError("gate and up must have the same strides")
     fb, db = (F + 127) // 128, (D + 127) // 128
-    f32 = torch.float32
+    in_blocks, out_blocks, chosen = (E, fb, db), (E, db, fb), (T, topk)
     if router is None and logits is None:
         raise ValueError("give router or logits")
-    pr = _packed("router", router, (E, D), f32) if router is not None else None
     if logits is None:
-        logits = torch.empty((T, E), device=device, dtype=f32)
+        logits = torch.empty((T, E), device=x.device, dtype=f32)
     if y is None:
-        y = torch.empty((T, D), device=device, dtype=x.dtype)
-    elif y.shape != x.shape or y.dtype != x.dtype:
-        raise ValueError("y must have x's shape and dtype")
+        y = torch.empty((T, D), device=x.device, dtype=x.dtype)
     if indices is None:
-        indices = torch.empty((T, topk), device=device, dtype=torch.int32)
+        indices = torch.empty(chosen, device=x.device, dtype=i32)
     if weights is None:
-        weights = torch.empty((T, topk), device=device, dtype=f32)
-    py, _, ldy = _matrix("y", y, (TYPE_F32, TYPE_BF16))
-    for t in (router, logits, gate, s_gate, up, s_up, down, s_down, y, indices, weights):
-        if t is not None and t.device != device:
-            raise ValueError("the operands must be on one device")
+        weights = torch.empty(chosen, device=x.device, dtype=f32)
+    py, y_type, ldy, y_rows, y_cols = _matrix("y", y, _FLOATS, device)
+    if y_type != x_type or y_rows != T or y_cols != D:
+        raise ValueError("y must have x's shape and dtype")
     st = load().sgemm_moe(
-        T, D, F, E, topk, px, x_type, ldx, pr, _packed("logits", logits, (T, E), f32), pg,
-        _packed("s_gate", s_gate, (E, fb, db), f32), pu, _packed("s_up", s_up, (E, fb, db), f32), ld_in,
-        stride_in, pd, _packed("s_down", s_down, (E, db, fb), f32), ld_down, stride_down,
-        int(renormalize), py, ldy, _packed("indices", indices, (T, topk), torch.int32),
-        _packed("weights", weights, (T, topk), f32),
+        T, D, F, E, topk, px, x_type, ldx,
+        None if router is None else _packed("router", router, (E, D), f32, device),
+        _packed("logits", logits, (T, E), f32, device), pg, _packed("s_gate", s_gate, in_blocks, f32, device),
+        pu, _packed("s_up", s_up, in_blocks, f32, device), ld_in, stride_in,
+        pd, _packed("s_down", s_down, out_blocks, f32, device), ld_down, stride_down, int(renormalize), py,
+        ldy, _packed("indices", indices, chosen, i32, device), _packed("weights", weights, chosen, f32, device),
         _current_stream(device) if stream is None else _stream(stream))
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_moe")
