@@ -80,6 +80,7 @@ struct Params {
     int64_t x_mn, x_k, y_mn, y_k;          // strides of the scales along N / M (per group) and per block of k
     int x_shift, y_shift;                  // a scale for each 1 << shift rows
     int c_vec;                             // quads of C may be accessed whole
+    int c_tma;                             // wide tiles: 1 stored by TMA, 2 added by TMA, 0 neither
     int x_mnmajor, y_mnmajor;              // operand stored across k
     int y_bytes;                           // bytes of Y per stage
     uint32_t idesc;
@@ -431,60 +432,111 @@ __global__ void __launch_bounds__(THREADS, 1)
 // share: the three issuing warps hand theirs over (setmaxnreg).
 // The epilogue turns 32 x 32 blocks around through shared memory.
 constexpr int WT = 256;                        // tile rows and columns
-constexpr int W_THREADS = 384;                 // TMA, MMA, 2 idle (a warpgroup), 8 promoters
 constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
-constexpr int W_STAGE_OUT = 32 * 32 * 4;       // epilogue staging per promoting warp
 
 template <bool YVEC>
 struct Wide {
-    // YVEC: the scales of a promoting warp's 128 columns, in a ring of its own
+    // Promoting warps after the first four (TMA, MMA, 2 idle: a warpgroup): 8 of 32 rows
+    // x 128 columns; YVEC, where two operations a value fill the FMA pipe and more warps
+    // cover their latency, 16 of 32 x 64 (4096 x 4096 x 8192 TN: 8 warps 258 us).
+    static constexpr int WARPS = YVEC ? 16 : 8;
+    static constexpr int THREADS = 32 * (4 + WARPS);
+    static constexpr int PC = WT / (WARPS / 4);            // columns per promoting warp
+    static constexpr int CH = YVEC ? 16 : 32;              // columns read or stored at a time
+    // registers: 384 x 168 = 128 x 40 + 256 x 232, 640 x 96 = 128 x 32 + 512 x 112
+    static constexpr int REGS_ISSUE = YVEC ? 32 : 40, REGS_PROMOTE = YVEC ? 112 : 232;
+    static constexpr int OUT = 32 * CH * 4;                // epilogue staging per warp
+    // YVEC: the scales of a warp's columns, in a ring of its own
     static constexpr int SLOTS = YVEC ? 6 : 0;
-    static constexpr int RING = SLOTS * (WT / 2);          // floats
-    static constexpr int FIXED = 1024 + PROMOTERS * (W_STAGE_OUT + RING * 4) + BAR_BYTES;
+    static constexpr int RING = SLOTS * PC;                // floats
+    static constexpr int FIXED = 1024 + WARPS * (OUT + RING * 4) + BAR_BYTES;
     static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
     static constexpr int SMEM = FIXED + STAGES * W_STAGE;
     static_assert(STAGES >= 4 && STAGES <= MAX_STAGES, "stages");
 };
 
-// One value of C's row m, columns n .. n + 3, from and to memory.
-__device__ __forceinline__ float4 load_c4(const Params &p, int64_t at, int cols, bool vec) {
-    if (vec && cols >= 4) {
-        if (!p.c_bf16) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p.C) + at);
-        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.C) + at);
-        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-    }
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (cols > 0) v.x = load_c(p, at);
-    if (cols > 1) v.y = load_c(p, at + 1);
-    if (cols > 2) v.z = load_c(p, at + 2);
-    if (cols > 3) v.w = load_c(p, at + 3);
-    return v;
+// The 16-byte chunk of a staged row of `bytes` (32, 64 or 128) where chunk c lies: TMA's
+// swizzle over that span.
+template <int BYTES>
+__device__ __forceinline__ int staged_chunk(int row, int c) {
+    return BYTES == 128 ? c ^ (row & 7) : BYTES == 64 ? c ^ ((row >> 1) & 3) : c ^ ((row >> 2) & 1);
 }
-__device__ __forceinline__ void store_c4(const Params &p, int64_t at, float4 a, float4 old, int cols, bool vec) {
-    if (vec && cols >= 4) {
-        const float4 v = make_float4(epilogue(p, a.x, old.x), epilogue(p, a.y, old.y), epilogue(p, a.z, old.z),
-                                     epilogue(p, a.w, old.w));
-        if (!p.c_bf16) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = v;
-        } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.C) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+
+__device__ __forceinline__ float4 epilogue4(const Params &p, float4 a, float4 old) {
+    return make_float4(epilogue(p, a.x, old.x), epilogue(p, a.y, old.y), epilogue(p, a.z, old.z), epilogue(p, a.w, old.w));
+}
+__device__ __forceinline__ float4 load4(const float *c) { return *reinterpret_cast<const float4 *>(c); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *c) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(c);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void store4(float *c, float4 v) { *reinterpret_cast<float4 *>(c) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *c, float4 v) {
+    *reinterpret_cast<uint2 *>(c) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+__device__ __forceinline__ float load1(const float *c) { return *c; }
+__device__ __forceinline__ float load1(const __nv_bfloat16 *c) { return __bfloat162float(*c); }
+__device__ __forceinline__ void store1(float *c, float v) { *c = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16 *c, float v) { *c = __float2bfloat16_rn(v); }
+
+// A staged block of 32 rows x CH columns of sums to C at (m0, n0), through the
+// epilogue: quads of columns where C allows, else a row's columns across the lanes.
+// Several rows' loads of C are under way together.
+template <typename T, int CH>
+__device__ __noinline__ void write_block(const Params &p, const float *stg, int m0, int n0) {
+    const int lane = threadIdx.x & 31;
+    T *C = static_cast<T *>(p.C) + (int64_t)m0 * p.ldc + n0;
+    const int rows = p.M - m0, cols = p.N - n0;
+    if (p.c_vec && cols >= CH) {
+        constexpr int Q = CH / 4, R = 32 / Q;              // quads of a row, rows at a time
+        const int c = lane % Q;
+#pragma unroll
+        for (int i0 = 0; i0 < Q; i0 += 4) {
+            float4 old[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (i0 + i) * R + lane / Q;
+                old[i] = p.beta != 0.0f && r < rows ? load4(C + (int64_t)r * p.ldc + 4 * c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (i0 + i) * R + lane / Q;
+                const float4 v = *reinterpret_cast<const float4 *>(stg + r * CH + 4 * staged_chunk<4 * CH>(r, c));
+                if (r < rows) store4(C + (int64_t)r * p.ldc + 4 * c, epilogue4(p, v, old[i]));
+            }
         }
-        return;
+    } else {
+        constexpr int R = 32 / CH;                         // rows at a time
+        const int c = lane % CH;
+        if (c >= cols) return;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / R; i0 += 8) {
+            float old[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (i0 + i) * R + lane / CH;
+                old[i] = p.beta != 0.0f && r < rows ? load1(C + (int64_t)r * p.ldc + c) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (i0 + i) * R + lane / CH;
+                const float v = stg[r * CH + 4 * staged_chunk<4 * CH>(r, c / 4) + c % 4];
+                if (r < rows) store1(C + (int64_t)r * p.ldc + c, epilogue(p, v, old[i]));
+            }
+        }
     }
-    if (cols > 0) store_c(p, at, a.x, old.x);
-    if (cols > 1) store_c(p, at + 1, a.y, old.y);
-    if (cols > 2) store_c(p, at + 2, a.z, old.z);
-    if (cols > 3) store_c(p, at + 3, a.w, old.w);
 }
 
 // YVEC: B has a scale for each of its rows (else one for each 128 x 128 block).
 template <bool YVEC>
-__global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
-                    const Params p) {
+                    const __grid_constant__ CUtensorMap tm_c, const Params p) {
     using K_ = Wide<YVEC>;
     constexpr int S = K_::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -492,8 +544,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t smem0 = smem_u32(smem);
     float *staging = reinterpret_cast<float *>(smem + S * W_STAGE);
-    float *scales = staging + PROMOTERS * W_STAGE_OUT / 4;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + PROMOTERS * K_::RING);
+    float *scales = staging + K_::WARPS * K_::OUT / 4;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + K_::WARPS * K_::RING);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -514,7 +566,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), 2 * PROMOTERS);   // of both CTAs, on the leader's
+            mbar_init(tempty(b), 2 * K_::WARPS);   // of both CTAs, on the leader's
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&tm_x);
@@ -529,7 +581,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
 
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(K_::REGS_ISSUE));
         if (warp == 0) {
             // ------------------------------------------------ TMA producer
             {
@@ -594,13 +646,13 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ promotion and epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        constexpr int PC = WT / 2, CH = 32, NC = PC / CH;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(K_::REGS_PROMOTE));
+        constexpr int PC = K_::PC, CH = K_::CH, NC = PC / CH;
         constexpr int BATCH = YVEC ? 2 : 4;        // blocks whose scales are fetched together
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
+        const int q = warp & 3, part = (warp - 4) >> 2;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * PC);
         const uint32_t lead_tempty0 = leader_addr(tempty(0));
-        float *stg = staging + (warp - 4) * (W_STAGE_OUT / 4);
+        float *stg = staging + (warp - 4) * (K_::OUT / 4);
         const float *ring = scales + (warp - 4) * K_::RING;
 
         // Scales are fetched a batch ahead, across tiles: what a block of k costs
@@ -611,7 +663,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
         // last scale: any valid one will do.
         int fu = group, fkb = 0, fslot = 0;        // the batch to fetch next
         const float *fx = nullptr, *fy = nullptr;
-        int fo[YVEC ? 4 : 1];
+        int fo[PC / 32];
         float nx[BATCH], ny[BATCH];
         auto fetch = [&]() {
             if (fu < units) {
@@ -619,12 +671,12 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                     int tx, ty;
                     tile_of(p, fu, tx, ty);
                     const int m = min(ty * WT + (int)rank * BX + q * 32 + lane, p.M - 1);
-                    const int n = min(tx * WT + half * PC, p.N - 1);
+                    const int n = min(tx * WT + part * PC, p.N - 1);
                     fx = p.SX + (int64_t)(m >> p.x_shift) * p.x_mn;
                     fy = p.SY + (int64_t)(n >> p.y_shift) * p.y_mn;
                     if (YVEC)                      // scales of single columns are neighbours
 #pragma unroll
-                        for (int j = 0; j < (YVEC ? 4 : 1); ++j) fo[j] = min(32 * j + lane, p.N - 1 - n);
+                        for (int j = 0; j < PC / 32; ++j) fo[j] = min(32 * j + lane, p.N - 1 - n);
                 }
 #pragma unroll
                 for (int a = 0; a < BATCH; ++a) {
@@ -634,7 +686,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                         if (YVEC) {
                             const uint32_t to = smem_u32(ring + (fslot + a) * PC) + 4u * (uint32_t)lane;
 #pragma unroll
-                            for (int j = 0; j < (YVEC ? 4 : 1); ++j) cp_async_4(to + 128u * j, fy + fo[j], 4);
+                            for (int j = 0; j < PC / 32; ++j) cp_async_4(to + 128u * j, fy + fo[j], 4);
                         }
                         fx += p.x_k;
                         fy += p.y_k;
@@ -650,13 +702,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
 
         int b = 0, slot = 0;
         uint32_t bph = 0;
-        uint32_t r[2][CH];
+        // (the reads under way while another chunk is added are held by the compiler in
+        // place: the kernel must not spill)
+        constexpr int NR = YVEC ? 1 : 2;           // chunks held
+        uint32_t r[NR][CH];
         // waits for the next buffer and starts reading it
         auto next_buffer = [&]() {
             ok = warp_wait(tfull(b), bph, lim);
             if (ok) {
                 tc_fence_after();
-                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+                if (NR > 1) tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
             }
         };
         for (int u = group; ok && u < units; u += groups) {
@@ -686,9 +741,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (YVEC && ++slot == K_::SLOTS) slot = 0;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    tmem_ld_wait(r[c & 1]);
+                    uint32_t(&v)[CH] = r[c % NR];
+                    if (NR == 1) tmem_ld_async(taddr + (uint32_t)(b * WT + c * CH), v);
+                    tmem_ld_wait(v);
                     if (c + 1 < NC) {
-                        tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) & 1]);
+                        if (NR > 1) tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) % NR]);
                     } else {
                         // the buffer is read: hand it back, and start on the next one
                         // while this chunk is added
@@ -696,12 +753,12 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                         __syncwarp();
                         if (lane == 0) remote_arrive_relaxed(lead_tempty0 + 8u * b);
                         if (++b == 2) { b = 0; bph ^= 1; }
-                        if (kb + 1 < p.nkb) next_buffer();
+                        if (NR > 1 && kb + 1 < p.nkb) next_buffer();
                     }
 #pragma unroll
                     for (int i = 0; i < CH; i += 4) {
-                        float2 t0 = make_float2(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1]));
-                        float2 t1 = make_float2(__uint_as_float(r[c & 1][i + 2]), __uint_as_float(r[c & 1][i + 3]));
+                        float2 t0 = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        float2 t1 = make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                         float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
                         if (YVEC) {
                             const float4 s4 = *reinterpret_cast<const float4 *>(sc + c * CH + i);
@@ -714,41 +771,61 @@ __global__ void __launch_bounds__(W_THREADS, 1) __cluster_dims__(2, 1, 1)
                             a1 = __ffma2_rn(t1, s2, a1);
                         }
                     }
+                    if (NR == 1 && c + 1 == NC && kb + 1 < p.nkb) next_buffer();
                 }
                 if (!ok) break;
             }
             if (!ok) break;
             // a tile ends within a batch: the ring's place of the next one
             if (YVEC && p.nkb % BATCH != 0 && (slot += BATCH - p.nkb % BATCH) >= K_::SLOTS) slot -= K_::SLOTS;
-            // 32 x 32 blocks: lane = row in, 4 rows x 8 quads of columns out; the
-            // 16-byte chunk index is flipped by the row's low 3 bits
-            const int m0 = ty * WT + (int)rank * BX + q * 32, n0 = tx * WT + half * PC;
+            // blocks of 32 rows x CH columns through shared memory (lane = row in), from
+            // there to C by a TMA store; by one that adds where C += sums; or, where C's
+            // alignment or the scalars do not allow it, by this warp
+            const int m0 = ty * WT + (int)rank * BX + q * 32, n0 = tx * WT + part * PC;
 #pragma unroll
-            for (int c = 0; c < PC / CH; ++c) {
-                __syncwarp();
+            for (int c = 0; c < NC; ++c) {
+                if (m0 >= p.M || n0 + c * CH >= p.N) break;
+                const float2 *a = acc + c * CH / 2;
+                if (p.c_tma != 0) {
+                    if (lane == 0) tma_store_read_wait();
+                    __syncwarp();
+                    uint8_t *row = reinterpret_cast<uint8_t *>(stg);
+                    if (p.c_bf16) {
+                        row += lane * 2 * CH;
 #pragma unroll
-                for (int i = 0; i < CH / 4; ++i) {
-                    const float2 a0 = acc[(c * CH + 4 * i) / 2], a1 = acc[(c * CH + 4 * i) / 2 + 1];
-                    *reinterpret_cast<float4 *>(stg + lane * 32 + ((i ^ (lane & 7)) << 2)) =
-                        make_float4(a0.x, a0.y, a1.x, a1.y);
-                }
-                __syncwarp();
-                const int n = n0 + c * CH + 4 * (lane & 7), cols = p.N - n;
-                float4 old[8];
+                        for (int i = 0; i < CH / 8; ++i)
+                            *reinterpret_cast<uint4 *>(row + 16 * staged_chunk<2 * CH>(lane, i)) = make_uint4(
+                                pack2(__fmul_rn(p.alpha, a[4 * i].x), __fmul_rn(p.alpha, a[4 * i].y)),
+                                pack2(__fmul_rn(p.alpha, a[4 * i + 1].x), __fmul_rn(p.alpha, a[4 * i + 1].y)),
+                                pack2(__fmul_rn(p.alpha, a[4 * i + 2].x), __fmul_rn(p.alpha, a[4 * i + 2].y)),
+                                pack2(__fmul_rn(p.alpha, a[4 * i + 3].x), __fmul_rn(p.alpha, a[4 * i + 3].y)));
+                    } else {
+                        row += lane * 4 * CH;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int m = m0 + 4 * i + (lane >> 3);
-                    old[i] = p.beta != 0.0f && m < p.M ? load_c4(p, (int64_t)m * p.ldc + n, cols, p.c_vec != 0)
-                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
+                        for (int i = 0; i < CH / 4; ++i)
+                            *reinterpret_cast<float4 *>(row + 16 * staged_chunk<4 * CH>(lane, i)) =
+                                make_float4(__fmul_rn(p.alpha, a[2 * i].x), __fmul_rn(p.alpha, a[2 * i].y),
+                                            __fmul_rn(p.alpha, a[2 * i + 1].x), __fmul_rn(p.alpha, a[2 * i + 1].y));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (p.c_tma == 1) tma_store_2d<false>(&tm_c, smem_u32(stg), n0 + c * CH, m0);
+                        else tma_store_2d<true>(&tm_c, smem_u32(stg), n0 + c * CH, m0);
+                    }
+                } else {
+                    __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3), m = m0 + r;
-                    const float4 v = *reinterpret_cast<const float4 *>(stg + r * 32 + (((lane & 7) ^ (r & 7)) << 2));
-                    if (m < p.M) store_c4(p, (int64_t)m * p.ldc + n, v, old[i], cols, p.c_vec != 0);
+                    for (int i = 0; i < CH / 4; ++i)
+                        *reinterpret_cast<float4 *>(stg + lane * CH + 4 * staged_chunk<4 * CH>(lane, i)) =
+                            make_float4(a[2 * i].x, a[2 * i].y, a[2 * i + 1].x, a[2 * i + 1].y);
+                    __syncwarp();
+                    if (p.c_bf16) write_block<__nv_bfloat16, CH>(p, stg, m0, n0 + c * CH);
+                    else write_block<float, CH>(p, stg, m0, n0 + c * CH);
                 }
             }
         }
+        if (lane == 0) tma_store_read_wait();
         if (YVEC) cp_async_wait_all();
     }
 
@@ -837,10 +914,9 @@ static bool byte_map(CUtensorMap *m, const void *base, int64_t rows, int64_t col
 }
 
 // One launch, with the shared-memory opt-in made once on each device (bit d of `done`).
-template <typename Kern>
-static int launch_kernel(Kern kern, uint64_t &done, const CUtensorMap &mx, const CUtensorMap &my,
-                         const fp8g::Params &p, int grid, int threads, int smem, int cluster, cudaStream_t s,
-                         bool dep) {
+template <typename Kern, typename... Args>
+static int launch_kernel(Kern kern, uint64_t &done, int grid, int threads, int smem, int cluster, cudaStream_t s,
+                         bool dep, const Args &...args) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
@@ -871,7 +947,7 @@ static int launch_kernel(Kern kern, uint64_t &done, const CUtensorMap &mx, const
     cfg.numAttrs = n;
     timing_mark(s, true);
     count_launch();
-    cudaLaunchKernelEx(&cfg, kern, mx, my, p);
+    cudaLaunchKernelEx(&cfg, kern, args...);
     timing_mark(s, false);
     return launch_status();
 }
@@ -880,16 +956,36 @@ template <int BY, bool XVEC>
 static int launch_fp8(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
                       int smem, cudaStream_t s, bool dep) {
     static uint64_t done = 0;
-    return launch_kernel(fp8g::fp8_gemm_kernel<BY, XVEC>, done, mx, my, p, grid, fp8g::THREADS, smem, p.ksplit,
-                         s, dep);
+    return launch_kernel(fp8g::fp8_gemm_kernel<BY, XVEC>, done, grid, fp8g::THREADS, smem, p.ksplit, s, dep, mx, my, p);
 }
 
 template <bool YVEC>
-static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, const fp8g::Params &p, int grid,
-                       cudaStream_t s, bool dep) {
+static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, fp8g::Params &p, int grid, cudaStream_t s,
+                       bool dep) {
+    using K_ = fp8g::Wide<YVEC>;
     static uint64_t done = 0;
-    return launch_kernel(fp8g::fp8_wide_kernel<YVEC>, done, mx, my, p, grid, fp8g::W_THREADS,
-                         fp8g::Wide<YVEC>::SMEM, 1, s, dep);
+    // C in boxes of 32 rows x CH columns, where TMA can write it: rows on 16 bytes,
+    // and nothing to read, or C += sums in fp32 (one rounding, as the epilogue's)
+    const int esize = p.c_bf16 ? 2 : 4;
+    CUtensorMap mc = mx;
+    p.c_tma = 0;
+    if (aligned16(p.C) && p.ldc * esize % 16 == 0 &&
+        (p.beta == 0.0f || (p.beta == 1.0f && p.alpha == 1.0f && !p.c_bf16))) {
+        EncodeTiledFn enc = encode_fn();
+        cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+        cuuint64_t strides[1] = {(cuuint64_t)(p.ldc * esize)};
+        cuuint32_t box[2] = {(cuuint32_t)K_::CH, 32};
+        cuuint32_t es[2] = {1, 1};
+        const int bytes = K_::CH * esize;
+        if (enc && enc(&mc, p.c_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.C, dims,
+                       strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                       : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B,
+                       CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+            p.c_tma = p.beta == 0.0f ? 1 : 2;
+    }
+    return launch_kernel(fp8g::fp8_wide_kernel<YVEC>, done, grid, K_::THREADS, K_::SMEM, 1, s, dep, mx, my, mc, p);
 }
 
 template <int BY>

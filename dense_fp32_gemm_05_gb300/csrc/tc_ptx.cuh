@@ -389,5 +389,22 @@ __device__ __forceinline__ int warp_index() {
     return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
 }
 
+// TMA store of a shared tile (or, ADD, its addition to what is there, in L2), by one
+// thread.  The tile's generic-proxy writes are fenced before; the thread waits
+// until the tile has been read before it is written again or its CTA exits.
+template <bool ADD>
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+    if (ADD)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%2, %3}], [%1];"
+                     :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                     :: "l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read_wait() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 }  // namespace tc
 }  // namespace sgemm_gb300

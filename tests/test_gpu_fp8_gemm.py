@@ -136,6 +136,17 @@ def test_many_tiles(layout, shape):
     _check(*shape, ta, tb, "e5m2", "e4m3", ga, gb)
 
 
+@pytest.mark.parametrize("ct,alpha,beta", [("f32", 1.0, 1.0), ("f32", 0.5, 1.0), ("f32", 1.0, -2.0),
+                                           ("bf16", 1.0, 1.0), ("bf16", 3.0, 0.0)])
+@pytest.mark.parametrize("layout", [("N", "T", 1, 128), ("T", "N", 1, 1)])
+@pytest.mark.parametrize("shape,pad,off", [((2560, 2304, 520), 0, 0), ((2500, 2312, 300), 4, 0),
+                                           ((2500, 2309, 300), 0, 0), ((2500, 2308, 300), 0, 1)])
+def test_wide_tiles_epilogue(ct, alpha, beta, layout, shape, pad, off):
+    """Stores by TMA, additions by TMA, quads and single elements of C."""
+    ta, tb, ga, gb = layout
+    _check(*shape, ta, tb, "e4m3", "e5m2", ga, gb, ct, alpha, beta, pads=(0, 0, 0, 0, pad), offs=(0, 0, off))
+
+
 def test_special_codes():
     def edit(a, sa, b, sb):
         a[2, 5] = 0x7f                # NaN (e5m2 code 0x7f too)
