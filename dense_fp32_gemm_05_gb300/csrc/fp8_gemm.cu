@@ -436,20 +436,18 @@ constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
 
 template <bool YVEC>
 struct Wide {
-    // Promoting warps after the first four (TMA, MMA, 2 idle: a warpgroup): 8 of 32 rows
-    // x 128 columns; YVEC, where two operations a value fill the FMA pipe and more warps
-    // cover their latency, 16 of 32 x 64 (4096 x 4096 x 8192 TN: 8 warps 258 us).
-    static constexpr int WARPS = YVEC ? 16 : 8;
-    static constexpr int THREADS = 32 * (4 + WARPS);
+    static constexpr int WARPS = 8;                        // promoting: 32 rows x 128 columns each
+    static constexpr int THREADS = 32 * (4 + WARPS);       // after TMA, MMA, scales, idle: a warpgroup
     static constexpr int PC = WT / (WARPS / 4);            // columns per promoting warp
-    static constexpr int CH = YVEC ? 16 : 32;              // columns read or stored at a time
-    // registers: 384 x 168 = 128 x 40 + 256 x 232, 640 x 96 = 128 x 32 + 512 x 112
-    static constexpr int REGS_ISSUE = YVEC ? 32 : 40, REGS_PROMOTE = YVEC ? 112 : 232;
+    static constexpr int CH = 32;                          // columns read or stored at a time
+    static constexpr int REGS_ISSUE = 40, REGS_PROMOTE = 232;   // 384 x 168 = 128 x 40 + 256 x 232
     static constexpr int OUT = 32 * CH * 4;                // epilogue staging per warp
-    // YVEC: the scales of a warp's columns, in a ring of its own
-    static constexpr int SLOTS = YVEC ? 6 : 0;
-    static constexpr int RING = SLOTS * PC;                // floats
-    static constexpr int FIXED = 1024 + WARPS * (OUT + RING * 4) + BAR_BYTES;
+    // YVEC: the scales of the CTA's rows and the tile's columns, BATCH blocks of k in a slot
+    static constexpr int BATCH = YVEC ? 2 : 4;
+    static constexpr int SLOTS = YVEC ? 3 : 0;
+    static constexpr int BLOCK = BX + WT;                  // floats for a block
+    static constexpr int RING = SLOTS * BATCH * BLOCK;
+    static constexpr int FIXED = 1024 + WARPS * OUT + RING * 4 + BAR_BYTES;
     static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
     static constexpr int SMEM = FIXED + STAGES * W_STAGE;
     static_assert(STAGES >= 4 && STAGES <= MAX_STAGES, "stages");
@@ -545,13 +543,15 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
     const uint32_t smem0 = smem_u32(smem);
     float *staging = reinterpret_cast<float *>(smem + S * W_STAGE);
     float *scales = staging + K_::WARPS * K_::OUT / 4;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + K_::WARPS * K_::RING);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + K_::RING);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4 + 2 * K_::SLOTS);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
     auto tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
     auto tempty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+    auto sfull = [&](int s) { return bar0 + 8u * (2 * S + 4 + s); };
+    auto sempty = [&](int s) { return bar0 + 8u * (2 * S + 4 + K_::SLOTS + s); };
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -567,6 +567,10 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
             mbar_init(tempty(b), 2 * K_::WARPS);   // of both CTAs, on the leader's
+        }
+        for (int s = 0; s < K_::SLOTS; ++s) {
+            mbar_init(sfull(s), 32);               // each lane's copies
+            mbar_init(sempty(s), K_::WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&tm_x);
@@ -642,76 +646,91 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                 if (issued > 0)                    // MMAs retire before tensor memory is freed
                     mbar_wait_for(tfull((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
             }
+        } else if (YVEC && warp == 2) {
+            // ------------------------------------------------ scales
+            // copied asynchronously, up to SLOTS batches under way.  Scales of single
+            // rows or columns are neighbours in memory; rows and columns past the
+            // matrix take its last: any valid one will do.
+            const uint32_t to = smem_u32(scales) + 4u * (uint32_t)lane;
+            int slot = 0;
+            uint32_t ph = 1;
+            for (int u = group; ok && u < units; u += groups) {
+                int tx, ty;
+                tile_of(p, u, tx, ty);
+                const int x0 = min(ty * WT + (int)rank * BX, p.M - 1), y0 = min(tx * WT, p.N - 1);
+                const float *sx = p.SX + (int64_t)(x0 >> p.x_shift) * p.x_mn;
+                const float *sy = p.SY + (int64_t)y0 * p.y_mn;
+                for (int kb = 0; kb < p.nkb; kb += K_::BATCH) {
+                    if (!warp_wait(sempty(slot), ph, lim)) { ok = false; break; }
+                    for (int a = 0; a < K_::BATCH && kb + a < p.nkb; ++a) {
+                        const uint32_t at = to + 4u * (uint32_t)((slot * K_::BATCH + a) * K_::BLOCK);
+#pragma unroll
+                        for (int j = 0; j < BX / 32; ++j)
+                            cp_async_4(at + 128u * j, sx + (p.x_shift ? 0 : min(32 * j + lane, p.M - 1 - x0)), 4);
+#pragma unroll
+                        for (int j = 0; j < WT / 32; ++j)
+                            cp_async_4(at + 4u * BX + 128u * j, sy + min(32 * j + lane, p.N - 1 - y0), 4);
+                        sx += p.x_k;
+                        sy += p.y_k;
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(slot)) : "memory");
+                    if (++slot == K_::SLOTS) { slot = 0; ph ^= 1; }
+                }
+            }
+            cp_async_wait_all();
         }
         __syncwarp();
     } else {
         // ------------------------------------------------ promotion and epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(K_::REGS_PROMOTE));
         constexpr int PC = K_::PC, CH = K_::CH, NC = PC / CH;
-        constexpr int BATCH = YVEC ? 2 : 4;        // blocks whose scales are fetched together
+        constexpr int BATCH = K_::BATCH;
         const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * PC);
         const uint32_t lead_tempty0 = leader_addr(tempty(0));
         float *stg = staging + (warp - 4) * (K_::OUT / 4);
-        const float *ring = scales + (warp - 4) * K_::RING;
 
-        // Scales are fetched a batch ahead, across tiles: what a block of k costs
-        // beside reading and adding its sums is what bounds this role, so nothing
-        // here waits for memory.  The row's (and the columns' block's) go to
-        // registers, single columns' to the warp's ring (asynchronous copies
-        // complete in order: no barrier).  Rows and columns past the matrix take its
-        // last scale: any valid one will do.
-        int fu = group, fkb = 0, fslot = 0;        // the batch to fetch next
+        // One scale of B for the columns: it and the row's are fetched a batch ahead into
+        // registers, across tiles, so that nothing here waits for memory: what a block
+        // of k costs beside reading and adding its sums is what bounds this role.
+        int fu = group, fkb = 0;                   // the batch to fetch next
         const float *fx = nullptr, *fy = nullptr;
-        int fo[PC / 32];
         float nx[BATCH], ny[BATCH];
         auto fetch = [&]() {
-            if (fu < units) {
-                if (fkb == 0) {
-                    int tx, ty;
-                    tile_of(p, fu, tx, ty);
-                    const int m = min(ty * WT + (int)rank * BX + q * 32 + lane, p.M - 1);
-                    const int n = min(tx * WT + part * PC, p.N - 1);
-                    fx = p.SX + (int64_t)(m >> p.x_shift) * p.x_mn;
-                    fy = p.SY + (int64_t)(n >> p.y_shift) * p.y_mn;
-                    if (YVEC)                      // scales of single columns are neighbours
-#pragma unroll
-                        for (int j = 0; j < PC / 32; ++j) fo[j] = min(32 * j + lane, p.N - 1 - n);
-                }
-#pragma unroll
-                for (int a = 0; a < BATCH; ++a) {
-                    if (fkb + a < p.nkb) {
-                        nx[a] = __ldg(fx);
-                        if (!YVEC) ny[a] = __ldg(fy);
-                        if (YVEC) {
-                            const uint32_t to = smem_u32(ring + (fslot + a) * PC) + 4u * (uint32_t)lane;
-#pragma unroll
-                            for (int j = 0; j < PC / 32; ++j) cp_async_4(to + 128u * j, fy + fo[j], 4);
-                        }
-                        fx += p.x_k;
-                        fy += p.y_k;
-                    }
-                }
-                fkb += BATCH;
-                if (fkb >= p.nkb) { fkb = 0; fu += groups; }
-                if (YVEC && (fslot += BATCH) == K_::SLOTS) fslot = 0;
+            if (YVEC || fu >= units) return;
+            if (fkb == 0) {
+                int tx, ty;
+                tile_of(p, fu, tx, ty);
+                const int m = min(ty * WT + (int)rank * BX + q * 32 + lane, p.M - 1);
+                const int n = min(tx * WT + part * PC, p.N - 1);
+                fx = p.SX + (int64_t)(m >> p.x_shift) * p.x_mn;
+                fy = p.SY + (int64_t)(n >> p.y_shift) * p.y_mn;
             }
-            if (YVEC) cp_async_commit();
+#pragma unroll
+            for (int a = 0; a < BATCH; ++a) {
+                if (fkb + a < p.nkb) {
+                    nx[a] = __ldg(fx);
+                    ny[a] = __ldg(fy);
+                    fx += p.x_k;
+                    fy += p.y_k;
+                }
+            }
+            fkb += BATCH;
+            if (fkb >= p.nkb) { fkb = 0; fu += groups; }
         };
         fetch();
 
         int b = 0, slot = 0;
-        uint32_t bph = 0;
+        uint32_t bph = 0, sph = 0;
         // (the reads under way while another chunk is added are held by the compiler in
         // place: the kernel must not spill)
-        constexpr int NR = YVEC ? 1 : 2;           // chunks held
-        uint32_t r[NR][CH];
+        uint32_t r[2][CH];
         // waits for the next buffer and starts reading it
         auto next_buffer = [&]() {
             ok = warp_wait(tfull(b), bph, lim);
             if (ok) {
                 tc_fence_after();
-                if (NR > 1) tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
             }
         };
         for (int u = group; ok && u < units; u += groups) {
@@ -725,27 +744,31 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             next_buffer();
             if (!ok) break;
             for (int kb = 0; kb < p.nkb; ++kb) {
-                if (kb % BATCH == 0) {
-#pragma unroll
-                    for (int a = 0; a < BATCH; ++a) sv[a] = YVEC ? nx[a] : __fmul_rn(nx[a], ny[a]);
-                    fetch();
-                    if (YVEC) {
-                        cp_async_wait_group<1>();  // all but the batch just begun
-                        __syncwarp();
+                float s;
+                const float *sc = scales + (slot * BATCH + kb % BATCH) * K_::BLOCK;
+                if (YVEC) {
+                    if (kb % BATCH == 0) {
+                        ok = warp_wait(sfull(slot), sph, lim);
+                        if (!ok) break;
                     }
-                }
-                const float2 s2 = make_float2(sv[0], sv[0]);
+                    s = sc[q * 32 + lane];
+                } else {
+                    if (kb % BATCH == 0) {
 #pragma unroll
-                for (int a = 0; a + 1 < BATCH; ++a) sv[a] = sv[a + 1];
-                const float *sc = ring + slot * PC;
-                if (YVEC && ++slot == K_::SLOTS) slot = 0;
+                        for (int a = 0; a < BATCH; ++a) sv[a] = __fmul_rn(nx[a], ny[a]);
+                        fetch();
+                    }
+                    s = sv[0];
+#pragma unroll
+                    for (int a = 0; a + 1 < BATCH; ++a) sv[a] = sv[a + 1];
+                }
+                const float2 s2 = make_float2(s, s);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    uint32_t(&v)[CH] = r[c % NR];
-                    if (NR == 1) tmem_ld_async(taddr + (uint32_t)(b * WT + c * CH), v);
+                    uint32_t(&v)[CH] = r[c & 1];
                     tmem_ld_wait(v);
                     if (c + 1 < NC) {
-                        if (NR > 1) tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) % NR]);
+                        tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) & 1]);
                     } else {
                         // the buffer is read: hand it back, and start on the next one
                         // while this chunk is added
@@ -753,7 +776,7 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                         __syncwarp();
                         if (lane == 0) remote_arrive_relaxed(lead_tempty0 + 8u * b);
                         if (++b == 2) { b = 0; bph ^= 1; }
-                        if (NR > 1 && kb + 1 < p.nkb) next_buffer();
+                        if (kb + 1 < p.nkb) next_buffer();
                     }
 #pragma unroll
                     for (int i = 0; i < CH; i += 4) {
@@ -761,7 +784,7 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                         float2 t1 = make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                         float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
                         if (YVEC) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + c * CH + i);
+                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + BX + part * PC + c * CH + i);
                             t0 = __fmul2_rn(t0, s2);
                             t1 = __fmul2_rn(t1, s2);
                             a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
@@ -771,13 +794,15 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                             a1 = __ffma2_rn(t1, s2, a1);
                         }
                     }
-                    if (NR == 1 && c + 1 == NC && kb + 1 < p.nkb) next_buffer();
+                }
+                if (YVEC && (kb % BATCH == BATCH - 1 || kb + 1 == p.nkb)) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty(slot));
+                    if (++slot == K_::SLOTS) { slot = 0; sph ^= 1; }
                 }
                 if (!ok) break;
             }
             if (!ok) break;
-            // a tile ends within a batch: the ring's place of the next one
-            if (YVEC && p.nkb % BATCH != 0 && (slot += BATCH - p.nkb % BATCH) >= K_::SLOTS) slot -= K_::SLOTS;
             // blocks of 32 rows x CH columns through shared memory (lane = row in), from
             // there to C by a TMA store; by one that adds where C += sums; or, where C's
             // alignment or the scalars do not allow it, by this warp
@@ -826,7 +851,6 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             }
         }
         if (lane == 0) tma_store_read_wait();
-        if (YVEC) cp_async_wait_all();
     }
 
     tc_fence_before();
