@@ -419,10 +419,13 @@ __device__ void route_lists(const Params &p, Routing &rt) {
 struct Work {
     int tiles, kb;                              // tiles per chunk, blocks per tile
     int total;
-    int n;                                      // CTAs with a range: none of these is empty
+    // CTAs with a range: none of these is empty, and a small product is not cut into
+    // more parts than it takes time to add (T = 1, D = 1024, F = 512: 21.6 -> 19.2 us)
+    int n;
+    static constexpr int MIN_BLOCKS = 4;
     int each, more;
     __device__ Work(int chunks, int tiles_, int kb_)
-        : tiles(tiles_), kb(kb_), total(chunks * tiles_ * kb_), n(max(1, min((int)gridDim.x, total))),
+        : tiles(tiles_), kb(kb_), total(chunks * tiles_ * kb_), n(max(1, min((int)gridDim.x, total / MIN_BLOCKS))),
           each(total / n), more(total - each * n) {}
     __device__ int begin(int c) const { return c >= n ? total : c * each + min(c, more); }
     __device__ int owner(int it) const {
