@@ -228,20 +228,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         {
             int s = 0, b = 0, issued = 0;
             uint32_t ph = 0, bph = 1;
+            const uint64_t dx0 = smem_desc_8bit(smem0, X_BYTES);
             const uint32_t x_step = p.x_mnmajor ? 4096u >> 4 : 32u >> 4;
             const uint32_t y_step = p.y_mnmajor ? 4096u >> 4 : 32u >> 4;
             for (int u = group; ok && u < units; u += groups) {
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!warp_wait(full(s), ph, lim) || !warp_wait(tempty(b), bph, lim)) { ok = false; break; }
+                    // (the two tests overlap: few columns leave little time for a block)
+                    const bool t0 = mbar_test(full(s), ph), t1 = mbar_test(tempty(b), bph);
+                    if (!__all_sync(0xffffffffu, t0 && t1) &&
+                        (!warp_wait(full(s), ph, lim) || !warp_wait(tempty(b), bph, lim))) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t x = smem0 + (uint32_t)(s * stage_bytes), y = x + X_BYTES;
-                    const uint64_t dx = smem_desc_8bit(x, X_BYTES), dy = smem_desc_8bit(y, X_BYTES);
+                    const uint64_t dx = dx0 + (uint32_t)(s * (stage_bytes >> 4)), dy = dx + (X_BYTES >> 4);
                     const uint32_t d = tmem + (uint32_t)(b * BY);
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < BK / 32; ++i)
                             umma_8bit<false>(d, dx + i * x_step, dy + i * y_step, p.idesc, i > 0);
-                        umma_commit(empty(s));
                         umma_commit(tfull(b));
                     }
                     ++issued;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------ promotion and epilogue
         const int q = warp & 3, half = (warp - 3) >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * PC);
-        int b = 0, slot = 0;
+        int stage = 0, b = 0, slot = 0;
         uint32_t bph = 0, sph = 0;
         for (int u = group; ok && u < units; u += groups) {
             int tx, ty;
@@ -323,6 +325,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                      mbar_wait_for(tfull(b), bph, lim, &g_error);
                 if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
                 tc_fence_after();
+                // the block's MMAs are done with its stage
+                if (warp == 3 && lane == 0) mbar_arrive(empty(stage));
+                if (++stage == p.stages) stage = 0;
                 const float *sc = scales + slot * BY + half * PC;
                 uint32_t r[2][CH];
                 tmem_ld_async(taddr + (uint32_t)(b * BY), r[0]);

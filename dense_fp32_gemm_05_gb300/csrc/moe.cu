@@ -671,20 +671,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok) {
             int s = 0, bs = 0, b = 0, issued = 0;
             uint32_t ph = 0, bph = 0, tph = 1;
+            const uint64_t da0 = smem_desc_8bit(a_at(0), A_BYTES), db0 = smem_desc_8bit(b_at(0), A_BYTES);
             auto multiply = [&](const Work &w, int parts) {
                 return for_pieces(w, [&](int u, int k0, int k1) {
                     const int n8 = (rt.c_n[u / w.tiles] + 7) / 8 * 8;
                     const uint32_t idesc = idesc_8bit(0, 0, 0, 0, ROWS, (parts * n8 + 15) / 16 * 16);
                     for (int kb = k0; kb < k1; ++kb) {
-                        if (!warp_wait(t_empty(b), tph, lim) || !warp_wait(a_full(s), ph, lim) ||
-                            !warp_wait(b_full(bs), bph, lim)) return false;
+                        // (the three tests overlap; what this role spends on a block is the
+                        // least time a block can take: 730 clocks with waits and commits in turn)
+                        const bool t0 = mbar_test(t_empty(b), tph), t1 = mbar_test(a_full(s), ph), t2 = mbar_test(b_full(bs), bph);
+                        if (!__all_sync(0xffffffffu, t0 && t1 && t2) &&
+                            (!warp_wait(t_empty(b), tph, lim) || !warp_wait(a_full(s), ph, lim) ||
+                             !warp_wait(b_full(bs), bph, lim))) return false;
                         tc_fence_after();
-                        const uint64_t da = smem_desc_8bit(a_at(s), A_BYTES), db = smem_desc_8bit(b_at(bs), A_BYTES);
+                        const uint64_t da = da0 + (uint32_t)(s * (A_BYTES >> 4)), db = db0 + (uint32_t)(bs * (K_::B_BYTES >> 4));
                         if (elect_one()) {
 #pragma unroll
                             for (int i = 0; i < BK / 32; ++i)
                                 umma_8bit<false>(tmem + (uint32_t)(b * 4 * NT), da + i * 2, db + i * 2, idesc, i > 0);
-                            umma_commit(a_empty(s));
                             umma_commit(t_full(b));
                         }
                         ++issued;
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ------------------------------------------------ promotion
         const int q = warp & 3, row = q * 32 + lane;
-        int b = 0, bs = 0;
+        int s = 0, b = 0, bs = 0;
         uint32_t tph = 0, fph = 1;
         auto promote = [&](const Work &w, bool second, auto parts_) {
             constexpr int PARTS = decltype(parts_)::value;
@@ -848,6 +852,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (kb + 1 < k1) ws_next = __ldg(ws + kb + 1);
                     if (!warp_wait(t_full(b), tph, lim)) return false;
                     tc_fence_after();
+                    // the block's MMAs are done with the weights' stage
+                    if (q == 0 && lane == 0) mbar_arrive(a_empty(s));
+                    if (++s == A_STAGES) s = 0;
                     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 4 * NT);
 #pragma unroll
                     for (int i0 = 0; i0 < NT; i0 += 8) {
