@@ -81,14 +81,14 @@ __device__ unsigned int g_error;               // sticky device error word of th
 // NT: tokens of one expert that a tile takes (columns for each part).
 template <int NT>
 struct Cfg {
-    static constexpr int A_STAGES = NT <= 8 ? 9 : NT <= 16 ? 7 : 6;   // 16 KB of weights each
+    static constexpr int A_STAGES = NT <= 8 ? 10 : 8;   // 16 KB of weights each
     static constexpr int B_BYTES = 4 * NT * BK;
     static constexpr int B_STAGES = NT >= 64 ? 2 : NT >= 32 ? 4 : 8;
     static constexpr uint32_t COLS = 8 * NT;    // two buffers of 4 NT columns
     static constexpr int SMEM = 1024 + A_STAGES * A_BYTES + B_STAGES * B_BYTES;
     static_assert(COLS <= 512, "tensor memory");
     static_assert(B_STAGES * B_BYTES >= (2 * MAX_E + MAX_TOPK) * 4, "a row of logits, a token's choices");
-    static_assert(SMEM + 32 * 1024 <= SMEM_MAX, "shared memory (the routing is static)");
+    static_assert(SMEM + 34 * 1024 <= SMEM_MAX, "shared memory (the routing is static)");
 };
 
 struct Params {
@@ -122,6 +122,7 @@ struct Routing {
     short expert[MAX_SLOTS];                   // of a slot
     short rank[MAX_SLOTS];                     // of a slot among its expert's
     short list[MAX_SLOTS];                     // slots by expert, ascending within one
+    short token[MAX_SLOTS];                    // their tokens
     int count[MAX_E];                          // an expert's slots
     short first[MAX_E];                        // its first in `list`
     short c_expert[MAX_CHUNKS], c_first[MAX_CHUNKS], c_n[MAX_CHUNKS];
@@ -410,7 +411,11 @@ __device__ void route_lists(const Params &p, Routing &rt) {
         if (lane == 0) rt.chunks = chunk_base;
     }
     __syncthreads();
-    for (int s = threadIdx.x; s < slots; s += THREADS) rt.list[rt.first[rt.expert[s]] + rt.rank[s]] = (short)s;
+    for (int s = threadIdx.x; s < slots; s += THREADS) {
+        const int at = rt.first[rt.expert[s]] + rt.rank[s];
+        rt.list[at] = (short)s;
+        rt.token[at] = (short)(s / p.topk);
+    }
 }
 
 // ------------------------------------------------------------ work ranges
@@ -490,9 +495,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // A lane's 4 values of a token's block -> its bytes of the column operand, and
 // (lane 0) the block's scale.  Part i of token c is row i * n8 + c: 128 bytes, the
-// 16-byte chunk index flipped by the row's low 3 bits (128-byte swizzle).
+// 16-byte chunk index flipped by the row's low 3 bits (128-byte swizzle), which are
+// c's.  These instructions, ~60 for a token's block, bound the layer when experts have
+// 8 tokens and more, so they are packed pairs where they can be.
 template <int PARTS>
-__device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, int c, int n8, int lane) {
+__device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, int c, uint32_t part_bytes, int lane) {
     const float hi = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
     const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
     const int e = (int)(amax >> 23);
@@ -508,24 +515,25 @@ __device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, 
     const int ub = min(max(261 - e, 1), 253);
     const float up = __uint_as_float((uint32_t)ub << 23);
     if (lane == 0) scale[c] = __uint_as_float((uint32_t)(254 - ub) << 23);
-    float y[4] = {__fmul_rn(v.x, up), __fmul_rn(v.y, up), __fmul_rn(v.z, up), __fmul_rn(v.w, up)};
+    float2 y01 = __fmul2_rn(make_float2(v.x, v.y), make_float2(up, up));
+    float2 y23 = __fmul2_rn(make_float2(v.z, v.w), make_float2(up, up));
+    uint32_t at = b + (uint32_t)(c * BK) + ((uint32_t)(((lane >> 2) ^ (c & 7)) << 4) | (uint32_t)(4 * (lane & 3)));
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
-        const uint32_t q = fp8::codes4<false>(y);
-        const int row = i * n8 + c;
-        const uint32_t at = b + (uint32_t)(row * BK) + ((uint32_t)(((lane >> 2) ^ (row & 7)) << 4) | (uint32_t)(4 * (lane & 3)));
-        asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(q) : "memory");
+        const uint32_t q01 = fp8::codes2<false>(y01.x, y01.y), q23 = fp8::codes2<false>(y23.x, y23.y);
+        asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(q01 | (q23 << 16)) : "memory");
         if (i + 1 < PARTS) {
+            // y = 32 (y - q), exact: 32 q is a half (at most 14336), and the multiply-add
+            // has nothing to round
+            at += part_bytes;
             uint32_t h01, h23;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"((uint16_t)(q & 0xffffu)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"((uint16_t)(q >> 16)));
-            const float2 d01 = __half22float2(*reinterpret_cast<__half2 *>(&h01));
-            const float2 d23 = __half22float2(*reinterpret_cast<__half2 *>(&h23));
-            // (y - q) * 32: exact
-            y[0] = __fmul_rn(__fsub_rn(y[0], d01.x), 32.0f);
-            y[1] = __fmul_rn(__fsub_rn(y[1], d01.y), 32.0f);
-            y[2] = __fmul_rn(__fsub_rn(y[2], d23.x), 32.0f);
-            y[3] = __fmul_rn(__fsub_rn(y[3], d23.y), 32.0f);
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"((uint16_t)q01));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"((uint16_t)q23));
+            const __half2 m32 = __float2half2_rn(-32.0f);
+            const float2 d01 = __half22float2(__hmul2(*reinterpret_cast<__half2 *>(&h01), m32));
+            const float2 d23 = __half22float2(__hmul2(*reinterpret_cast<__half2 *>(&h23), m32));
+            y01 = __ffma2_rn(y01, make_float2(32.0f, 32.0f), d01);
+            y23 = __ffma2_rn(y23, make_float2(32.0f, 32.0f), d23);
         }
     }
 }
@@ -543,7 +551,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Routing rt;
-    __shared__ float b_scale[SB][NT];
+    __shared__ alignas(16) float b_scale[SB][NT];
     __shared__ uint64_t bars[2 * A_STAGES + 2 * SB + 6];
     __shared__ uint32_t tmem_slot;
     __shared__ unsigned int s_last;
@@ -714,10 +722,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int me = warp - 2;
             int bs = 0;
             uint32_t bph = 1;
-            auto split = [&](const Work &w, bool second, auto *base, auto row_of, int width, int64_t ld, bool vec, auto parts) {
+            auto split = [&](const Work &w, bool second, auto *base, int width, int64_t ld, bool vec, auto parts) {
                 constexpr int PARTS = decltype(parts)::value;
                 return for_pieces(w, [&](int u, int k0, int k1) {
-                    const int ch = u / w.tiles, n = rt.c_n[ch], n8 = (n + 7) / 8 * 8, first = rt.c_first[ch];
+                    const int ch = u / w.tiles, n = rt.c_n[ch], first = rt.c_first[ch];
+                    const uint32_t part_bytes = (uint32_t)((n + 7) / 8 * 8 * BK);
                     if (second) {                  // the chunk's h is whole?
                         bool go = true;
                         if (lane == 0) go = grid_wait(done + ch, (unsigned)w1.tiles, lim);
@@ -734,8 +743,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     auto fetch = [&]() {
                         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (fk < k1) {
-                            const int slot = rt.list[first + fi];
-                            v = load_quad(base + (int64_t)row_of(slot) * ld, fk * BK + 4 * lane, width, vec);
+                            const int row = second ? rt.list[first + fi] : rt.token[first + fi];
+                            v = load_quad(base + (int64_t)row * ld, fk * BK + 4 * lane, width, vec);
                             advance(fk, fi);
                         }
                         return v;
@@ -748,7 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 const float4 v = v0;
                                 v0 = v1;
                                 v1 = fetch();
-                                split_block<PARTS>(v, b_at(bs), b_scale[bs], i, n8, lane);
+                                split_block<PARTS>(v, b_at(bs), b_scale[bs], i, part_bytes, lane);
                                 advance(ik, i);
                             } while (ik == kb);
                             // generic-proxy stores must be visible to the tensor core's reads
@@ -761,11 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return true;
                 });
             };
-            const int topk = p.topk;
-            if (split(w1, false, static_cast<const XT *>(p.x), [&](int slot) { return slot / topk; }, p.D, p.ldx,
-                      p.x_vec != 0, std::integral_constant<int, P1>{}))
-                split(w2, true, static_cast<const float *>(p.h), [](int slot) { return slot; }, p.F, p.ldh, true,
-                      std::integral_constant<int, P2>{});
+            if (split(w1, false, static_cast<const XT *>(p.x), p.D, p.ldx, p.x_vec != 0, std::integral_constant<int, P1>{}))
+                split(w2, true, static_cast<const float *>(p.h), p.F, p.ldh, true, std::integral_constant<int, P2>{});
         }
     } else if (warp == FINISHER) {
         // ------------------------------------------------ finished tiles
@@ -862,12 +868,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                         uint32_t r[PARTS][8];
                         tmem_ld_parts(ta + (uint32_t)i0, (uint32_t)n8, r);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float t = __uint_as_float(r[PARTS - 1][j]);
+                        for (int j = 0; j < 8; j += 2) {
+                            const float2 ts = *reinterpret_cast<const float2 *>(&b_scale[bs][i0 + j]);
+                            float2 t = make_float2(__uint_as_float(r[PARTS - 1][j]), __uint_as_float(r[PARTS - 1][j + 1]));
 #pragma unroll
                             for (int i = PARTS - 2; i >= 0; --i)
-                                t = __fmaf_rn(t, 1.0f / 32.0f, __uint_as_float(r[i][j]));
-                            acc[i0 + j] = __fmaf_rn(t, __fmul_rn(sw, b_scale[bs][i0 + j]), acc[i0 + j]);
+                                t = __ffma2_rn(t, make_float2(1.0f / 32.0f, 1.0f / 32.0f),
+                                               make_float2(__uint_as_float(r[i][j]), __uint_as_float(r[i][j + 1])));
+                            const float2 a = __ffma2_rn(t, __fmul2_rn(make_float2(sw, sw), ts), make_float2(acc[i0 + j], acc[i0 + j + 1]));
+                            acc[i0 + j] = a.x;
+                            acc[i0 + j + 1] = a.y;
                         }
                     }
                     tc_fence_before();
