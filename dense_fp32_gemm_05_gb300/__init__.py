@@ -115,7 +115,7 @@ def _declare(lib):
     lib.sgemm_fp8.argtypes = [c, c, i64, i64, i64, f32, vp, i32, i64, vp, i32, i64, vp, i32, i64, vp,
                               i32, i64, f32, vp, i32, i64, vp]
     lib.sgemm_fp8.restype = i32
-    lib.sgemm_fp8_plan.argtypes = [i64, i64, i64, i32, ip, ip, ip]
+    lib.sgemm_fp8_plan.argtypes = [i64, i64, i64, i32, i32, ip, ip, ip]
     lib.sgemm_fp8_plan.restype = i32
     lib.sgemm_moe.argtypes = [i64, i64, i64, i64, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64,
                               vp, vp, i64, i64, i32, vp, i64, vp, vp, vp]
@@ -390,10 +390,10 @@ def sgemm_fp8(transA, transB, M, N, K, alpha, A, a_type, lda, SA, a_group, ldsa,
                             B, b_type, ldb, SB, b_group, ldsb, beta, C, c_type, ldc, _stream(stream))
 
 
-def sgemm_fp8_plan(M, N, K, num_sms=152):
+def sgemm_fp8_plan(M, N, K, b_group=128, num_sms=152):
     """The 8-bit product's tile and cluster size, without a GPU: (status, dict)."""
     outs = [ctypes.c_int(0) for _ in range(3)]
-    st = load().sgemm_fp8_plan(M, N, K, num_sms, *[ctypes.byref(o) for o in outs])
+    st = load().sgemm_fp8_plan(M, N, K, b_group, num_sms, *[ctypes.byref(o) for o in outs])
     return st, {k: o.value for k, o in zip(("tile_m", "tile_n", "ksplit"), outs)}
 
 

@@ -1094,7 +1094,7 @@ static int run_fp8(char ta, char tb, int64_t M, int64_t N, int64_t K, float alph
     if (lda % 16 != 0) lda = up16(lda);
     if (ldb % 16 != 0) ldb = up16(ldb);
 
-    const Fp8Plan pl = fp8_plan(M, N, K, sms);
+    const Fp8Plan pl = fp8_plan(M, N, K, b_group, sms);
     const bool dep = copy_a || copy_b;
     // scales: strides along M or N and along the sum, for each operand
     const int64_t a_mn_stride = a_group == 1 || a_mn ? 1 : ldsa, a_k_stride = a_group == 1 || a_mn ? ldsa : 1;
@@ -1188,13 +1188,14 @@ extern "C" int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t
     }
 }
 
-extern "C" int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int *out_tile_m,
+extern "C" int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int num_sms, int *out_tile_m,
                               int *out_tile_n, int *out_ksplit) {
     if (M < 1 || M > INT32_MAX - 255) return -1;
     if (N < 1 || N > INT32_MAX - 255) return -2;
     if (K < 1 || K > INT32_MAX - 255) return -3;
-    if (num_sms <= 0) return -4;
-    const Fp8Plan pl = fp8_plan(M, N, K, num_sms);
+    if (b_group != 1 && b_group != fp8::GROUP) return -4;
+    if (num_sms <= 0) return -5;
+    const Fp8Plan pl = fp8_plan(M, N, K, b_group, num_sms);
     if (out_tile_m) *out_tile_m = pl.by;
     if (out_tile_n) *out_tile_n = pl.bx;
     if (out_ksplit) *out_ksplit = pl.ksplit;

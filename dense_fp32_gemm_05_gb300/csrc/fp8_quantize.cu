@@ -12,8 +12,10 @@
 //
 // Memory bound: x is read once into registers (a tile of 32 x 128 for row
 // groups, 128 x 128 for the others), reduced, converted and stored.
-// Measured on GB300: 16384 x 8192 fp32 in 128 x 128 blocks: see the figures
-// at launch_quantize.
+// Measured on GB300: 16384 x 8192 fp32 in 128 x 128 blocks 104.8 us, 6.40 TB/s, 0.94 of
+// the measured copy; three CTAs an SM (85 registers) and streaming stores took it
+// there from 119 us with two and plain ones: a CTA loads its whole tile before it
+// stores, so others have to load meanwhile.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -69,7 +71,7 @@ __device__ __forceinline__ uint32_t code_any(float x, float inv) {
 // each lane: neighbours with VEC (whole-quad loads and stores; every row of X
 // and Q starts on a quad), else 32 apart (element loads, still coalesced).
 template <typename T, bool E5M2, int MODE, bool VEC>
-__global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quantize_kernel(const Params p) {
     constexpr int RT = MODE == ROWS ? 32 : 128;
     constexpr int R = RT / WARPS;
     constexpr float LARGEST = E5M2 ? 57344.0f : 448.0f;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
             for (int j = 0; j < 4; ++j) q |= code_any<E5M2>(v[i][j], f[j]) << (8 * j);
         }
         if (quad) {
-            *reinterpret_cast<uint32_t *>(dst + c0 + 4 * lane) = q;
+            __stcs(reinterpret_cast<uint32_t *>(dst + c0 + 4 * lane), q);
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)

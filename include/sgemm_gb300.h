@@ -477,13 +477,13 @@ int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float a
               float beta, void *C, int c_type, int64_t ldc, sgemm_stream_t stream);
 
 /*
- * sgemm_fp8_plan - how sgemm_fp8 computes an M x N x K problem on a GPU with
- * num_sms SMs, without touching one: the tile of C and the CTAs of a cluster
+ * sgemm_fp8_plan - how sgemm_fp8 computes an M x N x K problem (with B's scales in
+ * groups of b_group, 1 or 128) on a GPU with num_sms SMs, without touching one: the tile of C and the CTAs of a cluster
  * that share a tile's sum.  Any output pointer may be NULL.  Returns SGEMM_OK
  * or a negative argument index.
  */
-int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int num_sms, int *out_tile_m, int *out_tile_n,
-                   int *out_ksplit);
+int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int num_sms, int *out_tile_m,
+                   int *out_tile_n, int *out_ksplit);
 
 /*
  * sgemm_moe - a mixture-of-experts layer for a few tokens (decode), whole:

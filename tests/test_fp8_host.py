@@ -87,12 +87,22 @@ def test_product_of_nothing_is_ok():
 
 def test_product_plan_covers_every_shape():
     rng = np.random.default_rng(0)
-    for _ in range(2000):
+    seen = set()
+    for _ in range(3000):
         M, N, K = (int(np.exp(rng.uniform(0, np.log(20000)))) for _ in range(3))
-        st, p = sg.sgemm_fp8_plan(M, N, K)
+        group = int(rng.choice([1, 128]))
+        st, p = sg.sgemm_fp8_plan(M, N, K, group)
         nkb = -(-K // 128)
-        assert st == 0 and p["tile_m"] in (16, 32, 64, 128, 256) and 1 <= p["ksplit"] <= min(8, nkb)
-    for args, want in (((0, 1, 1), -1), ((1, 0, 1), -2), ((1, 1, 0), -3), ((1, 1, 1, 0), -4)):
+        assert st == 0 and 1 <= p["ksplit"] <= min(8, nkb)
+        assert (p["tile_m"], p["tile_n"]) in {(16, 128), (32, 128), (64, 128), (128, 128), (256, 256)}
+        tiles = -(-M // p["tile_m"]) * -(-N // p["tile_n"])
+        if p["ksplit"] > 1:                     # clusters are resident at once
+            assert p["tile_n"] == 128 and tiles * p["ksplit"] <= 152
+        if p["tile_m"] > 16:
+            assert p["tile_m"] < 2 * M
+        seen.add((p["tile_m"], p["ksplit"] > 1))
+    assert len(seen) == 9                       # every tile, the narrow ones with and without clusters
+    for args, want in (((0, 1, 1), -1), ((1, 0, 1), -2), ((1, 1, 0), -3), ((1, 1, 1, 2), -4), ((1, 1, 1, 1, 0), -5)):
         assert sg.sgemm_fp8_plan(*args)[0] == want
 
 
