@@ -31,6 +31,7 @@ namespace sgemm_gb300 {
 namespace fp8q {
 
 enum { ROWS = 0, COLS = 1, BLOCKS = 2 };   // group shape: 1 x 128, 128 x 1, 128 x 128
+constexpr int tile_rows(int mode, bool tall) { return mode != ROWS ? 128 : tall ? 64 : 32; }
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr uint32_t INF_BITS = 0x7f800000u;
@@ -46,17 +47,23 @@ struct Params {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Four consecutive elements (16-byte fp32, 8-byte bf16 loads).
-__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
-    const float4 t = __ldcs(reinterpret_cast<const float4 *>(p));
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
-    const uint2 t = __ldcs(reinterpret_cast<const uint2 *>(p));
+// Four elements as loaded (16 bytes of fp32, 8 of bf16), and their values.  They are
+// held as loaded: converted at once, the compiler had few of a tile's bf16 loads
+// under way (8192 x 8192 in blocks 103 us).
+template <typename T> struct Quad;
+template <> struct Quad<float> { using Raw = float4; };
+template <> struct Quad<__nv_bfloat16> { using Raw = uint2; };
+__device__ __forceinline__ void values(float4 t, float (&v)[4]) { v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w; }
+__device__ __forceinline__ void values(uint2 t, float (&v)[4]) {
     v[0] = __uint_as_float(t.x << 16);
     v[1] = __uint_as_float(t.x & 0xffff0000u);
     v[2] = __uint_as_float(t.y << 16);
     v[3] = __uint_as_float(t.y & 0xffff0000u);
+}
+__device__ __forceinline__ float4 pack(float a, float b, float c, float d, const float *) { return make_float4(a, b, c, d); }
+__device__ __forceinline__ uint2 pack(float a, float b, float c, float d, const __nv_bfloat16 *) {
+    return make_uint2((__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u),
+                      (__float_as_uint(c) >> 16) | (__float_as_uint(d) & 0xffff0000u));
 }
 
 // One value that may be infinite or NaN.
@@ -67,12 +74,13 @@ __device__ __forceinline__ uint32_t code_any(float x, float inv) {
     return fp8::codes2<E5M2>(__fmul_rn(x, inv), 0.0f) & 0xffu;
 }
 
-// A tile is RT rows (RT / 8 for each warp) x 128 columns, four of them for
+// A tile is RT rows (RT / 8 for each warp; TALL: more of them where there are many, so
+// that more loads are under way) x 128 columns, four of them for
 // each lane: neighbours with VEC (whole-quad loads and stores; every row of X
 // and Q starts on a quad), else 32 apart (element loads, still coalesced).
-template <typename T, bool E5M2, int MODE, bool VEC>
+template <typename T, bool E5M2, int MODE, bool VEC, bool TALL>
 __global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quantize_kernel(const Params p) {
-    constexpr int RT = MODE == ROWS ? 32 : 128;
+    constexpr int RT = tile_rows(MODE, TALL);
     constexpr int R = RT / WARPS;
     constexpr float LARGEST = E5M2 ? 57344.0f : 448.0f;
     __shared__ uint32_t red[WARPS][fp8::GROUP];
@@ -83,17 +91,18 @@ __global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quan
     auto col = [&](int j) { return VEC ? c0 + 4 * lane + j : c0 + 32 * j + lane; };
     const bool quad = VEC && c0 + 4 * lane + 3 < p.cols;
 
-    float v[R][4];
+    typename Quad<T>::Raw raw[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int r = r0 + i;
         const T *src = X + (int64_t)r * p.ldx;
         if (r < p.rows && quad) {
-            load4(src + c0 + 4 * lane, v[i]);
+            raw[i] = __ldcs(reinterpret_cast<const typename Quad<T>::Raw *>(src + c0 + 4 * lane));
         } else {
+            float e[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[i][j] = r < p.rows && col(j) < p.cols ? to_f32(src[col(j)]) : 0.0f;
+            for (int j = 0; j < 4; ++j) e[j] = r < p.rows && col(j) < p.cols ? to_f32(src[col(j)]) : 0.0f;
+            raw[i] = pack(e[0], e[1], e[2], e[3], X);
         }
     }
     // largest finite |x|, as bits (non-negative fp32 values order as integers)
@@ -102,14 +111,17 @@ __global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quan
 #pragma unroll
     for (int i = 0; i < (MODE == ROWS ? R : 4); ++i) m[i] = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+        float v[4];
+        values(raw[i], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t b = __float_as_uint(v[i][j]) & 0x7fffffffu;
+            const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
             uint32_t &to = m[MODE == ROWS ? i : j];
             any = max(any, b);
             to = max(to, b < INF_BITS ? b : 0u);
         }
+    }
     float inv[MODE == ROWS ? R : (MODE == COLS ? 4 : 1)];
     if (MODE == ROWS) {
         // lane i < R holds row i's maximum: one division for each row
@@ -158,17 +170,18 @@ __global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quan
         if (r >= p.rows) break;
         uint8_t *dst = p.Q + (int64_t)r * p.ldq;
         uint32_t q;
-        float f[4];
+        float f[4], v[4];
+        values(raw[i], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = inv[MODE == ROWS ? i : (MODE == COLS ? j : 0)];
         if (!odd) {
-            const float y[4] = {__fmul_rn(v[i][0], f[0]), __fmul_rn(v[i][1], f[1]),
-                                __fmul_rn(v[i][2], f[2]), __fmul_rn(v[i][3], f[3])};
+            const float y[4] = {__fmul_rn(v[0], f[0]), __fmul_rn(v[1], f[1]),
+                                __fmul_rn(v[2], f[2]), __fmul_rn(v[3], f[3])};
             q = fp8::codes4<E5M2>(y);
         } else {
             q = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q |= code_any<E5M2>(v[i][j], f[j]) << (8 * j);
+            for (int j = 0; j < 4; ++j) q |= code_any<E5M2>(v[j], f[j]) << (8 * j);
         }
         if (quad) {
             __stcs(reinterpret_cast<uint32_t *>(dst + c0 + 4 * lane), q);
@@ -182,15 +195,23 @@ __global__ void __launch_bounds__(THREADS, !VEC ? 2 : MODE == ROWS ? 4 : 3) quan
 
 }  // namespace fp8q
 
-template <typename T, bool E5M2, int MODE>
-static int launch_quantize(const fp8q::Params &p, bool vec, cudaStream_t s) {
-    const int rt = MODE == fp8q::ROWS ? 32 : 128;
+template <typename T, bool E5M2, int MODE, bool VEC, bool TALL>
+static int launch_quantize_tiles(const fp8q::Params &p, cudaStream_t s) {
+    const int rt = fp8q::tile_rows(MODE, TALL);
     const int64_t grid = (((int64_t)p.rows + rt - 1) / rt) * p.tiles_c;
     if (grid > INT32_MAX) return SGEMM_ERR_UNSUPPORTED;
     count_launch();
-    if (vec) fp8q::quantize_kernel<T, E5M2, MODE, true><<<(unsigned)grid, fp8q::THREADS, 0, s>>>(p);
-    else fp8q::quantize_kernel<T, E5M2, MODE, false><<<(unsigned)grid, fp8q::THREADS, 0, s>>>(p);
+    fp8q::quantize_kernel<T, E5M2, MODE, VEC, TALL><<<(unsigned)grid, fp8q::THREADS, 0, s>>>(p);
     return launch_status();
+}
+
+template <typename T, bool E5M2, int MODE>
+static int launch_quantize(const fp8q::Params &p, bool vec, cudaStream_t s) {
+    if (!vec) return launch_quantize_tiles<T, E5M2, MODE, false, false>(p, s);
+    // tall tiles once short ones would fill the SMs twice over (8 CTAs each)
+    const bool tall = MODE == fp8q::ROWS && (int64_t)(p.rows / 32) * p.tiles_c >= 2400;
+    return tall ? launch_quantize_tiles<T, E5M2, MODE, true, MODE == fp8q::ROWS>(p, s)
+                : launch_quantize_tiles<T, E5M2, MODE, true, false>(p, s);
 }
 
 template <typename T, bool E5M2>
