@@ -26,7 +26,7 @@
 //     timing.
 //
 // Phases, one CTA per SM, cooperative launch:
-//   0  router logits: 4 tokens x 2 experts x a slice of D for each warp of the grid
+//   0  x in parts, to memory; router logits: 4 tokens x 2 experts x a slice of D for each warp of the grid
 //      (fp32 FMAs); after a grid barrier softmax and top-k, a token each on
 //      different CTAs; after another every CTA lists the experts' tokens for itself;
 //   1  h = silu(gate x) * (up x): tiles of 64 gate rows and the same 64 up rows.
@@ -36,8 +36,8 @@
 //      had the same experts, not for the slowest;
 //   3  after a last grid barrier y = sum over a token's experts, all threads.
 //
-// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-10 split activations
-// into the MMA's column operand; 11 publishes finished tiles; 12-15 promotion (128
+// Warps: 0 TMA producer; 1 tensor memory and MMA issue; 2-10 the MMA's column
+// operand: x's parts as they are, h split into its; 11 publishes finished tiles; 12-15 promotion (128
 // rows, one per thread).
 // Every wait is bounded: a role that gives up sets the device error word and
 // stops; every CTA still arrives at every grid barrier, so that the counters
@@ -50,6 +50,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "plan.h"
@@ -111,6 +112,8 @@ struct Params {
     unsigned int *arrivals;
     int n_arrivals;
     float *logit_parts;                        // [slices][T][E]
+    uint32_t *x_parts;                         // [token][block][part][128 bytes]
+    float *x_scales;                           // [token][block]
     float *h;                                  // [slot][ldh]
     float *parts;                              // [phase][CTA][first, last tile of its range][token][ROWS]
     float *out;                                // [slot][ldo]: down h
@@ -493,13 +496,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// A lane's 4 values of a token's block -> its bytes of the column operand, and
-// (lane 0) the block's scale.  Part i of token c is row i * n8 + c: 128 bytes, the
-// 16-byte chunk index flipped by the row's low 3 bits (128-byte swizzle), which are
-// c's.  These instructions, ~60 for a token's block, bound the layer when experts have
+// A lane's 4 values of a token's block -> its bytes of each part, and (lane 0) the
+// block's scale.  These instructions, ~60 for a token's block, bound the layer when experts have
 // 8 tokens and more, so they are packed pairs where they can be.
-template <int PARTS>
-__device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, int c, uint32_t part_bytes, int lane) {
+// `store` takes part i's 4 bytes.
+template <int PARTS, typename Store>
+__device__ __forceinline__ void split_block(float4 v, float *scale, int lane, Store store) {
     const float hi = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
     const uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
     const int e = (int)(amax >> 23);
@@ -514,18 +516,16 @@ __device__ __forceinline__ void split_block(float4 v, uint32_t b, float *scale, 
     // 2^(7 - floor(log2 amax)), within the powers whose reciprocal is a normal number
     const int ub = min(max(261 - e, 1), 253);
     const float up = __uint_as_float((uint32_t)ub << 23);
-    if (lane == 0) scale[c] = __uint_as_float((uint32_t)(254 - ub) << 23);
+    if (lane == 0) *scale = __uint_as_float((uint32_t)(254 - ub) << 23);
     float2 y01 = __fmul2_rn(make_float2(v.x, v.y), make_float2(up, up));
     float2 y23 = __fmul2_rn(make_float2(v.z, v.w), make_float2(up, up));
-    uint32_t at = b + (uint32_t)(c * BK) + ((uint32_t)(((lane >> 2) ^ (c & 7)) << 4) | (uint32_t)(4 * (lane & 3)));
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
         const uint32_t q01 = fp8::codes2<false>(y01.x, y01.y), q23 = fp8::codes2<false>(y23.x, y23.y);
-        asm volatile("st.shared.u32 [%0], %1;" :: "r"(at), "r"(q01 | (q23 << 16)) : "memory");
+        store(i, q01 | (q23 << 16));
         if (i + 1 < PARTS) {
             // y = 32 (y - q), exact: 32 q is a half (at most 14336), and the multiply-add
             // has nothing to round
-            at += part_bytes;
             uint32_t h01, h23;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"((uint16_t)q01));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"((uint16_t)q23));
@@ -599,6 +599,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int i = warp * (int)G + blockIdx.x; i < tt * et * p.slices; i += (THREADS / 32) * G) {
             const int slice = i % p.slices, tile = i / p.slices;
             logits_task<XT>(p, tile / et * LOGIT_T, tile % et * LOGIT_E, slice);
+        }
+    }
+    // x in parts, once for all the tiles that read it
+    {
+        const int blocks = (p.D + BK - 1) / BK;
+        const XT *x = static_cast<const XT *>(p.x);
+        for (int i = warp * (int)G + blockIdx.x; i < p.T * blocks; i += (THREADS / 32) * G) {
+            const int t = i / blocks, kb = i - t * blocks;
+            const float4 v = load_quad(x + (int64_t)t * p.ldx, kb * BK + 4 * lane, p.D, p.x_vec != 0);
+            uint32_t *to = p.x_parts + (int64_t)i * (P1 * BK / 4) + lane;
+            split_block<P1>(v, p.x_scales + i, lane, [&](int part, uint32_t q) { to[part * (BK / 4)] = q; });
         }
     }
     bool ok = true;
@@ -722,12 +733,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int me = warp - 2;
             int bs = 0;
             uint32_t bph = 1;
-            auto split = [&](const Work &w, bool second, auto *base, int width, int64_t ld, bool vec, auto parts) {
+            auto split = [&](const Work &w, auto second_, auto parts) {
+                constexpr bool SECOND = decltype(second_)::value;
                 constexpr int PARTS = decltype(parts)::value;
                 return for_pieces(w, [&](int u, int k0, int k1) {
                     const int ch = u / w.tiles, n = rt.c_n[ch], first = rt.c_first[ch];
                     const uint32_t part_bytes = (uint32_t)((n + 7) / 8 * 8 * BK);
-                    if (second) {                  // the chunk's h is whole?
+                    if (SECOND) {                  // the chunk's h is whole?
                         bool go = true;
                         if (lane == 0) go = grid_wait(done + ch, (unsigned)w1.tiles, lim);
                         if (!__all_sync(0xffffffffu, go)) return false;
@@ -740,24 +752,46 @@ __global__ void __launch_bounds__(THREADS, 1)
                         c += di;
                         if (c >= n) { c -= n; ++k; }
                     };
+                    // h: 4 values of a token's block; x: 16 bytes of its parts, and its scale
+                    struct Loaded { float4 v; float scale; };
                     auto fetch = [&]() {
-                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        Loaded f{make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f};
                         if (fk < k1) {
-                            const int row = second ? rt.list[first + fi] : rt.token[first + fi];
-                            v = load_quad(base + (int64_t)row * ld, fk * BK + 4 * lane, width, vec);
+                            if (SECOND) {
+                                f.v = load_quad(p.h + (int64_t)rt.list[first + fi] * p.ldh, fk * BK + 4 * lane, p.F, true);
+                            } else {
+                                const int64_t at = (int64_t)rt.token[first + fi] * w.kb + fk;
+                                if (lane < 8 * PARTS)
+                                    f.v = __ldcg(reinterpret_cast<const float4 *>(p.x_parts + at * (PARTS * BK / 4)) + lane);
+                                f.scale = __ldcg(p.x_scales + at);
+                            }
                             advance(fk, fi);
                         }
-                        return v;
+                        return f;
                     };
-                    float4 v0 = fetch(), v1 = fetch();
+                    Loaded v0 = fetch(), v1 = fetch();
                     for (int kb = k0; kb < k1; ++kb) {
                         if (!warp_wait(b_empty(bs), bph, lim)) return false;
                         if (ik == kb) {
                             do {
-                                const float4 v = v0;
+                                const Loaded l = v0;
                                 v0 = v1;
                                 v1 = fetch();
-                                split_block<PARTS>(v, b_at(bs), b_scale[bs], i, part_bytes, lane);
+                                // part j of token i is row j n8 + i: 128 bytes, the 16-byte chunk
+                                // index flipped by the row's low 3 bits (128-byte swizzle), i's
+                                const uint32_t row = b_at(bs) + (uint32_t)(i * BK);
+                                if (SECOND) {
+                                    const uint32_t to = row + ((uint32_t)(((lane >> 2) ^ (i & 7)) << 4) | (uint32_t)(4 * (lane & 3)));
+                                    split_block<PARTS>(l.v, &b_scale[bs][i], lane, [&](int j, uint32_t q) {
+                                        asm volatile("st.shared.u32 [%0], %1;" :: "r"(to + j * part_bytes), "r"(q) : "memory");
+                                    });
+                                } else {
+                                    const uint32_t to = row + (uint32_t)(lane >> 3) * part_bytes + (uint32_t)(((lane & 7) ^ (i & 7)) << 4);
+                                    if (lane < 8 * PARTS)
+                                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                                                     :: "r"(to), "f"(l.v.x), "f"(l.v.y), "f"(l.v.z), "f"(l.v.w) : "memory");
+                                    if (lane == 0) b_scale[bs][i] = l.scale;
+                                }
                                 advance(ik, i);
                             } while (ik == kb);
                             // generic-proxy stores must be visible to the tensor core's reads
@@ -770,8 +804,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     return true;
                 });
             };
-            if (split(w1, false, static_cast<const XT *>(p.x), p.D, p.ldx, p.x_vec != 0, std::integral_constant<int, P1>{}))
-                split(w2, true, static_cast<const float *>(p.h), p.F, p.ldh, true, std::integral_constant<int, P2>{});
+            if (split(w1, std::false_type{}, std::integral_constant<int, P1>{}))
+                split(w2, std::true_type{}, std::integral_constant<int, P2>{});
         }
     } else if (warp == FINISHER) {
         // ------------------------------------------------ finished tiles
@@ -1051,15 +1085,18 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     if (st != SGEMM_OK) return st;
     if (fresh && cudaMemsetAsync(sync, 0, 256, s) != cudaSuccess) return launch_status();
     const size_t b_arr = up256((size_t)arrivals * 4), b_log = up256((size_t)p.slices * T * E * 4),
-                 b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)2 * sms * 2 * nt * moe::ROWS * 4),
+                 b_xp = up256((size_t)T * fp8::blocks_of(D) * (x_type == SGEMM_TYPE_F32 ? 4 : 2) * moe::BK),
+                 b_xs = up256((size_t)T * fp8::blocks_of(D) * 4), b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)2 * sms * 2 * nt * moe::ROWS * 4),
                  b_out = up256((size_t)slots * p.ldo * 4);
-    st = workspace(s, b_arr + b_log + b_h + b_parts + b_out, &ws);
+    st = workspace(s, b_arr + b_log + b_xp + b_xs + b_h + b_parts + b_out, &ws);
     if (st != SGEMM_OK) return st;
     char *w = static_cast<char *>(ws);
     p.sync = static_cast<unsigned int *>(sync);
     p.arrivals = reinterpret_cast<unsigned int *>(w);
     p.logit_parts = reinterpret_cast<float *>(w += b_arr);
-    p.h = reinterpret_cast<float *>(w += b_log);
+    p.x_parts = reinterpret_cast<uint32_t *>(w += b_log);
+    p.x_scales = reinterpret_cast<float *>(w += b_xp);
+    p.h = reinterpret_cast<float *>(w += b_xs);
     p.parts = reinterpret_cast<float *>(w += b_h);
     p.out = reinterpret_cast<float *>(w += b_parts);
     p.wait_ns = tc_wait_limit();
