@@ -8,31 +8,34 @@
 // codes are exact in fp32); the scales differ from block to block, so each
 // P_b is brought into registers once and added there with its scales.
 //
-// Orientation: the MMA's M (tensor-memory lanes) is the result's N, its N
-// (columns) is the result's M.  A warp then holds 32 neighbouring columns of C
-// for each row m, so that C is stored straight from registers, whole sectors
-// at a time; and few rows (decode) become a narrow MMA, BY = 16 .. 128 columns,
-// against 128 rows of the weights.
+// Two kernels.  Large results take 256 x 256 tiles on SM pairs (fp8_wide_kernel,
+// below), the others narrow tiles (fp8_gemm_kernel), by the rule in fp8_plan.h.
 //
-// Kernel (352 threads; one CTA per SM):
+// Narrow tiles: the MMA's M (tensor-memory lanes) is the result's N, its N (columns)
+// the result's M.  A warp then holds 32 neighbouring columns of C for each row m, so
+// that C is stored straight from registers, whole sectors at a time; and few rows
+// (decode) become a narrow MMA, BY = 16 .. 128 columns, against 128 full rows of the
+// weights, which are read once.  352 threads, one CTA per SM:
 //   warp 0      TMA producer: per block of 128 k one 128 x 128 tile of B (the
 //               "X" operand) and a BY x 128 tile of A ("Y") into a ring of
 //               stages.  Either operand may be stored along k or across it
 //               (MN-major descriptors read the tile as it lies);
-//   warp 1      tensor memory, and one lane that issues the 4 MMAs of a block
-//               into one of two buffers of BY columns;
+//   warp 1      tensor memory, and the 4 MMAs of a block into one of two buffers of
+//               BY columns;
 //   warp 2      the block's scales, sA(m,b) for each column (times sB where
 //               that is one value for the CTA's 128 rows), in a small ring;
 //   warps 3-10  add a block's P_b to the accumulators: tcgen05.ld, then one
-//               fused multiply-add for each value (two where both operands
-//               have a scale for each row).  128 x BY fp32 accumulators live in
-//               their registers: warp w has lanes 32 (w % 4) .. + 31 and half
-//               of the columns.  They release the buffer as soon as it is read.
+//               fused multiply-add for each value (two where B has a scale for each
+//               row).  128 x BY fp32 accumulators live in their registers: warp w has
+//               lanes 32 (w % 4) .. + 31 and half of the columns.  They release the
+//               buffer as soon as it is read.
 // Each CTA walks tiles of C (grouped raster), the rings run on across tiles.
-//
 // Few tiles: a cluster of KS CTAs shares a tile's blocks in contiguous ranges
 // and adds the partial sums through distributed shared memory in ascending
 // order, each CTA its share of the columns: no workspace, no atomics.
+// Decode is bound by the weights' stream: 16 x 16384 x 8192 25.1 us, 5.4 TB/s over the
+// call (0.79 of the measured copy), of which ~4 us are the launch, the first loads and
+// the last tile; small ones by latency (256^3 4.3 us).
 //
 // Every wait is bounded, as in the tensor-core GEMM: on expiry the device error
 // word is set, the role stops, copies and MMAs in flight are waited for (again
@@ -430,12 +433,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 // the two tensor-memory buffers.  Here the lanes are C's rows: a row's scale is one
 // register, and where B has one scale for its 128 x 128 block the product of the
 // two is one value for each thread and block of k, so that promotion is one
-// multiply-add per value and nothing else.  (With C's columns on the lanes, as
-// in the narrow kernel, every column's scale comes from shared memory for
-// every block, beside the MMAs' own reads: 1.34 against PFLOP/s at 8192^3.)
-// 128 accumulators per promoting thread need more registers than an equal
-// share: the three issuing warps hand theirs over (setmaxnreg).
-// The epilogue turns 32 x 32 blocks around through shared memory.
+// multiply-add per value and nothing else.  (With C's columns on the lanes every
+// column's scale comes from shared memory for every block, beside the MMAs' own
+// reads: 820 us at 8192^3, on single SMs.)  128 accumulators per promoting thread
+// need more registers than an equal share: the first warpgroup hands its over
+// (setmaxnreg).
+// 8192^3 NT 392 us, 2.80 PFLOP/s (0.74 of twice the measured bf16 rate).  What bounds
+// it is the turn-round of the two buffers, which fill tensor memory: release to the
+// MMA's start 230 clocks, the MMAs (512) and their commit's arrival 900, reading 580,
+// for two blocks; the MMAs fed by TMA alone would take 671 a block, not 857.
+// With a scale for each row of B promotion is a multiply and a multiply-add, and the
+// columns' scales come from shared memory: ~1600 clocks a block (4096 x 4096 x 8192
+// TN 222 us, 1.24 PFLOP/s).
 constexpr int WT = 256;                        // tile rows and columns
 constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
 

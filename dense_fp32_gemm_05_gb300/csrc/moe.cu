@@ -182,10 +182,10 @@ __device__ __forceinline__ float4 quad(const __nv_bfloat16 *p) {
 template <typename T>
 __device__ __noinline__ float4 load_elements(const T *row, int k, int n) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (k < n) v.x = to_f32(row[k]);
-    if (k + 1 < n) v.y = to_f32(row[k + 1]);
-    if (k + 2 < n) v.z = to_f32(row[k + 2]);
-    if (k + 3 < n) v.w = to_f32(row[k + 3]);
+    if (k < n) v.x = to_f32(__ldcg(row + k));
+    if (k + 1 < n) v.y = to_f32(__ldcg(row + k + 1));
+    if (k + 2 < n) v.z = to_f32(__ldcg(row + k + 2));
+    if (k + 3 < n) v.w = to_f32(__ldcg(row + k + 3));
     return v;
 }
 template <typename T>
@@ -1081,7 +1081,7 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     // the barriers keep a workspace of their own: they are zero between calls
     void *sync = nullptr, *ws = nullptr;
     bool fresh = false;
-    st = workspace(s, 256, &sync, 2, &fresh);
+    st = workspace(s, 256, &sync, 3, &fresh);
     if (st != SGEMM_OK) return st;
     if (fresh && cudaMemsetAsync(sync, 0, 256, s) != cudaSuccess) return launch_status();
     const size_t b_arr = up256((size_t)arrivals * 4), b_log = up256((size_t)p.slices * T * E * 4),

@@ -59,7 +59,9 @@ uint64_t tc_wait_limit();
 // kernel launch on `s` when timing is enabled (no-op otherwise).
 void timing_mark(cudaStream_t s, bool begin);
 
-// Library-owned per-(device, stream, slot) workspace, grown on demand.
+// Library-owned per-(device, stream, slot) workspace, grown on demand.  Slots: 0 a
+// call's scratch, 1 sgemm_host's staging buffers, 2 the thin path's partial sums, 3
+// the mixture-of-experts kernel's grid barriers (zero between calls, so no other's).
 // `fresh`, if given, tells whether this call allocated it.
 int workspace(cudaStream_t stream, size_t bytes, void **out, int which = 0, bool *fresh = nullptr);
 

@@ -299,13 +299,14 @@ int sgemm_device_error(sgemm_stream_t stream);
 
 /*
  * sgemm_set_wait_limit - spin limit for the device-side waits of the
- * tensor-core path and of the thin-problem kernel that stages its large
- * operand through shared memory, in nanoseconds of %globaltimer (0 restores
+ * tensor-core path, of the 8-bit operators and of the thin-problem kernel that
+ * stages its large operand through shared memory, in nanoseconds of %globaltimer (0 restores
  * the default of 2 s).  A test hook: a tiny limit makes a wait run out on
  * purpose so that the timeout path can be checked without hanging anything.
  * In the staged thin-problem kernel a limit below 100 us bounds a single
  * mbarrier try_wait's suspension instead, so that a wait not complete within
- * it runs out whatever the timer's resolution.
+ * it runs out whatever the timer's resolution; in the 8-bit operators a limit below
+ * 1 us allows one test of a barrier and no wait.
  */
 int sgemm_set_wait_limit(uint64_t nanoseconds);
 
@@ -513,8 +514,9 @@ int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int num_sms, in
  * One kernel: routing, both expert products and the combination, with the
  * weights of the chosen experts read once.  Weights never leave 8 bits:
  * activations are split into E4M3 parts that add up to the activation (bf16:
- * 2 parts, exact to 2^-21 of the largest of 128; fp32 and h: 4 parts, 2^-20 of
- * each value), so results have fp32 accuracy.  Every sum is in fp32, in a
+ * 2 parts, exact to 2^-21 of the largest of 128; fp32: 4 parts, 2^-20 of each value;
+ * h: 4 parts for fp32 y, 3 for bf16 y, 2^-15 of each value), so results have the
+ * accuracy of y's type.  Every sum is in fp32, in a
  * fixed order.  Device workspace as sgemm's.  The kernel's CTAs wait for one
  * another (cooperative launch, bounded waits): SGEMM_ERR_CUDA if the device
  * cannot hold one CTA per SM at once.

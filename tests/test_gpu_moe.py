@@ -74,7 +74,8 @@ def _x(T, D, dtype, seed=1):
     (1, 256, 128, 4, 1), (1, 128, 64, 2, 2), (1, 1024, 512, 8, 2), (2, 512, 256, 16, 4), (5, 300, 200, 7, 3),
     (8, 257, 129, 3, 3), (9, 384, 320, 8, 2), (16, 256, 192, 33, 8), (17, 640, 100, 5, 2), (32, 256, 256, 4, 4),
     (33, 320, 160, 6, 3), (64, 256, 128, 2, 1), (64, 512, 384, 40, 8), (100, 200, 130, 3, 2), (128, 256, 128, 64, 16),
-    (128, 128, 64, 2, 2), (3, 1, 1, 1, 1), (4, 17, 16, 9, 9)])
+    (128, 128, 64, 2, 2), (3, 1, 1, 1, 1), (4, 17, 16, 9, 9), (6, 128, 64, 128, 8), (5, 128, 64, 130, 7),
+    (2, 64, 32, 512, 16)])
 def test_layer(dtype, T, D, F, E, topk):
     Layer(D, F, E, seed=T).check(_x(T, D, dtype), topk, renormalize=T % 2 == 0)
 
@@ -172,6 +173,25 @@ def test_same_result_every_time_on_any_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert sg.sgemm_device_error() == 0
     assert all(torch.equal(outs[0], o) for o in outs[1:]) and torch.equal(outs[0], y)
+
+
+def test_between_other_calls():
+    """The kernel's barriers are its own: the GEMM's paths on the same stream, whose
+    workspaces hold anything, change nothing."""
+    import torch
+    layer = Layer(1024, 512, 16, seed=12)
+    x = _x(3, 1024, "bfloat16")
+    good = layer.run(x, 4, True)[0].clone()
+    small, big = torch.randn(16, 4096, device="cuda"), torch.randn(4096, 2048, device="cuda")
+    square = torch.randn(700, 700, device="cuda")
+    for _ in range(3):
+        sg.gemm(small, big, torch.empty(16, 2048, device="cuda"))
+        sg.gemm(small[:2], big, torch.empty(2, 2048, device="cuda"))
+        sg.gemm(square, square, torch.empty(700, 700, device="cuda"))
+        assert torch.equal(layer.run(x, 4, True)[0], good)
+    layer.check(x, 4, True)
+    sg.sgemm_release_workspace()
+    assert torch.equal(layer.run(x, 4, True)[0], good)
 
 
 def test_two_streams_at_once():
