@@ -365,6 +365,18 @@ __device__ void route_token(const Params &p, int t, float *buf, int *chosen) {
 template <int NT>
 __device__ void route_lists(const Params &p, Routing &rt) {
     const int lane = threadIdx.x & 31, slots = p.T * p.topk;
+    if (p.T == 1) {                             // its experts differ: a chunk for each
+        if ((int)threadIdx.x < slots) {
+            const int s = threadIdx.x;
+            rt.c_expert[s] = (short)min((unsigned)__ldcg(p.indices + s), (unsigned)(p.E - 1));
+            rt.c_first[s] = (short)s;
+            rt.c_n[s] = 1;
+            rt.list[s] = (short)s;
+            rt.token[s] = 0;
+        }
+        if (threadIdx.x == 0) rt.chunks = slots;
+        return;
+    }
     for (int s = threadIdx.x; s < slots; s += THREADS) {
         // (an index out of range is left by a router that gave up: its error is reported)
         rt.expert[s] = (short)min((unsigned)__ldcg(p.indices + s), (unsigned)(p.E - 1));
@@ -624,17 +636,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     ok = s_last != 0;
     // each token is routed by one CTA, the result read by all after another barrier
-    // (every CTA routing every token: 36 us of T = 64's 115)
-    for (int t = blockIdx.x; ok && t < p.T; t += G) {
+    // (every CTA routing every token: 36 us of T = 64's 115); one token alone by every
+    // CTA for itself (all write the same), which is shorter than the barrier
+    const bool alone = p.T == 1;
+    for (int t = alone ? 0 : (int)blockIdx.x; ok && t < p.T; t += G) {
         float *buf = reinterpret_cast<float *>(smem + A_STAGES * A_BYTES);   // (where activations go later)
         if (p.router) token_logits(p, t, buf);
         __syncthreads();
         if (warp == 0) route_token(p, t, buf, reinterpret_cast<int *>(buf + 2 * MAX_E));
         __syncthreads();
     }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        add_release(&p.sync[1]);
-        s_last = ok && grid_wait(&p.sync[1], G, lim);
+        if (!alone) add_release(&p.sync[1]);
+        s_last = ok && (alone || grid_wait(&p.sync[1], G, lim));
     }
     __syncthreads();
     ok = s_last != 0;
