@@ -443,8 +443,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // MMA's start 230 clocks, the MMAs (512) and their commit's arrival 900, reading 580,
 // for two blocks; the MMAs fed by TMA alone would take 671 a block, not 857.
 // With a scale for each row of B promotion is a multiply and a multiply-add, and the
-// columns' scales come from shared memory: ~1600 clocks a block (4096 x 4096 x 8192
-// TN 222 us, 1.24 PFLOP/s).
+// columns' scales come from shared memory.  There a thread reads pairs of columns in
+// four rows, so that a pair of scales is loaded once for four pairs of values and the
+// rows' scales are four registers: with a row in each thread, as above, the loads of
+// 16 bytes for every four values took shared memory's whole rate (4096 x 4096 x 8192
+// TN, beta = 1: 225 -> 192 us, 1.43 PFLOP/s).  A block takes ~1450 clocks; the
+// promoting warps wait for 180 of them.
 constexpr int WT = 256;                        // tile rows and columns
 constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
 
@@ -739,14 +743,19 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
         int b = 0, slot = 0;
         uint32_t bph = 0, sph = 0;
         // (the reads under way while another chunk is added are held by the compiler in
-        // place: the kernel must not spill)
+        // place: no accumulator or sum may spill)
         uint32_t r[2][CH];
+        auto read = [&](int c, uint32_t(&v)[CH]) {
+            const uint32_t at = taddr + (uint32_t)(b * WT + c * CH);
+            if (YVEC) tmem_ld_rows_async(at, v);
+            else tmem_ld_async(at, v);
+        };
         // waits for the next buffer and starts reading it
         auto next_buffer = [&]() {
             ok = warp_wait(tfull(b), bph, lim);
             if (ok) {
                 tc_fence_after();
-                tmem_ld_async(taddr + (uint32_t)(b * WT), r[0]);
+                read(0, r[0]);
             }
         };
         for (int u = group; ok && u < units; u += groups) {
@@ -760,31 +769,40 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             next_buffer();
             if (!ok) break;
             for (int kb = 0; kb < p.nkb; ++kb) {
-                float s;
+                float2 s2[YVEC ? 4 : 1];
                 const float *sc = scales + (slot * BATCH + kb % BATCH) * K_::BLOCK;
                 if (YVEC) {
                     if (kb % BATCH == 0) {
                         ok = warp_wait(sfull(slot), sph, lim);
                         if (!ok) break;
                     }
-                    s = sc[q * 32 + lane];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float s = sc[q * 32 + 8 * i + lane / 4];
+                        s2[i] = make_float2(s, s);
+                    }
                 } else {
                     if (kb % BATCH == 0) {
 #pragma unroll
                         for (int a = 0; a < BATCH; ++a) sv[a] = __fmul_rn(nx[a], ny[a]);
                         fetch();
                     }
-                    s = sv[0];
+                    s2[0] = make_float2(sv[0], sv[0]);
 #pragma unroll
                     for (int a = 0; a + 1 < BATCH; ++a) sv[a] = sv[a + 1];
                 }
-                const float2 s2 = make_float2(s, s);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     uint32_t(&v)[CH] = r[c & 1];
+                    float2 y2[CH / 8];             // (loaded while the sums arrive)
+                    if (YVEC) {
+#pragma unroll
+                        for (int g = 0; g < CH / 8; ++g)
+                            y2[g] = *reinterpret_cast<const float2 *>(sc + BX + part * PC + c * CH + 8 * g + 2 * (lane & 3));
+                    }
                     tmem_ld_wait(v);
                     if (c + 1 < NC) {
-                        tmem_ld_async(taddr + (uint32_t)(b * WT + (c + 1) * CH), r[(c + 1) & 1]);
+                        read(c + 1, r[(c + 1) & 1]);
                     } else {
                         // the buffer is read: hand it back, and start on the next one
                         // while this chunk is added
@@ -794,20 +812,23 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                         if (++b == 2) { b = 0; bph ^= 1; }
                         if (kb + 1 < p.nkb) next_buffer();
                     }
+                    if (YVEC) {
 #pragma unroll
-                    for (int i = 0; i < CH; i += 4) {
-                        float2 t0 = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                        float2 t1 = make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                        float2 &a0 = acc[(c * CH + i) / 2], &a1 = acc[(c * CH + i) / 2 + 1];
-                        if (YVEC) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + BX + part * PC + c * CH + i);
-                            t0 = __fmul2_rn(t0, s2);
-                            t1 = __fmul2_rn(t1, s2);
-                            a0 = __ffma2_rn(t0, make_float2(s4.x, s4.y), a0);
-                            a1 = __ffma2_rn(t1, make_float2(s4.z, s4.w), a1);
-                        } else {
-                            a0 = __ffma2_rn(t0, s2, a0);
-                            a1 = __ffma2_rn(t1, s2, a1);
+                        for (int g = 0; g < CH / 8; ++g) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int k = 16 * (i / 2) + 4 * g + 2 * (i % 2);
+                                const float2 t = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                                float2 &a = acc[(c * CH + k) / 2];
+                                a = __ffma2_rn(__fmul2_rn(t, s2[i]), y2[g], a);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2) {
+                            const float2 t = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            float2 &a = acc[(c * CH + i) / 2];
+                            a = __ffma2_rn(t, s2[0], a);
                         }
                     }
                 }
@@ -831,7 +852,20 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                     if (lane == 0) tma_store_read_wait();
                     __syncwarp();
                     uint8_t *row = reinterpret_cast<uint8_t *>(stg);
-                    if (p.c_bf16) {
+                    if (YVEC) {
+                        // (pairs of columns, of four rows a group)
+#pragma unroll
+                        for (int i = 0; i < CH / 2; ++i) {
+                            const int y = lane / 4 + 8 * (i / 8 * 2 + i % 2), g = i / 2 % 4;
+                            const float2 v = make_float2(__fmul_rn(p.alpha, a[i].x), __fmul_rn(p.alpha, a[i].y));
+                            if (p.c_bf16)
+                                *reinterpret_cast<uint32_t *>(row + y * 2 * CH + 16 * staged_chunk<2 * CH>(y, g) +
+                                                              4 * (lane & 3)) = pack2(v.x, v.y);
+                            else
+                                *reinterpret_cast<float2 *>(row + y * 4 * CH + 16 * staged_chunk<4 * CH>(y, 2 * g + (lane & 3) / 2) +
+                                                            8 * (lane & 1)) = v;
+                        }
+                    } else if (p.c_bf16) {
                         row += lane * 2 * CH;
 #pragma unroll
                         for (int i = 0; i < CH / 8; ++i)
@@ -856,10 +890,19 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                     }
                 } else {
                     __syncwarp();
+                    if (YVEC) {
 #pragma unroll
-                    for (int i = 0; i < CH / 4; ++i)
-                        *reinterpret_cast<float4 *>(stg + lane * CH + 4 * staged_chunk<4 * CH>(lane, i)) =
-                            make_float4(a[2 * i].x, a[2 * i].y, a[2 * i + 1].x, a[2 * i + 1].y);
+                        for (int i = 0; i < CH / 2; ++i) {
+                            const int y = lane / 4 + 8 * (i / 8 * 2 + i % 2), g = i / 2 % 4;
+                            *reinterpret_cast<float2 *>(stg + y * CH + 4 * staged_chunk<4 * CH>(y, 2 * g + (lane & 3) / 2) +
+                                                        2 * (lane & 1)) = a[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CH / 4; ++i)
+                            *reinterpret_cast<float4 *>(stg + lane * CH + 4 * staged_chunk<4 * CH>(lane, i)) =
+                                make_float4(a[2 * i].x, a[2 * i].y, a[2 * i + 1].x, a[2 * i + 1].y);
+                    }
                     __syncwarp();
                     const int64_t at = (int64_t)m0 * p.ldc + n0 + c * CH;
                     const int rows = p.M - m0, cols = p.N - n0 - c * CH;

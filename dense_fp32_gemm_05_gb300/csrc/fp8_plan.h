@@ -21,7 +21,7 @@ struct Fp8Plan {
 //   32        4.9    0.20     1.4        0.24
 //   64        6.1    0.24     2.0        0.32
 //   128       8.4    0.375    3.0        0.53
-//   256 x 256 4.0    0.42     1.1        0.83
+//   256 x 256 4.0    0.42     1.1        0.71
 //
 // A cluster of k CTAs takes 1/k of the blocks and 1.5 us to add; clusters have to be
 // resident at once (more than ~136 CTAs in clusters take two waves and more: 512 x
@@ -37,7 +37,7 @@ inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int sms) {
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     Fp8Plan best;
     const bool vec = b_group == 1;
-    const double block = vec ? 0.83 : 0.42;
+    const double block = vec ? 0.71 : 0.42;
     double best_us = M > 128 && N > 128
                          ? 4.0 + (double)ceil_div(ceil_div(M, 256) * ceil_div(N, 256), std::max(sms / 2, 1)) * (block * (double)nkb + 1.1)
                          : 1e30;

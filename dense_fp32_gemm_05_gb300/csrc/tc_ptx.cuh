@@ -238,6 +238,24 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                  :: "memory");
 }
 
+// 32 lanes x 32 columns, asynchronous, a row over four lanes: for column group g and
+// i = 0 .. 3, register 16 (i / 2) + 4 g + 2 (i % 2) + j holds row lane / 4 + 8 i and
+// column 8 g + 2 (lane % 4) + j.
+__device__ __forceinline__ void tmem_ld_rows_async(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("{\n\t"
+                 "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+                 "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t}"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+                   "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr), "r"(taddr + (16u << 16)));
+}
+
 // 32 lanes x 8 columns at each of several places `step` columns apart, complete when
 // it returns: one statement, so that no register can be moved while a read is
 // under way.
