@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // four rows, so that a pair of scales is loaded once for four pairs of values and the
 // rows' scales are four registers: with a row in each thread, as above, the loads of
 // 16 bytes for every four values took shared memory's whole rate (4096 x 4096 x 8192
-// TN, beta = 1: 225 -> 192 us, 1.43 PFLOP/s).  A block takes ~1450 clocks; the
-// promoting warps wait for 180 of them.
+// TN, beta = 1: 225 -> 192 us; 168 us, 1.64 PFLOP/s, with the waits below).  The
+// promoting warps bound it.
 constexpr int WT = 256;                        // tile rows and columns
 constexpr int W_STAGE = 2 * X_BYTES;           // per CTA
 
@@ -460,11 +460,11 @@ struct Wide {
     static constexpr int CH = 32;                          // columns read or stored at a time
     static constexpr int REGS_ISSUE = 40, REGS_PROMOTE = 232;   // 384 x 168 = 128 x 40 + 256 x 232
     static constexpr int OUT = 32 * CH * 4;                // epilogue staging per warp
-    // YVEC: the scales of the CTA's rows and the tile's columns, BATCH blocks of k in a slot
-    static constexpr int BATCH = YVEC ? 2 : 4;
-    static constexpr int SLOTS = YVEC ? 3 : 0;
+    static constexpr int BATCH = 4;                        // blocks of k whose scales are fetched together
+    // YVEC: the scales of the CTA's rows and the tile's columns for a block of k in a slot
+    static constexpr int SLOTS = YVEC ? 6 : 0;
     static constexpr int BLOCK = BX + WT;                  // floats for a block
-    static constexpr int RING = SLOTS * BATCH * BLOCK;
+    static constexpr int RING = SLOTS * BLOCK;
     static constexpr int FIXED = 1024 + WARPS * OUT + RING * 4 + BAR_BYTES;
     static constexpr int STAGES = (SMEM_MAX - FIXED) / W_STAGE;
     static constexpr int SMEM = FIXED + STAGES * W_STAGE;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             }
         } else if (YVEC && warp == 2) {
             // ------------------------------------------------ scales
-            // copied asynchronously, up to SLOTS batches under way.  Scales of single
+            // copied asynchronously, up to SLOTS blocks' under way.  Scales of single
             // rows or columns are neighbours in memory; rows and columns past the
             // matrix take its last: any valid one will do.
             const uint32_t to = smem_u32(scales) + 4u * (uint32_t)lane;
@@ -680,19 +680,17 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                 const int x0 = min(ty * WT + (int)rank * BX, p.M - 1), y0 = min(tx * WT, p.N - 1);
                 const float *sx = p.SX + (int64_t)(x0 >> p.x_shift) * p.x_mn;
                 const float *sy = p.SY + (int64_t)y0 * p.y_mn;
-                for (int kb = 0; kb < p.nkb; kb += K_::BATCH) {
+                for (int kb = 0; kb < p.nkb; ++kb) {
                     if (!warp_wait(sempty(slot), ph, lim)) { ok = false; break; }
-                    for (int a = 0; a < K_::BATCH && kb + a < p.nkb; ++a) {
-                        const uint32_t at = to + 4u * (uint32_t)((slot * K_::BATCH + a) * K_::BLOCK);
+                    const uint32_t at = to + 4u * (uint32_t)(slot * K_::BLOCK);
 #pragma unroll
-                        for (int j = 0; j < BX / 32; ++j)
-                            cp_async_4(at + 128u * j, sx + (p.x_shift ? 0 : min(32 * j + lane, p.M - 1 - x0)), 4);
+                    for (int j = 0; j < BX / 32; ++j)
+                        cp_async_4(at + 128u * j, sx + (p.x_shift ? 0 : min(32 * j + lane, p.M - 1 - x0)), 4);
 #pragma unroll
-                        for (int j = 0; j < WT / 32; ++j)
-                            cp_async_4(at + 4u * BX + 128u * j, sy + min(32 * j + lane, p.N - 1 - y0), 4);
-                        sx += p.x_k;
-                        sy += p.y_k;
-                    }
+                    for (int j = 0; j < WT / 32; ++j)
+                        cp_async_4(at + 4u * BX + 128u * j, sy + min(32 * j + lane, p.N - 1 - y0), 4);
+                    sx += p.x_k;
+                    sy += p.y_k;
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(slot)) : "memory");
                     if (++slot == K_::SLOTS) { slot = 0; ph ^= 1; }
                 }
@@ -750,9 +748,15 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             if (YVEC) tmem_ld_rows_async(at, v);
             else tmem_ld_async(at, v);
         };
-        // waits for the next buffer and starts reading it
+        // waits for the next buffer (and its block's scales) and starts reading it: one
+        // branch for both, with no read under way across it (two waits, the scales'
+        // at the block's start: 192 us, not 167, at 4096 x 4096 x 8192 TN)
         auto next_buffer = [&]() {
-            ok = warp_wait(tfull(b), bph, lim);
+            bool there = mbar_test(tfull(b), bph) && (!YVEC || mbar_test(sfull(slot), sph));
+            if (!there)
+                there = mbar_wait_for(tfull(b), bph, lim, &g_error) &&
+                        (!YVEC || mbar_wait_for(sfull(slot), sph, lim, &g_error));
+            ok = __all_sync(0xffffffffu, there);
             if (ok) {
                 tc_fence_after();
                 read(0, r[0]);
@@ -770,12 +774,8 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             if (!ok) break;
             for (int kb = 0; kb < p.nkb; ++kb) {
                 float2 s2[YVEC ? 4 : 1];
-                const float *sc = scales + (slot * BATCH + kb % BATCH) * K_::BLOCK;
+                const float *sc = scales + slot * K_::BLOCK;
                 if (YVEC) {
-                    if (kb % BATCH == 0) {
-                        ok = warp_wait(sfull(slot), sph, lim);
-                        if (!ok) break;
-                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float s = sc[q * 32 + 8 * i + lane / 4];
@@ -810,6 +810,10 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                         __syncwarp();
                         if (lane == 0) remote_arrive_relaxed(lead_tempty0 + 8u * b);
                         if (++b == 2) { b = 0; bph ^= 1; }
+                        if (YVEC) {            // (its scales are in registers)
+                            if (lane == 0) mbar_arrive(sempty(slot));
+                            if (++slot == K_::SLOTS) { slot = 0; sph ^= 1; }
+                        }
                         if (kb + 1 < p.nkb) next_buffer();
                     }
                     if (YVEC) {
@@ -831,11 +835,6 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                             a = __ffma2_rn(t, s2[0], a);
                         }
                     }
-                }
-                if (YVEC && (kb % BATCH == BATCH - 1 || kb + 1 == p.nkb)) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sempty(slot));
-                    if (++slot == K_::SLOTS) { slot = 0; sph ^= 1; }
                 }
                 if (!ok) break;
             }

@@ -21,7 +21,7 @@ struct Fp8Plan {
 //   32        4.9    0.20     1.4        0.24
 //   64        6.1    0.24     2.0        0.32
 //   128       8.4    0.375    3.0        0.53
-//   256 x 256 4.0    0.42     1.1        0.71
+//   256 x 256 4.0    0.42     1.1        0.65
 //
 // A cluster of k CTAs takes 1/k of the blocks and 1.5 us to add; clusters have to be
 // resident at once (more than ~136 CTAs in clusters take two waves and more: 512 x
@@ -30,14 +30,15 @@ struct Fp8Plan {
 // 64 rows 8.0 / 8.3, 256 x 256 8.5 / 9.0, 16 rows 12.4 / 12.4; 128 x 4096 x 4096 32 rows
 // 11.3 / 11.4, 128 rows in clusters of 4 12.9 / 14.7; 100 x 16384 x 8192 128 rows 32.4 / 34.5,
 // 32 rows 61 / 60; 300 x 300 x 8192 64 rows in clusters of 8 9.5 / 9.0; 2048 x 1024 x 4096
-// 256 x 256 18.5 / 18.5, 128 rows 20.4 / 21.2.
+// 256 x 256 18.5 / 18.5, 128 rows 20.4 / 21.2; the same with a scale for each row of B
+// 256 x 256 25.9 / 25.7, 128 rows 25.4 / 21.4.
 inline Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int sms) {
     constexpr int kClusterCtas = 136;
     const int64_t nkb = (K + 127) / 128;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     Fp8Plan best;
     const bool vec = b_group == 1;
-    const double block = vec ? 0.71 : 0.42;
+    const double block = vec ? 0.65 : 0.42;
     double best_us = M > 128 && N > 128
                          ? 4.0 + (double)ceil_div(ceil_div(M, 256) * ceil_div(N, 256), std::max(sms / 2, 1)) * (block * (double)nkb + 1.1)
                          : 1e30;
