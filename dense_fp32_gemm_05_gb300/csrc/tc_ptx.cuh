@@ -270,20 +270,6 @@ __device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uin
                    "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7])
                  : "r"(taddr), "r"(taddr + 1 * step) : "memory");
 }
-__device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uint32_t (&r)[3][8]) {
-    asm volatile("{\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;\n\t}"
-                 : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]),
-                   "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]),
-                   "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]),
-                   "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]),
-                   "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[2][2]), "=r"(r[2][3]),
-                   "=r"(r[2][4]), "=r"(r[2][5]), "=r"(r[2][6]), "=r"(r[2][7])
-                 : "r"(taddr), "r"(taddr + 1 * step), "r"(taddr + 2 * step) : "memory");
-}
 __device__ __forceinline__ void tmem_ld_parts(uint32_t taddr, uint32_t step, uint32_t (&r)[4][8]) {
     asm volatile("{\n\t"
                  "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"

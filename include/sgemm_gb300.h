@@ -515,7 +515,7 @@ int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int num_sms, in
  * weights of the chosen experts read once.  Weights never leave 8 bits:
  * activations are split into E4M3 parts that add up to the activation (bf16:
  * 2 parts, exact to 2^-21 of the largest of 128; fp32: 4 parts, 2^-20 of each value;
- * h: 4 parts for fp32 y, 3 for bf16 y, 2^-15 of each value), so results have the
+ * h: 4 parts, 2^-20 of each value), so results have the
  * accuracy of y's type.  Every sum is in fp32, in a
  * fixed order.  Device workspace as sgemm's.  The kernel's CTAs wait for one
  * another (cooperative launch, bounded waits): SGEMM_ERR_CUDA if the device

@@ -1,0 +1,33 @@
+"""How near sgemm_moe's results are to the 64-bit ones, beyond the worst-case bounds
+of test_gpu_moe.py: those leave room for a part too few."""
+import numpy as np
+import pytest
+
+import dense_fp32_gemm_05_gb300 as sg
+from tests import fp8_plain as fp
+from tests.test_gpu_moe import Layer, _x
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,D,F,E,topk", [(16, 2048, 512, 4, 2), (4, 4096, 256, 6, 3), (40, 1000, 300, 2, 1)])
+def test_bf16_results_are_rounded_once(T, D, F, E, topk):
+    """Nearly every bf16 output is the 64-bit result rounded.
+
+    A bf16 step is 2^-8 .. 2^-7 of a value, so an error of r of it turns the rounding with
+    probability r / 2^-7.5.  h is held to 2^-19 of each value or better and the sums are in fp32,
+    so r is about 2^-20 where terms do not cancel: one output in 2^12.5.  16 times that are
+    allowed for sums that cancel.  (One 8-bit part less gives 32 times the rate.)"""
+    import torch
+    layer = Layer(D, F, E, seed=T)
+    x = _x(T, D, "bfloat16")
+    logits = torch.randn((T, E), generator=torch.Generator().manual_seed(1)).cuda()
+    y = layer.run(x, topk, True, logits=logits)[0]
+    assert sg.sgemm_device_error(torch.cuda.current_stream()) == 0
+    want, _, _, _, _ = fp.moe(x.double().cpu().numpy(), None, layer.val["gate"], layer.val["up"], layer.val["down"],
+                              topk, True, logits=logits.double().cpu().numpy())
+    # (the step to bf16 in one rounding: torch's conversion from float64 goes through fp32)
+    step = np.exp2(np.floor(np.log2(np.abs(want))) - 7)
+    rounded = np.rint(want / step) * step
+    share = np.mean(y.double().cpu().numpy() != rounded)
+    assert share <= 2.0 ** -8.5, share
