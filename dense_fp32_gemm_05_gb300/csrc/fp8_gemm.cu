@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int a = 0; a < AHEAD; ++a) {
                     if (kb + a >= kb1) break;
-                    if (!mbar_wait_for(sempty(slot), ph, lim, &g_error)) { ok = false; break; }
+                    if (!warp_wait(sempty(slot), ph, lim)) { ok = false; break; }
 #pragma unroll
                     for (int j = 0; j < J; ++j)
                         if (32 * j + lane < BY) scales[slot * BY + 32 * j + lane] = t[a][j];

@@ -1,0 +1,45 @@
+"""The 8-bit product's bounded waits, on every kind of tile: with a limit of 1 ns a role
+gives up at its first wait for anything that is not there yet.  The call still ends, says
+so, and leaves nothing behind: the next call gives the right result."""
+import pytest
+
+import dense_fp32_gemm_05_gb300 as sg
+
+pytestmark = pytest.mark.gpu
+
+NARROW = [  # M, N, K, groups of B, tile rows, CTAs in a cluster
+    (16, 2000, 4000, 128, 16, 8), (400, 1500, 200, 128, 16, 1), (300, 130, 3000, 128, 32, 4),
+    (70, 10000, 100, 128, 32, 1), (300, 130, 8000, 128, 64, 8), (100, 6000, 100, 128, 64, 1),
+    (673, 818, 9611, 128, 128, 2), (104, 10016, 411, 128, 128, 1),
+    (300, 130, 2000, 1, 16, 2), (127, 10000, 100, 1, 32, 1), (400, 300, 4000, 1, 64, 4), (117, 10621, 393, 1, 128, 1)]
+
+
+def _run(M, N, K, group):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    qx, sx = sg.fp8_quantize(torch.randn((M, K), generator=g, device="cuda"))
+    qw, sw = sg.fp8_quantize(torch.randn((N, K), generator=g, device="cuda"), (group, 128))
+    C = torch.empty((M, N), device="cuda")
+    call = lambda: sg.fp8_gemm(qx, sx, qw, sw, C, b_group=group)  # noqa: E731
+    good = call().clone()
+    stream = torch.cuda.current_stream()
+    assert sg.sgemm_device_error(stream) == 0
+    try:
+        assert sg.sgemm_set_wait_limit(1) == 0
+        for _ in range(3):
+            call()
+            assert sg.sgemm_device_error(stream) == sg.SGEMM_ERR_TIMEOUT
+    finally:
+        sg.sgemm_set_wait_limit(0)
+    for _ in range(2):
+        C.fill_(float("nan"))
+        call()
+        assert sg.sgemm_device_error(stream) == 0
+        assert torch.equal(C, good)
+
+
+@pytest.mark.parametrize("M,N,K,group,tile_m,ksplit", NARROW)
+def test_narrow_tiles(M, N, K, group, tile_m, ksplit):
+    plan = {"tile_m": tile_m, "tile_n": 128, "ksplit": ksplit}
+    assert sg.sgemm_fp8_plan(M, N, K, group) == (0, plan)
+    _run(M, N, K, group)
