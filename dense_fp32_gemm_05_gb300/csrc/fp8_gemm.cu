@@ -130,6 +130,9 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ float load_cluster(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -565,6 +568,8 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
     float *scales = staging + K_::WARPS * K_::OUT / 4;
     uint64_t *bars = reinterpret_cast<uint64_t *>(scales + K_::RING);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S + 4 + 2 * K_::SLOTS);
+    uint32_t *counts = tmem_slot + 1;              // stages filled by either CTA, blocks the leader multiplied
+    static_assert((2 * S + 4 + 2 * K_::SLOTS) * 8 + 16 <= BAR_BYTES, "barriers");
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
@@ -578,6 +583,12 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
     const int group = (int)blockIdx.x >> 1, groups = (int)gridDim.x >> 1;
     const int units = p.tiles_x * p.tiles_y;
     const uint64_t lim = p.wait_ns;
+    auto publish = [&](int which, int n) {         // to both CTAs
+        if (lane == 0) {
+            counts[which] = (uint32_t)n;
+            store_cluster(peer_addr(smem_u32(counts + which), rank ^ 1u), (uint32_t)n);
+        }
+    };
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < S; ++s) {
@@ -630,12 +641,7 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                         if (++s == S) { s = 0; ph ^= 1; }
                     }
                 }
-                // copies in flight land (both CTAs', counted here) before shared memory goes
-                for (int i = 0; rank == 0 && i < min(filled, S); ++i) {
-                    if (s == 0) { s = S; ph ^= 1; }
-                    --s;
-                    mbar_wait_for(full(s), ph ^ 1u, kDrainNs, &g_error);
-                }
+                publish((int)rank, filled);
             }
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issuer (the leader's)
@@ -665,6 +671,7 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                 }
                 if (issued > 0)                    // MMAs retire before tensor memory is freed
                     mbar_wait_for(tfull((issued - 1) & 1), (uint32_t)((issued - 1) >> 1) & 1u, kDrainNs, &g_error);
+                publish(2, issued);
             }
         } else if (YVEC && warp == 2) {
             // ------------------------------------------------ scales
@@ -923,6 +930,35 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
 
     tc_fence_before();
     cluster_sync_all();                            // no CTA leaves while its peer may still signal it
+    const int f0 = (int)counts[0], f1 = (int)counts[1], multiplied = (int)counts[2];
+    if (f0 != multiplied || f1 != multiplied) {
+        // A role gave up, and stages were filled that no MMA waited for.  A stage is
+        // complete with both CTAs' copies (counted on the leader's barrier): the CTA that
+        // filled fewer fills the missing ones, which are free, since the other was let
+        // into them; then the leader waits for what no MMA did.  Commits that reach both
+        // CTAs have done so.
+        if (warp == 0) {
+            const int most = max(f0, f1);
+            for (int i = rank == 0 ? f0 : f1; i < most; ++i) {
+                const uint32_t x = smem0 + (uint32_t)(i % S * W_STAGE);
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect_tx(full(i % S), 2 * W_STAGE);
+                    tma_load_2d_pair(x, &tm_x, leader_addr(full(i % S)), 0, 0);
+                    tma_load_2d_pair(x + X_BYTES, &tm_y, leader_addr(full(i % S)), 0, 0);
+                }
+                __syncwarp();
+            }
+            for (int i = max(most - S, 0); rank == 0 && i < most; ++i)
+                mbar_wait_for(full(i % S), (uint32_t)(i / S) & 1u, kDrainNs, &g_error);
+            if (rank == 1 && multiplied > 0) {
+                const int last = multiplied - 1;
+                mbar_wait_for(empty(last % S), (uint32_t)(last / S) & 1u, kDrainNs, &g_error);
+                mbar_wait_for(tfull(last & 1), (uint32_t)(last >> 1) & 1u, kDrainNs, &g_error);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_free<true>(tmem, 512);

@@ -14,13 +14,16 @@ NARROW = [  # M, N, K, groups of B, tile rows, CTAs in a cluster
     (300, 130, 2000, 1, 16, 2), (127, 10000, 100, 1, 32, 1), (400, 300, 4000, 1, 64, 4), (117, 10621, 393, 1, 128, 1)]
 
 
-def _run(M, N, K, group):
+def _run(M, N, K, group, layout="NT"):
     import torch
     g = torch.Generator(device="cuda").manual_seed(M + N + K)
-    qx, sx = sg.fp8_quantize(torch.randn((M, K), generator=g, device="cuda"))
-    qw, sw = sg.fp8_quantize(torch.randn((N, K), generator=g, device="cuda"), (group, 128))
+    ta, tb = layout
+    shape = lambda n, along: (n, K) if along else (K, n)  # noqa: E731
+    group_of = lambda n, along: (128, 128) if n == 128 else (1, 128) if along else (128, 1)  # noqa: E731
+    qx, sx = sg.fp8_quantize(torch.randn(shape(M, ta == "N"), generator=g, device="cuda"), group_of(1, ta == "N"))
+    qw, sw = sg.fp8_quantize(torch.randn(shape(N, tb == "T"), generator=g, device="cuda"), group_of(group, tb == "T"))
     C = torch.empty((M, N), device="cuda")
-    call = lambda: sg.fp8_gemm(qx, sx, qw, sw, C, b_group=group)  # noqa: E731
+    call = lambda: sg.fp8_gemm(qx, sx, qw, sw, C, ta, tb, b_group=group)  # noqa: E731
     good = call().clone()
     stream = torch.cuda.current_stream()
     assert sg.sgemm_device_error(stream) == 0
@@ -43,3 +46,16 @@ def test_narrow_tiles(M, N, K, group, tile_m, ksplit):
     plan = {"tile_m": tile_m, "tile_n": 128, "ksplit": ksplit}
     assert sg.sgemm_fp8_plan(M, N, K, group) == (0, plan)
     _run(M, N, K, group)
+
+
+WIDE = [  # M, N, K, layout, groups of B
+    (400, 1500, 100, "NT", 128), (2000, 1900, 2000, "NT", 128), (2500, 2300, 700, "NN", 128),
+    (2000, 1900, 2000, "TN", 1), (3000, 2300, 700, "TN", 1), (2000, 300, 100, "NT", 1)]
+
+
+@pytest.mark.parametrize("M,N,K,layout,group", WIDE)
+def test_wide_tiles(M, N, K, layout, group):
+    """Tiles on pairs of SMs: what either has under way when a role gives up lands before they leave."""
+    plan = {"tile_m": 256, "tile_n": 256, "ksplit": 1}
+    assert sg.sgemm_fp8_plan(M, N, K, group) == (0, plan)
+    _run(M, N, K, group, layout)
