@@ -314,7 +314,8 @@ _FLOATS, _CODES, _SCALES = (TYPE_F32, TYPE_BF16), (TYPE_E4M3, TYPE_E5M2), (TYPE_
 
 def _matrix(name, t, types, device=None):
     """(address, type, leading dimension, rows, columns) of a 2-D row-major CUDA
-    tensor on `device` (an index).  Small calls take as long as this takes."""
+    tensor on `device` (an index).  Rows may not overlap: one that is broadcast over
+    others (stride 0) is refused.  Small calls take as long as this takes."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
@@ -325,7 +326,12 @@ def _matrix(name, t, types, device=None):
                          "stride along its last dimension")
     if device is not None and t.get_device() != device:
         raise ValueError("the operands must be on one device")
-    return t.data_ptr(), code, (ld if rows > 1 and ld > cols else cols or 1), rows, cols
+    if rows <= 1:
+        ld = cols                    # (a single row's stride means nothing)
+    elif ld < cols:
+        raise ValueError(f"{name}'s rows overlap (strides {(ld, unit)}, {cols} columns): give it "
+                         "contiguous")
+    return t.data_ptr(), code, ld or 1, rows, cols
 
 
 _raw_stream = None
