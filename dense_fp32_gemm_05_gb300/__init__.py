@@ -348,6 +348,18 @@ def _current_stream(device):
     return _raw_stream(device)
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a call's result: of the stream that the call runs on, so that torch gives
+    it no memory that work on another stream still uses."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, device=device, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=device, dtype=dtype)
+
+
 def sgemm_fp8_quantize(rows, cols, X, x_type, ldx, group_rows, group_cols, Q, q_type, ldq, S, lds,
                        stream=None) -> int:
     """Codes Q and scales S of the rows x cols matrix X; device addresses (int)."""
@@ -362,15 +374,16 @@ def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
     Codes are of ``dtype`` (torch.float8_e4m3fn by default, or float8_e5m2);
     scales are float32, of shape (ceil(cols / 128), rows), (ceil(rows / 128),
     cols) or (ceil(rows / 128), ceil(cols / 128)).  ``Q`` and ``S`` take
-    buffers to write into.  Asynchronous on ``stream`` (default: torch's current
-    stream on X's device); raises SgemmError on any non-zero status.
+    buffers to write into; new ones belong to the stream of the call.  Asynchronous
+    on ``stream`` (default: torch's current stream on X's device); raises SgemmError
+    on any non-zero status.
     """
     device = X.get_device()
     px, tx, ldx, rows, cols = _matrix("X", X, _FLOATS)
     gr, gc = group
     if Q is None:
         import torch
-        Q = torch.empty((rows, cols), device=X.device, dtype=dtype or torch.float8_e4m3fn)
+        Q = _new((rows, cols), dtype or torch.float8_e4m3fn, X.device, stream)
     elif dtype is not None and dtype != Q.dtype:
         raise ValueError("Q is not of the given dtype")
     pq, tq, ldq, q_rows, q_cols = _matrix("Q", Q, _CODES, device)
@@ -378,7 +391,7 @@ def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
                       ((rows + 127) // 128, cols if gc == 1 else (cols + 127) // 128))
     if S is None:
         import torch
-        S = torch.empty((s_rows, s_cols), device=X.device, dtype=torch.float32)
+        S = _new((s_rows, s_cols), torch.float32, X.device, stream)
     ps, _, lds, have_rows, have_cols = _matrix("S", S, _SCALES, device)
     if q_rows != rows or q_cols != cols or have_rows != s_rows or have_cols != s_cols:
         raise ValueError(f"Q must have X's shape and S the shape ({s_rows}, {s_cols})")
@@ -480,9 +493,9 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     is no multiple of 16).  Each token takes its ``topk`` experts of the largest
     logits with their softmax weights (``renormalize``: divided by their sum);
     an expert is down (silu(gate x) * (up x)).  y, logits, indices (int32) and
-    weights take buffers to write into.  Asynchronous on ``stream`` (default:
-    torch's current stream on x's device); raises SgemmError on any non-zero
-    status.
+    weights take buffers to write into; new ones belong to the stream of the call.
+    Asynchronous on ``stream`` (default: torch's current stream on x's device);
+    raises SgemmError on any non-zero status.
     """
     import torch
 
@@ -501,13 +514,13 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     if router is None and logits is None:
         raise ValueError("give router or logits")
     if logits is None:
-        logits = torch.empty((T, E), device=x.device, dtype=f32)
+        logits = _new((T, E), f32, x.device, stream)
     if y is None:
-        y = torch.empty((T, D), device=x.device, dtype=x.dtype)
+        y = _new((T, D), x.dtype, x.device, stream)
     if indices is None:
-        indices = torch.empty(chosen, device=x.device, dtype=i32)
+        indices = _new(chosen, i32, x.device, stream)
     if weights is None:
-        weights = torch.empty(chosen, device=x.device, dtype=f32)
+        weights = _new(chosen, f32, x.device, stream)
     py, y_type, ldy, y_rows, y_cols = _matrix("y", y, _FLOATS, device)
     if y_type != x_type or y_rows != T or y_cols != D:
         raise ValueError("y must have x's shape and dtype")
