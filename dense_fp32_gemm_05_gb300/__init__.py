@@ -348,6 +348,19 @@ def _current_stream(device):
     return _raw_stream(device)
 
 
+_raw_device = None
+
+
+def _check_device(device):
+    """The library launches on the current device: tensors of another are refused."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if _raw_device() != device:
+        raise ValueError(f"the operands are on device {device}, which is not the current one")
+
+
 def _new(shape, dtype, device, stream):
     """A tensor for a call's result: of the stream that the call runs on, so that torch gives
     it no memory that work on another stream still uses."""
@@ -374,12 +387,13 @@ def fp8_quantize(X, group=(1, 128), dtype=None, Q=None, S=None, stream=None):
     Codes are of ``dtype`` (torch.float8_e4m3fn by default, or float8_e5m2);
     scales are float32, of shape (ceil(cols / 128), rows), (ceil(rows / 128),
     cols) or (ceil(rows / 128), ceil(cols / 128)).  ``Q`` and ``S`` take
-    buffers to write into; new ones belong to the stream of the call.  Asynchronous
-    on ``stream`` (default: torch's current stream on X's device); raises SgemmError
-    on any non-zero status.
+    buffers to write into; new ones belong to the stream of the call.  The tensors
+    are on the current device.  Asynchronous on ``stream`` (default: torch's current
+    stream); raises SgemmError on any non-zero status.
     """
     device = X.get_device()
     px, tx, ldx, rows, cols = _matrix("X", X, _FLOATS)
+    _check_device(device)
     gr, gc = group
     if Q is None:
         import torch
@@ -426,13 +440,14 @@ def fp8_gemm(A, SA, B, SB, C, transA="N", transB="T", alpha=1.0, beta=0.0, a_gro
     op(A) and 128 of the sum (groups of 1 x 128 for transA 'N', 128 x 1 for 'T');
     128: for each 128 x 128 block.  ``b_group`` likewise.  A linear layer's forward
     product is the default layout, x (1 x 128) times W^T (128 x 128 blocks).
-    Asynchronous on ``stream`` (default: torch's current stream on C's device);
-    raises SgemmError on any non-zero status.
+    The tensors are on the current device.  Asynchronous on ``stream`` (default:
+    torch's current stream); raises SgemmError on any non-zero status.
     """
     device = C.get_device()
     pa, a_type, lda, a_rows, a_cols = _matrix("A", A, _CODES, device)
     pb, b_type, ldb, b_rows, b_cols = _matrix("B", B, _CODES, device)
     pc, c_type, ldc, M, N = _matrix("C", C, _FLOATS)
+    _check_device(device)
     psa, _, ldsa, sa_rows, sa_cols = _matrix("SA", SA, _SCALES, device)
     psb, _, ldsb, sb_rows, sb_cols = _matrix("SB", SB, _SCALES, device)
     a_trans, b_trans = transA in "TtCc", transB in "TtCc"
@@ -494,14 +509,15 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     logits with their softmax weights (``renormalize``: divided by their sum);
     an expert is down (silu(gate x) * (up x)).  y, logits, indices (int32) and
     weights take buffers to write into; new ones belong to the stream of the call.
-    Asynchronous on ``stream`` (default: torch's current stream on x's device);
-    raises SgemmError on any non-zero status.
+    The tensors are on the current device.  Asynchronous on ``stream`` (default:
+    torch's current stream); raises SgemmError on any non-zero status.
     """
     import torch
 
     f32, i32 = torch.float32, torch.int32
     device = x.get_device()
     px, x_type, ldx, T, D = _matrix("x", x, _FLOATS)
+    _check_device(device)
     E, F, _ = gate.shape
     inner, outer = (E, F, D), (E, D, F)
     pg, ld_in, stride_in = _experts("gate", gate, inner, device)

@@ -39,6 +39,7 @@ def calls(monkeypatch):
 
     monkeypatch.setattr(sg, "load", lambda: Library())
     monkeypatch.setattr(sg, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(sg, "_raw_device", lambda: 0, raising=False)
     return made
 
 
@@ -114,3 +115,13 @@ def test_leading_dimensions(calls):
     _product(A=_codes(16, 512)[:, 128:384], C=_f32(16, 41)[:, :40])
     args = calls.pop()[1]
     assert args[8] == 512 and args[-2] == 41
+
+
+@pytest.mark.parametrize("run", [_quantize, _product, _moe])
+def test_tensors_of_another_device_than_the_current_one_are_refused(calls, run, monkeypatch):
+    run()
+    assert len(calls) == 1
+    monkeypatch.setattr(sg, "_raw_device", lambda: 1, raising=False)
+    with pytest.raises(ValueError, match="device"):
+        run()
+    assert len(calls) == 1
