@@ -1098,10 +1098,8 @@ static int run_moe(moe::Params p, int x_type, const void *gate, const void *up, 
     auto up256 = [](size_t b) { return (b + 255) & ~size_t(255); };
     // the barriers keep a workspace of their own: they are zero between calls
     void *sync = nullptr, *ws = nullptr;
-    bool fresh = false;
-    st = workspace(s, 256, &sync, 3, &fresh);
+    st = workspace(s, 256, &sync, 3, true);
     if (st != SGEMM_OK) return st;
-    if (fresh && cudaMemsetAsync(sync, 0, 256, s) != cudaSuccess) return launch_status();
     const size_t b_arr = up256((size_t)arrivals * 4), b_log = up256((size_t)p.slices * T * E * 4),
                  b_xp = up256((size_t)T * fp8::blocks_of(D) * (x_type == SGEMM_TYPE_F32 ? 4 : 2) * moe::BK),
                  b_xs = up256((size_t)T * fp8::blocks_of(D) * 4), b_h = up256((size_t)slots * p.ldh * 4), b_parts = up256((size_t)2 * sms * 2 * nt * moe::ROWS * 4),

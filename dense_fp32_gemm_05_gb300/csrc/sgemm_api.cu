@@ -18,6 +18,7 @@
 #include "plan.h"
 #include "gemv.h"
 #include "tc_gemm.h"
+#include "workspace.h"
 
 namespace sgemm_gb300 {
 
@@ -32,17 +33,18 @@ static std::mutex g_mu;
 static std::map<int, DeviceState> g_dev;
 // per (device, stream, slot) workspace so that concurrent streams never share
 // one; slot 0 is the kernels' scratch, slot 1 the staging buffers of sgemm_host
-struct WsKey {
-    int dev;
-    cudaStream_t stream;
-    int slot;
-    bool operator<(const WsKey &o) const {
-        if (dev != o.dev) return dev < o.dev;
-        if (stream != o.stream) return stream < o.stream;
-        return slot < o.slot;
+struct CudaApi {
+    using Stream = cudaStream_t;
+    static bool done(cudaError_t e) {
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess;
     }
+    bool alloc(void **p, size_t n, Stream s) { return done(cudaMallocAsync(p, n, s)); }
+    void free(void *p, Stream s) { cudaFreeAsync(p, s); }
+    bool zero(void *p, size_t n, Stream s) { return done(cudaMemsetAsync(p, 0, n, s)); }
+    void release(void *p) { cudaFree(p); }
 };
-static std::map<WsKey, std::pair<void *, size_t>> g_ws;
+static Workspaces<CudaApi> g_ws;
 
 static int device_state(DeviceState **out) {
     int dev = 0;
@@ -62,26 +64,11 @@ static int device_state(DeviceState **out) {
 
 // Returns a workspace of at least `bytes` private to (device, stream, slot).
 // It is allocated and, when it must grow, freed in stream order on `stream`.
-int workspace(cudaStream_t stream, size_t bytes, void **out, int which, bool *fresh) {
-    if (fresh) *fresh = false;
+int workspace(cudaStream_t stream, size_t bytes, void **out, int which, bool zeroed) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    auto &slot = g_ws[WsKey{dev, stream, which}];
-    if (slot.second < bytes) {
-        if (slot.first) cudaFreeAsync(slot.first, stream);
-        slot = {nullptr, 0};
-        size_t want = std::max<size_t>(bytes, size_t(1) << 20);
-        void *p = nullptr;
-        if (cudaMallocAsync(&p, want, stream) != cudaSuccess) {
-            cudaGetLastError();
-            return SGEMM_ERR_NOMEM;
-        }
-        slot = {p, want};
-        if (fresh) *fresh = true;
-    }
-    *out = slot.first;
-    return SGEMM_OK;
+    return g_ws.get(dev, stream, which, bytes, zeroed, out);
 }
 
 // ------------------------------------------------------------ timing hook
@@ -543,14 +530,7 @@ extern "C" int sgemm_release_workspace(void) {
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     if (cudaDeviceSynchronize() != cudaSuccess) return SGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    for (auto it = g_ws.begin(); it != g_ws.end();) {
-        if (it->first.dev == dev) {
-            if (it->second.first) cudaFree(it->second.first);
-            it = g_ws.erase(it);
-        } else {
-            ++it;
-        }
-    }
+    g_ws.release(dev);
     return SGEMM_OK;
 }
 

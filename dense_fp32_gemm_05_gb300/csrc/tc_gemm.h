@@ -62,8 +62,8 @@ void timing_mark(cudaStream_t s, bool begin);
 // Library-owned per-(device, stream, slot) workspace, grown on demand.  Slots: 0 a
 // call's scratch, 1 sgemm_host's staging buffers, 2 the thin path's partial sums, 3
 // the mixture-of-experts kernel's grid barriers (zero between calls, so no other's).
-// `fresh`, if given, tells whether this call allocated it.
-int workspace(cudaStream_t stream, size_t bytes, void **out, int which = 0, bool *fresh = nullptr);
+// `zeroed`: of zeros when it is new.
+int workspace(cudaStream_t stream, size_t bytes, void **out, int which = 0, bool zeroed = false);
 
 // The SM count of the current device; SGEMM_ERR_UNSUPPORTED unless it is of
 // compute capability 10.3.
