@@ -43,6 +43,29 @@ struct CudaApi {
     void free(void *p, Stream s) { cudaFreeAsync(p, s); }
     bool zero(void *p, size_t n, Stream s) { return done(cudaMemsetAsync(p, 0, n, s)); }
     void release(void *p) { cudaFree(p); }
+    bool capturing(Stream s) {
+        cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+        return done(cudaStreamIsCapturing(s, &st)) && st != cudaStreamCaptureStatusNone;
+    }
+    // What a thread may not do while it captures, it may in this mode: calls that have
+    // nothing to do with the capture.
+    struct Relaxed {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+        ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    };
+    bool alloc_apart(void **p, size_t n) {
+        const Relaxed relaxed;
+        return done(cudaMalloc(p, n));
+    }
+    bool zero_apart(void *p, size_t n) {
+        const Relaxed relaxed;
+        cudaStream_t own = nullptr;
+        if (!done(cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking))) return false;
+        const bool set = done(cudaMemsetAsync(p, 0, n, own)) && done(cudaStreamSynchronize(own));
+        cudaStreamDestroy(own);
+        return set;
+    }
 };
 static Workspaces<CudaApi> g_ws;
 
@@ -63,7 +86,8 @@ static int device_state(DeviceState **out) {
 }
 
 // Returns a workspace of at least `bytes` private to (device, stream, slot).
-// It is allocated and, when it must grow, freed in stream order on `stream`.
+// It is allocated and, when it must grow, freed in stream order on `stream` (apart from
+// any stream while that is being captured).
 int workspace(cudaStream_t stream, size_t bytes, void **out, int which, bool zeroed) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;

@@ -7,12 +7,22 @@
 //   void free(void *p, Stream)               in stream order
 //   bool zero(void *p, size_t n, Stream)     in stream order
 //   void release(void *p)                    once nothing runs on the device
+//   bool capturing(Stream)                   is the stream being captured into a graph?
+//   bool alloc_apart(void **p, size_t n)     in no stream, no part of any capture
+//   bool zero_apart(void *p, size_t n)       the same; done when it returns
+//
+// While its stream is being captured a workspace is allocated apart: allocated in
+// stream order it would be the graph's, and the table would hand the graph's
+// memory to later calls.  Nor is the one that it replaces freed in stream order
+// then; it is kept until everything is released.
 #pragma once
 
 #include <algorithm>
 #include <cstddef>
 #include <map>
 #include <tuple>
+#include <utility>
+#include <vector>
 
 #include "../../include/sgemm_gb300.h"
 
@@ -30,16 +40,20 @@ public:
     int get(int dev, Stream stream, int slot, size_t bytes, bool zeroed, void **out) {
         Block &b = blocks_[Key{dev, stream, slot}];
         if (b.bytes < bytes) {
-            if (b.p) api_.free(b.p, stream);
+            const bool apart = api_.capturing(stream);
+            if (b.p && (apart || b.apart)) kept_.emplace_back(dev, b.p);
+            else if (b.p) api_.free(b.p, stream);
             b = Block{};
             const size_t want = std::max<size_t>(bytes, size_t(1) << 20);
             void *p = nullptr;
-            if (!api_.alloc(&p, want, stream)) return SGEMM_ERR_NOMEM;
-            if (zeroed && !api_.zero(p, want, stream)) {
-                api_.free(p, stream);            // (kept, the next call would take it as zeroed)
+            if (!(apart ? api_.alloc_apart(&p, want) : api_.alloc(&p, want, stream))) return SGEMM_ERR_NOMEM;
+            if (zeroed && !(apart ? api_.zero_apart(p, want) : api_.zero(p, want, stream))) {
+                // (kept, the next call would take it as zeroed)
+                if (apart) kept_.emplace_back(dev, p);
+                else api_.free(p, stream);
                 return SGEMM_ERR_CUDA;
             }
-            b = Block{p, want};
+            b = Block{p, want, apart};
         }
         *out = b.p;
         return SGEMM_OK;
@@ -55,6 +69,14 @@ public:
                 ++it;
             }
         }
+        for (auto it = kept_.begin(); it != kept_.end();) {
+            if (it->first == dev) {
+                api_.release(it->second);
+                it = kept_.erase(it);
+            } else {
+                ++it;
+            }
+        }
     }
 
     Api &api() { return api_; }
@@ -64,9 +86,11 @@ private:
     struct Block {
         void *p = nullptr;
         size_t bytes = 0;
+        bool apart = false;                      // not allocated in stream order
     };
     Api api_;
     std::map<Key, Block> blocks_;
+    std::vector<std::pair<int, void *>> kept_;   // replaced, but not freed
 };
 
 }  // namespace sgemm_gb300

@@ -33,6 +33,12 @@
  * workspace (per device, grown on demand with cudaMallocAsync on the calling
  * stream, kept until sgemm_release_workspace()).
  *
+ * Stream capture: calls may be captured into a graph, the first on a stream too
+ * (the workspace is then allocated outside the graph).  A captured call uses the
+ * capture stream's workspace at every replay, so a graph may not run at the same
+ * time as another graph captured on that stream, or as calls made on it; and not
+ * after sgemm_release_workspace().
+ *
  * Errors: arguments are checked before anything is launched.  A negative
  * return value -i names the i-th argument (1-based, BLAS style) as invalid:
  * -1 transA, -2 transB, -3 M, -4 N, -5 K, -7 A, -8 lda, -9 B, -10 ldb,
@@ -347,7 +353,8 @@ int sgemm_probe_tf32_rate(int reps, double *mac_per_clock);
  */
 int64_t sgemm_launch_count(void);
 
-/* Free the current device's workspace (synchronises the device). */
+/* Free the current device's workspace (synchronises the device).  Graphs captured
+ * before may not be launched any more. */
 int sgemm_release_workspace(void);
 
 /*
