@@ -14,7 +14,8 @@
 // While its stream is being captured a workspace is allocated apart: allocated in
 // stream order it would be the graph's, and the table would hand the graph's
 // memory to later calls.  Nor is the one that it replaces freed in stream order
-// then; it is kept until everything is released.
+// then.  One that a graph uses stays when a later call needs more: the graph may
+// run again.  Both are kept until everything is released.
 #pragma once
 
 #include <algorithm>
@@ -39,9 +40,9 @@ public:
     // is new.
     int get(int dev, Stream stream, int slot, size_t bytes, bool zeroed, void **out) {
         Block &b = blocks_[Key{dev, stream, slot}];
+        const bool apart = api_.capturing(stream);
         if (b.bytes < bytes) {
-            const bool apart = api_.capturing(stream);
-            if (b.p && (apart || b.apart)) kept_.emplace_back(dev, b.p);
+            if (b.p && (apart || b.graph)) kept_.emplace_back(dev, b.p);
             else if (b.p) api_.free(b.p, stream);
             b = Block{};
             const size_t want = std::max<size_t>(bytes, size_t(1) << 20);
@@ -53,8 +54,9 @@ public:
                 else api_.free(p, stream);
                 return SGEMM_ERR_CUDA;
             }
-            b = Block{p, want, apart};
+            b = Block{p, want};
         }
+        b.graph = b.graph || apart;
         *out = b.p;
         return SGEMM_OK;
     }
@@ -86,7 +88,7 @@ private:
     struct Block {
         void *p = nullptr;
         size_t bytes = 0;
-        bool apart = false;                      // not allocated in stream order
+        bool graph = false;                      // a graph uses it
     };
     Api api_;
     std::map<Key, Block> blocks_;

@@ -90,3 +90,19 @@ def test_a_second_capture_grows_the_workspace_of_plain_calls():
         with torch.cuda.stream(s):
             for c in calls:
                 _right(*c)
+
+
+def test_a_graph_after_larger_calls_on_its_stream():
+    calls = _calls()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for i in (0, 2, 4):
+            _right(*calls[i])
+    graphs = [_capture(calls[i][0], s) for i in (0, 2, 4)]        # their workspaces were there before
+    with torch.cuda.stream(s):
+        for i in (1, 3, 5):                                       # larger ones
+            _right(*calls[i])
+        scribble = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
+    for g, i in zip(graphs, (0, 2, 4)):
+        _right(g.replay, *calls[i][1:])
+    del scribble

@@ -16,7 +16,8 @@ def program(tmp_path_factory):
     return out
 
 
-@pytest.mark.parametrize("what", ["reuse_and_growth", "an_allocation_fails", "zeroing_fails", "a_stream_that_is_captured"])
+@pytest.mark.parametrize("what", ["reuse_and_growth", "an_allocation_fails", "zeroing_fails", "a_stream_that_is_captured",
+                                  "growth_after_a_capture"])
 def test_workspaces(program, what):
     r = subprocess.run([program, what], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout

@@ -137,12 +137,31 @@ static void a_stream_that_is_captured() {
     CHECK(g.live.empty());
 }
 
+static void growth_after_a_capture() {
+    // the memory that a captured call uses outlives a larger call on its stream
+    Workspaces<Fake> w;
+    void *a = nullptr, *b = nullptr, *c = nullptr;
+    CHECK(w.get(0, 1, 0, 100, false, &a) == SGEMM_OK);                    // allocated before the capture
+    g.capturing = true;
+    CHECK(w.get(0, 1, 0, 100, false, &b) == SGEMM_OK && b == a);
+    g.capturing = false;
+    CHECK(w.get(0, 1, 0, 2 << 20, false, &b) == SGEMM_OK && b != a && g.live.count(a));
+    CHECK(w.get(0, 1, 0, 4 << 20, false, &c) == SGEMM_OK && c != b && !g.live.count(b));   // (no graph's)
+    g.capturing = true;
+    CHECK(w.get(0, 1, 0, 8 << 20, false, &b) == SGEMM_OK && g.apart[b]);  // allocated under it
+    g.capturing = false;
+    CHECK(w.get(0, 1, 0, 16 << 20, false, &c) == SGEMM_OK && g.live.count(b) && g.live.count(a));
+    w.release(0);
+    CHECK(g.live.empty());
+}
+
 int main(int, char **argv) {
     const std::string what = argv[1];
     if (what == "reuse_and_growth") reuse_and_growth();
     else if (what == "an_allocation_fails") an_allocation_fails();
     else if (what == "zeroing_fails") zeroing_fails();
     else if (what == "a_stream_that_is_captured") a_stream_that_is_captured();
+    else if (what == "growth_after_a_capture") growth_after_a_capture();
     else return 2;
     return 0;
 }
