@@ -927,7 +927,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int i = PARTS - 2; i >= 0; --i)
                                 t = __ffma2_rn(t, make_float2(1.0f / 32.0f, 1.0f / 32.0f),
                                                make_float2(__uint_as_float(r[i][j]), __uint_as_float(r[i][j + 1])));
-                            const float2 a = __ffma2_rn(t, __fmul2_rn(make_float2(sw, sw), ts), make_float2(acc[i0 + j], acc[i0 + j + 1]));
+                            // (the weights' scale first: times a small token's, a power of two from 2^-126
+                            // up, it could lose bits below the normal numbers that the result has)
+                            const float2 a = __ffma2_rn(__fmul2_rn(t, make_float2(sw, sw)), ts, make_float2(acc[i0 + j], acc[i0 + j + 1]));
                             acc[i0 + j] = a.x;
                             acc[i0 + j + 1] = a.y;
                         }

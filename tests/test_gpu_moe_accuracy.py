@@ -31,3 +31,23 @@ def test_bf16_results_are_rounded_once(T, D, F, E, topk):
     rounded = np.rint(want / step) * step
     share = np.mean(y.double().cpu().numpy() != rounded)
     assert share <= 2.0 ** -8.5, share
+
+
+@pytest.mark.parametrize("exponent,s_down", [(0, 1.0), (-30, 1.0), (-48, 2.0 ** -25), (-54, 2.0 ** -12), (30, 2.0 ** 30)])
+def test_small_and_large_tokens_keep_their_bits(exponent, s_down):
+    """h is of the order of the square of x, so its blocks' powers of two reach 2^-126 while the
+    result is a normal number.  Relative to y's norm: 2^-19 of each h at most, sums in fp32 (2^-23
+    each, some tens of them, at random): below 2^-18, whatever the size."""
+    import torch
+    D, F, E, T = 128, 128, 2, 6
+    layer = Layer(D, F, E, seed=3)
+    s = torch.full((E, 1, 1), 0.0031 * 1.2345678 * s_down, device="cuda")
+    codes = layer.dev["down"].float().double().cpu().numpy()
+    layer.dev["s_down"], layer.val["down"] = s, codes * s.double().cpu().numpy()
+    x = _x(T, D, "float32", seed=2) * 2.0 ** exponent
+    logits = torch.randn((T, E), generator=torch.Generator().manual_seed(1)).cuda()
+    y = layer.run(x, 1, True, logits=logits)[0].double().cpu().numpy()
+    want = fp.moe(x.double().cpu().numpy(), None, layer.val["gate"], layer.val["up"], layer.val["down"], 1, True,
+                  logits=logits.double().cpu().numpy())[0]
+    assert np.abs(want).mean() > 2.0 ** -122
+    assert np.linalg.norm(y - want) <= 2.0 ** -18 * np.linalg.norm(want)
