@@ -13,9 +13,11 @@
 //     [128, 256)) and split into PARTS E4M3 numbers,
 //       x = 2^-e (q_0 + q_1 / 32 + q_2 / 1024 + ...),
 //     q_i the rounding of what the parts before left, times 32^i: each part adds
-//     5 bits.  bf16 takes 2 parts (exact but for values below 2^-14 of the
-//     block's largest, and those to 2^-22 of it), fp32 takes 4 (2^-20 of each
-//     value).  The parts are separate columns of one MMA: it costs the same
+//     5 bits.  E4M3's smallest step is 2^-9, so what is small beside the block's
+//     largest value keeps an absolute error.  bf16 takes 2 parts (exact but for
+//     values below 2^-14 of the block's largest, and those to 2^-22 of it), fp32 and
+//     h take 4 (to the larger of 2^-19 of the value and 2^-32 of the block's largest).
+//     The parts are separate columns of one MMA: it costs the same
 //     (few columns), and the products are exact;
 //   * a block's sums come back from tensor memory, the parts are added and the
 //     block's scales (weights' and token's) applied in fp32 registers;

@@ -519,12 +519,16 @@ int sgemm_fp8_plan(int64_t M, int64_t N, int64_t K, int b_group, int num_sms, in
  *   indices, weights   T x topk int32 and fp32 packed: e_j and w(t,j) (written)
  *
  * One kernel: routing, both expert products and the combination, with the
- * weights of the chosen experts read once.  Weights never leave 8 bits:
- * activations are split into E4M3 parts that add up to the activation (bf16:
- * 2 parts, exact to 2^-21 of the largest of 128; fp32: 4 parts, 2^-20 of each value;
- * h: 4 parts, 2^-20 of each value), so results have the
- * accuracy of y's type.  Every sum is in fp32, in a
- * fixed order.  Device workspace as sgemm's.  The kernel's CTAs wait for one
+ * weights of the chosen experts read once (again for each 8 to 64 tokens of an
+ * expert that has more than twice the average).  Weights never leave 8 bits:
+ * activations are split into E4M3 parts that add up to the activation.  bf16 x: 2
+ * parts, exact, but values below 2^-14 of the largest of their block of 128 to
+ * 2^-22 of that.  fp32 x, and h: 4 parts, each value to the larger of 2^-19 of it
+ * and 2^-32 of the largest of its block.  Every sum is in fp32, in a fixed order.
+ * For values of like size y is as near to the exact result as fp32 arithmetic
+ * comes, to a factor of 2 (6.5e-7 of its norm); beside values 2^13 times (bf16:
+ * 2^14 times) larger that meet weights of zero it keeps fewer bits.
+ * Device workspace as sgemm's.  The kernel's CTAs wait for one
  * another (cooperative launch, bounded waits): SGEMM_ERR_CUDA if the device
  * cannot hold one CTA per SM at once.
  */

@@ -51,3 +51,44 @@ def test_small_and_large_tokens_keep_their_bits(exponent, s_down):
                   logits=logits.double().cpu().numpy())[0]
     assert np.abs(want).mean() > 2.0 ** -122
     assert np.linalg.norm(y - want) <= 2.0 ** -18 * np.linalg.norm(want)
+
+
+def _split_error(v, of_value, of_largest):
+    """The documented error of a row of values held in 8-bit parts."""
+    blocks = np.pad(np.abs(v), ((0, 0), (0, -v.shape[1] % 128))).reshape(len(v), -1, 128)
+    largest = np.repeat(blocks.max(2), 128, axis=1)[:, : v.shape[1]]
+    return np.maximum(np.abs(v) * of_value, largest * of_largest)
+
+
+@pytest.mark.parametrize("dtype,outlier", [("float32", 2.0 ** 18), ("float32", 2.0 ** 24), ("bfloat16", 2.0 ** 12)])
+def test_an_outlier_that_meets_weights_of_zero(dtype, outlier):
+    """One value of the token far above the others, with gate and up codes of 0 where it is: the
+    result hangs on the small values, whose parts' error is relative to the outlier.
+
+    Bound: the parts' documented errors through both products, and (128 + blocks + 16) roundings
+    of 2^-23 of the magnitudes for each sum, 2^-20 of h for its function, one rounding of y."""
+    import torch
+    D, F, E, T = 256, 192, 2, 5
+    layer = Layer(D, F, E, seed=4)
+    x = _x(T, D, dtype, seed=3)
+    x[:, 77] = outlier
+    for name in ("gate", "up"):
+        layer.val[name][:, :, 77] = 0
+        layer.dev[name].view(torch.uint8)[:, :, 77] = 0
+    logits = torch.randn((T, E), generator=torch.Generator().manual_seed(1)).cuda()
+    y = layer.run(x, 1, True, logits=logits)[0].double().cpu().numpy()
+    x, which = x.double().cpu().numpy(), logits.argmax(1).tolist()
+    dx = _split_error(x, 2.0 ** -19 if dtype == "float32" else 0.0, 2.0 ** -32 if dtype == "float32" else 2.0 ** -22)
+    r1, r2 = (128 + D / 128 + 16) * 2.0 ** -23, (128 + F / 128 + 16) * 2.0 ** -23
+    for t, e in enumerate(which):
+        W, U, V = (layer.val[n][e] for n in ("gate", "up", "down"))
+        g, u = W @ x[t], U @ x[t]
+        dg, du = (np.abs(m) @ dx[t] + r1 * (np.abs(m) @ np.abs(x[t])) for m in (W, U))
+        s = g / (1 + np.exp(-g))
+        h = s * u
+        dh = 1.1 * dg * np.abs(u) + np.abs(s) * du + 1.1 * dg * du + 2.0 ** -20 * np.abs(h)
+        dh += _split_error((np.abs(h) + dh)[None], 2.0 ** -19, 2.0 ** -32)[0]
+        want = V @ h
+        tol = np.abs(V) @ dh + r2 * (np.abs(V) @ (np.abs(h) + dh))
+        tol += (2.0 ** -24 if dtype == "float32" else 2.0 ** -8) * (np.abs(want) + tol)
+        assert np.all(np.abs(y[t] - want) <= tol)
