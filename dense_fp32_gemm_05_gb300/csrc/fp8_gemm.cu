@@ -83,7 +83,8 @@ struct Params {
     int64_t x_mn, x_k, y_mn, y_k;          // strides of the scales along N / M (per group) and per block of k
     int x_shift, y_shift;                  // a scale for each 1 << shift rows
     int c_vec;                             // quads of C may be accessed whole
-    int c_tma;                             // wide tiles: 1 stored by TMA, 2 added by TMA, 0 neither
+    int c_tma;                             // wide tiles: columns of C from 0 that TMA writes (0: none)
+    int c_add;                             // it adds them to what is there
     int x_mnmajor, y_mnmajor;              // operand stored across k
     int y_bytes;                           // bytes of Y per stage
     uint32_t idesc;
@@ -854,9 +855,9 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
             for (int c = 0; c < NC; ++c) {
                 if (m0 >= p.M || n0 + c * CH >= p.N) break;
                 const float2 *a = acc + c * CH / 2;
-                if (p.c_tma != 0) {
-                    if (lane == 0) tma_store_read_wait();
-                    __syncwarp();
+                if (lane == 0) tma_store_read_wait();
+                __syncwarp();
+                if (n0 + c * CH < p.c_tma) {
                     uint8_t *row = reinterpret_cast<uint8_t *>(stg);
                     if (YVEC) {
                         // (pairs of columns, of four rows a group)
@@ -891,11 +892,10 @@ __global__ void __launch_bounds__(Wide<YVEC>::THREADS, 1) __cluster_dims__(2, 1,
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        if (p.c_tma == 1) tma_store_2d<false>(&tm_c, smem_u32(stg), n0 + c * CH, m0);
+                        if (!p.c_add) tma_store_2d<false>(&tm_c, smem_u32(stg), n0 + c * CH, m0);
                         else tma_store_2d<true>(&tm_c, smem_u32(stg), n0 + c * CH, m0);
                     }
                 } else {
-                    __syncwarp();
                     if (YVEC) {
 #pragma unroll
                         for (int i = 0; i < CH / 2; ++i) {
@@ -1093,10 +1093,13 @@ static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, fp8g::Param
     using K_ = fp8g::Wide<YVEC>;
     static uint64_t done = 0;
     // C in boxes of 32 rows x CH columns, where TMA can write it: rows on 16 bytes,
-    // and nothing to read, or C += sums in fp32 (one rounding, as the epilogue's)
+    // and nothing to read, or C += sums in fp32 (one rounding, as the epilogue's).  A
+    // store writes all 16 bytes that hold C's last column (measured on GB300), so the last
+    // box goes the other way where C ends inside them.
     const int esize = p.c_bf16 ? 2 : 4;
     CUtensorMap mc = mx;
     p.c_tma = 0;
+    p.c_add = p.beta != 0.0f;
     if (aligned16(p.C) && p.ldc * esize % 16 == 0 &&
         (p.beta == 0.0f || (p.beta == 1.0f && p.alpha == 1.0f && !p.c_bf16))) {
         EncodeTiledFn enc = encode_fn();
@@ -1111,7 +1114,7 @@ static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, fp8g::Param
                        : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                      : CU_TENSOR_MAP_SWIZZLE_32B,
                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
-            p.c_tma = p.beta == 0.0f ? 1 : 2;
+            p.c_tma = (int64_t)p.N * esize % 16 == 0 ? p.N : p.N / K_::CH * K_::CH;
     }
     return launch_kernel(fp8g::fp8_wide_kernel<YVEC>, done, grid, K_::THREADS, K_::SMEM, 1, s, dep, mx, my, mc, p);
 }
