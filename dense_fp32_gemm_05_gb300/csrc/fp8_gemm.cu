@@ -1093,7 +1093,8 @@ static int launch_wide(const CUtensorMap &mx, const CUtensorMap &my, fp8g::Param
     using K_ = fp8g::Wide<YVEC>;
     static uint64_t done = 0;
     // C in boxes of 32 rows x CH columns, where TMA can write it: rows on 16 bytes,
-    // and nothing to read, or C += sums in fp32 (one rounding, as the epilogue's).  A
+    // and nothing to read, or C += sums in fp32 (one rounding, as the epilogue's;
+    // subnormal numbers are kept, measured on GB300).  A
     // store writes all 16 bytes that hold C's last column (measured on GB300), so the last
     // box goes the other way where C ends inside them.
     const int esize = p.c_bf16 ? 2 : 4;
