@@ -1,4 +1,4 @@
-"""The 8-bit product's bounded waits, on every kind of tile: with a limit of 1 ns a role
+"""The 8-bit kernels' bounded waits, on every kind of tile: with a limit of 1 ns a role
 gives up at its first wait for anything that is not there yet.  The call still ends, says
 so, and leaves nothing behind: the next call gives the right result."""
 import pytest
@@ -59,3 +59,25 @@ def test_wide_tiles(M, N, K, layout, group):
     plan = {"tile_m": 256, "tile_n": 256, "ksplit": 1}
     assert sg.sgemm_fp8_plan(M, N, K, group) == (0, plan)
     _run(M, N, K, group, layout)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,E,topk", [(1, 8, 2), (12, 8, 2), (40, 8, 4), (100, 5, 3)])
+def test_layer(dtype, T, E, topk):
+    """The layer with 8, 16, 32 and 64 columns for an expert."""
+    import torch
+    from tests.test_gpu_moe import Layer, _x
+    layer = Layer(640, 320, E, seed=T)
+    x, stream = _x(T, 640, dtype), torch.cuda.current_stream()
+    good = layer.run(x, topk, True)[0].clone()
+    assert sg.sgemm_device_error(stream) == 0
+    try:
+        assert sg.sgemm_set_wait_limit(1) == 0
+        for _ in range(3):
+            layer.run(x, topk, True)
+            assert sg.sgemm_device_error(stream) == sg.SGEMM_ERR_TIMEOUT
+    finally:
+        sg.sgemm_set_wait_limit(0)
+    for _ in range(2):
+        assert torch.equal(layer.run(x, topk, True)[0], good)
+        assert sg.sgemm_device_error(stream) == 0
