@@ -33,9 +33,9 @@
 // Few tiles: a cluster of KS CTAs shares a tile's blocks in contiguous ranges
 // and adds the partial sums through distributed shared memory in ascending
 // order, each CTA its share of the columns: no workspace, no atomics.
-// Decode is bound by the weights' stream: 16 x 16384 x 8192 25.1 us, 5.4 TB/s over the
-// call (0.79 of the measured copy), of which ~4 us are the launch, the first loads and
-// the last tile; small ones by latency (256^3 4.3 us).
+// Decode is bound by the weights' stream: 16 x 16384 x 8192 25.1 us on the GPU alone, 5.4
+// TB/s (0.81 of the measured copy), 26.7 us among other calls, of which ~4 us are the
+// launch, the first loads and the last tile; small ones by latency (256^3 4.3 us).
 //
 // Every wait is bounded, as in the tensor-core GEMM: on expiry the device error
 // word is set, the role stops, copies and MMAs in flight are waited for (again
@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // reads: 820 us at 8192^3, on single SMs.)  128 accumulators per promoting thread
 // need more registers than an equal share: the first warpgroup hands its over
 // (setmaxnreg).
-// 8192^3 NT 392 us, 2.80 PFLOP/s (0.74 of twice the measured bf16 rate).  What bounds
+// 8192^3 NT 392 us in short runs, 2.80 PFLOP/s (0.73 of twice the measured bf16 rate),
+// 435 us under the power cap.  What bounds
 // it is the turn-round of the two buffers, which fill tensor memory: release to the
 // MMA's start 230 clocks, the MMAs (512) and their commit's arrival 900, reading 580,
 // for two blocks; the MMAs fed by TMA alone would take 671 a block, not 857.

@@ -466,8 +466,9 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int x_type, in
  * its gradients dx = dy W, dW = dy^T x are the layouts NT, NN and TN.
  *
  * Arithmetic: the products of codes are exact and are added in fp32 on the
- * tensor cores within a block of 128; sA * sB is rounded once (with b_group 1
- * instead: the block's sum times sA, then a fused multiply-add by sB);
+ * tensor cores within a block of 128; sA * sB is rounded once, to fewer bits below
+ * 2^-126 (with b_group 1 instead: the block's sum times sA, then a fused
+ * multiply-add by sB);
  * blocks are added in fp32 in ascending order (or, K split over CTAs of a
  * cluster, in contiguous ranges added in ascending order: no atomics, the
  * same result every time).  Then alpha * acc (beta == 0: C not read) or
