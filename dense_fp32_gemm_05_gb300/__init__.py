@@ -22,7 +22,8 @@ __all__ = [
     "sgemm_timing_read", "sgemm_launch_count", "sgemm_probe_tf32_rate", "gemm",
     "exported_symbols", "TYPE_F32", "TYPE_BF16", "TYPE_E4M3", "TYPE_E5M2",
     "sgemm_fp8_quantize", "fp8_quantize", "sgemm_fp8", "sgemm_fp8_plan", "fp8_gemm",
-    "sgemm_moe", "moe",
+    "sgemm_moe", "moe", "ACT_SILU", "ACT_GELU", "sgemm_ffn", "ffn", "sgemm_ffn_backward",
+    "ffn_backward", "sgemm_ffn_plan",
 ]
 
 SGEMM_OK = 0
@@ -40,6 +41,8 @@ PATH_TF32 = 3
 PATH_GEMV = 4
 ACT_NONE = 0
 ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
 
 TYPE_F32 = 0
 TYPE_BF16 = 1
@@ -120,6 +123,15 @@ def _declare(lib):
     lib.sgemm_moe.argtypes = [i64, i64, i64, i64, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64,
                               vp, vp, i64, i64, i32, vp, i64, vp, vp, vp]
     lib.sgemm_moe.restype = i32
+    lib.sgemm_ffn.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp, vp, i64, vp, vp, i64,
+                              vp, i64, vp, i64, vp]
+    lib.sgemm_ffn.restype = i32
+    lib.sgemm_ffn_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp, vp,
+                                       i64, vp, vp, i64, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, i64, vp,
+                                       i64, vp]
+    lib.sgemm_ffn_backward.restype = i32
+    lib.sgemm_ffn_plan.argtypes = [i64, i64, i64, i32, i32, ip, ip]
+    lib.sgemm_ffn_plan.restype = i32
 
 
 def load():
@@ -147,7 +159,8 @@ def exported_symbols(lib=None):
             "sgemm_set_wait_limit", "sgemm_release_workspace", "sgemm_version",
             "sgemm_ffma_static_scratch", "sgemm_timing_enable", "sgemm_timing_read",
             "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize",
-            "sgemm_fp8", "sgemm_fp8_plan", "sgemm_moe"]
+            "sgemm_fp8", "sgemm_fp8_plan", "sgemm_moe", "sgemm_ffn", "sgemm_ffn_backward",
+            "sgemm_ffn_plan"]
 
 
 def _b(t: str) -> bytes:
@@ -551,3 +564,162 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_moe")
     return y, logits, indices, weights
+
+
+def sgemm_ffn(T, D, F, x, ldx, gate, up, ld_in, down, ld_down, activation, kept_type, g, u, ld_kept, sg, su,
+              ld_scales, h, ldh, y, ldy, stream=None) -> int:
+    """A gated feed-forward block's forward pass; device addresses (int), 0 = none."""
+    return load().sgemm_ffn(T, D, F, x, ldx, gate, up, ld_in, down, ld_down, activation, kept_type, g or None,
+                            u or None, ld_kept, sg or None, su or None, ld_scales, h, ldh, y, ldy,
+                            _stream(stream))
+
+
+def sgemm_ffn_backward(T, D, F, dy, lddy, x, ldx, gate, up, ld_in, down, ld_down, activation, kept_type, g, u,
+                       ld_kept, sg, su, ld_scales, dg, du, h, ldh, dx, lddx, grad_type, accumulate, dgate, dup,
+                       ld_din, ddown, ld_ddown, stream=None) -> int:
+    """A gated feed-forward block's gradients; device addresses (int)."""
+    return load().sgemm_ffn_backward(T, D, F, dy, lddy, x, ldx, gate, up, ld_in, down, ld_down, activation,
+                                     kept_type, g, u, ld_kept, sg or None, su or None, ld_scales, dg, du, h, ldh,
+                                     dx, lddx, grad_type, int(accumulate), dgate, dup, ld_din, ddown, ld_ddown,
+                                     _stream(stream))
+
+
+def sgemm_ffn_plan(T, D, F, kept_type=TYPE_BF16, num_sms=152):
+    """The tiles of a block's launches, without a GPU: (status, dict of (rows, columns))."""
+    rows, cols = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
+    st = load().sgemm_ffn_plan(T, D, F, kept_type, num_sms, rows, cols)
+    return st, {k: (rows[i], cols[i]) for i, k in enumerate(("gated", "down", "slope", "gradients"))}
+
+
+_BF16, _KEPT = (TYPE_BF16,), (TYPE_BF16, TYPE_E4M3)
+
+
+def _of_shape(name, t, types, shape, device):
+    """(address, type, leading dimension) of a matrix of a given shape."""
+    p, code, ld, rows, cols = _matrix(name, t, types, device)
+    if (rows, cols) != shape:
+        raise ValueError(f"{name} must have the shape {shape}")
+    return p, code, ld
+
+
+def _same_step(name, a, b):
+    if a[2] != b[2]:
+        raise ValueError(f"{name} must have the same strides")
+
+
+def _ffn_weights(x, gate, up, down):
+    """The checked arguments that both passes begin with."""
+    device = x.get_device()
+    px, _, ldx, T, D = _matrix("x", x, _BF16)
+    _check_device(device)
+    F = gate.shape[0] if gate.dim() == 2 else -1
+    g, u = (_of_shape(n, t, _BF16, (F, D), device) for n, t in (("gate", gate), ("up", up)))
+    _same_step("gate and up", g, u)
+    d = _of_shape("down", down, _BF16, (D, F), device)
+    return device, T, D, F, (px, ldx), (g[0], u[0], g[2], d[0], d[2])
+
+
+def _ffn_kept(kept, T, F, device):
+    """(type, g, u, leading dimension, sg, su, leading dimension of the scales)."""
+    if len(kept) not in (2, 4):
+        raise ValueError("kept holds g and u, and with 8-bit codes their scales")
+    g, u = (_of_shape(n, t, _KEPT, (T, F), device) for n, t in zip(("kept g", "kept u"), kept))
+    _same_step("kept g and u", g, u)
+    if g[1] != u[1] or (g[1] == TYPE_E4M3) != (len(kept) == 4):
+        raise ValueError("kept holds g and u in bfloat16, or in float8_e4m3fn and their scales")
+    if len(kept) == 2:
+        return g[1], g[0], u[0], g[2], None, None, 1
+    sg, su = (_of_shape(n, t, _BF16, ((F + 127) // 128, T), device) for n, t in zip(("scales of g", "scales of u"),
+                                                                                    kept[2:]))
+    _same_step("the scales", sg, su)
+    # (one row of scales, whose stride means nothing, still has a token in each column)
+    return g[1], g[0], u[0], g[2], sg[0], su[0], sg[2]
+
+
+def _scratch_rows(T, F, like, stream):
+    """A T x F bf16 matrix whose rows start on 16 bytes."""
+    return _new((T, (F + 7) // 8 * 8), like.dtype, like.device, stream)[:, :F]
+
+
+def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=None, stream=None):
+    """(y, kept): a gated feed-forward block, y = (act(x gate^T) * (x up^T)) down^T.
+
+    x: T x D, gate and up: F x D (with the same strides), down: D x F, all bfloat16 CUDA
+    tensors whose rows start on 16 bytes (pad them where D or F is no multiple of 8).
+    ``activation``: ACT_SILU, ACT_GELU (tanh form), ACT_RELU or ACT_NONE.  ``keep``:
+    torch.bfloat16 or torch.float8_e4m3fn keeps x gate^T and x up^T for
+    ``ffn_backward`` as (g, u), or as (g, u, sg, su): codes, and bfloat16 scales
+    of shape (ceil(F / 128), T) for each 128 columns of a row; None keeps nothing,
+    and kept is None.  ``kept``, ``y`` and ``h`` (T x F, the product's other operand, rows on
+    16 bytes) take buffers to write into; new ones belong to the stream of the call.
+    The tensors are on the current device.  Asynchronous on ``stream`` (default:
+    torch's current stream); raises SgemmError on any non-zero status.
+    """
+    import torch
+
+    device, T, D, F, (px, ldx), (pg, pu, ld_in, pd, ld_down) = _ffn_weights(x, gate, up, down)
+    if kept is None and keep is not None:
+        if keep not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("keep must be torch.bfloat16, torch.float8_e4m3fn or None")
+        kept = tuple(_new((T, F), keep, x.device, stream) for _ in range(2))
+        if keep != torch.bfloat16:
+            kept += tuple(_new(((F + 127) // 128, T), torch.bfloat16, x.device, stream) for _ in range(2))
+    elif kept is not None and keep is not None and kept[0].dtype != keep:
+        raise ValueError("kept is not of the type that keep asks for")
+    k = (TYPE_BF16, None, None, max(F, 1), None, None, 1) if kept is None else _ffn_kept(kept, T, F, device)
+    if y is None:
+        y = _new((T, D), x.dtype, x.device, stream)
+    if h is None:
+        h = _scratch_rows(T, F, x, stream)
+    py, _, ldy = _of_shape("y", y, _BF16, (T, D), device)
+    ph, _, ldh = _of_shape("h", h, _BF16, (T, F), device)
+    st = load().sgemm_ffn(T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down, activation, *k, ph, ldh, py, ldy,
+                          _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_ffn")
+    return y, kept
+
+
+def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgate=None, dup=None, ddown=None,
+                 accumulate=False, scratch=None, stream=None):
+    """(dx, dgate, dup, ddown): the gradients of ``ffn``'s x, gate, up and down.
+
+    dy: T x D bfloat16, rows on 16 bytes like x; ``kept`` and ``activation`` as ``ffn`` had
+    them.  dx is bfloat16; dgate, dup and ddown are bfloat16 or, in buffers given,
+    all float32.  ``accumulate`` adds to the three weight gradients (which are given
+    then).  ``scratch``: three T x F bfloat16 buffers with the same strides, rows on
+    16 bytes.  Buffers, device, stream and errors as in ``ffn``.
+    """
+    device, T, D, F, (px, ldx), (pg, pu, ld_in, pd, ld_down) = _ffn_weights(x, gate, up, down)
+    pdy, _, lddy = _of_shape("dy", dy, _BF16, (T, D), device)
+    k = _ffn_kept(kept, T, F, device)
+    if accumulate and (dgate is None or dup is None or ddown is None):
+        raise ValueError("accumulate needs the three weight gradients")
+    if dx is None:
+        dx = _new((T, D), x.dtype, x.device, stream)
+    if dgate is None:
+        dgate = _new((F, D), x.dtype, x.device, stream)
+    if dup is None:
+        dup = _new((F, D), x.dtype, x.device, stream)
+    if ddown is None:
+        ddown = _new((D, F), x.dtype, x.device, stream)
+    if scratch is None:
+        scratch = tuple(_scratch_rows(T, F, x, stream) for _ in range(3))
+    s = [_of_shape(f"scratch {i}", t, _BF16, (T, F), device) for i, t in enumerate(scratch)]
+    if len(s) != 3:
+        raise ValueError("scratch is three buffers")
+    _same_step("the scratch buffers", s[0], s[1])
+    _same_step("the scratch buffers", s[0], s[2])
+    pdx, _, lddx = _of_shape("dx", dx, _BF16, (T, D), device)
+    dg, du = (_of_shape(n, t, _FLOATS, (F, D), device) for n, t in (("dgate", dgate), ("dup", dup)))
+    _same_step("dgate and dup", dg, du)
+    dd = _of_shape("ddown", ddown, _FLOATS, (D, F), device)
+    if dg[1] != du[1] or dg[1] != dd[1]:
+        raise ValueError("the weight gradients must be of one type")
+    st = load().sgemm_ffn_backward(
+        T, D, F, pdy, lddy, px, ldx, pg, pu, ld_in, pd, ld_down, activation, *k, s[0][0], s[1][0], s[2][0],
+        s[0][2], pdx, lddx, dg[1], int(accumulate), dg[0], du[0], dg[2], dd[0], dd[2],
+        _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_ffn_backward")
+    return dx, dgate, dup, ddown

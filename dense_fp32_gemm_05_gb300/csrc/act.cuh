@@ -1,0 +1,59 @@
+// Activations of the gated feed-forward operators, in fp32:
+//
+//   none  act(g) = g          silu  act(g) = g p,  p = 1 / (1 + exp(-g))
+//   relu  act(g) = max(g, 0)  gelu  act(g) = g p,  p = 1 / (1 + exp(-v)), v = 2 c (g + a g^3),
+//                             c = sqrt(2 / pi), a = 0.044715: the tanh form, (1 + tanh(v / 2)) / 2 = p
+//
+// act(g) = factor * g, and act'(g) = p (1 + g (1 - p) v'(g)): both from one exponential.
+// NaN passes through (relu: 0 at NaN's derivative, as a comparison has it).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/sgemm_gb300.h"
+
+namespace sgemm_gb300 {
+namespace act {
+
+inline bool is_activation(int a) { return a >= SGEMM_ACT_NONE && a <= SGEMM_ACT_GELU; }
+
+// p, 1 - p's slope factor v'(g), for silu and gelu.  gelu takes v from g cut to +-64, where p
+// is 0 or 1 to the last bit: g^3 and v' stay finite.  __expf's error is 2 units and
+// a few more as its argument grows; where that counts p is far below a bf16 unit of 1.
+__device__ __forceinline__ float factor_of(int a, float g, float &dv) {
+    float v = g;
+    dv = 1.0f;
+    if (a == SGEMM_ACT_GELU) {
+        const float t = fabsf(g) > 64.0f ? copysignf(64.0f, g) : g;
+        const float s = t * t;
+        v = 1.5957691216057308f * t * (1.0f + 0.044715f * s);
+        dv = 1.5957691216057308f * (1.0f + 0.134145f * s);
+    }
+    return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+__device__ __forceinline__ float value(int a, float g) {
+    if (a == SGEMM_ACT_NONE) return g;
+    if (a == SGEMM_ACT_RELU) return g < 0.0f ? 0.0f : g;
+    float dv;
+    return g * factor_of(a, g, dv);
+}
+
+// act(g), and its derivative.
+__device__ __forceinline__ float value_slope(int a, float g, float &slope) {
+    if (a == SGEMM_ACT_NONE) {
+        slope = 1.0f;
+        return g;
+    }
+    if (a == SGEMM_ACT_RELU) {
+        slope = g > 0.0f ? 1.0f : 0.0f;
+        return g < 0.0f ? 0.0f : g;
+    }
+    float dv;
+    const float p = factor_of(a, g, dv);
+    slope = p * (1.0f + g * (1.0f - p) * dv);
+    return g * p;
+}
+
+}  // namespace act
+}  // namespace sgemm_gb300

@@ -487,7 +487,8 @@ extern "C" int sgemm_device_error(sgemm_stream_t stream) {
     const int g = gemv_take_device_error();
     const int f = fp8_take_device_error();
     const int m = moe_take_device_error();
-    return t != SGEMM_OK ? t : g != SGEMM_OK ? g : f != SGEMM_OK ? f : m;
+    const int n = ffn_take_device_error();
+    return t != SGEMM_OK ? t : g != SGEMM_OK ? g : f != SGEMM_OK ? f : m != SGEMM_OK ? m : n;
 }
 
 extern "C" int sgemm_set_wait_limit(uint64_t nanoseconds) {

@@ -50,6 +50,7 @@ int tc_probe_tf32_rate(int reps, double *mac_per_clock);
 int tc_take_device_error();
 int fp8_take_device_error();
 int moe_take_device_error();
+int ffn_take_device_error();
 
 // Sets the bounded-wait limit (ns; 0 = default).
 void tc_set_wait_limit(uint64_t ns);

@@ -84,10 +84,12 @@ typedef enum {
                                   sgemm_ffma_static_scratch holds            */
 } sgemm_status;
 
-/* Activation of the fused epilogue (sgemm_epilogue). */
+/* Activation of the fused epilogue (sgemm_epilogue), and of gated feed-forward blocks. */
 typedef enum {
     SGEMM_ACT_NONE = 0,
-    SGEMM_ACT_RELU = 1     /* max(x, 0); NaN passes through */
+    SGEMM_ACT_RELU = 1,    /* max(x, 0); NaN passes through */
+    SGEMM_ACT_SILU = 2,    /* x / (1 + exp(-x)) (sgemm_ffn and sgemm_q4 only) */
+    SGEMM_ACT_GELU = 3     /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 (the same) */
 } sgemm_activation;
 
 /* Arithmetic path.  AUTO lets the per-shape selector choose among the
@@ -539,6 +541,80 @@ int sgemm_moe(int64_t T, int64_t D, int64_t F, int64_t E, int64_t topk, const vo
               int64_t stride_in, const void *down, const float *s_down, int64_t ld_down,
               int64_t stride_down, int renormalize, void *y, int64_t ldy, int32_t *indices,
               float *weights, sgemm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A gated feed-forward block in bf16, for training and serving.
+ *
+ * sgemm_ffn - the forward pass, for T tokens of width D and an inner width F:
+ *
+ *   g = x gate^T,  u = x up^T,  h = act(g) * u,  y = h down^T
+ *
+ *   x      T x D (ldx >= D);  gate, up  F x D (both ld_in >= D);
+ *   down   D x F (ld_down >= F);  y  T x D (ldy >= D): bf16, row-major
+ *   activation   any sgemm_activation
+ *   g, u   NULL: nothing is kept.  Else both are written for sgemm_ffn_backward,
+ *          T x F with leading dimension ld_kept >= F, as kept_type says:
+ *          SGEMM_TYPE_BF16, or SGEMM_TYPE_E4M3: codes, with bf16 scales sg and su,
+ *          S[(column / 128) * ld_scales + row], ld_scales >= T, of each 128 columns of a row:
+ *              scale = bf16(max(amax / 448, 2^-126)), amax the largest finite |value|
+ *              code  = value * (1 / scale), rounded to nearest even
+ *          (half the memory; NaN and infinities become NaN and stay out of amax)
+ *   h      T x F (ldh >= F), written: bf16, scratch of the call that a caller may read
+ *
+ * Products of bf16 values are exact and added in fp32 on the tensor cores; act(g) * u is
+ * computed in fp32 and rounded once to bf16, y once.  Kept values come from the fp32
+ * sums.  NaN and infinities give the IEEE result.
+ *
+ * x, gate, up, down and h are read by TMA: they start on 16 bytes and their leading
+ * dimensions are multiples of 8 (pad rows where D or F is none), else
+ * SGEMM_ERR_UNSUPPORTED; g, u, scales and y may lie anywhere.  The outputs may not
+ * overlap one another or an input.  T or D zero: nothing is done (D zero with values to
+ * keep: SGEMM_ERR_UNSUPPORTED); F zero: y = 0.  No library workspace.  Execution, errors
+ * and the bounded waits as sgemm; needs compute capability 10.3.
+ */
+int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t ldx, const void *gate,
+              const void *up, int64_t ld_in, const void *down, int64_t ld_down, int activation,
+              int kept_type, void *g, void *u, int64_t ld_kept, void *sg, void *su,
+              int64_t ld_scales, void *h, int64_t ldh, void *y, int64_t ldy, sgemm_stream_t stream);
+
+/*
+ * sgemm_ffn_backward - the block's gradients from dy (T x D bf16, lddy >= D) and what
+ * sgemm_ffn kept:
+ *
+ *   dh = dy down,  dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
+ *   dx    = dg gate + du up           T x D bf16 (lddx >= D)
+ *   dgate = dg^T x,  dup = du^T x     F x D (both ld_din >= D)
+ *   ddown = dy^T h                    D x F (ld_ddown >= F)
+ *
+ * dgate, dup and ddown are of grad_type (SGEMM_TYPE_BF16 or SGEMM_TYPE_F32); accumulate
+ * nonzero: they are added to what is there (in fp32, rounded once), as for a batch in
+ * parts.  dg, du and h (T x F bf16, all with leading dimension ldh >= F) are scratch of
+ * the call: dg, du and h are rounded to bf16 for the products that read them, which
+ * is most of the error of fp32 gradients (2^-9 of each of their terms).
+ * relu's derivative at 0 is 0.  With kept codes g and u are code * scale.
+ *
+ * No atomics: the same result every time.  dy, x, gate, up, down and the scratch start on
+ * 16 bytes with leading dimensions that are multiples of 8, else
+ * SGEMM_ERR_UNSUPPORTED.  A size of zero: gradients of empty sums are zero (left as they
+ * are with accumulate).  Otherwise as sgemm_ffn.
+ */
+int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *dy, int64_t lddy, const void *x,
+                       int64_t ldx, const void *gate, const void *up, int64_t ld_in,
+                       const void *down, int64_t ld_down, int activation, int kept_type,
+                       const void *g, const void *u, int64_t ld_kept, const void *sg,
+                       const void *su, int64_t ld_scales, void *dg, void *du, void *h, int64_t ldh,
+                       void *dx, int64_t lddx, int grad_type, int accumulate, void *dgate, void *dup,
+                       int64_t ld_din, void *ddown, int64_t ld_ddown, sgemm_stream_t stream);
+
+/*
+ * sgemm_ffn_plan - the tiles of a block's launches on a GPU with num_sms SMs, without
+ * touching one: rows and columns of the results' tiles, four of each (either pointer may
+ * be NULL): the gated product, the down product, the backward pass' first
+ * launch and its second.  kept_type as sgemm_ffn's (SGEMM_TYPE_E4M3: codes are kept).
+ * Returns SGEMM_OK or a negative argument index.
+ */
+int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows,
+                   int *out_cols);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,262 @@
+"""sgemm_ffn and sgemm_ffn_backward against the definition in 64 bits: every tile, kept type
+and activation, odd sizes, strides, single tokens, empty ones, and what lies around the outputs."""
+import pytest
+
+import dense_fp32_gemm_05_gb300 as sg
+from tests import ffn_plain as fp
+
+pytestmark = pytest.mark.gpu
+
+ACT = {"none": sg.ACT_NONE, "relu": sg.ACT_RELU, "silu": sg.ACT_SILU, "gelu": sg.ACT_GELU}
+
+
+def _inputs(T, D, F, seed=0, pad=8):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed + 3 * T + 5 * D + 7 * F)
+    x = fp.matrix(gen, T, D, 1.0, pad)
+    gate, up = (fp.matrix(gen, F, D, 1.5 / max(D, 1) ** 0.5, pad) for _ in range(2))
+    down = fp.matrix(gen, D, F, 1.0 / max(F, 1) ** 0.5, pad)
+    dy = fp.matrix(gen, T, D, 0.1, pad)
+    return dy, x, gate, up, down
+
+
+def _kept_bands(T, F, keep, gap=0, offset=0):
+    import torch
+    if keep is None:
+        return []
+    if keep == "bf16":
+        return [fp.Band(T, F, torch.bfloat16, 8, offset, gap=gap) for _ in range(2)]
+    return ([fp.Band(T, F, torch.float8_e4m3fn, 16, offset, gap=gap) for _ in range(2)] +
+            [fp.Band(-(-F // 128), T, torch.bfloat16, 1, 0, gap=gap) for _ in range(2)])
+
+
+def _check_kept(kept, want, keep):
+    import torch
+    for i, name in enumerate(("g", "u")):
+        v, e = want[name]
+        if keep == "bf16":
+            fp.close(name, kept[i], v, e + fp.BF16 * (v.abs() + e) + fp.TINY)
+            continue
+        F = v.shape[1]
+        groups = torch.nn.functional.pad(v.abs() + e, (0, -F % 128)).view(v.shape[0], -1, 128).amax(2).t()
+        low = torch.nn.functional.pad(v.abs() - e, (0, -F % 128)).view(v.shape[0], -1, 128).amax(2).t()
+        s = kept[2 + i].double()
+        assert bool((s <= groups / 448 * (1 + fp.BF16 + 2 * fp.SUM)).all())
+        assert bool((s >= low / 448 * (1 - fp.BF16 - 2 * fp.SUM)).all())
+        wide = s.t().repeat_interleave(128, 1)[:, :F]
+        # (half a step: 2^-4 of the value, or half of the smallest code, 2^-10)
+        fp.close(name, kept[i].double() * wide, v, e + 2.0 ** -4 * (1 + 2.0 ** -20) * (v.abs() + e) + 2.0 ** -10 * wide)
+
+
+def _forward(T, D, F, act="silu", keep=None, pad=8, gap=0, offset=0, seed=0):
+    import torch
+    _, x, gate, up, down = _inputs(T, D, F, seed, pad)
+    bands = _kept_bands(T, F, keep, gap, offset)
+    y, h = fp.Band(T, D, torch.bfloat16, 1 if gap else 8, offset, gap=gap), fp.Band(T, F, torch.bfloat16, 8)
+    kept = tuple(b.t for b in bands) or None
+    got, back = sg.ffn(x, gate, up, down, ACT[act], kept=kept, y=y.t, h=h.t)
+    assert got is y.t and back is kept
+    want = fp.forward(x, gate, up, down, act)
+    fp.close("y", got, *want["y"])
+    if keep:
+        _check_kept(kept, want, keep)
+    assert y.untouched() and h.untouched() and all(b.untouched() for b in bands)
+    assert sg.sgemm_device_error(torch.cuda.current_stream()) == 0
+    return y.t, kept
+
+
+SIZES = [(1, 64, 64), (1, 1, 1), (2, 7, 3), (5, 40, 129), (33, 100, 31), (64, 129, 255), (127, 65, 300), (130, 250, 1000),
+         (257, 512, 640), (300, 8, 2000), (515, 700, 513), (1000, 264, 1288)]
+
+
+@pytest.mark.parametrize("keep", [None, "bf16", "e4m3"])
+@pytest.mark.parametrize("T,D,F", SIZES)
+def test_forward(T, D, F, keep):
+    _forward(T, D, F, "silu", keep)
+
+
+@pytest.mark.parametrize("act", fp.ACTS)
+@pytest.mark.parametrize("keep", [None, "bf16", "e4m3"])
+def test_forward_activations(act, keep):
+    _forward(140, 200, 300, act, keep)
+
+
+@pytest.mark.parametrize("keep,gap,offset", [(None, 1, 1), ("bf16", 3, 1), ("bf16", 8, 8), ("e4m3", 5, 3), ("e4m3", 16, 0)])
+def test_forward_strides(keep, gap, offset):
+    """Outputs with odd strides and starts; inputs with wide rows."""
+    for T, D, F in ((70, 90, 140), (300, 260, 520)):
+        _forward(T, D, F, "gelu", keep, 64, gap, offset)
+
+
+def _backward(T, D, F, act="silu", keep="bf16", grad="bf16", add=False, pad=8, gap=0, offset=0, edit=None):
+    import torch
+    dy, x, gate, up, down = _inputs(T, D, F, 1, pad)
+    if edit:
+        edit(dy, x, gate, up, down)
+    kept = sg.ffn(x, gate, up, down, ACT[act], keep=torch.bfloat16 if keep == "bf16" else torch.float8_e4m3fn)[1]
+    g, u = fp.kept_values(kept)
+    want = fp.backward(dy, x, gate, up, down, g, u, act)
+    kind = torch.bfloat16 if grad == "bf16" else torch.float32
+    step = 1 if gap else 8
+    bands = {"dx": fp.Band(T, D, torch.bfloat16, step, offset, gap=gap), "dgate": fp.Band(F, D, kind, step, offset, gap=gap),
+             "dup": fp.Band(F, D, kind, step, offset, gap=gap), "ddown": fp.Band(D, F, kind, step, offset, gap=gap)}
+    scratch = [fp.Band(T, F, torch.bfloat16, 8) for _ in range(3)]
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    before = {}
+    for n, b in bands.items():
+        b.t.copy_(torch.randn(b.t.shape, generator=gen, device="cuda"))
+        before[n] = b.t.double().clone()
+    out = sg.ffn_backward(dy, x, gate, up, down, kept, ACT[act], accumulate=add, scratch=tuple(b.t for b in scratch),
+                          **{n: b.t for n, b in bands.items()})
+    for n, got in zip(bands, out):
+        assert got is bands[n].t
+        v, e = want[n]
+        if add and n != "dx":
+            v, e = v + before[n], e + 2.0 ** -24 * (v + before[n]).abs()
+        half = 2.0 ** -24 if grad == "f32" and n != "dx" else fp.BF16
+        fp.close(n, got, v, e + half * (v.abs() + e) + fp.TINY)
+    assert all(b.untouched() for b in list(bands.values()) + scratch)
+    assert sg.sgemm_device_error(torch.cuda.current_stream()) == 0
+
+
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,D,F", SIZES)
+def test_backward(T, D, F, keep):
+    _backward(T, D, F, "silu", keep)
+
+
+@pytest.mark.parametrize("act", fp.ACTS)
+@pytest.mark.parametrize("keep", ["bf16", "e4m3"])
+def test_backward_activations(act, keep):
+    _backward(140, 200, 300, act, keep)
+
+
+@pytest.mark.parametrize("grad,add", [("f32", False), ("f32", True), ("bf16", True)])
+@pytest.mark.parametrize("gap,offset", [(0, 0), (3, 1)])
+def test_backward_types_strides_and_sums(grad, add, gap, offset):
+    for T, D, F in ((70, 90, 140), (300, 260, 520)):
+        _backward(T, D, F, "gelu", "e4m3", grad, add, 64, gap, offset)
+
+
+def test_every_tile():
+    """Each launch of a block on each kind of tile that it can take, by sizes that the plan says take it."""
+    seen = {n: set() for n in ("gated", "gated, codes", "down", "slope", "gradients")}
+    for T, D, F in ((1, 64, 64), (100, 200, 4000), (100, 4000, 300), (700, 300, 3000), (700, 3000, 300), (2000, 200, 1500),
+                    (4000, 300, 2500), (3000, 2000, 300), (2000, 2000, 500), (1500, 500, 2000), (600, 520, 2600), (300, 1000, 9000),
+                    (9000, 300, 600), (1000, 1100, 1200)):
+        bf16, codes = (sg.sgemm_ffn_plan(T, D, F, k)[1] for k in (sg.TYPE_BF16, sg.TYPE_E4M3))
+        new = False
+        for n in seen:
+            tile = codes["gated"] if n == "gated, codes" else bf16[n]
+            new = new or tile not in seen[n]
+            seen[n].add(tile)
+        if new:
+            for keep in ("bf16", "e4m3"):
+                _forward(T, D, F, "silu", keep)
+                _backward(T, D, F, "silu", keep)
+    every = {(256, 256), (128, 128), (128, 64)}
+    assert seen["gated"] | seen["down"] | seen["slope"] | seen["gradients"] == every, seen
+    print(seen)
+
+
+def test_new_buffers_and_another_stream():
+    import torch
+    dy, x, gate, up, down = _inputs(200, 96, 160)
+    want, kept = sg.ffn(x, gate, up, down, keep=torch.float8_e4m3fn)
+    grads = sg.ffn_backward(dy, x, gate, up, down, kept)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y, kept2 = sg.ffn(x, gate, up, down, keep=torch.float8_e4m3fn, stream=side)
+    grads2 = sg.ffn_backward(dy, x, gate, up, down, kept2, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(kept, kept2))
+    assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
+
+
+def test_captured_and_replayed():
+    import torch
+    dy, x, gate, up, down = _inputs(300, 136, 264)
+    y, kept = sg.ffn(x, gate, up, down, keep=torch.bfloat16)
+    first = [y.clone()] + [g.clone() for g in sg.ffn_backward(dy, x, gate, up, down, kept)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, kept = sg.ffn(x, gate, up, down, keep=torch.bfloat16)
+        grads = sg.ffn_backward(dy, x, gate, up, down, kept)
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, first[0]) and all(torch.equal(a, b) for a, b in zip(grads, first[1:]))
+    x2 = _inputs(300, 136, 264, seed=50)[1]
+    x.copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, sg.ffn(x2, gate, up, down)[0])
+
+
+def test_nothing_to_do():
+    import torch
+    dy, x, gate, up, down = _inputs(0, 32, 64)
+    assert sg.ffn(x, gate, up, down)[0].shape == (0, 32)
+    dgate, dup, ddown = (torch.full(s, 7.0, device="cuda") for s in ((64, 32), (64, 32), (32, 64)))
+    kept = tuple(torch.empty((0, 64), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sg.ffn_backward(dy, x, gate, up, down, kept, dgate=dgate, dup=dup, ddown=ddown, accumulate=True)
+    assert all(bool((t == 7.0).all()) for t in (dgate, dup, ddown))
+    sg.ffn_backward(dy, x, gate, up, down, kept, dgate=dgate, dup=dup, ddown=ddown)
+    assert all(bool((t == 0.0).all()) for t in (dgate, dup, ddown))
+    dy, x, gate, up, down = _inputs(5, 32, 0)
+    y = torch.full((5, 32), 7.0, device="cuda", dtype=torch.bfloat16)
+    assert bool((sg.ffn(x, gate, up, down, y=y)[0] == 0).all())
+    dx = torch.full((5, 32), 7.0, device="cuda", dtype=torch.bfloat16)
+    kept = tuple(torch.empty((5, 0), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    assert bool((sg.ffn_backward(dy, x, gate, up, down, kept, dx=dx)[0] == 0).all())
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_non_finite(T):
+    """Infinities and NaN reach the rows and groups that they belong to, and no others."""
+    import torch
+    dy, x, gate, up, down = _inputs(T, 96, 300)
+    clean, kept0 = sg.ffn(x, gate, up, down, keep=torch.float8_e4m3fn)
+    x = x.clone()
+    x[1, 5] = float("nan")
+    y, kept = sg.ffn(x, gate, up, down, keep=torch.float8_e4m3fn)
+    assert bool(y[1].isnan().all()) and bool(kept[0][1].float().isnan().all())
+    assert bool((kept[2][:, 1].float() == 2.0 ** -126).all())            # no finite value in the group
+    others = [t for t in range(T) if t != 1]
+    assert torch.equal(y[others], clean[others]) and torch.equal(kept[2][:, others], kept0[2][:, others])
+    gate = gate.clone()
+    gate[7] = 0
+    gate[7, 0] = float("inf")
+    x[1, 5], x[:, 0] = 1.0, 2.0
+    y, kept = sg.ffn(x, gate, up, down, keep=torch.float8_e4m3fn)
+    assert bool(kept[0][:, 7].float().isnan().all()) and not bool(kept[0][:, 8:].float().isnan().any())
+    assert bool(kept[2].float().isfinite().all())
+    y, kept = sg.ffn(x, gate, up, down, keep=torch.bfloat16)
+    assert bool((kept[0][:, 7].float() == float("inf")).all())
+
+
+def test_gradients_against_differences():
+    """The 64-bit block's difference quotient along a direction is what the kernels' gradients give."""
+    import torch
+    T, D, F = 200, 64, 160
+    dy, x, gate, up, down = _inputs(T, D, F)
+    kept = sg.ffn(x, gate, up, down, ACT["gelu"], keep=torch.bfloat16)[1]
+    new = [torch.empty(s, device="cuda") for s in ((F, D), (F, D), (D, F))]
+    grads = sg.ffn_backward(dy, x, gate, up, down, kept, ACT["gelu"], dgate=new[0], dup=new[1], ddown=new[2])
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    at = [t.double() for t in (x, gate, up, down)]
+    along = [torch.randn(t.shape, generator=gen, device="cuda", dtype=torch.float64) for t in at]
+
+    def loss(eps):
+        x_, g_, u_, d_ = (a + eps * b for a, b in zip(at, along))
+        return float((dy.double() * ((fp.act("gelu", x_ @ g_.t()) * (x_ @ u_.t())) @ d_.t())).sum())
+
+    eps = 1e-5
+    slope = (loss(eps) - loss(-eps)) / (2 * eps)
+    mine = sum(float((g.double() * b).sum()) for g, b in zip(grads, along))
+    # the kept values, dg, du, h and dx are rounded to bf16: each term of the sum is off by at most
+    # a few 2^-8; the terms' size bounds the sum's error (their signs are as good as random)
+    size = sum(float((g.double() * b).square().sum()) for g, b in zip(grads, along)) ** 0.5
+    assert abs(mine - slope) <= 8 * fp.BF16 * size, (mine, slope, size)
