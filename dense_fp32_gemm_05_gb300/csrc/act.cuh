@@ -17,13 +17,14 @@ namespace act {
 
 inline bool is_activation(int a) { return a >= SGEMM_ACT_NONE && a <= SGEMM_ACT_GELU; }
 
-// p, 1 - p's slope factor v'(g), for silu and gelu.  gelu takes v from g cut to +-64, where p
-// is 0 or 1 to the last bit: g^3 and v' stay finite.  __expf's error is 2 units and
-// a few more as its argument grows; where that counts p is far below a bf16 unit of 1.
-__device__ __forceinline__ float factor_of(int a, float g, float &dv) {
+// p and v'(g) of silu and gelu.  gelu takes v from g cut to +-64, where p is 0 or 1 to
+// the last bit: g^3 and v' stay finite.  __expf's error is 2 units and a few more as its
+// argument grows; where that counts p is far below a bf16 unit of 1.
+template <int A>
+__device__ __forceinline__ float factor_of(float g, float &dv) {
     float v = g;
     dv = 1.0f;
-    if (a == SGEMM_ACT_GELU) {
+    if (A == SGEMM_ACT_GELU) {
         const float t = fabsf(g) > 64.0f ? copysignf(64.0f, g) : g;
         const float s = t * t;
         v = 1.5957691216057308f * t * (1.0f + 0.044715f * s);
@@ -32,27 +33,44 @@ __device__ __forceinline__ float factor_of(int a, float g, float &dv) {
     return __fdividef(1.0f, 1.0f + __expf(-v));
 }
 
-__device__ __forceinline__ float value(int a, float g) {
-    if (a == SGEMM_ACT_NONE) return g;
-    if (a == SGEMM_ACT_RELU) return g < 0.0f ? 0.0f : g;
+template <int A>
+__device__ __forceinline__ float value(float g) {
+    if (A == SGEMM_ACT_NONE) return g;
+    if (A == SGEMM_ACT_RELU) return g < 0.0f ? 0.0f : g;
     float dv;
-    return g * factor_of(a, g, dv);
+    return g * factor_of<A>(g, dv);
 }
 
 // act(g), and its derivative.
-__device__ __forceinline__ float value_slope(int a, float g, float &slope) {
-    if (a == SGEMM_ACT_NONE) {
+template <int A>
+__device__ __forceinline__ float value_slope(float g, float &slope) {
+    if (A == SGEMM_ACT_NONE) {
         slope = 1.0f;
         return g;
     }
-    if (a == SGEMM_ACT_RELU) {
+    if (A == SGEMM_ACT_RELU) {
         slope = g > 0.0f ? 1.0f : 0.0f;
         return g < 0.0f ? 0.0f : g;
     }
     float dv;
-    const float p = factor_of(a, g, dv);
+    const float p = factor_of<A>(g, dv);
     slope = p * (1.0f + g * (1.0f - p) * dv);
     return g * p;
+}
+
+// f(A) with the activation as a constant.  A loop over many values belongs inside f: with a
+// branch at each value their exponentials and quotients, ~150 clocks one after
+// the other, do not overlap.
+template <int A>
+struct Constant {
+    static constexpr int value = A;
+};
+template <typename Fn>
+__device__ __forceinline__ void with(int a, Fn f) {
+    if (a == SGEMM_ACT_SILU) f(Constant<SGEMM_ACT_SILU>());
+    else if (a == SGEMM_ACT_GELU) f(Constant<SGEMM_ACT_GELU>());
+    else if (a == SGEMM_ACT_RELU) f(Constant<SGEMM_ACT_RELU>());
+    else f(Constant<SGEMM_ACT_NONE>());
 }
 
 }  // namespace act

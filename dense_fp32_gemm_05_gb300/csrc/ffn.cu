@@ -18,11 +18,11 @@
 // A tensor-memory row then holds g and u of the same columns: act(g) u, and the codes of
 // whole groups of 128, need nothing from another thread.
 //
-// 384 threads: warp 0 TMA, warp 1 MMAs and tensor memory, warps 4-7 and 8-11 epilogues of
-// even and odd tiles, each from its own buffer of tensor memory, so that a tile's
-// epilogue has two tiles' MMAs to hide behind and no exchange between warps.  A thread
-// holds one row; 32 columns at a time go through shared memory (swizzled) to
-// rows of 16-byte pieces, or element by element where alignment or the edge asks for it.
+// 384 threads: warp 0 TMA, warp 1 MMAs and tensor memory, warps 4-7 and 8-11 the
+// epilogue of one of two buffers of tensor memory while the MMAs fill the other; the two
+// warpgroups share a tile's columns.  A thread holds one row; 32 columns at a time
+// go through shared memory (swizzled) to rows of 16-byte pieces, or element by element
+// where alignment or the edge asks for it.
 //
 // Roundings: g, u (kept) and h, dg, du are rounded to bf16 (or codes) once, because the
 // products that read them take bf16; sums, activations and derivatives are fp32.
@@ -61,6 +61,7 @@ constexpr int CH = 32;                         // columns of the epilogue at a t
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
 constexpr int STAGING = 3 * 32 * CH * 2;       // bytes of an epilogue warp: three bf16 blocks, or one fp32
+constexpr int REGS_ISSUE = 56, REGS_EPILOGUE = 224;      // 384 x 168 = 128 x 56 + 256 x 224
 constexpr int SMEM_MAX = 232448;
 constexpr int BAR_BYTES = 256;
 constexpr int MAX_STAGES = 8;
@@ -305,10 +306,10 @@ __device__ __forceinline__ void kept_values(uint8_t *block, float scale, float (
 // buffer included).  `block`: the warp's STAGING bytes.
 
 template <int BN>
-__device__ __forceinline__ void store_tile(const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0) {
+__device__ __forceinline__ void store_tile(const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0, int c0) {
     const int lane = threadIdx.x & 31, rows = q.M - m0;
 #pragma unroll 1
-    for (int c = 0; c < BN && n0 + c < q.N; c += CH) {
+    for (int c = c0; c < BN && n0 + c < q.N; c += 2 * CH) {
         uint32_t r[CH];
         tmem_ld32(tmem + c, r);
         if (rows <= 0) continue;
@@ -357,12 +358,14 @@ __device__ __forceinline__ void store_tile(const Product &q, uint32_t tmem, uint
 
 // KEEP: 0 nothing, 1 bf16, 2 codes (tiles with 128 columns of each matrix).
 template <int BN, int KEEP>
-__device__ __forceinline__ void gated_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0) {
+__device__ __forceinline__ void gated_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0,
+                                           int c0) {
     constexpr int HALF = BN / 2;
     const int lane = threadIdx.x & 31, rows = q.M - m0;
     float ig = 0.0f, iu = 0.0f;
     if (KEEP == 2) {
-        // the group's scales first: a second read of tensor memory costs less than holding 256 values
+        // the group's scales first, by each warpgroup for itself: reading tensor memory twice
+        // costs less than holding 256 values, or than an exchange between warps
         float mg = 0.0f, mu = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < HALF && n0 + c < q.N; c += CH) {     // (columns past N are zeros)
@@ -377,14 +380,14 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
         const float a = kept_scale(mg), b = kept_scale(mu);
         ig = __fdiv_rn(1.0f, a);
         iu = __fdiv_rn(1.0f, b);
-        if (lane < rows) {
+        if (c0 == 0 && lane < rows) {
             const int64_t at = (int64_t)(n0 / 128) * p.ld_scales + m0 + lane;
             p.sg[at] = __float2bfloat16_rn(a);
             p.su[at] = __float2bfloat16_rn(b);
         }
     }
 #pragma unroll 1
-    for (int c = 0; c < HALF && n0 + c < q.N; c += CH) {
+    for (int c = c0; c < HALF && n0 + c < q.N; c += 2 * CH) {
         uint32_t r[CH];
         float g[CH], u[CH];
         tmem_ld32(tmem + c, r);
@@ -404,8 +407,10 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
             put_codes(bg, g, ig);
             put_codes(bu, u, iu);
         }
+        act::with(p.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) g[i] = act::value(p.act, g[i]) * u[i];
+            for (int i = 0; i < CH; ++i) g[i] = act::value<a.value>(g[i]) * u[i];
+        });
         put_bf16(bh, g);
         __syncwarp();
         put_rows(bh, p.h + row * p.ldh + col, p.ldh, rows, cols, true);
@@ -420,49 +425,118 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
     }
 }
 
-template <int BN, bool CODES>
-__device__ __forceinline__ void slope_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0) {
-    using E = typename std::conditional<CODES, uint8_t, __nv_bfloat16>::type;
-    const int lane = threadIdx.x & 31, rows = q.M - m0;
-    float sg = 1.0f, su = 1.0f;
-#pragma unroll 1
-    for (int c = 0; c < BN && n0 + c < q.N; c += CH) {
-        const int cols = q.N - n0 - c;
-        const int64_t row = m0, col = n0 + c;
-        uint8_t *bg = block, *bu = block + 32 * CH * 2, *bh = block + 2 * 32 * CH * 2;
-        if (rows > 0) {
-            get_rows(bg, static_cast<const E *>(p.g) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-            get_rows(bu, static_cast<const E *>(p.u) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-            if (CODES && (c == 0 || col % 128 == 0)) {
-                const int64_t at = (col / 128) * p.ld_scales + m0 + lane;
-                sg = lane < rows ? __bfloat162float(p.sg[at]) : 0.0f;
-                su = lane < rows ? __bfloat162float(p.su[at]) : 0.0f;
+// Kept values of 32 rows x 32 columns on their way from memory: a lane's pieces of rows, or
+// (alignment, the edge) its column's elements.
+template <typename E>
+struct Fetched {
+    static constexpr int WORDS = CH * (int)sizeof(E) / 4;
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ void fetch(const void *from, int64_t at, int64_t ld, int rows, int cols, bool vec) {
+        constexpr int PER = WORDS / 4, STEP = 32 / PER;
+        const int lane = threadIdx.x & 31;
+        if (vec && cols >= CH) {
+            const E *in = static_cast<const E *>(from) + at + (lane / PER) * ld + lane % PER * (16 / (int)sizeof(E));
+#pragma unroll
+            for (int i = 0; i < PER; ++i, in += STEP * ld) {
+                const uint4 v = i * STEP + lane / PER < rows ? *reinterpret_cast<const uint4 *>(in) : make_uint4(0, 0, 0, 0);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
             }
+        } else {
+            using Bits = typename std::conditional<sizeof(E) == 1, uint8_t, uint16_t>::type;
+            constexpr int IN_WORD = 4 / (int)sizeof(E);
+            const Bits *in = static_cast<const Bits *>(from) + at + lane;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+            for (int r = 0; r < 32; ++r, in += ld)
+                if (lane < cols && r < rows) w[r / IN_WORD] |= (uint32_t)*in << (r % IN_WORD * 8 * (int)sizeof(E));
         }
-        __syncwarp();
+    }
+
+    __device__ __forceinline__ void stash(uint8_t *block, int cols, bool vec) const {
+        constexpr int BYTES = CH * sizeof(E), PER = WORDS / 4, STEP = 32 / PER;
+        const int lane = threadIdx.x & 31;
+        if (vec && cols >= CH) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                *piece_at<BYTES>(block, i * STEP + lane / PER, lane % PER) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+            using Bits = typename std::conditional<sizeof(E) == 1, uint8_t, uint16_t>::type;
+            constexpr int IN_WORD = 4 / (int)sizeof(E);
+            const int byte = lane * (int)sizeof(E);
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+                *reinterpret_cast<Bits *>(reinterpret_cast<uint8_t *>(piece_at<BYTES>(block, r, byte / 16)) + byte % 16) =
+                    (Bits)(w[r / IN_WORD] >> (r % IN_WORD * 8 * (int)sizeof(E)));
+        }
+    }
+};
+
+// The kept values of a chunk of columns: fetched before the accumulators are waited
+// for, and a chunk ahead of the one that is computed.
+template <bool CODES>
+struct Kept {
+    using E = typename std::conditional<CODES, uint8_t, __nv_bfloat16>::type;
+    Fetched<E> g, u;
+    __nv_bfloat16 sg, su;
+
+    __device__ __forceinline__ void fetch(const Params &p, int row, int rows, int col, int cols) {
+        if (rows <= 0 || cols <= 0) return;
+        const int64_t at = row * p.ld_kept + col;
+        g.fetch(p.g, at, p.ld_kept, rows, cols, p.kept_vec);
+        u.fetch(p.u, at, p.ld_kept, rows, cols, p.kept_vec);
+        if (CODES) {
+            const int64_t scale = (col / 128) * p.ld_scales + row + min((int)(threadIdx.x & 31), rows - 1);
+            sg = p.sg[scale];
+            su = p.su[scale];
+        }
+    }
+};
+
+template <int BN, bool CODES>
+__device__ __forceinline__ void slope_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0,
+                                           int c0, Kept<CODES> &kept) {
+    const int rows = q.M - m0;
+    uint8_t *bg = block, *bu = block + 32 * CH * 2, *bh = block + 2 * 32 * CH * 2;
+#pragma unroll 1
+    for (int c = c0; c < BN && n0 + c < q.N; c += 2 * CH) {
+        const int cols = q.N - n0 - c;
+        const int64_t at = m0 * p.ldh + n0 + c;
         uint32_t r[CH];
         tmem_ld32(tmem + c, r);
         if (rows <= 0) continue;
+        kept.g.stash(bg, cols, p.kept_vec);
+        kept.u.stash(bu, cols, p.kept_vec);
+        const float sg = CODES ? __bfloat162float(kept.sg) : 1.0f, su = CODES ? __bfloat162float(kept.su) : 1.0f;
+        __syncwarp();
+        if (c + 2 * CH < BN) kept.fetch(p, m0, rows, n0 + c + 2 * CH, cols - 2 * CH);
         float g[CH], u[CH], h[CH];
         kept_values<CODES>(bg, sg, g);
         kept_values<CODES>(bu, su, u);
         if (CODES) __syncwarp();               // (rows of codes are shorter than the ones that replace them)
+        act::with(p.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const float dh = __uint_as_float(r[i]);
-            float slope;
-            const float a = act::value_slope(p.act, g[i], slope);
-            h[i] = a * u[i];
-            g[i] = dh * u[i] * slope;
-            u[i] = dh * a;
-        }
+            for (int i = 0; i < CH; ++i) {
+                const float dh = __uint_as_float(r[i]);
+                float slope;
+                const float v = act::value_slope<a.value>(g[i], slope);
+                h[i] = v * u[i];
+                g[i] = dh * u[i] * slope;
+                u[i] = dh * v;
+            }
+        });
         put_bf16(bg, g);
         put_bf16(bu, u);
         put_bf16(bh, h);
         __syncwarp();
-        put_rows(bg, p.dg + row * p.ldh + col, p.ldh, rows, cols, true);
-        put_rows(bu, p.du + row * p.ldh + col, p.ldh, rows, cols, true);
-        put_rows(bh, p.h + row * p.ldh + col, p.ldh, rows, cols, true);
+        put_rows(bg, p.dg + at, p.ldh, rows, cols, true);
+        put_rows(bu, p.du + at, p.ldh, rows, cols, true);
+        put_rows(bh, p.h + at, p.ldh, rows, cols, true);
         __syncwarp();
     }
 }
@@ -512,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(tempty(b), (PAIR ? 2 : 1) * EPI_WARPS / 2);    // of both CTAs, on the leader's
+            mbar_init(tempty(b), (PAIR ? 2 : 1) * EPI_WARPS);    // of both CTAs, on the leader's
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < p.count; ++i) {
@@ -528,115 +602,128 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
     pdl_wait();                                    // the kernel before may write what is read here
     pdl_trigger();                                 // (the next one waits for this one's end all the same)
 
+    // The epilogues hold 32 rows' values of three matrices and those under way: registers
+    // that the first warpgroup does not need.
     bool ok = true;
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        int s = 0, filled = 0;
-        uint32_t ph = 1;
-        for (int unit = first; ok && unit < p.units; unit += step) {
-            int tm, tn;
-            const int i = tile_of(p, unit, tm, tn);
-            const Product &q = p.product[i];
-            const Maps &maps = p.maps[i];
-            const int m = tm * T_::ROWS + (int)rank * BM;
-            // GATED: gate and up on the pair's CTAs, or one after the other
-            const int n = tn * WIDTH + (PAIR && EPI != GATED ? (int)rank * B_ROWS : 0);
-            const int nk0 = q.nk0, nk = q.nk;
-            const bool a_mn = q.a_mn != 0, b_mn = q.b_mn != 0;
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
-                const bool second = kb >= nk0;
-                const int k = (second ? kb - nk0 : kb) * BK;
-                const uint32_t a = smem0 + (uint32_t)(s * T_::STAGE), b = a + A_BYTES;
-                const uint32_t bar = PAIR ? leader_addr(full(s)) : full(s);
-                const CUtensorMap *ma = &maps.a[second], *mb = &maps.b[EPI == GATED ? (int)rank : (int)second];
-                auto load = [&](uint32_t to, const CUtensorMap *map, int c0, int c1) {
-                    if (PAIR) tma_load_2d_pair(to, map, bar, c0, c1);
-                    else tma_load_2d(to, map, bar, c0, c1);
-                };
-                if (elect_one()) {
-                    if (rank == 0) mbar_expect_tx(full(s), (PAIR ? 2 : 1) * T_::STAGE);
-                    if (a_mn) {
-                        load(a, ma, m, k);
-                        load(a + CHUNK, ma, m + 64, k);
-                    } else {
-                        load(a, ma, k, m);
-                    }
-                    if (EPI == GATED) {
-                        load(b, mb, k, n);
-                        if (!PAIR) load(b + B_ROWS * BK, &maps.b[1], k, n);
-                    } else if (b_mn) {
-#pragma unroll
-                        for (int j = 0; j < B_ROWS; j += 64) load(b + (uint32_t)(j / 64 * CHUNK), mb, n + j, k);
-                    } else {
-                        load(b, mb, k, n);
-                    }
-                }
-                __syncwarp();
-                ++filled;
-                if (++s == S) { s = 0; ph ^= 1; }
-            }
-        }
-        publish((int)rank, filled);
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (the leader's)
-        if (rank == 0) {
-            int s = 0, b = 0, issued = 0;
-            uint32_t ph = 0, bph = 1;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS_ISSUE));
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer
+            int s = 0, filled = 0;
+            uint32_t ph = 1;
             for (int unit = first; ok && unit < p.units; unit += step) {
                 int tm, tn;
-                const Product &q = p.product[tile_of(p, unit, tm, tn)];
-                const uint32_t a_step = q.a_mn ? 2048u >> 4 : 32u >> 4, b_step = q.b_mn ? 2048u >> 4 : 32u >> 4;
-                const uint32_t idesc = q.idesc, d = tmem + (uint32_t)(b * BN);
-                const int nk = q.nk;
-                if (!warp_wait(tempty(b), bph, lim)) { ok = false; break; }
+                const int i = tile_of(p, unit, tm, tn);
+                const Product &q = p.product[i];
+                const Maps &maps = p.maps[i];
+                const int m = tm * T_::ROWS + (int)rank * BM;
+                // GATED: gate and up on the pair's CTAs, or one after the other
+                const int n = tn * WIDTH + (PAIR && EPI != GATED ? (int)rank * B_ROWS : 0);
+                const int nk0 = q.nk0, nk = q.nk;
+                const bool a_mn = q.a_mn != 0, b_mn = q.b_mn != 0;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!warp_wait(full(s), ph, lim)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a = smem0 + (uint32_t)(s * T_::STAGE);
-                    const uint64_t da = smem_desc_8bit(a, CHUNK), db = smem_desc_8bit(a + A_BYTES, CHUNK);
+                    if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
+                    const bool second = kb >= nk0;
+                    const int k = (second ? kb - nk0 : kb) * BK;
+                    const uint32_t a = smem0 + (uint32_t)(s * T_::STAGE), b = a + A_BYTES;
+                    const uint32_t bar = PAIR ? leader_addr(full(s)) : full(s);
+                    const CUtensorMap *ma = &maps.a[second], *mb = &maps.b[EPI == GATED ? (int)rank : (int)second];
+                    auto load = [&](uint32_t to, const CUtensorMap *map, int c0, int c1) {
+                        if (PAIR) tma_load_2d_pair(to, map, bar, c0, c1);
+                        else tma_load_2d(to, map, bar, c0, c1);
+                    };
                     if (elect_one()) {
+                        if (rank == 0) mbar_expect_tx(full(s), (PAIR ? 2 : 1) * T_::STAGE);
+                        if (a_mn) {
+                            load(a, ma, m, k);
+                            load(a + CHUNK, ma, m + 64, k);
+                        } else {
+                            load(a, ma, k, m);
+                        }
+                        if (EPI == GATED) {
+                            load(b, mb, k, n);
+                            if (!PAIR) load(b + B_ROWS * BK, &maps.b[1], k, n);
+                        } else if (b_mn) {
 #pragma unroll
-                        for (int i = 0; i < BK / 16; ++i)
-                            umma_bf16<PAIR>(d, da + i * a_step, db + i * b_step, idesc, kb > 0 || i > 0);
-                        if (PAIR) umma_commit_pair(empty(s));
-                        else umma_commit(empty(s));
-                        if (kb + 1 == nk) {
-                            if (PAIR) umma_commit_pair(tfull(b));
-                            else umma_commit(tfull(b));
+                            for (int j = 0; j < B_ROWS; j += 64) load(b + (uint32_t)(j / 64 * CHUNK), mb, n + j, k);
+                        } else {
+                            load(b, mb, k, n);
                         }
                     }
                     __syncwarp();
-                    ++issued;
+                    ++filled;
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
-                if (++b == 2) { b = 0; bph ^= 1; }
             }
-            publish(2, issued);
+            publish((int)rank, filled);
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer (the leader's)
+            if (rank == 0) {
+                int s = 0, b = 0, issued = 0;
+                uint32_t ph = 0, bph = 1;
+                for (int unit = first; ok && unit < p.units; unit += step) {
+                    int tm, tn;
+                    const Product &q = p.product[tile_of(p, unit, tm, tn)];
+                    const uint32_t a_step = q.a_mn ? 2048u >> 4 : 32u >> 4, b_step = q.b_mn ? 2048u >> 4 : 32u >> 4;
+                    const uint32_t idesc = q.idesc, d = tmem + (uint32_t)(b * BN);
+                    const int nk = q.nk;
+                    if (!warp_wait(tempty(b), bph, lim)) { ok = false; break; }
+                    for (int kb = 0; kb < nk; ++kb) {
+                        if (!warp_wait(full(s), ph, lim)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t a = smem0 + (uint32_t)(s * T_::STAGE);
+                        const uint64_t da = smem_desc_8bit(a, CHUNK), db = smem_desc_8bit(a + A_BYTES, CHUNK);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int i = 0; i < BK / 16; ++i)
+                                umma_bf16<PAIR>(d, da + i * a_step, db + i * b_step, idesc, kb > 0 || i > 0);
+                            if (PAIR) umma_commit_pair(empty(s));
+                            else umma_commit(empty(s));
+                            if (kb + 1 == nk) {
+                                if (PAIR) umma_commit_pair(tfull(b));
+                                else umma_commit(tfull(b));
+                            }
+                        }
+                        __syncwarp();
+                        ++issued;
+                        if (++s == S) { s = 0; ph ^= 1; }
+                    }
+                    if (++b == 2) { b = 0; bph ^= 1; }
+                }
+                publish(2, issued);
+            }
         }
-    } else if (warp >= 4) {
-        // ------------------------------------------------ epilogues: one warpgroup's tiles use one buffer
-        const int quad = warp & 3, b = (warp - 4) >> 2;
-        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BN);
-        const uint32_t lead_tempty = PAIR ? leader_addr(tempty(b)) : tempty(b);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REGS_EPILOGUE));
+        // ------------------------------------------------ epilogues
+        // Chunks of 32 columns alternate between the two warpgroups, and the first
+        // changes sides from tile to tile (a narrow GATED tile is a single chunk).
+        const int quad = warp & 3, group = (warp - 4) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t lead_tempty0 = PAIR ? leader_addr(tempty(0)) : tempty(0);
         uint8_t *block = staging + (warp - 4) * STAGING;
+        int b = 0, side = group;
         uint32_t ph = 0;
-        for (int unit = first + b * step; unit < p.units; unit += 2 * step) {
+        for (int unit = first; unit < p.units; unit += step) {
             int tm, tn;
             const Product &q = p.product[tile_of(p, unit, tm, tn)];
+            const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH, c0 = side * CH;
+            const uint32_t at = lanes + (uint32_t)(b * BN);
+            Kept<KEEP == 2> kept;
+            if (EPI == SLOPE) kept.fetch(p, m0, q.M - m0, n0 + c0, q.N - n0 - c0);
             if (!warp_wait(tfull(b), ph, lim)) break;
             tc_fence_after();
-            const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH;
-            if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0);
-            else if (EPI == GATED) gated_tile<BN, KEEP>(p, q, at, block, m0, n0);
-            else slope_tile<BN, KEEP == 2>(p, q, at, block, m0, n0);
+            if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0, c0);
+            else if (EPI == GATED) gated_tile<BN, KEEP>(p, q, at, block, m0, n0, c0);
+            else slope_tile<BN, KEEP == 2>(p, q, at, block, m0, n0, c0, kept);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) remote_arrive_cluster(lead_tempty);
-                else mbar_arrive(lead_tempty);
+                if (PAIR) remote_arrive_cluster(lead_tempty0 + 8u * b);
+                else mbar_arrive(lead_tempty0 + 8u * b);
             }
-            ph ^= 1;
+            side ^= 1;
+            if (++b == 2) { b = 0; ph ^= 1; }
         }
     }
     __syncwarp();
@@ -759,6 +846,11 @@ int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (!bit || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & bit)) {
+        // (a block launched with fewer registers than its warpgroups ask for would wait for ever)
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return launch_status();
+        if (attr.numRegs * ffn::THREADS < 128 * ffn::REGS_ISSUE + 32 * ffn::EPI_WARPS * ffn::REGS_EPILOGUE)
+            return SGEMM_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T_::SMEM) != cudaSuccess)
             return launch_status();
         __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
