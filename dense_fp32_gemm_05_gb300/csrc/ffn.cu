@@ -477,8 +477,8 @@ struct Fetched {
     }
 };
 
-// The kept values of a chunk of columns: fetched before the accumulators are waited
-// for, and a chunk ahead of the one that is computed.
+// The kept values of a chunk of columns: fetched a chunk ahead of the one that is
+// computed, across tiles.
 template <bool CODES>
 struct Kept {
     using E = typename std::conditional<CODES, uint8_t, __nv_bfloat16>::type;
@@ -498,9 +498,10 @@ struct Kept {
     }
 };
 
-template <int BN, bool CODES>
+// fetch_next(): the kept values of the first chunk of this warp's next tile.
+template <int BN, bool CODES, typename Next>
 __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0,
-                                           int c0, Kept<CODES> &kept) {
+                                           int c0, Kept<CODES> &kept, Next fetch_next) {
     const int rows = q.M - m0;
     uint8_t *bg = block, *bu = block + 32 * CH * 2, *bh = block + 2 * 32 * CH * 2;
 #pragma unroll 1
@@ -509,12 +510,17 @@ __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, ui
         const int64_t at = m0 * p.ldh + n0 + c;
         uint32_t r[CH];
         tmem_ld32(tmem + c, r);
-        if (rows <= 0) continue;
+        const bool last = c + 2 * CH >= BN || cols <= 2 * CH;
+        if (rows <= 0) {
+            if (last) fetch_next();
+            continue;
+        }
         kept.g.stash(bg, cols, p.kept_vec);
         kept.u.stash(bu, cols, p.kept_vec);
         const float sg = CODES ? __bfloat162float(kept.sg) : 1.0f, su = CODES ? __bfloat162float(kept.su) : 1.0f;
         __syncwarp();
-        if (c + 2 * CH < BN) kept.fetch(p, m0, rows, n0 + c + 2 * CH, cols - 2 * CH);
+        if (last) fetch_next();
+        else kept.fetch(p, m0, rows, n0 + c + 2 * CH, cols - 2 * CH);
         float g[CH], u[CH], h[CH];
         kept_values<CODES>(bg, sg, g);
         kept_values<CODES>(bu, su, u);
@@ -704,22 +710,36 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
         uint8_t *block = staging + (warp - 4) * STAGING;
         int b = 0, side = group;
         uint32_t ph = 0;
+        Kept<KEEP == 2> kept;
+        auto fetch_first = [&](int unit, int s) {
+            if (EPI != SLOPE || unit >= p.units) return;
+            int tm, tn;
+            const Product &q = p.product[tile_of(p, unit, tm, tn)];
+            const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, c = tn * WIDTH + s * CH;
+            kept.fetch(p, m0, q.M - m0, c, q.N - c);
+        };
+        fetch_first(first, side);
         for (int unit = first; unit < p.units; unit += step) {
             int tm, tn;
             const Product &q = p.product[tile_of(p, unit, tm, tn)];
             const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH, c0 = side * CH;
             const uint32_t at = lanes + (uint32_t)(b * BN);
-            Kept<KEEP == 2> kept;
-            if (EPI == SLOPE) kept.fetch(p, m0, q.M - m0, n0 + c0, q.N - n0 - c0);
             if (!warp_wait(tfull(b), ph, lim)) break;
             tc_fence_after();
             if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0, c0);
             else if (EPI == GATED) gated_tile<BN, KEEP>(p, q, at, block, m0, n0, c0);
-            else slope_tile<BN, KEEP == 2>(p, q, at, block, m0, n0, c0, kept);
+            else {
+                auto next = [&]() { fetch_first(unit + step, side ^ 1); };
+                // (a tile without a chunk for this warp: past the last column)
+                if (n0 + c0 >= q.N) next();
+                else slope_tile<BN, KEEP == 2>(p, q, at, block, m0, n0, c0, kept, next);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) remote_arrive_cluster(lead_tempty0 + 8u * b);
+                // (nothing but tensor-memory reads, which are complete, is ordered by it: a
+                // release would wait for this warp's stores)
+                if (PAIR) remote_arrive_relaxed(lead_tempty0 + 8u * b);
                 else mbar_arrive(lead_tempty0 + 8u * b);
             }
             side ^= 1;
