@@ -23,7 +23,7 @@ __all__ = [
     "exported_symbols", "TYPE_F32", "TYPE_BF16", "TYPE_E4M3", "TYPE_E5M2",
     "sgemm_fp8_quantize", "fp8_quantize", "sgemm_fp8", "sgemm_fp8_plan", "fp8_gemm",
     "sgemm_moe", "moe", "ACT_SILU", "ACT_GELU", "sgemm_ffn", "ffn", "sgemm_ffn_backward",
-    "ffn_backward", "sgemm_ffn_plan",
+    "ffn_backward", "sgemm_ffn_plan", "sgemm_q4_quantize", "q4_quantize", "sgemm_q4", "q4_gemm",
 ]
 
 SGEMM_OK = 0
@@ -132,6 +132,10 @@ def _declare(lib):
     lib.sgemm_ffn_backward.restype = i32
     lib.sgemm_ffn_plan.argtypes = [i64, i64, i64, i32, i32, ip, ip]
     lib.sgemm_ffn_plan.restype = i32
+    lib.sgemm_q4_quantize.argtypes = [i64, i64, vp, i32, i64, i32, vp, i64, vp, vp, i64, vp, i32, i64, vp]
+    lib.sgemm_q4_quantize.restype = i32
+    lib.sgemm_q4.argtypes = [i64, i64, i64, vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, i32, i64, vp]
+    lib.sgemm_q4.restype = i32
 
 
 def load():
@@ -160,7 +164,7 @@ def exported_symbols(lib=None):
             "sgemm_ffma_static_scratch", "sgemm_timing_enable", "sgemm_timing_read",
             "sgemm_launch_count", "sgemm_probe_tf32_rate", "sgemm_fp8_quantize",
             "sgemm_fp8", "sgemm_fp8_plan", "sgemm_moe", "sgemm_ffn", "sgemm_ffn_backward",
-            "sgemm_ffn_plan"]
+            "sgemm_ffn_plan", "sgemm_q4_quantize", "sgemm_q4"]
 
 
 def _b(t: str) -> bytes:
@@ -723,3 +727,125 @@ def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgat
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_ffn_backward")
     return dx, dgate, dup, ddown
+
+
+def sgemm_q4_quantize(rows, cols, X, x_type, ldx, group, Q, ldq, S, Z, lds, V=0, v_type=TYPE_F32, ldv=1,
+                      stream=None) -> int:
+    """4-bit codes Q, scales S and zero codes Z of X; device addresses (int), Z or V 0 = none."""
+    return load().sgemm_q4_quantize(rows, cols, X, x_type, ldx, group, Q, ldq, S, Z or None, lds, V or None,
+                                    v_type, ldv, _stream(stream))
+
+
+def sgemm_q4(M, N, K, X, x_type, ldx, Q, S, Z, Q2, S2, Z2, ldq, lds, group, activation, C, c_type, ldc,
+             stream=None) -> int:
+    """C = X W^T or act(X W^T) * (X W2^T) with 4-bit matrices; device addresses (int), 0 = none."""
+    return load().sgemm_q4(M, N, K, X, x_type, ldx, Q, S, Z or None, Q2 or None, S2 or None, Z2 or None, ldq, lds,
+                           group, activation, C, c_type, ldc, _stream(stream))
+
+
+def _bytes(name, t, shape, device):
+    """(address, row stride) of a matrix of bytes."""
+    import torch
+
+    if t.dim() != 2 or t.dtype != torch.uint8 or tuple(t.shape) != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor of uint8 of shape {shape} on the operands' device")
+    ld, unit = t.stride()
+    if (unit != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+        raise ValueError(f"{name} must have unit stride along its last dimension and rows that do not overlap")
+    return t.data_ptr(), (ld if shape[0] > 1 else shape[1]) or 1
+
+
+def q4_quantize(W, group=128, symmetric=True, Q=None, S=None, Z=None, V=None, stream=None):
+    """(codes, scales, zero codes) of a 2-D float32 or bfloat16 CUDA tensor, 4 bits each.
+
+    Codes are uint8 of shape (rows, ceil(cols / 2)), the even column in a byte's low half;
+    new ones have rows that start on 16 bytes, as ``q4_gemm`` reads them.  Scales are
+    float32 and zero codes uint8 of shape (ceil(cols / group), rows), for groups of 32, 64 or 128 in a
+    row; ``symmetric``: no zero codes, and the result's third is None.  ``Q``, ``S``, ``Z`` take
+    buffers to write into; new ones belong to the stream of the call.  ``V`` (W's shape,
+    float32 or bfloat16) takes the codes' values.  The tensors are on the current device.
+    Asynchronous on ``stream`` (default: torch's current stream); raises SgemmError on any
+    non-zero status.
+    """
+    import torch
+
+    device = W.get_device()
+    pw, w_type, ldw, rows, cols = _matrix("W", W, _FLOATS)
+    _check_device(device)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if symmetric and Z is not None:
+        raise ValueError("symmetric codes have no zero codes")
+    half, groups = (cols + 1) // 2, (cols + group - 1) // group
+    if Q is None:
+        Q = _new((rows, (half + 15) // 16 * 16), torch.uint8, W.device, stream)[:, :half]
+    if S is None:
+        S = _new((groups, rows), torch.float32, W.device, stream)
+    if Z is None and not symmetric:
+        Z = _new((groups, rows), torch.uint8, W.device, stream)
+    pq, ldq = _bytes("Q", Q, (rows, half), device)
+    ps, _, lds = _of_shape("S", S, _SCALES, (groups, rows), device)
+    pz = None
+    if Z is not None:
+        pz, ldz = _bytes("Z", Z, (groups, rows), device)
+        if ldz != lds:
+            raise ValueError("S and Z must have the same strides")
+    pv, v_type, ldv = (None, TYPE_F32, 1) if V is None else _of_shape("V", V, _FLOATS, (rows, cols), device)
+    st = load().sgemm_q4_quantize(rows, cols, pw, w_type, ldw, group, pq, ldq, ps, pz, lds, pv, v_type, ldv,
+                                  _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_q4_quantize")
+    return Q, S, Z
+
+
+def q4_gemm(X, Q, S, C=None, Z=None, Q2=None, S2=None, Z2=None, group=128, activation=None, dtype=None,
+            stream=None):
+    """X W^T, or act(X W^T) * (X W2^T), for a few rows of X and 4-bit matrices.
+
+    X: M x K, bfloat16 or float32.  Q, S, Z (and Q2, S2, Z2 with the same strides): codes,
+    scales and zero codes (None: symmetric) of N x K matrices as ``q4_quantize`` makes them
+    with that ``group``; rows of codes start on 16 bytes.  ``activation``: of two matrices,
+    ACT_SILU by default.  C: M x N, bfloat16 or float32, written and returned; a new one is
+    of ``dtype`` (default X's) and belongs to the stream of the call.  The weights are
+    read once for each 64 rows of X (21 in float32).  The tensors are on the current
+    device.  Asynchronous on ``stream`` (default: torch's current stream); raises
+    SgemmError on any non-zero status.
+    """
+    device = X.get_device()
+    px, x_type, ldx, M, K = _matrix("X", X, _FLOATS)
+    _check_device(device)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    N = Q.shape[0]
+    codes, scales = (N, (K + 1) // 2), ((K + group - 1) // group, N)
+    pq, ldq = _bytes("Q", Q, codes, device)
+    ps, _, lds = _of_shape("S", S, _SCALES, scales, device)
+    pz = p2 = ps2 = pz2 = None
+    if Z is not None:
+        pz, ldz = _bytes("Z", Z, scales, device)
+        if ldz != lds:
+            raise ValueError("S and Z must have the same strides")
+    if Q2 is not None:
+        p2, ldq2 = _bytes("Q2", Q2, codes, device)
+        ps2, _, lds2 = _of_shape("S2", S2, _SCALES, scales, device)
+        if (Z2 is None) != (Z is None):
+            raise ValueError("Z and Z2 are both given or neither")
+        ldz2 = lds
+        if Z2 is not None:
+            pz2, ldz2 = _bytes("Z2", Z2, scales, device)
+        if ldq2 != ldq or lds2 != lds or ldz2 != lds:
+            raise ValueError("both matrices must have the same strides")
+    elif S2 is not None or Z2 is not None:
+        raise ValueError("S2 and Z2 belong to Q2")
+    if activation is None:
+        activation = ACT_NONE if Q2 is None else ACT_SILU
+    if C is None:
+        C = _new((M, N), dtype or X.dtype, X.device, stream)
+    elif dtype is not None and dtype != C.dtype:
+        raise ValueError("C is not of the given dtype")
+    pc, c_type, ldc = _of_shape("C", C, _FLOATS, (M, N), device)
+    st = load().sgemm_q4(M, N, K, px, x_type, ldx, pq, ps, pz, p2, ps2, pz2, ldq, lds, group, activation, pc, c_type,
+                         ldc, _current_stream(device) if stream is None else _stream(stream))
+    if st != SGEMM_OK:
+        raise SgemmError(st, "sgemm_q4")
+    return C

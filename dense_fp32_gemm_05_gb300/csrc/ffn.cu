@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "act.cuh"
+#include "few.h"
 #include "ffn_plan.h"
 #include "fp8.cuh"
 #include "plan.h"
@@ -60,7 +61,8 @@ constexpr int CHUNK = 64 * BK * 2;             // 64 rows or columns x 64 k
 constexpr int CH = 32;                         // columns of the epilogue at a time
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
-constexpr int STAGING = 3 * 32 * CH * 2;       // bytes of an epilogue warp: three bf16 blocks, or one fp32
+constexpr int BLOCK = 32 * CH * 2;             // bytes of 32 rows x 32 bf16 columns
+constexpr int STAGING = 2 * BLOCK;             // of an epilogue warp: two bf16 blocks, or one fp32
 constexpr int REGS_ISSUE = 56, REGS_EPILOGUE = 224;      // 384 x 168 = 128 x 56 + 256 x 224
 constexpr int SMEM_MAX = 232448;
 constexpr int BAR_BYTES = 256;
@@ -90,7 +92,8 @@ struct Product {
 struct Params {
     Maps maps[PRODUCTS];
     Product product[PRODUCTS];
-    int count, units, stages;
+    int count, units;
+    int first_units, extra;                    // see unit_of
     int act;
     // kept values, GATED and SLOPE
     void *g, *u;
@@ -151,10 +154,28 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// The k-th tile of a lane (a CTA or pair, of `lanes`), or units: none.  The first
+// product's tiles (dx: the longest sums) go round the lanes; what is left goes first
+// to the lanes that got one fewer of them, `extra` tiles each, then round all of them, from the
+// last lane down.  (Plain rounds gave some lanes a long tile and as many short ones
+// as the others: 49 us, not 43, for the gradients of 777 x 1000 x 2501.)
+__device__ __forceinline__ int unit_of(const Params &p, int k, int lane, int lanes) {
+    const int mine = (p.first_units - lane + lanes - 1) / lanes;
+    if (k < mine) return lane + k * lanes;
+    const int more = p.first_units % lanes;        // lanes below have one more of the first
+    int j = k - mine, unit = p.first_units;
+    if (lane >= more) {
+        if (j < p.extra) return min(unit + j * (lanes - more) + lane - more, p.units);
+        j -= p.extra;
+    }
+    unit += p.extra * (lanes - more) + j * lanes + lanes - 1 - lane;
+    return min(unit, p.units);
+}
+
 // Product and tile of unit `unit`: GROUP tile rows of the result at a time, so
 // that the tiles in flight share operand panels in L2.
 __device__ __forceinline__ int tile_of(const Params &p, int unit, int &tm, int &tn) {
-    constexpr int GROUP = 8;
+    constexpr int GROUP = 16;
     int i = 0;
     while (i + 1 < p.count && unit >= p.product[i + 1].first) ++i;
     const Product &q = p.product[i];
@@ -399,28 +420,29 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
         if (rows <= 0) continue;
         const int cols = q.N - n0 - c;
         const int64_t row = m0, col = n0 + c;
-        uint8_t *bg = block, *bu = block + 32 * CH * 2, *bh = block + 2 * 32 * CH * 2;
+        uint8_t *other = block + BLOCK;
+        const int64_t at = row * p.ld_kept + col;
         if (KEEP == 1) {
-            put_bf16(bg, g);
-            put_bf16(bu, u);
+            put_bf16(block, g);
+            put_bf16(other, u);
+            __syncwarp();
+            put_rows(block, static_cast<__nv_bfloat16 *>(p.g) + at, p.ld_kept, rows, cols, p.kept_vec);
+            put_rows(other, static_cast<__nv_bfloat16 *>(p.u) + at, p.ld_kept, rows, cols, p.kept_vec);
         } else if (KEEP == 2) {
-            put_codes(bg, g, ig);
-            put_codes(bu, u, iu);
+            put_codes(block, g, ig);
+            put_codes(other, u, iu);
+            __syncwarp();
+            put_rows(block, static_cast<uint8_t *>(p.g) + at, p.ld_kept, rows, cols, p.kept_vec);
+            put_rows(other, static_cast<uint8_t *>(p.u) + at, p.ld_kept, rows, cols, p.kept_vec);
         }
         act::with(p.act, [&](auto a) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) g[i] = act::value<a.value>(g[i]) * u[i];
         });
-        put_bf16(bh, g);
         __syncwarp();
-        put_rows(bh, p.h + row * p.ldh + col, p.ldh, rows, cols, true);
-        if (KEEP == 1) {
-            put_rows(bg, static_cast<__nv_bfloat16 *>(p.g) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-            put_rows(bu, static_cast<__nv_bfloat16 *>(p.u) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-        } else if (KEEP == 2) {
-            put_rows(bg, static_cast<uint8_t *>(p.g) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-            put_rows(bu, static_cast<uint8_t *>(p.u) + row * p.ld_kept + col, p.ld_kept, rows, cols, p.kept_vec);
-        }
+        put_bf16(block, g);
+        __syncwarp();
+        put_rows(block, p.h + row * p.ldh + col, p.ldh, rows, cols, true);
         __syncwarp();
     }
 }
@@ -503,7 +525,7 @@ template <int BN, bool CODES, typename Next>
 __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0,
                                            int c0, Kept<CODES> &kept, Next fetch_next) {
     const int rows = q.M - m0;
-    uint8_t *bg = block, *bu = block + 32 * CH * 2, *bh = block + 2 * 32 * CH * 2;
+    uint8_t *bg = block, *bu = block + BLOCK;
 #pragma unroll 1
     for (int c = c0; c < BN && n0 + c < q.N; c += 2 * CH) {
         const int cols = q.N - n0 - c;
@@ -538,11 +560,13 @@ __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, ui
         });
         put_bf16(bg, g);
         put_bf16(bu, u);
-        put_bf16(bh, h);
         __syncwarp();
         put_rows(bg, p.dg + at, p.ldh, rows, cols, true);
         put_rows(bu, p.du + at, p.ldh, rows, cols, true);
-        put_rows(bh, p.h + at, p.ldh, rows, cols, true);
+        __syncwarp();
+        put_bf16(bg, h);
+        __syncwarp();
+        put_rows(bg, p.h + at, p.ldh, rows, cols, true);
         __syncwarp();
     }
 }
@@ -571,8 +595,9 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0u;
-    const int first = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
-    const int step = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    const int self = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const int lanes = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    auto unit_at = [&](int k) { return unit_of(p, k, self, lanes); };
     const uint64_t lim = p.wait_ns;
     auto publish = [&](int which, int n) {         // to both CTAs
         if (lane == 0) {
@@ -617,7 +642,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
             // ------------------------------------------------ TMA producer
             int s = 0, filled = 0;
             uint32_t ph = 1;
-            for (int unit = first; ok && unit < p.units; unit += step) {
+            int unit;
+            for (int k = 0; ok && (unit = unit_at(k)) < p.units; ++k) {
                 int tm, tn;
                 const int i = tile_of(p, unit, tm, tn);
                 const Product &q = p.product[i];
@@ -630,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
                     const bool second = kb >= nk0;
-                    const int k = (second ? kb - nk0 : kb) * BK;
+                    const int at = (second ? kb - nk0 : kb) * BK;
                     const uint32_t a = smem0 + (uint32_t)(s * T_::STAGE), b = a + A_BYTES;
                     const uint32_t bar = PAIR ? leader_addr(full(s)) : full(s);
                     const CUtensorMap *ma = &maps.a[second], *mb = &maps.b[EPI == GATED ? (int)rank : (int)second];
@@ -641,19 +667,19 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
                     if (elect_one()) {
                         if (rank == 0) mbar_expect_tx(full(s), (PAIR ? 2 : 1) * T_::STAGE);
                         if (a_mn) {
-                            load(a, ma, m, k);
-                            load(a + CHUNK, ma, m + 64, k);
+                            load(a, ma, m, at);
+                            load(a + CHUNK, ma, m + 64, at);
                         } else {
-                            load(a, ma, k, m);
+                            load(a, ma, at, m);
                         }
                         if (EPI == GATED) {
-                            load(b, mb, k, n);
-                            if (!PAIR) load(b + B_ROWS * BK, &maps.b[1], k, n);
+                            load(b, mb, at, n);
+                            if (!PAIR) load(b + B_ROWS * BK, &maps.b[1], at, n);
                         } else if (b_mn) {
 #pragma unroll
-                            for (int j = 0; j < B_ROWS; j += 64) load(b + (uint32_t)(j / 64 * CHUNK), mb, n + j, k);
+                            for (int j = 0; j < B_ROWS; j += 64) load(b + (uint32_t)(j / 64 * CHUNK), mb, n + j, at);
                         } else {
-                            load(b, mb, k, n);
+                            load(b, mb, at, n);
                         }
                     }
                     __syncwarp();
@@ -667,7 +693,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
             if (rank == 0) {
                 int s = 0, b = 0, issued = 0;
                 uint32_t ph = 0, bph = 1;
-                for (int unit = first; ok && unit < p.units; unit += step) {
+                int unit;
+                for (int k = 0; ok && (unit = unit_at(k)) < p.units; ++k) {
                     int tm, tn;
                     const Product &q = p.product[tile_of(p, unit, tm, tn)];
                     const uint32_t a_step = q.a_mn ? 2048u >> 4 : 32u >> 4, b_step = q.b_mn ? 2048u >> 4 : 32u >> 4;
@@ -705,7 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
         // Chunks of 32 columns alternate between the two warpgroups, and the first
         // changes sides from tile to tile (a narrow GATED tile is a single chunk).
         const int quad = warp & 3, group = (warp - 4) >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t tmem_rows = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t lead_tempty0 = PAIR ? leader_addr(tempty(0)) : tempty(0);
         uint8_t *block = staging + (warp - 4) * STAGING;
         int b = 0, side = group;
@@ -718,18 +745,19 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
             const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, c = tn * WIDTH + s * CH;
             kept.fetch(p, m0, q.M - m0, c, q.N - c);
         };
-        fetch_first(first, side);
-        for (int unit = first; unit < p.units; unit += step) {
+        fetch_first(unit_at(0), side);
+        int unit;
+        for (int k = 0; (unit = unit_at(k)) < p.units; ++k) {
             int tm, tn;
             const Product &q = p.product[tile_of(p, unit, tm, tn)];
             const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH, c0 = side * CH;
-            const uint32_t at = lanes + (uint32_t)(b * BN);
+            const uint32_t at = tmem_rows + (uint32_t)(b * BN);
             if (!warp_wait(tfull(b), ph, lim)) break;
             tc_fence_after();
             if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0, c0);
             else if (EPI == GATED) gated_tile<BN, KEEP>(p, q, at, block, m0, n0, c0);
             else {
-                auto next = [&]() { fetch_first(unit + step, side ^ 1); };
+                auto next = [&]() { fetch_first(unit_at(k + 1), side ^ 1); };
                 // (a tile without a chunk for this warp: past the last column)
                 if (n0 + c0 >= q.N) next();
                 else slope_tile<BN, KEEP == 2>(p, q, at, block, m0, n0, c0, kept, next);
@@ -876,8 +904,7 @@ int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
         __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
-    const int lanes = std::max(1, sms / (PAIR ? 2 : 1));
-    cfg.gridDim = dim3((unsigned)(std::min(p.units, lanes) * (PAIR ? 2 : 1)));
+    cfg.gridDim = dim3((unsigned)(ffn_lanes(PAIR ? 2 : 1, p.units, sms) * (PAIR ? 2 : 1)));
     cfg.blockDim = dim3((unsigned)ffn::THREADS);
     cfg.dynamicSmemBytes = (size_t)T_::SMEM;
     cfg.stream = s;
@@ -915,6 +942,14 @@ int launch_variant(int variant, const ffn::Params &p, int sms, cudaStream_t s, b
 int launch(Launch &l, int keep, int sms, cudaStream_t s, bool dep) {
     if (!l.ok || l.units > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     l.p.units = (int)l.units;
+    l.p.first_units = l.p.count > 1 ? l.p.product[1].first : l.p.units;
+    l.p.extra = 0;
+    if (l.p.count > 1) {
+        // the tiles of the others that take as long as one of the first
+        const int lanes = ffn_lanes(kFfnTiles[l.variant].ctas, l.p.units, sms), less = lanes - l.p.first_units % lanes;
+        const double ratio = ffn_tile_time(l.variant, l.p.product[0].nk) / ffn_tile_time(l.variant, l.p.product[1].nk);
+        if (less < lanes) l.p.extra = (int)std::min(ratio + 0.5, (double)((l.p.units - l.p.first_units) / less));
+    }
     l.p.wait_ns = tc_wait_limit();
     if (l.epi == ffn::STORE) return launch_variant<ffn::STORE, 0>(l.variant, l.p, sms, s, dep);
     if (l.epi == ffn::SLOPE)
@@ -985,6 +1020,21 @@ int run_forward(const Block &b, void *y, int64_t ldy, cudaStream_t s) {
     int sms = 0;
     int st = usable_device(&sms);
     if (st != SGEMM_OK) return st;
+    if (b.keep == 0 && b.T <= kFfnFewTokens) {
+        FewCall c{};
+        c.M = b.T; c.N = b.F; c.K = b.D;
+        c.x = b.x.p; c.ldx = b.x.ld;
+        c.w = b.gate.p; c.w2 = b.up.p; c.ldw = 2 * b.gate.ld;
+        c.act = b.act;
+        c.c = b.h; c.ldc = b.ldh;
+        st = run_few(c, sms, s, false);
+        if (st != SGEMM_OK) return st;
+        c.N = b.D; c.K = b.F;
+        c.x = b.h; c.ldx = b.ldh;
+        c.w = b.down.p; c.w2 = nullptr; c.ldw = 2 * b.down.ld;
+        c.c = y; c.ldc = ldy;
+        return run_few(c, sms, s, true);
+    }
     const FfnPlan pl = ffn_plan(b.T, b.D, b.F, b.keep == 2, sms);
     Launch gated(pl.variant[0], ffn::GATED);
     b.fill(gated.p);

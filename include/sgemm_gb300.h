@@ -616,6 +616,58 @@ int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *dy, int64_t 
 int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows,
                    int *out_cols);
 
+/* ------------------------------------------------------------------------
+ * Matrices of 4-bit codes with a scale for each group of a row, for serving.
+ *
+ * A matrix of rows x cols is codes, two in a byte (column 2j in the low half of byte j
+ * of its row, column 2j + 1 in the high half), fp32 scales S and, unless it is
+ * symmetric, zero codes Z (a byte each, 0 .. 15), for each group (32, 64 or 128) of neighbours
+ * in a row:
+ *
+ *   value(r, c) = (code(r, c) - zero) * scale,  scale = S[(c / group) * lds + r],
+ *   zero = Z[(c / group) * lds + r], or 8 where Z is NULL
+ *
+ * sgemm_q4_quantize - codes, scales and zero codes of X (row-major, ldx >= cols,
+ * SGEMM_TYPE_F32 or SGEMM_TYPE_BF16):
+ *
+ *   Z NULL  scale = max(amax / 7, 2^-126),  zero = 8
+ *   else    scale = max(high / 15 - low / 15, 2^-126), high and low the extremes of the
+ *           group's finite values and 0;  zero = rint(-low * (1 / scale))
+ *   code    = rint(x * (1 / scale)) + zero, cut to 0 .. 15; NaN: zero
+ *
+ * each operation in fp32, rounded to nearest; infinities and NaN enter no scale.
+ * V, unless NULL: the codes' values, of v_type, ldv >= cols (what is lost is X - V; for
+ * training through the quantiser).  ldq >= ceil(cols / 2) bytes; a ldq and base that
+ * are multiples of 16 let sgemm_q4 read the codes.  An odd row's last half byte is 0.
+ * Any alignment of X's and V's elements.  Outputs may not overlap X.  rows or cols
+ * zero: nothing is done.  Returns SGEMM_OK, a negative argument index or an
+ * sgemm_status.
+ */
+int sgemm_q4_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int64_t ldx, int group,
+                      void *Q, int64_t ldq, float *S, uint8_t *Z, int64_t lds, void *V, int v_type,
+                      int64_t ldv, sgemm_stream_t stream);
+
+/*
+ * sgemm_q4 - the product of a few rows of x (decode) with 4-bit matrices:
+ *
+ *   Q2 NULL  C = X W^T                          W N x K (Q, S, Z), activation SGEMM_ACT_NONE
+ *   else     C = act(X W^T) * (X W2^T)          W2 N x K (Q2, S2, Z2): a gated block's gate and up
+ *
+ *   X   M x K, SGEMM_TYPE_BF16 or SGEMM_TYPE_F32, ldx >= K;  C  M x N, either type, ldc >= N
+ *   Q, Q2  both with row stride ldq bytes; 16-byte aligned, ldq a multiple of 16 (else
+ *          SGEMM_ERR_UNSUPPORTED); scales and zero codes with lds >= N; Z and Z2 both or neither
+ *
+ * The weights are read once for each 64 rows of bf16 X (21 of fp32), as they are.
+ * Values of x times codes are exact (fp32 x as three bf16 parts that add up to it) and added
+ * in fp32 within a group; its sum times the scale is added in fp32: fp32 accuracy
+ * throughout, C is rounded once.  A fixed order, no atomics, no workspace.
+ * NaN and infinities of X give the IEEE result.  K == 0: C = 0.  Execution and errors as sgemm.
+ */
+int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_type, int64_t ldx, const void *Q,
+             const float *S, const uint8_t *Z, const void *Q2, const float *S2, const uint8_t *Z2,
+             int64_t ldq, int64_t lds, int group, int activation, void *C, int c_type, int64_t ldc,
+             sgemm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
