@@ -807,7 +807,7 @@ def q4_gemm(X, Q, S, C=None, Z=None, Q2=None, S2=None, Z2=None, group=128, activ
     with that ``group``; rows of codes start on 16 bytes.  ``activation``: of two matrices,
     ACT_SILU by default.  C: M x N, bfloat16 or float32, written and returned; a new one is
     of ``dtype`` (default X's) and belongs to the stream of the call.  The weights are
-    read once for each 64 rows of X (21 in float32).  The tensors are on the current
+    read once for each 64 rows of X (32 in float32).  The tensors are on the current
     device.  Asynchronous on ``stream`` (default: torch's current stream); raises
     SgemmError on any non-zero status.
     """

@@ -32,38 +32,52 @@ struct FewCall {
 int run_few(const FewCall &c, int sms, cudaStream_t s, bool dep);
 
 // How a call is cut: blocks of 8 nt columns (rows of x, times their parts), wk warps of a
-// CTA and ks CTAs of a cluster along the sum, `depth` chunks of k that a CTA holds of x at a time.
+// CTA and ks CTAs of a cluster along the sum, `depth` stages of k that a CTA holds of x at a
+// time, `ring` stages of weights that each warp has under way.
 struct FewPlan {
-    int nt, wk, ks, depth;
+    int nt, wk, ks, depth, ring;
 };
 
 constexpr int kFewWarps = 8;
+constexpr int kFewStage = 4096;        // bytes of weights: 128 of each of 32 rows
 
-inline int64_t few_chunk(int group) { return group ? 128 : 32; }       // k: 64 bytes of a row
+inline int64_t few_stage_k(int group) { return group ? 256 : 64; }
+inline int few_parts(int group, bool x_f32) { return group && x_f32 ? 2 : 1; }
+// Shared memory of a stage of x: its pieces for `cols` columns, and for 4 bits their units for
+// all columns of a block; and of the partial sums, the warps' and the CTA's.
+inline int64_t few_x_bytes(int group, int64_t cols, int nt) { return few_stage_k(group) * 2 * cols + (group ? 2 * 32 * nt : 0); }
+inline int64_t few_sums_bytes(int nt, int64_t rows, int wk) {
+    return (int64_t)kFewWarps * nt * 8 * 36 * 4 + 32 * (kFewWarps / wk) * rows * 4;
+}
 
 inline FewPlan few_plan(int64_t M, int64_t N, int64_t K, int parts, bool gated, int group, int sms) {
     FewPlan p;
-    const int64_t chunks = (K + few_chunk(group) - 1) / few_chunk(group);
+    const int64_t stages = (K + few_stage_k(group) - 1) / few_stage_k(group);
     // columns for all rows of x, where their tiles' accumulators fit the registers
-    const int64_t cols = M * parts;
-    const int tiles[] = {1, 2, 4, 6, 8};
-    p.nt = 8;
-    for (int t : tiles)
-        if (cols <= 8 * t) {
-            p.nt = t;
-            break;
-        }
+    const int64_t all = M * parts;
+    p.nt = all <= 8 ? 1 : all <= 16 ? 2 : all <= 32 ? 4 : 8;
+    const int64_t cols = std::min<int64_t>(M, 8 * p.nt / parts) * parts, x_stage = few_x_bytes(group, cols, p.nt);
     // Warps for the rows (32 each, or 16 of both matrices), times slices of the sum until
-    // there are twelve for each SM.
+    // there would be more than the GPU holds (a second round of CTAs starts late).  Few columns: the slices are a CTA's warps; with
+    // more, a cluster's CTAs first, since each CTA lays out x for its rows.
     const int64_t rows = (N + (gated ? 15 : 31)) / (gated ? 16 : 32);
     int64_t slices = 1;
-    while (slices < 64 && rows * slices < (int64_t)sms * 12 && 2 * slices <= chunks) slices *= 2;
-    p.wk = (int)std::min<int64_t>(slices, kFewWarps);
-    p.ks = (int)(slices / p.wk);
-    // x in shared memory: the CTA's whole range where it fits
-    const int64_t chunk_bytes = few_chunk(group) * 16 * p.nt, most = p.nt <= 2 ? 65536 : 131072;
-    const int64_t mine = (chunks + p.ks - 1) / p.ks;
-    p.depth = (int)std::max<int64_t>(1, std::min<int64_t>(mine, most / chunk_bytes));
+    const int64_t warps = (int64_t)sms * kFewWarps * (p.nt <= 2 ? 2 : 1);        // that are resident
+    while (slices < 64 && 2 * rows * slices <= warps && 2 * slices <= stages) slices *= 2;
+    if (p.nt == 1) {
+        p.wk = (int)std::min<int64_t>(slices, kFewWarps);
+        p.ks = (int)(slices / p.wk);
+    } else {
+        // (clusters of 8 whole SMs: some of 16 have to wait for another to end)
+        p.ks = (int)std::min<int64_t>(slices, p.nt == 2 ? 8 : 4);
+        p.wk = (int)(slices / p.ks);
+    }
+    // Shared memory, of which a CTA has half an SM's with few columns: the ring takes up to
+    // three stages of each warp, x its whole range where that leaves two.
+    const int64_t most = p.nt <= 2 ? 110 * 1024 : 216 * 1024, one = (int64_t)kFewWarps * kFewStage;
+    const int64_t mine = (stages + p.ks - 1) / p.ks, each = (mine + p.wk - 1) / p.wk;
+    p.depth = (int)std::max<int64_t>(1, std::min<int64_t>(mine, (most - 2 * one) / x_stage));
+    p.ring = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(each, 4), (most - p.depth * x_stage) / one));
     return p;
 }
 

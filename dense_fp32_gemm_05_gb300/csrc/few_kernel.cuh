@@ -3,26 +3,41 @@
 //
 //   c(m,n) = sum over groups b of s(n,b) (sum_{k in b} x(m,k) (code(n,k) - zero(n,b)))
 //
-// Bound by the weights' stream, so the kernel is built around it.  A warp holds 32
-// rows of W (or 16 of each of two matrices) and walks chunks of 64 bytes of each row, several
-// chunks' 16-byte loads under way in registers (no staging: nothing else
-// reads them).  The products are mma.sync.m16n8k16 (bf16, exact; fp32 sums): W's rows
-// are the MMA's 16 rows, x's rows its 8 columns.  Which k an MMA calls its first is
-// free as long as both operands agree, so a lane's 16 neighbouring bytes are its share of the
-// fragments as they lie; x is laid out once in shared memory in the order in
-// which lanes read it.
-//   4 bits: the codes of a word come out in four pairs, a code in each half, by a shift and
-//   one logic operation that also sets the exponent of 128: 128 + code, exact in bf16;
-//   128 + zero is subtracted (exact), so that nothing cancels and infinities in x keep
-//   their meaning: 11 instructions for 8 codes.  An MMA never spans two groups; a
-//   group's sum is scaled into the fp32 accumulator.
-//   x in fp32: three bf16 parts that add up to it exactly, in columns of their own.
-// The sum is cut over the warps of a CTA (which take chunks in turn, so that neighbours in
+// Bound by the weights' stream, and with 4 bits nearly as much by the instructions that take
+// them apart.  A warp holds 32 rows of W (or 16 of each of two matrices) and walks stages of
+// 128 bytes of each row, brought by TMA into a ring of its own: what is under way does
+// not depend on how far the warp is, and starts before x is there; a row's or the
+// matrix's end reads as zeros.  The products are mma.sync (exact products, fp32 sums): W's
+// rows are the MMA's 16 rows, x's rows its 8 columns.  Which k an MMA calls its first is
+// free as long as both operands agree, so a lane's neighbouring bytes are its share of the
+// fragments as they lie; x is laid out once in shared memory in the order in which
+// lanes read it.
+//   4 bits: the codes of a word come out by one shift and four logic operations, which also
+//   set the exponent of 1024 in each half: 1024 + code, or 1024 + 16 code for the upper four
+//   bits of a byte, exact in fp16; the same with the zero code is subtracted (exact), so that
+//   nothing cancels and infinities in x keep their meaning; x is divided by 16 where codes
+//   are 16 times larger.  x is held in fp16, each block of 128 of a row times a power of two
+//   that brings its largest value to 2^14 .. 2^15: bf16 as it is, but for values below 2^-27 of
+//   the block's largest; fp32 in two parts, in columns of their own, the second 2^11
+//   times what the first leaves.  An MMA never spans two groups; a group's sum is scaled
+//   into the fp32 accumulator.
+//   Tried for 1 x 16384 x 8192, which takes FIGURE us: codes as bf16 numbers, 128 + code (11
+//   operations a word, not 9), 27 us; as E4M3 bytes (3, but the MMA is made of conversions and
+//   fp16 MMAs) 29; zero codes taken off a group's sum instead (5 a word, but fp32 results
+//   2e-6 off, four times as much as fp32 arithmetic) 25, with loads into registers.  A code's
+//   bits alone are an fp16 number, too, but a subnormal one, which the MMA aligns with the
+//   smallest normal numbers: sums lose up to 7 bits (1.4e-6 off).
+//   8-bit integer MMAs take 65 clocks each, 8 times these.
+// The sum is cut over the warps of a CTA (which take stages in turn, so that neighbours in
 // memory are read together) and over a cluster of CTAs; the partial sums meet
 // through (distributed) shared memory in a fixed order: no workspace, no atomics.
+// Waits for TMA are bounded; where one runs out the error word is set, and the warp leaves
+// after what it has under way has landed (waited for, again bounded).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -32,188 +47,213 @@
 #include "plan.h"
 #include "ptx_util.cuh"
 #include "tc_gemm.h"
+#include "tc_ptx.cuh"
 
 namespace sgemm_gb300 {
 namespace few {
 
+using namespace tc;
+
 constexpr int WARPS = kFewWarps;
 constexpr int THREADS = 32 * WARPS;
+constexpr int STAGE = kFewStage;
+constexpr int MOST_RING = 4;
 constexpr int RED = 36;                        // floats of a column of 32 partial sums: no bank twice
+constexpr uint64_t kDrainNs = 1000000000ull;
 
 struct Params {
     const void *x;
     int64_t ldx;
-    const uint8_t *w[2];                       // the warp's two tiles of 16 rows: of one matrix or of two
-    int64_t ldw;
     const float *s[2];
     const uint8_t *z[2];
-    int64_t lds;
+    uint32_t lds;
     void *c;
     int64_t ldc;
     int M, N, K;
-    int gated, act, c_f32, x_f32, x_vec;
+    int gated, act, c_f32, c_vec, x_f32, x_vec;
     int per_block;                             // rows of x in a block of columns
-    int wk, ks, chunks, depth;
+    int wk, ks, stages, depth, ring;
+    unsigned int *error;                       // device error word
+    unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ uint4 stream16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 stream8(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint32_t stream4(const void *p) {
-    uint32_t v;
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
-}
-
+template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// (word & mask) | the exponents of 1024, in one operation (as C++ it became two, each with a
+// constant of its own).
+__device__ __forceinline__ uint32_t codes_of(uint32_t word, uint32_t mask) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word), "r"(mask), "r"(0x64006400u));
+    return v;
+}
 __device__ __forceinline__ uint32_t subtract(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&v);
+    uint32_t v;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(a), "r"(b));
+    return v;
 }
 
-// G: 0 bf16, else the group.  A lane's words of a row's 64 bytes: word i holds the values from
-// k_of(i, t) on, 2 of bf16 or 8 codes, t the lane's place among the four of a row.
+// G: 0 bf16, else the group.  A stage is two chunks of 64 bytes of a row, of which a lane
+// has four words; t is its place among the four lanes of a row.
 template <int G>
 struct Row {
     static constexpr int KC = G ? 128 : 32;                // k of a chunk
-    static constexpr int WORDS = 4;
     static constexpr int GROUPS = G ? 128 / (G ? G : 1) : 1;   // of a chunk
-    static constexpr int IN_GROUP = WORDS / GROUPS;        // words of a lane in a group
-    static constexpr int UNITS = G ? 4 : 1;                // 16-byte pieces of x for a lane and column
-    // the first k of piece i of x (8 values): a word of codes, or all of a lane's bf16
+    static constexpr int IN_GROUP = 4 / GROUPS;            // words of a lane in a group
+    static constexpr int UNITS = G ? 4 : 1;                // 16-byte pieces of x for a lane, column and chunk
+    // the first k of word i's 8 codes, or of a lane's 8 bf16
     __device__ static __forceinline__ int k_of(int i, int t) {
         return G ? i / IN_GROUP * G + t * (G / 4) + 8 * (i % IN_GROUP) : 8 * t;
     }
-};
-
-// A lane's weights of one chunk: two tiles, rows lane / 4 and lane / 4 + 8 of each.
-template <int G, bool ZEROS>
-struct Chunk {
-    using R = Row<G>;
-    uint32_t w[2][2][4];
-    float s[2][2][R::GROUPS];
-    uint32_t z[2][2][R::GROUPS];
-
-    // at: byte of the chunk in a row; bytes: of a row
-    __device__ __forceinline__ void load(const Params &p, const uint32_t (&row)[2][2], const int (&n)[2][2], int chunk) {
-        const int t = threadIdx.x & 3;
-        const int at = chunk * 64, bytes = G ? (p.K + 1) / 2 : 2 * p.K;
-        const bool whole = at + 64 <= bytes;
+    // A lane's words of chunk `half` of a staged row: its 16-byte pieces are where TMA's
+    // swizzle put them.
+    __device__ static __forceinline__ void words(const uint8_t *stage, int row, int half, int t, uint32_t (&w)[4]) {
+        const uint8_t *at = stage + row * 128;
+        auto piece = [&](int c) { return at + 16 * ((4 * half + c) ^ (row & 7)); };
+        if (G == 0 || G == 128) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(piece(t));
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else if (G == 64) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(piece(t / 2) + 8 * (t & 1));
+            const uint2 b = *reinterpret_cast<const uint2 *>(piece(2 + t / 2) + 8 * (t & 1));
+            w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t(&v)[4] = w[i][j];
-                const uint8_t *from = p.w[i] + (uint64_t)row[i][j] * 16 + at;
-                if (whole) {
-                    if (G == 0 || G == 128) {
-                        const uint4 q = stream16(from + 16 * t);
-                        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-                    } else if (G == 64) {
-                        const uint2 a = stream8(from + 8 * t), b = stream8(from + 32 + 8 * t);
-                        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = stream4(from + 16 * k + 4 * t);
-                    }
-                } else {
-                    // the row ends in this chunk: what lies behind it is not read, and zero
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int b0 = G == 0 || G == 128 ? 16 * t + 4 * k : G == 64 ? k / 2 * 32 + 8 * t + 4 * (k % 2)
-                                                                                     : 16 * k + 4 * t;
-                        v[k] = 0;
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (at + b0 + b < bytes) v[k] |= (uint32_t)from[b0 + b] << (8 * b);
-                    }
-                }
-                if (G) {
-#pragma unroll
-                    for (int g = 0; g < R::GROUPS; ++g) {
-                        const int64_t group = (int64_t)chunk * R::GROUPS + g;
-                        const bool there = group * G < p.K;
-                        s[i][j][g] = there ? __ldg(p.s[i] + group * p.lds + n[i][j]) : 0.0f;
-                        if (ZEROS) z[i][j][g] = there ? __ldg(p.z[i] + group * p.lds + n[i][j]) : 0u;
-                    }
-                }
-            }
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(piece(i) + 4 * t);
         }
     }
 };
 
-// Parts of an fp32 value: bf16 values of 8 bits that add up to it; one that is not finite is its
-// own first part.
-__device__ __forceinline__ uint32_t part_of(float v, int part) {
-    const uint32_t bits = __float_as_uint(v);
-    if ((bits & 0x7f800000u) == 0x7f800000u)
-        return part ? 0u : (bits >> 16) | ((bits & 0x7fffffu) ? 0x40u : 0u);
-    float r = v;
-    for (int i = 0; i < part; ++i) r -= __uint_as_float(__float_as_uint(r) & 0xffff0000u);
-    return __float_as_uint(r) >> 16;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float load_rank(uint32_t addr, uint32_t rank) {
-    float v;
+__device__ __forceinline__ float4 load_rank(uint32_t addr, uint32_t rank) {
+    float4 v;
     asm volatile("{\n\t.reg .u32 a;\n\t"
-                 "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-                 "ld.shared::cluster.f32 %0, [a];\n\t}" : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+                 "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
+__device__ __forceinline__ void add4(float4 &a, const float4 &b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
 
-// Chunks of weights under way: what two blocks' registers hold with few columns, one block's with more.
-constexpr int ahead(int g, int nt) { return nt > 4 ? 2 : g == 0 ? 4 : g == 128 ? 3 : 2; }
+// Eight values of a row of x from k on (zero from K on): bf16 as they are, in pairs, or as fp32.
+__device__ __forceinline__ void load_bf16(const Params &p, int m, int k, uint32_t (&v)[4]) {
+    const uint16_t *from = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
+    if (p.x_vec && k + 8 <= p.K) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(from);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = (k + 2 * e < p.K ? (uint32_t)from[2 * e] : 0u) | (k + 2 * e + 1 < p.K ? (uint32_t)from[2 * e + 1] << 16 : 0u);
+    }
+}
+__device__ __forceinline__ void load_x(const Params &p, int m, int k, float (&v)[8]) {
+    if (p.x_f32) {
+        const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
+        if (p.x_vec && k + 8 <= p.K) {
+            const float4 a = *reinterpret_cast<const float4 *>(from), b = *reinterpret_cast<const float4 *>(from + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k + e < p.K ? from[e] : 0.0f;
+        }
+    } else {
+        uint32_t w[4];
+        load_bf16(p, m, k, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    }
+}
 
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
 template <int G, bool ZEROS, int NT>
-__global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
+    few_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1, const Params p) {
     using R = Row<G>;
-    constexpr int KC = R::KC, AHEAD = ahead(G, NT);
-    extern __shared__ uint4 xs[];                          // [chunk][piece][tile of 8 columns][lane]
-    float *red = reinterpret_cast<float *>(xs);            // [warp][column][RED], after the products
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+    constexpr int KC = R::KC, U = R::UNITS, GROUPS = 2 * R::GROUPS;       // groups of a stage
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[WARPS][MOST_RING];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + p.ring * WARPS * STAGE);  // [chunk][piece][column][t]
+    float *red = reinterpret_cast<float *>(smem);          // [warp][column][RED], after the products
+    const int lane = threadIdx.x & 31, warp = warp_index(), t = lane & 3;
     const int rank = p.ks > 1 ? (int)cluster_rank() : 0;
     const int kw = warp % p.wk, rw = warp / p.wk;
     const int per_warp = p.gated ? 16 : 32, per_cta = per_warp * (WARPS / p.wk);
     const int block_row = (int)blockIdx.x / p.ks * per_cta, row0 = block_row + rw * per_warp;
     const int m0 = (int)blockIdx.y * p.per_block;
-    const int parts = p.x_f32 ? 3 : 1;
-    const int cols = min(p.per_block, p.M - m0) * parts;
-    // this CTA's chunks, and this warp's among them: kw, kw + wk, ..
-    const int c_begin = (int)((int64_t)p.chunks * rank / p.ks), c_end = (int)((int64_t)p.chunks * (rank + 1) / p.ks);
+    const int parts = G && p.x_f32 ? 2 : 1;
+    const int rows = min(p.per_block, p.M - m0), cols = rows * parts;
+    // (4 bits) of each chunk, the power of two that each column is to be multiplied by
+    float *units = reinterpret_cast<float *>(xs + 2 * p.depth * U * cols * 4);
+    // this CTA's stages, and this warp's among them: kw, kw + wk, ..
+    const int s_begin = (int)((int64_t)p.stages * rank / p.ks), s_end = (int)((int64_t)p.stages * (rank + 1) / p.ks);
+    const int mine = max(0, (s_end - s_begin - kw + p.wk - 1) / p.wk);
+    uint8_t *ring = smem + warp * p.ring * STAGE;
+    const uint32_t ring0 = smem_u32(ring), bar0 = smem_u32(&bars[warp][0]);
 
-    int n[2][2];
-    uint32_t row[2][2];                                    // in 16 bytes from w
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            n[i][j] = min(row0 + lane / 4 + 8 * j + (p.gated ? 0 : 16 * i), p.N - 1);    // (rows past N: any valid one)
-            row[i][j] = (uint32_t)(n[i][j] * (p.ldw / 16));
+    auto issue = [&](int i, int slot) {                    // the warp's i-th stage
+        if (elect_one()) {
+            const uint32_t to = ring0 + (uint32_t)(slot * STAGE), bar = bar0 + 8u * slot;
+            const int at = (s_begin + kw + i * p.wk) * 128;
+            mbar_expect_tx(bar, STAGE);
+            tma_load_2d(to, &map0, bar, at, row0);
+            if (p.gated) tma_load_2d(to + STAGE / 2, &map1, bar, at, row0);
         }
+        __syncwarp();
+    };
+    if (lane == 0) {
+        for (int i = 0; i < p.ring; ++i) mbar_init(bar0 + 8u * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    int issued = 0;
+    for (; issued < min(p.ring, mine); ++issued) issue(issued, issued);
 
+    // scales and zero codes of a stage: lane l has those of the warp's row l
+    const int which = p.gated ? lane >> 4 : 0;
+    const uint32_t n = (uint32_t)min(row0 + (p.gated ? lane & 15 : lane), p.N - 1);     // (rows past N: any valid one)
+    float scale[G ? GROUPS : 1], zero[G ? GROUPS : 1];
+    auto fetch = [&](int i) {
+        if constexpr (G != 0) {
+            if (i >= mine) return;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const uint32_t group = (uint32_t)((s_begin + kw + i * p.wk) * GROUPS + g), at = group * p.lds + n;
+                const bool there = (int64_t)group * G < p.K;
+                scale[g] = there ? __ldg(p.s[which] + at) : 0.0f;
+                // (a pair of fp16 numbers, as the codes)
+                if (ZEROS) zero[g] = __uint_as_float(there ? __ldg(p.z[which] + at) * 0x10001u + 0x64006400u : 0x64006400u);
+            }
+        }
+    };
+    fetch(0);
+
+    // (lanes of columns past the last read the last: their sums reach nothing)
+    int column[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) column[j] = min(8 * j + lane / 4, cols - 1) * 4 + t;
     float acc[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -222,80 +262,148 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_kernel(const Par
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
 
-    Chunk<G, ZEROS> ring[AHEAD];
-    for (int c0 = c_begin; c0 < c_end; c0 += p.depth) {
-        const int c1 = min(c0 + p.depth, c_end);
+    pdl_wait();                                            // x may be written by the kernel before
+    pdl_trigger();
+    bool ok = true;
+    int done = 0, slot = 0;
+    uint32_t phase = 0;
+    for (int s0 = s_begin; s0 < s_end; s0 += p.depth) {
+        const int s1 = min(s0 + p.depth, s_end);
+        if (s0 != s_begin) __syncthreads();                // x is no longer read
+        // x into the order of the fragments: 64 quads of threads, each at (row, chunk) in turn
+        const int chunks = 2 * (s1 - s0), quad = (int)threadIdx.x >> 2;
+        int m = quad / chunks, chunk = quad % chunks;
+        const int step_m = (THREADS / 4) / chunks, step = (THREADS / 4) % chunks;
+        auto next = [&]() {
+            m += step_m;
+            chunk += step;
+            if (chunk >= chunks) {
+                chunk -= chunks;
+                ++m;
+            }
+        };
+        if (G == 0) {
+            while (m < rows) {
+                constexpr int BATCH = 4;                   // loads under way
+                int at[BATCH];
+                uint32_t v[BATCH][4];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-            if (c0 + kw + u * p.wk < c1) ring[u].load(p, row, n, c0 + kw + u * p.wk);
-        if (c0 == c_begin) {
-            pdl_wait();                                    // x may be written by the kernel before
-            pdl_trigger();
-        } else {
-            __syncthreads();                               // (x is still read)
-        }
-        // x into the order of the fragments.  Columns past the last hold what was there: they
-        // reach nothing but their own sums, which no one reads.
-        const int pieces = (c1 - c0) * R::UNITS * NT * 32;
-        for (int i = threadIdx.x; i < pieces; i += THREADS) {
-            const int l = i & 31, unit = i >> 5, j = unit % NT, piece = unit / NT;
-            const int col = 8 * j + l / 4;
-            if (col >= cols) continue;
-            const int k = (c0 + piece / R::UNITS) * KC + R::k_of(piece % R::UNITS, l & 3);
-            uint32_t v[4];
-            if (p.x_f32) {
-                const float *from = static_cast<const float *>(p.x) + (int64_t)(m0 + col / 3) * p.ldx + k;
-                float f[8];
-                if (p.x_vec && k + 8 <= p.K) {
-                    const float4 a = *reinterpret_cast<const float4 *>(from), b = *reinterpret_cast<const float4 *>(from + 4);
-                    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-                    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = k + e < p.K ? from[e] : 0.0f;
+                for (int b = 0; b < BATCH; ++b) {
+                    at[b] = m < rows ? (chunk * cols + m) * 4 + t : -1;
+                    if (m < rows) load_bf16(p, m0 + m, (2 * s0 + chunk) * KC + 8 * t, v[b]);
+                    next();
                 }
-                const int part = col % 3;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = part_of(f[2 * e], part) | (part_of(f[2 * e + 1], part) << 16);
-            } else {
-                const uint16_t *from = static_cast<const uint16_t *>(p.x) + (int64_t)(m0 + col) * p.ldx + k;
-                if (p.x_vec && k + 8 <= p.K) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(from);
-                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                } else {
+                for (int b = 0; b < BATCH; ++b)
+                    if (at[b] >= 0) xs[at[b]] = make_uint4(v[b][0], v[b][1], v[b][2], v[b][3]);
+            }
+        } else {
+            constexpr int BATCH = NT > 2 ? 2 : 1;          // chunks of 128 of a row for each quad, their loads under way
+            while (__any_sync(0xffffffffu, m < rows)) {
+                float v[BATCH][4][8];
+                int row[BATCH], place[BATCH];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = (k + 2 * e < p.K ? (uint32_t)from[2 * e] : 0u) |
-                               (k + 2 * e + 1 < p.K ? (uint32_t)from[2 * e + 1] << 16 : 0u);
+                for (int b = 0; b < BATCH; ++b) {
+                    row[b] = m;
+                    place[b] = chunk;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (m < rows) {
+                            load_x(p, m0 + m, (2 * s0 + chunk) * KC + R::k_of(i, t), v[b][i]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[b][i][e] = 0.0f;
+                        }
+                    }
+                    next();
+                }
+#pragma unroll
+                for (int b = 0; b < BATCH; ++b) {
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t bits = __float_as_uint(v[b][i][e]) & 0x7fffffffu;
+                            most = max(most, bits < 0x7f800000u ? bits : 0u);
+                        }
+                    // (blocks below 2^-101 as if their largest were that: the factors stay normal)
+                    const int exponent = max((int)(quad_max(most) >> 23), 26);
+                    const float power = __uint_as_float((uint32_t)(268 - exponent) << 23);
+                    if (row[b] >= rows) continue;
+                    for (int part = 0; part < parts; ++part) {
+                        const int col = row[b] * parts + part;
+                        uint4 *to = xs + (place[b] * U * cols + col) * 4 + t;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                // (odd codes come out 16 times larger)
+                                const float x = part ? v[b][i][e] : v[b][i][e] * (e % 2 ? power * 0.0625f : power);
+                                const __half half = __float2half_rn(x);
+                                const float back = __half2float(half);
+                                h[e] = __half_as_ushort(half);
+                                // what a second part holds: nothing of what is not finite
+                                v[b][i][e] = fabsf(back) < __int_as_float(0x7f800000) ? (x - back) * 2048.0f : 0.0f;
+                            }
+                            // codes leave a word as (0, 4), (1, 5), (2, 6), (3, 7)
+                            to[i * 4 * cols] = make_uint4(h[0] | (h[4] << 16), h[1] | (h[5] << 16), h[2] | (h[6] << 16),
+                                                          h[3] | (h[7] << 16));
+                        }
+                        if (t == 0)
+                            units[place[b] * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
+                    }
                 }
             }
-            // codes leave a word as (0, 4), (1, 5), (2, 6), (3, 7)
-            xs[i] = G ? make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
-                                   __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632))
-                      : make_uint4(v[0], v[1], v[2], v[3]);
         }
         __syncthreads();
 
-        for (int c = c0 + kw; c < c1; c += AHEAD * p.wk) {
+        for (; ok && done < mine && s_begin + kw + done * p.wk < s1; ++done) {
+            float sc[G ? GROUPS : 1], ze[G ? GROUPS : 1];
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const int at = c + u * p.wk;
-                if (at >= c1) break;
-                Chunk<G, ZEROS> &q = ring[u];
-                const uint4 *xc = xs + (int64_t)(at - c0) * R::UNITS * NT * 32 + lane;
+            for (int g = 0; g < (G ? GROUPS : 1); ++g) {
+                sc[g] = scale[g];
+                ze[g] = ZEROS ? zero[g] : 0.0f;
+            }
+            fetch(done + 1);
+            ok = __all_sync(0xffffffffu, mbar_wait_for(bar0 + 8u * slot, phase, p.wait_ns, p.error));
+            if (!ok) break;
+            const uint8_t *stage = ring + slot * STAGE;
+            const uint4 *xc = xs + (s_begin + kw + done * p.wk - s0) * (2 * U * 4) * cols;
+#pragma unroll
+            for (int half = 0; half < 2; ++half, xc += U * 4 * cols) {
+                uint32_t w[2][2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) R::words(stage, 16 * i + 8 * j + lane / 4, half, t, w[i][j]);
                 if (G == 0) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        const uint4 b = xc[j * 32];
+                        const uint4 b = xc[column[j]];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            mma(acc[i][j], q.w[i][0][0], q.w[i][1][0], q.w[i][0][1], q.w[i][1][1], b.x, b.y);
-                            mma(acc[i][j], q.w[i][0][2], q.w[i][1][2], q.w[i][0][3], q.w[i][1][3], b.z, b.w);
+                            mma<false>(acc[i][j], w[i][0][0], w[i][1][0], w[i][0][1], w[i][1][1], b.x, b.y);
+                            mma<false>(acc[i][j], w[i][0][2], w[i][1][2], w[i][0][3], w[i][1][3], b.z, b.w);
                         }
                     }
                 } else {
+                    const int chunk = 2 * (s_begin + kw + done * p.wk - s0) + half;
+                    const float *unit = units + chunk * (8 * NT) + 2 * t;
 #pragma unroll
                     for (int g = 0; g < R::GROUPS; ++g) {
+                        float s[2][2];
+                        uint32_t z[2][2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int from = 16 * i + 8 * j + lane / 4;
+                                s[i][j] = __shfl_sync(0xffffffffu, sc[half * R::GROUPS + g], from);
+                                z[i][j] = ZEROS ? __float_as_uint(__shfl_sync(0xffffffffu, ze[half * R::GROUPS + g], from))
+                                                : 0x64086408u;
+                            }
                         float sum[2][NT][4];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -305,105 +413,167 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1) few_kernel(const Par
                                 for (int k = 0; k < 4; ++k) sum[i][j][k] = 0.0f;
 #pragma unroll
                         for (int k = 0; k < R::IN_GROUP; ++k) {
+                            const int word = g * R::IN_GROUP + k;
                             uint32_t a[2][2][4];           // pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const uint32_t word = q.w[i][j][g * R::IN_GROUP + k];
-                                    const uint32_t zero = ZEROS ? 0x43004300u + q.z[i][j][g] * 0x10001u : 0x43084308u;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        a[i][j][e] = subtract(((word >> (4 * e)) & 0x000f000fu) | 0x43004300u, zero);
+                                    const uint32_t first = w[i][j][word], second = first >> 8, z1 = z[i][j];
+                                    const uint32_t z16 = 0x64006400u + ((z1 & 0x000f000fu) << 4);
+                                    a[i][j][0] = subtract(codes_of(first, 0x000f000fu), z1);
+                                    a[i][j][1] = subtract(codes_of(first, 0x00f000f0u), z16);
+                                    a[i][j][2] = subtract(codes_of(second, 0x000f000fu), z1);
+                                    a[i][j][3] = subtract(codes_of(second, 0x00f000f0u), z16);
                                 }
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
-                                const uint4 b = xc[((g * R::IN_GROUP + k) * NT + j) * 32];
+                                const uint4 b = xc[word * 4 * cols + column[j]];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    mma(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);
-                                    mma(sum[i][j], a[i][0][2], a[i][1][2], a[i][0][3], a[i][1][3], b.z, b.w);
+                                    mma<true>(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);
+                                    mma<true>(sum[i][j], a[i][0][2], a[i][1][2], a[i][0][3], a[i][1][3], b.z, b.w);
                                 }
                             }
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int j = 0; j < NT; ++j) {
+                            const float2 d = *reinterpret_cast<const float2 *>(unit + 8 * j);
 #pragma unroll
-                            for (int j = 0; j < NT; ++j)
+                            for (int i = 0; i < 2; ++i)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    acc[i][j][k] = __fmaf_rn(sum[i][j][k], q.s[i][k / 2][g], acc[i][j][k]);
+                                    acc[i][j][k] = __fmaf_rn(__fmul_rn(sum[i][j][k], k % 2 ? d.y : d.x), s[i][k / 2], acc[i][j][k]);
+                        }
                     }
                 }
-                if (at + AHEAD * p.wk < c1) q.load(p, row, n, at + AHEAD * p.wk);
             }
+            __syncwarp();                                  // the slot is read
+            if (issued < mine) {
+                issue(issued, slot);
+                ++issued;
+            }
+            if (++slot == p.ring) { slot = 0; phase ^= 1; }
         }
     }
+    // a warp that gave up: what it has under way lands before its memory is used again
+    for (; done < issued; ++done) {
+        mbar_wait_for(bar0 + 8u * slot, phase, kDrainNs, p.error);
+        if (++slot == p.ring) { slot = 0; phase ^= 1; }
+    }
 
-    // partial sums, a column's 32 rows next to each other
+    // Partial sums, a column's 32 rows next to each other; then the CTA's for each output, and
+    // the cluster's.  Outputs next to each other in a row of C by neighbours in a warp.
     __syncthreads();
-    float *mine = red + warp * (NT * 8 * RED);
+    float *to = red + warp * (NT * 8 * RED);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mine[(8 * j + 2 * t + k % 2) * RED + 16 * i + lane / 4 + 8 * (k / 2)] = acc[i][j][k];
-    if (p.ks > 1) cluster_sync_all();
-    else __syncthreads();
-    // each output by one thread, neighbours in a row of C by neighbours in a warp
-    const int rows = min(per_cta, p.N - block_row), tokens = cols / parts;
-    const uint32_t red0 = smem_u32(red);
-    for (int o = rank * THREADS + threadIdx.x; o < per_cta * tokens; o += p.ks * THREADS) {
-        const int r = o % per_cta, m = o / per_cta;
-        if (r >= rows) continue;
-        const int at = (r / per_warp * p.wk) * (NT * 8 * RED) + m * parts * RED + r % per_warp;
-        auto total = [&](int place0) {
-            float v = 0.0f;
-            for (int q = 0; q < p.ks; ++q)
-                for (int w = 0; w < p.wk; ++w)
-                    for (int part = parts - 1; part >= 0; --part) {
-                        const int place = place0 + w * (NT * 8 * RED) + part * RED;
-                        v += p.ks > 1 ? load_rank(red0 + 4u * place, (uint32_t)q) : red[place];
-                    }
-            return v;
-        };
-        float out = total(at);
+            for (int k = 0; k < 4; ++k) to[(8 * j + 2 * t + k % 2) * RED + 16 * i + lane / 4 + 8 * (k / 2)] = acc[i][j][k];
+    __syncthreads();
+    // (a CTA's rows are a power of two; four of them, next to each other in red and in a row
+    // of C, at a time)
+    const int log_rows = 31 - __clz(per_cta), log_warp = p.gated ? 4 : 5, all = rows << log_rows;
+    const int outs = min(per_cta, p.N - block_row);
+    float *own = red + WARPS * NT * 8 * RED;               // [matrix][row of x][row of W]
+    auto finish = [&](int o, float4 g, float4 u) {
+        const int r = o & (per_cta - 1), m = o >> log_rows;
+        float v[4] = {g.x, g.y, g.z, g.w};
         if (p.gated) {
-            const float u = total(at + 16);
-            act::with(p.act, [&](auto a) { out = act::value<a.value>(out) * u; });
+            const float w[4] = {u.x, u.y, u.z, u.w};
+            act::with(p.act, [&](auto a) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = act::value<a.value>(v[i]) * w[i];
+            });
         }
-        const int64_t to = (int64_t)(m0 + m) * p.ldc + block_row + r;
-        if (p.c_f32) static_cast<float *>(p.c)[to] = out;
-        else static_cast<__nv_bfloat16 *>(p.c)[to] = __float2bfloat16_rn(out);
+        const int64_t place = (int64_t)(m0 + m) * p.ldc + block_row + r;
+        if (p.c_f32) {
+            float *c = static_cast<float *>(p.c) + place;
+            if (p.c_vec && r + 4 <= outs) {
+                *reinterpret_cast<float4 *>(c) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + i < outs) c[i] = v[i];
+            }
+        } else {
+            __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(p.c) + place;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+            if (p.c_vec && r + 4 <= outs) {
+                *reinterpret_cast<uint2 *>(c) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+            } else {
+                if (r < outs) c[0] = a.x;
+                if (r + 1 < outs) c[1] = a.y;
+                if (r + 2 < outs) c[2] = b.x;
+                if (r + 3 < outs) c[3] = b.y;
+            }
+        }
+    };
+    for (int o = 4 * threadIdx.x; o < all; o += 4 * THREADS) {
+        const int r = o & (per_cta - 1), m = o >> log_rows;
+        const float *from = red + ((r >> log_warp) * p.wk) * (NT * 8 * RED) + m * parts * RED + (r & (per_warp - 1));
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = v;
+        for (int w = 0; w < p.wk; ++w, from += NT * 8 * RED)
+            for (int part = parts - 1; part >= 0; --part) {
+                add4(v, *reinterpret_cast<const float4 *>(from + part * RED));
+                if (p.gated) add4(u, *reinterpret_cast<const float4 *>(from + part * RED + 16));
+            }
+        if (p.ks == 1) {
+            finish(o, v, u);
+        } else {
+            *reinterpret_cast<float4 *>(own + o) = v;
+            if (p.gated) *reinterpret_cast<float4 *>(own + all + o) = u;
+        }
     }
-    if (p.ks > 1) cluster_sync_all();                      // no CTA leaves while a peer reads its sums
+    if (p.ks == 1) return;
+    cluster_sync_all();
+    const uint32_t own0 = smem_u32(own);
+    for (int o = 4 * (rank * THREADS + threadIdx.x); o < all; o += 4 * p.ks * THREADS) {
+        const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 v[8], u = none;                             // (every CTA's under way together)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < p.ks ? load_rank(own0 + 4u * o, (uint32_t)q) : none;
+        if (p.gated)
+            for (int q = 0; q < p.ks; ++q) add4(u, load_rank(own0 + 4u * (all + o), (uint32_t)q));
+#pragma unroll
+        for (int q = 1; q < 8; ++q) add4(v[0], v[q]);
+        finish(o, v[0], u);
+    }
+    cluster_sync_all();                                    // no CTA leaves while a peer reads its sums
 }
 
 }  // namespace few
 
+struct FewLaunch {
+    CUtensorMap map[2];
+    few::Params p;
+    int nt, grid_x, grid_y, smem;
+};
+
 template <int G, bool ZEROS, int NT>
-int launch_kernel(const few::Params &p, int grid_x, int grid_y, int smem, cudaStream_t s, bool dep) {
+int launch_kernel(const FewLaunch &l, cudaStream_t s, bool dep) {
     static uint64_t done = 0;
     auto kern = few::few_kernel<G, ZEROS, NT>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (!bit || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) & bit)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 163840) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024) != cudaSuccess)
             return launch_status();
         __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid_x, (unsigned)grid_y);
+    cfg.gridDim = dim3((unsigned)l.grid_x, (unsigned)l.grid_y);
     cfg.blockDim = dim3((unsigned)few::THREADS);
-    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.dynamicSmemBytes = (size_t)l.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (p.ks > 1) {
+    if (l.p.ks > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)p.ks;
+        attr[n].val.clusterDim.x = (unsigned)l.p.ks;
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
@@ -415,23 +585,22 @@ int launch_kernel(const few::Params &p, int grid_x, int grid_y, int smem, cudaSt
     cfg.numAttrs = n;
     timing_mark(s, true);
     count_launch();
-    cudaLaunchKernelEx(&cfg, kern, p);
+    cudaLaunchKernelEx(&cfg, kern, l.map[0], l.map[1], l.p);
     timing_mark(s, false);
     return launch_status();
 }
 
 // One group's kernels, by the columns' tiles (instantiated in a file of its own).
 template <int G>
-int launch_few(int nt, const few::Params &p, int grid_x, int grid_y, int smem, cudaStream_t s, bool dep);
+int launch_few(const FewLaunch &l, cudaStream_t s, bool dep);
 
 template <int G, bool ZEROS>
-int launch_tiles(int nt, const few::Params &p, int grid_x, int grid_y, int smem, cudaStream_t s, bool dep) {
-    switch (nt) {
-    case 1: return launch_kernel<G, ZEROS, 1>(p, grid_x, grid_y, smem, s, dep);
-    case 2: return launch_kernel<G, ZEROS, 2>(p, grid_x, grid_y, smem, s, dep);
-    case 4: return launch_kernel<G, ZEROS, 4>(p, grid_x, grid_y, smem, s, dep);
-    case 6: return launch_kernel<G, ZEROS, 6>(p, grid_x, grid_y, smem, s, dep);
-    default: return launch_kernel<G, ZEROS, 8>(p, grid_x, grid_y, smem, s, dep);
+int launch_tiles(const FewLaunch &l, cudaStream_t s, bool dep) {
+    switch (l.nt) {
+    case 1: return launch_kernel<G, ZEROS, 1>(l, s, dep);
+    case 2: return launch_kernel<G, ZEROS, 2>(l, s, dep);
+    case 4: return launch_kernel<G, ZEROS, 4>(l, s, dep);
+    default: return launch_kernel<G, ZEROS, 8>(l, s, dep);
     }
 }
 

@@ -488,7 +488,8 @@ extern "C" int sgemm_device_error(sgemm_stream_t stream) {
     const int f = fp8_take_device_error();
     const int m = moe_take_device_error();
     const int n = ffn_take_device_error();
-    return t != SGEMM_OK ? t : g != SGEMM_OK ? g : f != SGEMM_OK ? f : m != SGEMM_OK ? m : n;
+    const int w = few_take_device_error();
+    return t != SGEMM_OK ? t : g != SGEMM_OK ? g : f != SGEMM_OK ? f : m != SGEMM_OK ? m : n != SGEMM_OK ? n : w;
 }
 
 extern "C" int sgemm_set_wait_limit(uint64_t nanoseconds) {

@@ -51,6 +51,7 @@ int tc_take_device_error();
 int fp8_take_device_error();
 int moe_take_device_error();
 int ffn_take_device_error();
+int few_take_device_error();
 
 // Sets the bounded-wait limit (ns; 0 = default).
 void tc_set_wait_limit(uint64_t ns);

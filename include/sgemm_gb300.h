@@ -657,11 +657,14 @@ int sgemm_q4_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int
  *   Q, Q2  both with row stride ldq bytes; 16-byte aligned, ldq a multiple of 16 (else
  *          SGEMM_ERR_UNSUPPORTED); scales and zero codes with lds >= N; Z and Z2 both or neither
  *
- * The weights are read once for each 64 rows of bf16 X (21 of fp32), as they are.
- * Values of x times codes are exact (fp32 x as three bf16 parts that add up to it) and added
- * in fp32 within a group; its sum times the scale is added in fp32: fp32 accuracy
- * throughout, C is rounded once.  A fixed order, no atomics, no workspace.
- * NaN and infinities of X give the IEEE result.  K == 0: C = 0.  Execution and errors as sgemm.
+ * The weights are read once for each 64 rows of bf16 X (32 of fp32), as they are.
+ * x is held in fp16 times a power of two for each block of 128 of a row: bf16 values
+ * exactly, but those below 2^-27 of their block's largest to 2^-35 of that; fp32 values
+ * in two parts, to the larger of 2^-23 of each and 2^-46 of their block's largest; blocks
+ * whose largest is below 2^-101 as if it were that.  Products with code - zero are exact and
+ * added in fp32 within a group, whose sum times its scale is added in fp32; C is rounded
+ * once.  A fixed order, no atomics, no workspace.  NaN and infinities of X give the IEEE
+ * result.  K == 0: C = 0.  Execution and errors as sgemm.
  */
 int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_type, int64_t ldx, const void *Q,
              const float *S, const uint8_t *Z, const void *Q2, const float *S2, const uint8_t *Z2,

@@ -47,14 +47,26 @@ def quantize(w, group, symmetric):
     return flat(code).astype(np.uint8), scale.T, zero.T.astype(np.uint8), flat(value)
 
 
+def held(x):
+    """How far what x is held as may be from it.  A block of 128 is scaled to 2^14 .. 2^15 at its
+    largest, where fp16's smallest half step, 2^-25 (16 times that where codes are 16
+    times larger), is 2^-35 of the largest; bf16 has no more bits than fp16.  Of fp32 a
+    first part leaves half a step, 2^-11 of its binade, and the second, 2^11 times larger,
+    half a step of that: 2^-23, and 2^-46 of the largest."""
+    M, K = x.shape
+    most = torch.nn.functional.pad(x.double().abs(), (0, -K % 128)).view(M, -1, 128).amax(2).repeat_interleave(128, 1)[:, :K]
+    if x.dtype == torch.bfloat16:
+        return 2.0 ** -35 * most
+    return 2.0 ** -23 * x.double().abs() + 2.0 ** -46 * most
+
+
 def product(x, w, group):
-    """(x w^T, bound): the terms of a group are added in fp32, its sum scaled and added in fp32
-    (a rounding or truncation each, 2^-23), then up to 64 partial sums; parts of an
-    fp32 x add up to no more than (1 + 2^-7) of its size."""
-    x = x.double()
-    c = x @ w.t()
-    steps = 3 * group + w.shape[1] // group + 160
-    return c, steps * fp.SUM * 1.01 * (x.abs() @ w.abs().t())
+    """(x w^T, bound): the terms of a group (of two parts at most, together 1 + 2^-10 of x's
+    size) are added in fp32, its sum is scaled twice and added in fp32 (a rounding or
+    truncation each, 2^-23), then up to 64 partial sums; and x is held to held(x)."""
+    c = x.double() @ w.t()
+    steps = 2 * group + 4 * (w.shape[1] // group) + 160
+    return c, 1.01 * steps * fp.SUM * (x.double().abs() @ w.abs().t()) + held(x) @ w.abs().t()
 
 
 def gated(x, w, w2, group, act):

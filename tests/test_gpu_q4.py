@@ -114,9 +114,9 @@ def _product(M, N, K, group=128, zeros=False, two=False, x="bf16", c="f32", act=
 @pytest.mark.parametrize("two", [False, True])
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("M", [1, 8, 13, 27, 48, 64])
+@pytest.mark.parametrize("M", [1, 7, 13, 27, 64, 70])
 def test_every_kernel(M, group, zeros, two):
-    """Each group and width of columns: 1, 1, 2, 4, 6 and 8 tiles of 8."""
+    """Each group and width of columns: 1, 1, 2, 4 and 8 tiles of 8, and two blocks of them."""
     for N, K in ((200, 516), (72, 2300)):
         _product(M, N, K, group, zeros, two)
 
@@ -152,17 +152,37 @@ def test_non_finite(x):
     _product(5, 90, 300, 64, True, False, x, "f32", edit=edit)
 
 
-def test_fp32_x_keeps_its_last_bits():
-    """x of 24 bits against codes of one: the sum of the parts is x."""
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_x_of_any_size(x):
+    """A code of one in each row: what x is held as.  Rows of x from small numbers to the largest,
+    and values far below their block's largest."""
     import torch
     K = 128
-    x = torch.randn((4, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(0))
-    x = x * torch.exp2(torch.randint(-60, 60, (4, K), device="cuda").float())
-    q = torch.full((K, 64), 0x88, device="cuda", dtype=torch.uint8)      # zeros, and ones down the diagonal
-    for i in range(K):
-        q[i, i // 2] = 0x89 if i % 2 == 0 else 0x98
-    got = sg.q4_gemm(x, q, torch.ones((1, K), device="cuda"))
-    assert torch.equal(got, x)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    v = torch.randn((40, K), device="cuda", generator=gen)
+    v *= torch.exp2(torch.linspace(-95, 124, 40, device="cuda"))[:, None]
+    v[20:] *= torch.exp2(torch.randint(-26, 1, (20, K), device="cuda", generator=gen).float())
+    X = v.to(_dtype(x))
+    for zero in (8, 0):
+        q = torch.full((K, 64), 17 * zero, device="cuda", dtype=torch.uint8)
+        for i in range(K):
+            q[i, i // 2] += 1 if i % 2 == 0 else 16
+        Z = None if zero else torch.zeros((1, K), device="cuda", dtype=torch.uint8)
+        got = sg.q4_gemm(X, q, torch.ones((1, K), device="cuda"), Z=Z, dtype=torch.float32).double()
+        fp.close("x", got, X.double(), qp.held(X) + fp.SUM * X.double().abs())
+
+
+def test_x_smaller_than_its_block_can_be():
+    """Blocks below 2^-101 are held as if their largest value were that."""
+    import torch
+    X = torch.full((3, 40), 2.0 ** -100, device="cuda")
+    X[1] = 2.0 ** -126
+    X[2] = 0.0
+    q = torch.full((5, 32), 0x99, device="cuda", dtype=torch.uint8)[:, :20]
+    got = sg.q4_gemm(X, q, torch.ones((1, 5), device="cuda"))
+    assert bool((got[0] == 40 * 2.0 ** -100).all()) and bool((got[2] == 0).all())
+    # (scaled by 2^115 it is 2^-11, exact)
+    assert bool((got[1] == 40 * 2.0 ** -126).all())
 
 
 def test_same_every_time_and_on_another_stream():
