@@ -130,7 +130,7 @@ def _declare(lib):
                                        i64, vp, vp, i64, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, i64, vp,
                                        i64, vp]
     lib.sgemm_ffn_backward.restype = i32
-    lib.sgemm_ffn_plan.argtypes = [i64, i64, i64, i32, i32, ip, ip]
+    lib.sgemm_ffn_plan.argtypes = [i64, i64, i64, i32, i32, ip, ip, ip]
     lib.sgemm_ffn_plan.restype = i32
     lib.sgemm_q4_quantize.argtypes = [i64, i64, vp, i32, i64, i32, vp, i64, vp, vp, i64, vp, i32, i64, vp]
     lib.sgemm_q4_quantize.restype = i32
@@ -589,10 +589,10 @@ def sgemm_ffn_backward(T, D, F, dy, lddy, x, ldx, gate, up, ld_in, down, ld_down
 
 
 def sgemm_ffn_plan(T, D, F, kept_type=TYPE_BF16, num_sms=152):
-    """The tiles of a block's launches, without a GPU: (status, dict of (rows, columns))."""
-    rows, cols = (ctypes.c_int * 4)(), (ctypes.c_int * 4)()
-    st = load().sgemm_ffn_plan(T, D, F, kept_type, num_sms, rows, cols)
-    return st, {k: (rows[i], cols[i]) for i, k in enumerate(("gated", "down", "slope", "gradients"))}
+    """How a block's launches are cut, without a GPU: (status, dict of (rows, columns, split))."""
+    rows, cols, split = ((ctypes.c_int * 5)() for _ in range(3))
+    st = load().sgemm_ffn_plan(T, D, F, kept_type, num_sms, rows, cols, split)
+    return st, {k: (rows[i], cols[i], split[i]) for i, k in enumerate(("gated", "down", "slope", "dx", "weights"))}
 
 
 _BF16, _KEPT = (TYPE_BF16,), (TYPE_BF16, TYPE_E4M3)
@@ -665,7 +665,7 @@ def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=
     if kept is None and keep is not None:
         if keep not in (torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError("keep must be torch.bfloat16, torch.float8_e4m3fn or None")
-        kept = tuple(_new((T, F), keep, x.device, stream) for _ in range(2))
+        kept = tuple(_new((T, (F + 15) // 16 * 16), keep, x.device, stream)[:, :F] for _ in range(2))
         if keep != torch.bfloat16:
             kept += tuple(_new(((F + 127) // 128, T), torch.bfloat16, x.device, stream) for _ in range(2))
     elif kept is not None and keep is not None and kept[0].dtype != keep:

@@ -86,7 +86,7 @@ struct Product {
     uint32_t idesc;
     void *out;
     int64_t ld;
-    int f32, add, vec;                         // fp32 result; added to what is there; rows of 16-byte pieces
+    int f32, add, width;                       // fp32 result; added to what is there; see put_rows
 };
 
 struct Params {
@@ -94,12 +94,13 @@ struct Params {
     Product product[PRODUCTS];
     int count, units;
     int first_units, extra;                    // see unit_of
+    int ks;                                    // CTAs of a cluster that share a tile's sum
     int act;
     // kept values, GATED and SLOPE
     void *g, *u;
     __nv_bfloat16 *sg, *su;
     int64_t ld_kept, ld_scales;
-    int kept_vec;
+    int kept_width;                            // see put_rows
     __nv_bfloat16 *h, *dg, *du;                // all with rows on 16 bytes
     int64_t ldh;
     unsigned long long wait_ns;
@@ -200,19 +201,34 @@ __device__ __forceinline__ uint4 *piece_at(uint8_t *block, int row, int c) {
     return reinterpret_cast<uint4 *>(block + row * BYTES + 16 * piece<BYTES>(row, c));
 }
 
+// Word `k` of a row of a block.
+template <int BYTES>
+__device__ __forceinline__ uint32_t *word_at(uint8_t *block, int row, int k) {
+    return reinterpret_cast<uint32_t *>(piece_at<BYTES>(block, row, k / 4)) + k % 4;
+}
+
 // `rows` x `cols` elements of E of the block to `out` (its first element), rows `ld`
-// elements apart.
+// elements apart, in units of `width` bytes: 16 or 4, where every row's elements
+// start on them, else one element (and at the matrix's edge).
 template <typename E>
-__device__ __forceinline__ void put_rows(uint8_t *block, E *out, int64_t ld, int rows, int cols, bool vec) {
-    constexpr int BYTES = CH * sizeof(E), PER = BYTES / 16, STEP = 32 / PER;
+__device__ __forceinline__ void put_rows(uint8_t *block, E *out, int64_t ld, int rows, int cols, int width) {
+    constexpr int BYTES = CH * sizeof(E), PER = BYTES / 16, STEP = 32 / PER, WORDS = BYTES / 4, ROWS = 32 / WORDS;
     const int lane = threadIdx.x & 31;
-    if (vec && cols >= CH) {
+    if (width == 16 && cols >= CH) {
         const int c = lane % PER;
         E *at = out + (lane / PER) * ld + c * (16 / (int)sizeof(E));
 #pragma unroll
         for (int i = 0; i < 32; i += STEP, at += STEP * ld) {
             const int r = i + lane / PER;
             if (r < rows) *reinterpret_cast<uint4 *>(at) = *piece_at<BYTES>(block, r, c);
+        }
+    } else if (width >= 4 && cols >= CH) {
+        const int k = lane % WORDS;
+        E *at = out + (lane / WORDS) * ld + k * (4 / (int)sizeof(E));
+#pragma unroll 8
+        for (int i = 0; i < 32; i += ROWS, at += ROWS * ld) {
+            const int r = i + lane / WORDS;
+            if (r < rows) *reinterpret_cast<uint32_t *>(at) = *word_at<BYTES>(block, r, k);
         }
     } else if (lane < cols) {
         E *at = out + lane;
@@ -223,33 +239,69 @@ __device__ __forceinline__ void put_rows(uint8_t *block, E *out, int64_t ld, int
     }
 }
 
-// The reverse; what lies outside is zero.
+// The reverse in two steps: fetched into registers (a lane's pieces or words of rows, or its
+// column's elements; what lies outside is zero), and put into the block.
 template <typename E>
-__device__ __forceinline__ void get_rows(uint8_t *block, const E *in, int64_t ld, int rows, int cols, bool vec) {
-    constexpr int BYTES = CH * sizeof(E), PER = BYTES / 16, STEP = 32 / PER;
-    const int lane = threadIdx.x & 31;
-    if (vec && cols >= CH) {
-        const int c = lane % PER;
-        const E *at = in + (lane / PER) * ld + c * (16 / (int)sizeof(E));
-        uint4 v[PER];
+struct Fetched {
+    static constexpr int WORDS = CH * (int)sizeof(E) / 4;
+    static constexpr int BYTES = CH * (int)sizeof(E), PER = BYTES / 16, STEP = 32 / PER;
+    using Bits = typename std::conditional<sizeof(E) == 1, uint8_t,
+                                           typename std::conditional<sizeof(E) == 2, uint16_t, uint32_t>::type>::type;
+    static constexpr int IN_WORD = 4 / (int)sizeof(E);
+    uint32_t w[WORDS];
+
+    __device__ __forceinline__ void fetch(const void *from, int64_t at, int64_t ld, int rows, int cols, int width) {
+        const int lane = threadIdx.x & 31;
+        if (width == 16 && cols >= CH) {
+            const E *in = static_cast<const E *>(from) + at + (lane / PER) * ld + lane % PER * (16 / (int)sizeof(E));
 #pragma unroll
-        for (int i = 0; i < PER; ++i, at += STEP * ld)
-            v[i] = i * STEP + lane / PER < rows ? *reinterpret_cast<const uint4 *>(at) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < PER; ++i, in += STEP * ld) {
+                const uint4 v = i * STEP + lane / PER < rows ? *reinterpret_cast<const uint4 *>(in) : make_uint4(0, 0, 0, 0);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else if (width >= 4 && cols >= CH) {
+            const E *in = static_cast<const E *>(from) + at + (lane / WORDS) * ld + lane % WORDS * IN_WORD;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) *piece_at<BYTES>(block, i * STEP + lane / PER, c) = v[i];
-    } else {
-        const E *at = in + lane;
-        const int byte = lane * (int)sizeof(E);
-        E v[32];                               // (all under way together)
+            for (int i = 0; i < WORDS; ++i, in += 32 / WORDS * ld)
+                w[i] = i * (32 / WORDS) + lane / WORDS < rows ? *reinterpret_cast<const uint32_t *>(in) : 0u;
+        } else {
+            const Bits *in = static_cast<const Bits *>(from) + at + lane;
 #pragma unroll
-        for (int r = 0; r < 32; ++r, at += ld) {
-            v[r] = E{};
-            if (lane < cols && r < rows) v[r] = *at;
+            for (int i = 0; i < WORDS; ++i) w[i] = 0;
+#pragma unroll
+            for (int r = 0; r < 32; ++r, in += ld)
+                if (lane < cols && r < rows) w[r / IN_WORD] |= (uint32_t)*in << (r % IN_WORD * 8 * (int)sizeof(E));
         }
-#pragma unroll
-        for (int r = 0; r < 32; ++r)
-            *reinterpret_cast<E *>(reinterpret_cast<uint8_t *>(piece_at<BYTES>(block, r, byte / 16)) + byte % 16) = v[r];
     }
+
+    __device__ __forceinline__ void stash(uint8_t *block, int cols, int width) const {
+        const int lane = threadIdx.x & 31;
+        if (width == 16 && cols >= CH) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                *piece_at<BYTES>(block, i * STEP + lane / PER, lane % PER) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if (width >= 4 && cols >= CH) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) *word_at<BYTES>(block, i * (32 / WORDS) + lane / WORDS, lane % WORDS) = w[i];
+        } else {
+            const int byte = lane * (int)sizeof(E);
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+                *reinterpret_cast<Bits *>(reinterpret_cast<uint8_t *>(piece_at<BYTES>(block, r, byte / 16)) + byte % 16) =
+                    (Bits)(w[r / IN_WORD] >> (r % IN_WORD * 8 * (int)sizeof(E)));
+        }
+    }
+};
+
+template <typename E>
+__device__ __forceinline__ void get_rows(uint8_t *block, const E *in, int64_t ld, int rows, int cols, int width) {
+    Fetched<E> f;
+    f.fetch(in, 0, ld, rows, cols, width);
+    f.stash(block, cols, width);
 }
 
 // A thread's row of 32 bf16 values into its block.
@@ -326,54 +378,86 @@ __device__ __forceinline__ void kept_values(uint8_t *block, float scale, float (
 // Its 32 rows start at m0 of the result; the accumulators at tmem (lane quadrant and
 // buffer included).  `block`: the warp's STAGING bytes.
 
+// A warpgroup's chunks: CHUNK columns, every other one.
+template <int BN>
+constexpr int store_chunk() { return BN >= 128 ? 2 * CH : CH; }
+
 template <int BN>
 __device__ __forceinline__ void store_tile(const Product &q, uint32_t tmem, uint8_t *block, int m0, int n0, int c0) {
-    const int lane = threadIdx.x & 31, rows = q.M - m0;
+    constexpr int WIDE = store_chunk<BN>();
+    const int lane = threadIdx.x & 31, rows = q.M - m0, N = q.N;
+    const int64_t ld = q.ld;
+    const int width = q.width;
 #pragma unroll 1
-    for (int c = c0; c < BN && n0 + c < q.N; c += 2 * CH) {
-        uint32_t r[CH];
-        tmem_ld32(tmem + c, r);
-        if (rows <= 0) continue;
-        const int cols = q.N - n0 - c;
-        float v[CH];
+    for (int c = c0; c < BN && n0 + c < N; c += 2 * WIDE) {
+        if (WIDE == 2 * CH && !q.f32 && !q.add) {
+            // both halves' reads of tensor memory, and whole lines of bf16, under way together
+            uint32_t r[2][CH];
+            tmem_ld_async(tmem + c, r[0]);
+            tmem_ld_async(tmem + c + CH, r[1]);
+            tmem_ld_wait(r[0]);
+            tmem_ld_wait(r[1]);
+            if (rows <= 0) continue;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
-        if (q.f32) {
-            float *out = static_cast<float *>(q.out) + (int64_t)m0 * q.ld + n0 + c;
-            if (q.add) {
-                get_rows(block, out, q.ld, rows, cols, q.vec);
-                __syncwarp();
-            }
+            for (int h = 0; h < 2; ++h) {
+                float v[CH];
 #pragma unroll
-            for (int i = 0; i < CH / 4; ++i) {
-                uint4 *at = piece_at<4 * CH>(block, lane, i);
-                if (q.add) {
-                    const uint4 o = *at;
-                    v[4 * i] += __uint_as_float(o.x);
-                    v[4 * i + 1] += __uint_as_float(o.y);
-                    v[4 * i + 2] += __uint_as_float(o.z);
-                    v[4 * i + 3] += __uint_as_float(o.w);
-                }
-                *at = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                 __float_as_uint(v[4 * i + 3]));
+                for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[h][i]);
+                put_bf16(block + h * BLOCK, v);
             }
             __syncwarp();
-            put_rows(block, out, q.ld, rows, cols, q.vec);
-        } else {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.out) + (int64_t)m0 * q.ld + n0 + c;
-            if (q.add) {
-                get_rows(block, out, q.ld, rows, cols, q.vec);
-                __syncwarp();
-                float o[CH];
-                kept_values<false>(block, 1.0f, o);
-#pragma unroll
-                for (int i = 0; i < CH; ++i) v[i] += o[i];
-            }
-            put_bf16(block, v);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.out) + (int64_t)m0 * ld + n0 + c;
+            put_rows(block, out, ld, rows, N - n0 - c, width);
+            put_rows(block + BLOCK, out + CH, ld, rows, N - n0 - c - CH, width);
             __syncwarp();
-            put_rows(block, out, q.ld, rows, cols, q.vec);
+            continue;
         }
-        __syncwarp();
+#pragma unroll 1
+        for (int d = c; d < c + WIDE && n0 + d < N; d += CH) {
+            uint32_t r[CH];
+            tmem_ld32(tmem + d, r);
+            if (rows <= 0) continue;
+            const int cols = N - n0 - d;
+            float v[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
+            if (q.f32) {
+                float *out = static_cast<float *>(q.out) + (int64_t)m0 * ld + n0 + d;
+                if (q.add) {
+                    get_rows(block, out, ld, rows, cols, width);
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < CH / 4; ++i) {
+                    uint4 *at = piece_at<4 * CH>(block, lane, i);
+                    if (q.add) {
+                        const uint4 o = *at;
+                        v[4 * i] += __uint_as_float(o.x);
+                        v[4 * i + 1] += __uint_as_float(o.y);
+                        v[4 * i + 2] += __uint_as_float(o.z);
+                        v[4 * i + 3] += __uint_as_float(o.w);
+                    }
+                    *at = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                     __float_as_uint(v[4 * i + 3]));
+                }
+                __syncwarp();
+                put_rows(block, out, ld, rows, cols, width);
+            } else {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.out) + (int64_t)m0 * ld + n0 + d;
+                if (q.add) {
+                    get_rows(block, out, ld, rows, cols, width);
+                    __syncwarp();
+                    float o[CH];
+                    kept_values<false>(block, 1.0f, o);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) v[i] += o[i];
+                }
+                put_bf16(block, v);
+                __syncwarp();
+                put_rows(block, out, ld, rows, cols, width);
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -426,14 +510,14 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
             put_bf16(block, g);
             put_bf16(other, u);
             __syncwarp();
-            put_rows(block, static_cast<__nv_bfloat16 *>(p.g) + at, p.ld_kept, rows, cols, p.kept_vec);
-            put_rows(other, static_cast<__nv_bfloat16 *>(p.u) + at, p.ld_kept, rows, cols, p.kept_vec);
+            put_rows(block, static_cast<__nv_bfloat16 *>(p.g) + at, p.ld_kept, rows, cols, p.kept_width);
+            put_rows(other, static_cast<__nv_bfloat16 *>(p.u) + at, p.ld_kept, rows, cols, p.kept_width);
         } else if (KEEP == 2) {
             put_codes(block, g, ig);
             put_codes(other, u, iu);
             __syncwarp();
-            put_rows(block, static_cast<uint8_t *>(p.g) + at, p.ld_kept, rows, cols, p.kept_vec);
-            put_rows(other, static_cast<uint8_t *>(p.u) + at, p.ld_kept, rows, cols, p.kept_vec);
+            put_rows(block, static_cast<uint8_t *>(p.g) + at, p.ld_kept, rows, cols, p.kept_width);
+            put_rows(other, static_cast<uint8_t *>(p.u) + at, p.ld_kept, rows, cols, p.kept_width);
         }
         act::with(p.act, [&](auto a) {
 #pragma unroll
@@ -442,62 +526,10 @@ __device__ __forceinline__ void gated_tile(const Params &p, const Product &q, ui
         __syncwarp();
         put_bf16(block, g);
         __syncwarp();
-        put_rows(block, p.h + row * p.ldh + col, p.ldh, rows, cols, true);
+        put_rows(block, p.h + row * p.ldh + col, p.ldh, rows, cols, 16);
         __syncwarp();
     }
 }
-
-// Kept values of 32 rows x 32 columns on their way from memory: a lane's pieces of rows, or
-// (alignment, the edge) its column's elements.
-template <typename E>
-struct Fetched {
-    static constexpr int WORDS = CH * (int)sizeof(E) / 4;
-    uint32_t w[WORDS];
-
-    __device__ __forceinline__ void fetch(const void *from, int64_t at, int64_t ld, int rows, int cols, bool vec) {
-        constexpr int PER = WORDS / 4, STEP = 32 / PER;
-        const int lane = threadIdx.x & 31;
-        if (vec && cols >= CH) {
-            const E *in = static_cast<const E *>(from) + at + (lane / PER) * ld + lane % PER * (16 / (int)sizeof(E));
-#pragma unroll
-            for (int i = 0; i < PER; ++i, in += STEP * ld) {
-                const uint4 v = i * STEP + lane / PER < rows ? *reinterpret_cast<const uint4 *>(in) : make_uint4(0, 0, 0, 0);
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
-            }
-        } else {
-            using Bits = typename std::conditional<sizeof(E) == 1, uint8_t, uint16_t>::type;
-            constexpr int IN_WORD = 4 / (int)sizeof(E);
-            const Bits *in = static_cast<const Bits *>(from) + at + lane;
-#pragma unroll
-            for (int i = 0; i < WORDS; ++i) w[i] = 0;
-#pragma unroll
-            for (int r = 0; r < 32; ++r, in += ld)
-                if (lane < cols && r < rows) w[r / IN_WORD] |= (uint32_t)*in << (r % IN_WORD * 8 * (int)sizeof(E));
-        }
-    }
-
-    __device__ __forceinline__ void stash(uint8_t *block, int cols, bool vec) const {
-        constexpr int BYTES = CH * sizeof(E), PER = WORDS / 4, STEP = 32 / PER;
-        const int lane = threadIdx.x & 31;
-        if (vec && cols >= CH) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                *piece_at<BYTES>(block, i * STEP + lane / PER, lane % PER) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        } else {
-            using Bits = typename std::conditional<sizeof(E) == 1, uint8_t, uint16_t>::type;
-            constexpr int IN_WORD = 4 / (int)sizeof(E);
-            const int byte = lane * (int)sizeof(E);
-#pragma unroll
-            for (int r = 0; r < 32; ++r)
-                *reinterpret_cast<Bits *>(reinterpret_cast<uint8_t *>(piece_at<BYTES>(block, r, byte / 16)) + byte % 16) =
-                    (Bits)(w[r / IN_WORD] >> (r % IN_WORD * 8 * (int)sizeof(E)));
-        }
-    }
-};
 
 // The kept values of a chunk of columns: fetched a chunk ahead of the one that is
 // computed, across tiles.
@@ -510,8 +542,8 @@ struct Kept {
     __device__ __forceinline__ void fetch(const Params &p, int row, int rows, int col, int cols) {
         if (rows <= 0 || cols <= 0) return;
         const int64_t at = row * p.ld_kept + col;
-        g.fetch(p.g, at, p.ld_kept, rows, cols, p.kept_vec);
-        u.fetch(p.u, at, p.ld_kept, rows, cols, p.kept_vec);
+        g.fetch(p.g, at, p.ld_kept, rows, cols, p.kept_width);
+        u.fetch(p.u, at, p.ld_kept, rows, cols, p.kept_width);
         if (CODES) {
             const int64_t scale = (col / 128) * p.ld_scales + row + min((int)(threadIdx.x & 31), rows - 1);
             sg = p.sg[scale];
@@ -537,8 +569,8 @@ __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, ui
             if (last) fetch_next();
             continue;
         }
-        kept.g.stash(bg, cols, p.kept_vec);
-        kept.u.stash(bu, cols, p.kept_vec);
+        kept.g.stash(bg, cols, p.kept_width);
+        kept.u.stash(bu, cols, p.kept_width);
         const float sg = CODES ? __bfloat162float(kept.sg) : 1.0f, su = CODES ? __bfloat162float(kept.su) : 1.0f;
         __syncwarp();
         if (last) fetch_next();
@@ -561,19 +593,58 @@ __device__ __forceinline__ void slope_tile(const Params &p, const Product &q, ui
         put_bf16(bg, g);
         put_bf16(bu, u);
         __syncwarp();
-        put_rows(bg, p.dg + at, p.ldh, rows, cols, true);
-        put_rows(bu, p.du + at, p.ldh, rows, cols, true);
+        put_rows(bg, p.dg + at, p.ldh, rows, cols, 16);
+        put_rows(bu, p.du + at, p.ldh, rows, cols, 16);
         __syncwarp();
         put_bf16(bg, h);
         __syncwarp();
-        put_rows(bg, p.h + at, p.ldh, rows, cols, true);
+        put_rows(bg, p.h + at, p.ldh, rows, cols, 16);
         __syncwarp();
     }
 }
 
+// SPLIT: this CTA's share of a tile's rows, the cluster's sums added in ascending order.
+template <int BN>
+__device__ __forceinline__ void add_parts(const Params &p, uint32_t sums, int unit, int part) {
+    int tm, tn;
+    const Product &q = p.product[tile_of(p, unit, tm, tn)];
+    const int first = BM * part / p.ks, rows = BM * (part + 1) / p.ks - first;
+    for (int i = (int)threadIdx.x - 128; i < rows * (BN / 4); i += 32 * EPI_WARPS) {
+        const int r = first + i / (BN / 4), c = i % (BN / 4) * 4, m = tm * BM + r, n = tn * BN + c;
+        if (m >= q.M || n >= q.N) continue;
+        float4 v[8];                               // (all under way together)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < p.ks)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
+                             : "r"(peer_addr(sums + 4u * (r * (BN + 4) + c), (uint32_t)k)) : "memory");
+        }
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            v[0].x += v[k].x;
+            v[0].y += v[k].y;
+            v[0].z += v[k].z;
+            v[0].w += v[k].w;
+        }
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(q.out) + (int64_t)m * q.ld + n;
+        if (q.width == 16 && n + 4 <= q.N) {
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2(v[0].x, v[0].y), pack2(v[0].z, v[0].w));
+        } else {
+            const float e[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n + k < q.N) out[k] = __float2bfloat16_rn(e[k]);
+        }
+    }
+}
+
 // ------------------------------------------------ the kernel
-// KEEP: GATED and SLOPE, as in the epilogues.
-template <bool PAIR, int BN, int EPI, int KEEP>
+// KEEP: GATED and SLOPE, as in the epilogues.  SPLIT (STORE on single SMs): the CTAs of a
+// cluster each sum a range of a tile's blocks, and add up a share of its rows through
+// distributed shared memory, in ascending order.
+template <bool PAIR, int BN, int EPI, int KEEP, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__ Params p) {
     using T_ = Tile<PAIR, BN>;
     constexpr int S = T_::STAGES;
@@ -595,9 +666,13 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0u;
-    const int self = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const int part = SPLIT ? (int)cluster_rank() : 0;
+    const int self = PAIR ? (int)blockIdx.x >> 1 : SPLIT ? (int)blockIdx.x / p.ks : (int)blockIdx.x;
     const int lanes = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
-    auto unit_at = [&](int k) { return unit_of(p, k, self, lanes); };
+    auto unit_at = [&](int k) { return SPLIT ? (k == 0 ? self : p.units) : unit_of(p, k, self, lanes); };
+    // the blocks of a product's sum that this CTA adds
+    auto block_from = [&](const Product &q) { return SPLIT ? (int)((int64_t)q.nk * part / p.ks) : 0; };
+    auto block_to = [&](const Product &q) { return SPLIT ? (int)((int64_t)q.nk * (part + 1) / p.ks) : q.nk; };
     const uint64_t lim = p.wait_ns;
     auto publish = [&](int which, int n) {         // to both CTAs
         if (lane == 0) {
@@ -606,7 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
         }
     };
     auto sync_all = [&]() {
-        if (PAIR) cluster_sync_all();
+        if (PAIR || SPLIT) cluster_sync_all();
         else __syncthreads();
     };
 
@@ -651,9 +726,9 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
                 const int m = tm * T_::ROWS + (int)rank * BM;
                 // GATED: gate and up on the pair's CTAs, or one after the other
                 const int n = tn * WIDTH + (PAIR && EPI != GATED ? (int)rank * B_ROWS : 0);
-                const int nk0 = q.nk0, nk = q.nk;
+                const int nk0 = q.nk0, to = block_to(q);
                 const bool a_mn = q.a_mn != 0, b_mn = q.b_mn != 0;
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = block_from(q); kb < to; ++kb) {
                     if (!warp_wait(empty(s), ph, lim)) { ok = false; break; }
                     const bool second = kb >= nk0;
                     const int at = (second ? kb - nk0 : kb) * BK;
@@ -699,7 +774,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
                     const Product &q = p.product[tile_of(p, unit, tm, tn)];
                     const uint32_t a_step = q.a_mn ? 2048u >> 4 : 32u >> 4, b_step = q.b_mn ? 2048u >> 4 : 32u >> 4;
                     const uint32_t idesc = q.idesc, d = tmem + (uint32_t)(b * BN);
-                    const int nk = q.nk;
+                    const int nk = block_to(q) - block_from(q);
                     if (!warp_wait(tempty(b), bph, lim)) { ok = false; break; }
                     for (int kb = 0; kb < nk; ++kb) {
                         if (!warp_wait(full(s), ph, lim)) { ok = false; break; }
@@ -750,11 +825,23 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
         for (int k = 0; (unit = unit_at(k)) < p.units; ++k) {
             int tm, tn;
             const Product &q = p.product[tile_of(p, unit, tm, tn)];
-            const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH, c0 = side * CH;
+            const int m0 = tm * T_::ROWS + (int)rank * BM + quad * 32, n0 = tn * WIDTH;
+            const int c0 = side * (EPI == STORE && !SPLIT ? store_chunk<BN>() : CH);
             const uint32_t at = tmem_rows + (uint32_t)(b * BN);
             if (!warp_wait(tfull(b), ph, lim)) break;
             tc_fence_after();
-            if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0, c0);
+            if (SPLIT) {
+                // (the ring is free: every stage of this CTA is multiplied)
+                float *sums = reinterpret_cast<float *>(smem) + (quad * 32 + lane) * (BN + 4);
+#pragma unroll 1
+                for (int c = c0; c < BN; c += 2 * CH) {
+                    uint32_t r[CH];
+                    tmem_ld32(at + c, r);
+#pragma unroll
+                    for (int i = 0; i < CH; i += 4)
+                        *reinterpret_cast<uint4 *>(sums + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                }
+            } else if (EPI == STORE) store_tile<BN>(q, at, block, m0, n0, c0);
             else if (EPI == GATED) gated_tile<BN, KEEP>(p, q, at, block, m0, n0, c0);
             else {
                 auto next = [&]() { fetch_first(unit_at(k + 1), side ^ 1); };
@@ -806,6 +893,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_kernel(const __grid_constant__
             mbar_wait_for(full(i % S), (uint32_t)(i / S) & 1u, kDrainNs, &g_error);
     }
     __syncwarp();
+    if (SPLIT && warp >= 4 && self < p.units) add_parts<BN>(p, smem_u32(smem), self, part);
     sync_all();
     if (warp == 1) {
         tc_fence_after();
@@ -854,7 +942,7 @@ struct Launch {
     int64_t units = 0;
     bool ok = true;
 
-    Launch(int variant_, int epi_) : variant(variant_), epi(epi_) {}
+    Launch(const FfnCut &cut, int epi_) : variant(cut.variant), epi(epi_) { p.ks = cut.ks; }
 
     // M x N result of a0 b0 (+ a1 b1), sums k0 (and k1) long; GATED: b0 is gate, b1 up.
     ffn::Product &add(int64_t M, int64_t N, int64_t k0, int64_t k1, const Operand &a0, const Operand &b0, const Operand &a1,
@@ -885,11 +973,11 @@ struct Launch {
     }
 };
 
-template <bool PAIR, int BN, int EPI, int KEEP>
+template <bool PAIR, int BN, int EPI, int KEEP, bool SPLIT = false>
 int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
     using T_ = ffn::Tile<PAIR, BN>;
     static uint64_t done = 0;
-    auto kern = ffn::ffn_kernel<PAIR, BN, EPI, KEEP>;
+    auto kern = ffn::ffn_kernel<PAIR, BN, EPI, KEEP, SPLIT>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
@@ -904,15 +992,15 @@ int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
         __atomic_fetch_or(&done, bit, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(ffn_lanes(PAIR ? 2 : 1, p.units, sms) * (PAIR ? 2 : 1)));
+    cfg.gridDim = dim3((unsigned)(SPLIT ? p.units * p.ks : ffn_lanes(PAIR ? 2 : 1, p.units, sms) * (PAIR ? 2 : 1)));
     cfg.blockDim = dim3((unsigned)ffn::THREADS);
     cfg.dynamicSmemBytes = (size_t)T_::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (PAIR) {
+    if (PAIR || SPLIT) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.x = PAIR ? 2 : (unsigned)p.ks;
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
@@ -942,15 +1030,19 @@ int launch_variant(int variant, const ffn::Params &p, int sms, cudaStream_t s, b
 int launch(Launch &l, int keep, int sms, cudaStream_t s, bool dep) {
     if (!l.ok || l.units > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     l.p.units = (int)l.units;
-    l.p.first_units = l.p.count > 1 ? l.p.product[1].first : l.p.units;
+    l.p.first_units = l.p.count == ffn::PRODUCTS ? l.p.product[1].first : l.p.units;
     l.p.extra = 0;
-    if (l.p.count > 1) {
+    if (l.p.count == ffn::PRODUCTS) {
         // the tiles of the others that take as long as one of the first
         const int lanes = ffn_lanes(kFfnTiles[l.variant].ctas, l.p.units, sms), less = lanes - l.p.first_units % lanes;
-        const double ratio = ffn_tile_time(l.variant, l.p.product[0].nk) / ffn_tile_time(l.variant, l.p.product[1].nk);
+        const double ratio = ffn_tile_time(FFN_STORE, l.variant, l.p.product[0].nk) /
+                             ffn_tile_time(FFN_STORE, l.variant, l.p.product[1].nk);
         if (less < lanes) l.p.extra = (int)std::min(ratio + 0.5, (double)((l.p.units - l.p.first_units) / less));
     }
     l.p.wait_ns = tc_wait_limit();
+    if (l.epi == ffn::STORE && l.p.ks > 1)
+        return l.variant == 1 ? launch_tiles<false, 128, ffn::STORE, 0, true>(l.p, sms, s, dep)
+                              : launch_tiles<false, 64, ffn::STORE, 0, true>(l.p, sms, s, dep);
     if (l.epi == ffn::STORE) return launch_variant<ffn::STORE, 0>(l.variant, l.p, sms, s, dep);
     if (l.epi == ffn::SLOPE)
         return keep == 2 ? launch_variant<ffn::SLOPE, 2>(l.variant, l.p, sms, s, dep)
@@ -964,19 +1056,32 @@ int launch(Launch &l, int keep, int sms, cudaStream_t s, bool dep) {
 bool tma_rows(const void *p, int64_t ld, int64_t rows) { return aligned16(p) && (ld % 8 == 0 || rows == 1); }
 int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
 
-// The tiles of a block's launches: gated, down, slope, gradients.
+// The cuts of a block's launches.  apart: dx has a launch of its own, else it is in the
+// weights' (whose tiles start while its longer sums run).
 struct FfnPlan {
-    int variant[4];
+    FfnCut gated, down, slope, dx, weights;
+    bool apart;
 };
 FfnPlan ffn_plan(int64_t T, int64_t D, int64_t F, bool codes, int sms) {
     FfnPlan pl;
     const FfnShape gated{T, 2 * F, k_blocks(D)}, down{T, D, k_blocks(F)}, slope{T, F, k_blocks(D)};
     const FfnShape grads[4] = {{T, D, 2 * k_blocks(F)}, {F, D, k_blocks(T)}, {F, D, k_blocks(T)}, {D, F, k_blocks(T)}};
-    pl.variant[0] = ffn_tile(&gated, 1, codes, sms);
-    pl.variant[1] = ffn_tile(&down, 1, false, sms);
-    pl.variant[2] = ffn_tile(&slope, 1, false, sms);
-    pl.variant[3] = ffn_tile(grads, 4, false, sms);
+    pl.gated = ffn_cut(FFN_GATED, &gated, 1, codes, false, sms);
+    pl.down = ffn_cut(FFN_STORE, &down, 1, false, true, sms);
+    pl.slope = ffn_cut(FFN_SLOPE, &slope, 1, false, false, sms);
+    pl.dx = ffn_cut(FFN_STORE, &grads[0], 1, false, true, sms);
+    const FfnCut together = ffn_cut(FFN_STORE, grads, 4, false, false, sms),
+                 weights = ffn_cut(FFN_STORE, grads + 1, 3, false, false, sms);
+    pl.apart = pl.dx.clocks + weights.clocks < together.clocks;
+    pl.weights = pl.apart ? weights : together;
+    if (!pl.apart) pl.dx = together;
     return pl;
+}
+
+// The units, 16 bytes, 4 or an element, on which every row starts.
+int row_width(const void *p, int64_t ld, int size) {
+    const uint64_t at = reinterpret_cast<uintptr_t>(p) | (uint64_t)ld * size;
+    return at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : size;
 }
 
 struct Block {
@@ -996,7 +1101,7 @@ struct Block {
         p.su = static_cast<__nv_bfloat16 *>(su);
         p.ld_kept = ld_kept;
         p.ld_scales = ld_scales;
-        p.kept_vec = aligned16(g) && aligned16(u) && ld_kept % (keep == 2 ? 16 : 8) == 0;
+        p.kept_width = std::min(row_width(g, ld_kept, keep == 2 ? 1 : 2), row_width(u, ld_kept, keep == 2 ? 1 : 2));
         p.h = static_cast<__nv_bfloat16 *>(h);
         p.ldh = ldh;
     }
@@ -1007,7 +1112,7 @@ void set_out(ffn::Product &q, void *out, int64_t ld, int type, int add) {
     q.ld = ld;
     q.f32 = type == SGEMM_TYPE_F32;
     q.add = add;
-    q.vec = aligned16(out) && ld % (q.f32 ? 4 : 8) == 0;
+    q.width = row_width(out, ld, q.f32 ? 4 : 2);
 }
 
 int zero_rows(void *p, int64_t ld, int64_t rows, int64_t cols, int bytes, cudaStream_t s) {
@@ -1036,13 +1141,13 @@ int run_forward(const Block &b, void *y, int64_t ldy, cudaStream_t s) {
         return run_few(c, sms, s, true);
     }
     const FfnPlan pl = ffn_plan(b.T, b.D, b.F, b.keep == 2, sms);
-    Launch gated(pl.variant[0], ffn::GATED);
+    Launch gated(pl.gated, ffn::GATED);
     b.fill(gated.p);
     gated.add(b.T, b.F, b.D, 0, b.x, b.gate, b.x, b.up);
     st = launch(gated, b.keep, sms, s, false);
     if (st != SGEMM_OK) return st;
     const Operand h{b.h, b.T, b.F, b.ldh, false};
-    Launch down(pl.variant[1], ffn::STORE);
+    Launch down(pl.down, ffn::STORE);
     set_out(down.add(b.T, b.D, b.F, 0, h, b.down, h, b.down), y, ldy, SGEMM_TYPE_BF16, 0);
     return launch(down, 0, sms, s, true);
 }
@@ -1068,7 +1173,7 @@ int run_backward(const Block &b, const Operand &dy, const Gradients &d, cudaStre
     int st = usable_device(&sms);
     if (st != SGEMM_OK) return st;
     const FfnPlan pl = ffn_plan(b.T, b.D, b.F, false, sms);
-    Launch slope(pl.variant[2], ffn::SLOPE);
+    Launch slope(pl.slope, ffn::SLOPE);
     b.fill(slope.p);
     slope.p.dg = static_cast<__nv_bfloat16 *>(d.dg);
     slope.p.du = static_cast<__nv_bfloat16 *>(d.du);
@@ -1076,8 +1181,13 @@ int run_backward(const Block &b, const Operand &dy, const Gradients &d, cudaStre
     st = launch(slope, b.keep, sms, s, false);
     if (st != SGEMM_OK) return st;
     const Operand dg{d.dg, b.T, b.F, b.ldh, false}, du{d.du, b.T, b.F, b.ldh, false}, h{b.h, b.T, b.F, b.ldh, true};
-    Launch grads(pl.variant[3], ffn::STORE);
-    set_out(grads.add(b.T, b.D, b.F, b.F, dg, across(b.gate), du, across(b.up)), d.dx, d.lddx, SGEMM_TYPE_BF16, 0);
+    Launch grads(pl.weights, ffn::STORE), apart(pl.dx, ffn::STORE);
+    Launch &first = pl.apart ? apart : grads;
+    set_out(first.add(b.T, b.D, b.F, b.F, dg, across(b.gate), du, across(b.up)), d.dx, d.lddx, SGEMM_TYPE_BF16, 0);
+    if (pl.apart) {
+        st = launch(apart, 0, sms, s, true);
+        if (st != SGEMM_OK) return st;
+    }
     const Operand x = across(b.x), dgt = across(dg), dut = across(du), dyt = across(dy);
     set_out(grads.add(b.F, b.D, b.T, 0, dgt, x, dgt, x), d.gate, d.ld_in, d.type, d.add);
     set_out(grads.add(b.F, b.D, b.T, 0, dut, x, dut, x), d.up, d.ld_in, d.type, d.add);
@@ -1224,15 +1334,18 @@ extern "C" int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *d
     }
 }
 
-extern "C" int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows, int *out_cols) {
+extern "C" int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows, int *out_cols,
+                              int *out_split) {
     if (T < 1 || T > kMost) return -1;
     if (D < 1 || D > kMost) return -2;
     if (F < 1 || F > kMost) return -3;
     if (num_sms <= 0) return -5;
     const FfnPlan pl = ffn_plan(T, D, F, kept_type == SGEMM_TYPE_E4M3, num_sms);
-    for (int i = 0; i < 4; ++i) {
-        if (out_rows) out_rows[i] = kFfnTiles[pl.variant[i]].rows;
-        if (out_cols) out_cols[i] = kFfnTiles[pl.variant[i]].cols;
+    const FfnCut *cuts[5] = {&pl.gated, &pl.down, &pl.slope, &pl.dx, &pl.weights};
+    for (int i = 0; i < 5; ++i) {
+        if (out_rows) out_rows[i] = kFfnTiles[cuts[i]->variant].rows;
+        if (out_cols) out_cols[i] = kFfnTiles[cuts[i]->variant].cols;
+        if (out_split) out_split[i] = i == 3 && !pl.apart ? 0 : cuts[i]->ks;
     }
     return SGEMM_OK;
 }

@@ -24,36 +24,50 @@ inline int ffn_lanes(int ctas, int64_t units, int sms) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(units, sms / ctas));
 }
 
-// Clocks of a lane for a tile among others, and for the last one's epilogue: the MMAs and
-// loads of a block of 64 k, or the epilogue where the sum is short.  Fitted to products of
-// 64 .. 4096 tokens: 4096 x 4096 x 8192 us, down 164, 225 and 350 with the three tiles; 64 x 2048 x 4096,
-// slope 25, 20 and 17.
-constexpr double kFfnBlock[] = {560, 450, 350}, kFfnEpilogue[] = {14000, 7000, 3500};
-inline double ffn_tile_time(int variant, double nk) { return std::max(nk * kFfnBlock[variant], kFfnEpilogue[variant]); }
+// Clocks of a lane for a tile among others: the MMAs and loads of a block of 64 k, or the
+// epilogue where the sum is short; and of a launch before its first block is there.  Fitted
+// to products of 64 .. 4096 tokens: 4096 x 4096 x 8192 us, down 164, 225 and 350 with the
+// three tiles; 64 x 2048 x 4096 us, weights 17, 17 and 21, first backward launch 21, 15 and 11.
+constexpr double kFfnBlock[] = {560, 450, 350}, kFfnStart = 6000;
+enum FfnKind { FFN_STORE, FFN_GATED, FFN_SLOPE };
+constexpr double kFfnEpilogue[][3] = {{5600, 3100, 2000}, {5600, 3100, 2000}, {16000, 7500, 4300}};
+inline double ffn_tile_time(FfnKind kind, int variant, double nk) {
+    return std::max(nk * kFfnBlock[variant], kFfnEpilogue[kind][variant]);
+}
 
-// The tile that a launch of `count` products takes: the shortest time of that model, a
-// lane's share of the tiles, or the longest tile with what its lane gets beside it.
+// How a launch is cut: its tile, and the CTAs of a cluster that share each tile's sum.
+struct FfnCut {
+    int variant, ks;
+    double clocks;
+};
+
+// The cut of a launch of `count` products: the shortest time of that model, a lane's share
+// of the tiles, or the longest tile with what its lane gets beside it.  One product with
+// few tiles may be cut along the sum, over clusters that the GPU holds at once (clusters
+// of 8 whole SMs: 14 of 19); they add the partial sums in 1500 clocks.
 // `whole_groups`: only tiles with 128 columns of gate and of up.
-inline int ffn_tile(const FfnShape *s, int count, bool whole_groups, int sms) {
-    int best = 0;
-    double least = 0;
+inline FfnCut ffn_cut(FfnKind kind, const FfnShape *s, int count, bool whole_groups, bool may_split, int sms) {
+    FfnCut best{0, 1, 0};
     for (int v = 0; v < (whole_groups ? 1 : 3); ++v) {
         const FfnTile &t = kFfnTiles[v];
         double total = 0, longest = 0;
         int64_t tiles = 0;
         for (int i = 0; i < count; ++i) {
             const int64_t n = ((s[i].m + t.rows - 1) / t.rows) * ((s[i].n + t.cols - 1) / t.cols);
-            const double one = ffn_tile_time(v, (double)s[i].nk);
+            const double one = ffn_tile_time(kind, v, (double)s[i].nk);
             tiles += n;
             total += (double)n * one;
             longest = std::max(longest, one);
         }
         const int64_t lanes = ffn_lanes(t.ctas, tiles, sms);
         const double rounds = (double)((tiles + lanes - 1) / lanes);
-        const double time = std::max(longest, count > 1 ? total / lanes : rounds * longest) + kFfnEpilogue[v];
-        if (v == 0 || time < least) {
-            least = time;
-            best = v;
+        const double time = std::max(longest, count > 1 ? total / lanes : rounds * longest) + kFfnEpilogue[kind][v] + kFfnStart;
+        if (v == 0 || time < best.clocks) best = FfnCut{v, 1, time};
+        if (!may_split || count > 1 || t.ctas > 1) continue;
+        for (int ks = 2; ks <= 8 && 4 * ks <= s[0].nk; ks *= 2) {
+            if (tiles * ks > (ks == 8 ? sms * 3 / 4 : ks == 4 ? sms * 9 / 10 : sms)) break;
+            const double split = (double)s[0].nk / ks * kFfnBlock[v] + kFfnEpilogue[kind][v] + kFfnStart + 1500;
+            if (split < best.clocks) best = FfnCut{v, ks, split};
         }
     }
     return best;

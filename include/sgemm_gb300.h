@@ -607,14 +607,15 @@ int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *dy, int64_t 
                        int64_t ld_din, void *ddown, int64_t ld_ddown, sgemm_stream_t stream);
 
 /*
- * sgemm_ffn_plan - the tiles of a block's launches on a GPU with num_sms SMs, without
- * touching one: rows and columns of the results' tiles, four of each (either pointer may
- * be NULL): the gated product, the down product, the backward pass' first
- * launch and its second.  kept_type as sgemm_ffn's (SGEMM_TYPE_E4M3: codes are kept).
- * Returns SGEMM_OK or a negative argument index.
+ * sgemm_ffn_plan - how a block's launches are cut on a GPU with num_sms SMs, without touching
+ * one: rows and columns of the results' tiles, and the CTAs that share a tile's sum, five of
+ * each (any pointer may be NULL): the gated product, the down product, the backward
+ * pass' first launch, dx, and the weights' gradients (dx' split 0: it is in their launch).
+ * kept_type as sgemm_ffn's (SGEMM_TYPE_E4M3: codes are kept).  Up to 16 tokens of which
+ * nothing is kept take other kernels forward.  Returns SGEMM_OK or a negative argument index.
  */
 int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows,
-                   int *out_cols);
+                   int *out_cols, int *out_split);
 
 /* ------------------------------------------------------------------------
  * Matrices of 4-bit codes with a scale for each group of a row, for serving.

@@ -59,16 +59,26 @@ def test_of_nothing_is_ok():
 
 def test_plan():
     tiles = {(256, 256), (128, 128), (128, 64)}
-    seen = set()
-    for T in (1, 50, 200, 1000, 4000, 20000):
-        for D, F in ((64, 64), (300, 2000), (4096, 8192), (8192, 512)):
+    seen = {}
+    for T in (1, 17, 50, 100, 200, 777, 1000, 4000, 20000):
+        for D, F in ((64, 64), (300, 2000), (1000, 2500), (2000, 9000), (4096, 8192), (8192, 512), (100, 20000)):
             st, p = sg.sgemm_ffn_plan(T, D, F)
-            assert st == 0 and set(p.values()) <= tiles
-            seen |= set(p.values())
+            assert st == 0
+            for name, (rows, cols, split) in p.items():
+                assert (rows, cols) in tiles
+                seen.setdefault(name, set()).add((rows, cols, split))
+                if split > 1:                  # whole sums are left, and clusters are resident at once
+                    n, k = (D, F) if name == "down" else (D, 2 * F)
+                    assert name in ("down", "dx") and (rows, cols) != (256, 256)
+                    assert -(-T // rows) * -(-n // cols) * split <= 152 and 4 * split <= -(-k // 64) + 1
+            if p["dx"][2] == 0:
+                assert p["dx"][:2] == p["weights"][:2]
             # groups of 128 kept columns lie in one tile
-            assert sg.sgemm_ffn_plan(T, D, F, E4M3)[1]["gated"] == (256, 256)
-    assert seen == tiles
-    assert sg.sgemm_ffn_plan(8192, 4096, 8192)[1]["gated"] == (256, 256)
+            assert sg.sgemm_ffn_plan(T, D, F, E4M3)[1]["gated"] == (256, 256, 1)
+    assert {t[:2] for s in seen.values() for t in s} == tiles
+    assert {t[2] for t in seen["down"]} == {1, 2, 4, 8} and len({t[2] for t in seen["dx"]}) > 2
+    assert {t[2] for n in ("gated", "slope", "weights") for t in seen[n]} == {1}
+    assert sg.sgemm_ffn_plan(8192, 4096, 8192)[1]["gated"] == (256, 256, 1)
     for args, want in (((0, 1, 1), -1), ((1, 0, 1), -2), ((1, 1, 0), -3), ((1, 1, 1, BF16, 0), -5)):
         assert sg.sgemm_ffn_plan(*args)[0] == want
 

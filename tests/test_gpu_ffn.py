@@ -81,7 +81,8 @@ def test_forward_activations(act, keep):
     _forward(140, 200, 300, act, keep)
 
 
-@pytest.mark.parametrize("keep,gap,offset", [(None, 1, 1), ("bf16", 3, 1), ("bf16", 8, 8), ("e4m3", 5, 3), ("e4m3", 16, 0)])
+@pytest.mark.parametrize("keep,gap,offset", [(None, 1, 1), ("bf16", 3, 1), ("bf16", 8, 8), ("bf16", 2, 2), ("e4m3", 5, 3), ("e4m3", 16, 0),
+                                            ("e4m3", 4, 4)])
 def test_forward_strides(keep, gap, offset):
     """Outputs with odd strides and starts; inputs with wide rows."""
     for T, D, F in ((70, 90, 140), (300, 260, 520)):
@@ -132,31 +133,30 @@ def test_backward_activations(act, keep):
 
 
 @pytest.mark.parametrize("grad,add", [("f32", False), ("f32", True), ("bf16", True)])
-@pytest.mark.parametrize("gap,offset", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("gap,offset", [(0, 0), (3, 1), (2, 2)])
 def test_backward_types_strides_and_sums(grad, add, gap, offset):
     for T, D, F in ((70, 90, 140), (300, 260, 520)):
         _backward(T, D, F, "gelu", "e4m3", grad, add, 64, gap, offset)
 
 
-def test_every_tile():
-    """Each launch of a block on each kind of tile that it can take, by sizes that the plan says take it."""
-    seen = {n: set() for n in ("gated", "gated, codes", "down", "slope", "gradients")}
-    for T, D, F in ((1, 64, 64), (100, 200, 4000), (100, 4000, 300), (700, 300, 3000), (700, 3000, 300), (2000, 200, 1500),
-                    (4000, 300, 2500), (3000, 2000, 300), (2000, 2000, 500), (1500, 500, 2000), (600, 520, 2600), (300, 1000, 9000),
-                    (9000, 300, 600), (1000, 1100, 1200)):
-        bf16, codes = (sg.sgemm_ffn_plan(T, D, F, k)[1] for k in (sg.TYPE_BF16, sg.TYPE_E4M3))
+def test_every_cut():
+    """Each launch of a block in each way that the plan cuts it, by sizes that it cuts so."""
+    seen = {n: set() for n in ("gated", "down", "slope", "dx", "weights")}
+    sizes = [(T, D, F) for T in (17, 100, 300, 777, 2000, 4000) for D, F in ((64, 96), (200, 1500), (500, 4000), (1000, 2501),
+                                                                          (2000, 300), (900, 9000), (3000, 200))]
+    sizes.append((2500, 2000, 4000))
+    for T, D, F in sizes:
         new = False
-        for n in seen:
-            tile = codes["gated"] if n == "gated, codes" else bf16[n]
-            new = new or tile not in seen[n]
-            seen[n].add(tile)
+        for n, cut in sg.sgemm_ffn_plan(T, D, F)[1].items():
+            new = new or cut not in seen[n]
+            seen[n].add(cut)
         if new:
             for keep in ("bf16", "e4m3"):
                 _forward(T, D, F, "silu", keep)
                 _backward(T, D, F, "silu", keep)
-    every = {(256, 256), (128, 128), (128, 64)}
-    assert seen["gated"] | seen["down"] | seen["slope"] | seen["gradients"] == every, seen
-    print(seen)
+            _forward(T, D, F, "silu", None, gap=1)
+    assert {c[:2] for c in seen["gated"]} == {c[:2] for c in seen["slope"]} == {(256, 256), (128, 128), (128, 64)}
+    assert {c[2] for c in seen["down"]} == {1, 2, 4, 8} and len({c[2] for c in seen["dx"]}) > 2, seen
 
 
 def test_new_buffers_and_another_stream():
