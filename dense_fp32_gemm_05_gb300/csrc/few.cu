@@ -7,13 +7,13 @@
 namespace sgemm_gb300 {
 
 template <>
-int launch_few<0>(const FewLaunch &l, cudaStream_t s, bool dep);
+int launch_few<0>(const FewLaunch &l, cudaStream_t s);
 template <>
-int launch_few<32>(const FewLaunch &l, cudaStream_t s, bool dep);
+int launch_few<32>(const FewLaunch &l, cudaStream_t s);
 template <>
-int launch_few<64>(const FewLaunch &l, cudaStream_t s, bool dep);
+int launch_few<64>(const FewLaunch &l, cudaStream_t s);
 template <>
-int launch_few<128>(const FewLaunch &l, cudaStream_t s, bool dep);
+int launch_few<128>(const FewLaunch &l, cudaStream_t s);
 
 namespace few {
 __device__ unsigned int g_error;               // sticky device error word of this path
@@ -39,7 +39,7 @@ int few_take_device_error() {
     return v == 0 ? SGEMM_OK : (int)v;
 }
 
-int run_few(const FewCall &c, int sms, cudaStream_t s, bool dep) {
+int run_few(const FewCall &c, int sms, cudaStream_t s, bool early) {
     const bool gated = c.w2 != nullptr;
     const int parts = few_parts(c.group, c.x_f32);
     const FewPlan pl = few_plan(c.M, c.N, c.K, parts, gated, c.group, sms);
@@ -69,6 +69,8 @@ int run_few(const FewCall &c, int sms, cudaStream_t s, bool dep) {
     p.stages = (int)((c.K + few_stage_k(c.group) - 1) / few_stage_k(c.group));
     p.depth = pl.depth;
     p.ring = pl.ring;
+    p.groups = c.group ? (int)((c.K + c.group - 1) / c.group) : 0;
+    p.early = early;
     p.wait_ns = tc_wait_limit();
     void *word = nullptr;
     if (cudaGetSymbolAddress(&word, few::g_error) != cudaSuccess) return launch_status();
@@ -90,10 +92,10 @@ int run_few(const FewCall &c, int sms, cudaStream_t s, bool dep) {
     l.grid_x = (int)grid_x;
     l.grid_y = (int)grid_y;
     switch (c.group) {
-    case 0: return launch_few<0>(l, s, dep);
-    case 32: return launch_few<32>(l, s, dep);
-    case 64: return launch_few<64>(l, s, dep);
-    default: return launch_few<128>(l, s, dep);
+    case 0: return launch_few<0>(l, s);
+    case 32: return launch_few<32>(l, s);
+    case 64: return launch_few<64>(l, s);
+    default: return launch_few<128>(l, s);
     }
 }
 

@@ -28,8 +28,9 @@ struct FewCall {
     int64_t ldc;
 };
 
-// dep: launched as the programmatic dependent of a kernel that writes nothing but x.
-int run_few(const FewCall &c, int sms, cudaStream_t s, bool dep);
+// early: the kernel before it in the stream is the library's, and writes none of its weights:
+// they may be read while that one still runs.
+int run_few(const FewCall &c, int sms, cudaStream_t s, bool early);
 
 // How a call is cut: blocks of 8 nt columns (rows of x, times their parts), wk warps of a
 // CTA and ks CTAs of a cluster along the sum, `depth` stages of k that a CTA holds of x at a

@@ -4,8 +4,8 @@
 namespace sgemm_gb300 {
 
 template <>
-int launch_few<0>(const FewLaunch &l, cudaStream_t s, bool dep) {
-    return launch_tiles<0, false>(l, s, dep);
+int launch_few<0>(const FewLaunch &l, cudaStream_t s) {
+    return launch_tiles<0, false>(l, s);
 }
 
 }  // namespace sgemm_gb300

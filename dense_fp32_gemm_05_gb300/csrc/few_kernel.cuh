@@ -73,10 +73,19 @@ struct Params {
     int gated, act, c_f32, c_vec, x_f32, x_vec;
     int per_block;                             // rows of x in a block of columns
     int wk, ks, stages, depth, ring;
+    int groups;
+    int early;                                 // weights may be read before pdl_wait
     unsigned int *error;                       // device error word
     unsigned long long wait_ns;
 };
 
+// The same from sums of zero.
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -229,7 +238,10 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     }
     __syncwarp();
     int issued = 0;
-    for (; issued < min(p.ring, mine); ++issued) issue(issued, issued);
+    auto fill = [&]() {
+        for (; issued < min(p.ring, mine); ++issued) issue(issued, issued);
+    };
+    if (p.early) fill();                                   // (the kernel before writes no weights)
 
     // scales and zero codes of a stage: lane l has those of the warp's row l
     const int which = p.gated ? lane >> 4 : 0;
@@ -240,15 +252,16 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
             if (i >= mine) return;
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                const uint32_t group = (uint32_t)((s_begin + kw + i * p.wk) * GROUPS + g), at = group * p.lds + n;
-                const bool there = (int64_t)group * G < p.K;
+                const int group = (s_begin + kw + i * p.wk) * GROUPS + g;
+                const uint32_t at = (uint32_t)group * p.lds + n;
+                const bool there = group < p.groups;
                 scale[g] = there ? __ldg(p.s[which] + at) : 0.0f;
                 // (a pair of fp16 numbers, as the codes)
                 if (ZEROS) zero[g] = __uint_as_float(there ? __ldg(p.z[which] + at) * 0x10001u + 0x64006400u : 0x64006400u);
             }
         }
     };
-    fetch(0);
+    if (p.early) fetch(0);
 
     // (lanes of columns past the last read the last: their sums reach nothing)
     int column[NT];
@@ -264,6 +277,10 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
 
     pdl_wait();                                            // x may be written by the kernel before
     pdl_trigger();
+    if (!p.early) {
+        fill();
+        fetch(0);
+    }
     bool ok = true;
     int done = 0, slot = 0;
     uint32_t phase = 0;
@@ -406,12 +423,6 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                             }
                         float sum[2][NT][4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) sum[i][j][k] = 0.0f;
-#pragma unroll
                         for (int k = 0; k < R::IN_GROUP; ++k) {
                             const int word = g * R::IN_GROUP + k;
                             uint32_t a[2][2][4];           // pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word
@@ -431,7 +442,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                                 const uint4 b = xc[word * 4 * cols + column[j]];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    mma<true>(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);
+                                    if (k == 0) mma_first(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);
+                                    else mma<true>(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);
                                     mma<true>(sum[i][j], a[i][0][2], a[i][1][2], a[i][0][3], a[i][1][3], b.z, b.w);
                                 }
                             }
@@ -553,7 +565,7 @@ struct FewLaunch {
 };
 
 template <int G, bool ZEROS, int NT>
-int launch_kernel(const FewLaunch &l, cudaStream_t s, bool dep) {
+int launch_kernel(const FewLaunch &l, cudaStream_t s) {
     static uint64_t done = 0;
     auto kern = few::few_kernel<G, ZEROS, NT>;
     int dev = 0;
@@ -577,10 +589,10 @@ int launch_kernel(const FewLaunch &l, cudaStream_t s, bool dep) {
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
-    if (dep) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    // (every kernel of this path waits for the one before it, whoever's that is, before it
+    // touches memory; what comes before the wait overlaps with that one's end)
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = n;
     timing_mark(s, true);
@@ -592,15 +604,15 @@ int launch_kernel(const FewLaunch &l, cudaStream_t s, bool dep) {
 
 // One group's kernels, by the columns' tiles (instantiated in a file of its own).
 template <int G>
-int launch_few(const FewLaunch &l, cudaStream_t s, bool dep);
+int launch_few(const FewLaunch &l, cudaStream_t s);
 
 template <int G, bool ZEROS>
-int launch_tiles(const FewLaunch &l, cudaStream_t s, bool dep) {
+int launch_tiles(const FewLaunch &l, cudaStream_t s) {
     switch (l.nt) {
-    case 1: return launch_kernel<G, ZEROS, 1>(l, s, dep);
-    case 2: return launch_kernel<G, ZEROS, 2>(l, s, dep);
-    case 4: return launch_kernel<G, ZEROS, 4>(l, s, dep);
-    default: return launch_kernel<G, ZEROS, 8>(l, s, dep);
+    case 1: return launch_kernel<G, ZEROS, 1>(l, s);
+    case 2: return launch_kernel<G, ZEROS, 2>(l, s);
+    case 4: return launch_kernel<G, ZEROS, 4>(l, s);
+    default: return launch_kernel<G, ZEROS, 8>(l, s);
     }
 }
 

@@ -4,8 +4,8 @@
 namespace sgemm_gb300 {
 
 template <>
-int launch_few<32>(const FewLaunch &l, cudaStream_t s, bool dep) {
-    return l.p.z[0] ? launch_tiles<32, true>(l, s, dep) : launch_tiles<32, false>(l, s, dep);
+int launch_few<32>(const FewLaunch &l, cudaStream_t s) {
+    return l.p.z[0] ? launch_tiles<32, true>(l, s) : launch_tiles<32, false>(l, s);
 }
 
 }  // namespace sgemm_gb300

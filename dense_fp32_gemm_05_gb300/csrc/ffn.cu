@@ -974,7 +974,7 @@ struct Launch {
 };
 
 template <bool PAIR, int BN, int EPI, int KEEP, bool SPLIT = false>
-int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
+int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s) {
     using T_ = ffn::Tile<PAIR, BN>;
     static uint64_t done = 0;
     auto kern = ffn::ffn_kernel<PAIR, BN, EPI, KEEP, SPLIT>;
@@ -1004,10 +1004,10 @@ int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
-    if (dep) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    // (every kernel of this path waits for the one before it, whoever's that is, before it
+    // touches memory; what comes before the wait overlaps with that one's end)
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = n;
     timing_mark(s, true);
@@ -1018,16 +1018,16 @@ int launch_tiles(const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
 }
 
 template <int EPI, int KEEP>
-int launch_variant(int variant, const ffn::Params &p, int sms, cudaStream_t s, bool dep) {
-    if (variant == 0) return launch_tiles<true, 256, EPI, KEEP>(p, sms, s, dep);
+int launch_variant(int variant, const ffn::Params &p, int sms, cudaStream_t s) {
+    if (variant == 0) return launch_tiles<true, 256, EPI, KEEP>(p, sms, s);
     if constexpr (!(EPI == ffn::GATED && KEEP == 2)) {       // (whole groups of 128 need the wide tiles)
-        if (variant == 1) return launch_tiles<false, 128, EPI, KEEP>(p, sms, s, dep);
-        return launch_tiles<false, 64, EPI, KEEP>(p, sms, s, dep);
+        if (variant == 1) return launch_tiles<false, 128, EPI, KEEP>(p, sms, s);
+        return launch_tiles<false, 64, EPI, KEEP>(p, sms, s);
     }
     return SGEMM_ERR_UNSUPPORTED;
 }
 
-int launch(Launch &l, int keep, int sms, cudaStream_t s, bool dep) {
+int launch(Launch &l, int keep, int sms, cudaStream_t s) {
     if (!l.ok || l.units > INT32_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
     l.p.units = (int)l.units;
     l.p.first_units = l.p.count == ffn::PRODUCTS ? l.p.product[1].first : l.p.units;
@@ -1041,15 +1041,15 @@ int launch(Launch &l, int keep, int sms, cudaStream_t s, bool dep) {
     }
     l.p.wait_ns = tc_wait_limit();
     if (l.epi == ffn::STORE && l.p.ks > 1)
-        return l.variant == 1 ? launch_tiles<false, 128, ffn::STORE, 0, true>(l.p, sms, s, dep)
-                              : launch_tiles<false, 64, ffn::STORE, 0, true>(l.p, sms, s, dep);
-    if (l.epi == ffn::STORE) return launch_variant<ffn::STORE, 0>(l.variant, l.p, sms, s, dep);
+        return l.variant == 1 ? launch_tiles<false, 128, ffn::STORE, 0, true>(l.p, sms, s)
+                              : launch_tiles<false, 64, ffn::STORE, 0, true>(l.p, sms, s);
+    if (l.epi == ffn::STORE) return launch_variant<ffn::STORE, 0>(l.variant, l.p, sms, s);
     if (l.epi == ffn::SLOPE)
-        return keep == 2 ? launch_variant<ffn::SLOPE, 2>(l.variant, l.p, sms, s, dep)
-                         : launch_variant<ffn::SLOPE, 1>(l.variant, l.p, sms, s, dep);
-    return keep == 0   ? launch_variant<ffn::GATED, 0>(l.variant, l.p, sms, s, dep)
-           : keep == 1 ? launch_variant<ffn::GATED, 1>(l.variant, l.p, sms, s, dep)
-                       : launch_variant<ffn::GATED, 2>(l.variant, l.p, sms, s, dep);
+        return keep == 2 ? launch_variant<ffn::SLOPE, 2>(l.variant, l.p, sms, s)
+                         : launch_variant<ffn::SLOPE, 1>(l.variant, l.p, sms, s);
+    return keep == 0   ? launch_variant<ffn::GATED, 0>(l.variant, l.p, sms, s)
+           : keep == 1 ? launch_variant<ffn::GATED, 1>(l.variant, l.p, sms, s)
+                       : launch_variant<ffn::GATED, 2>(l.variant, l.p, sms, s);
 }
 
 // Rows on 16 bytes, as TMA reads them (a single row may have any leading dimension).
@@ -1144,12 +1144,12 @@ int run_forward(const Block &b, void *y, int64_t ldy, cudaStream_t s) {
     Launch gated(pl.gated, ffn::GATED);
     b.fill(gated.p);
     gated.add(b.T, b.F, b.D, 0, b.x, b.gate, b.x, b.up);
-    st = launch(gated, b.keep, sms, s, false);
+    st = launch(gated, b.keep, sms, s);
     if (st != SGEMM_OK) return st;
     const Operand h{b.h, b.T, b.F, b.ldh, false};
     Launch down(pl.down, ffn::STORE);
     set_out(down.add(b.T, b.D, b.F, 0, h, b.down, h, b.down), y, ldy, SGEMM_TYPE_BF16, 0);
-    return launch(down, 0, sms, s, true);
+    return launch(down, 0, sms, s);
 }
 
 struct Gradients {
@@ -1178,21 +1178,21 @@ int run_backward(const Block &b, const Operand &dy, const Gradients &d, cudaStre
     slope.p.dg = static_cast<__nv_bfloat16 *>(d.dg);
     slope.p.du = static_cast<__nv_bfloat16 *>(d.du);
     slope.add(b.T, b.F, b.D, 0, dy, across(b.down), dy, across(b.down));
-    st = launch(slope, b.keep, sms, s, false);
+    st = launch(slope, b.keep, sms, s);
     if (st != SGEMM_OK) return st;
     const Operand dg{d.dg, b.T, b.F, b.ldh, false}, du{d.du, b.T, b.F, b.ldh, false}, h{b.h, b.T, b.F, b.ldh, true};
     Launch grads(pl.weights, ffn::STORE), apart(pl.dx, ffn::STORE);
     Launch &first = pl.apart ? apart : grads;
     set_out(first.add(b.T, b.D, b.F, b.F, dg, across(b.gate), du, across(b.up)), d.dx, d.lddx, SGEMM_TYPE_BF16, 0);
     if (pl.apart) {
-        st = launch(apart, 0, sms, s, true);
+        st = launch(apart, 0, sms, s);
         if (st != SGEMM_OK) return st;
     }
     const Operand x = across(b.x), dgt = across(dg), dut = across(du), dyt = across(dy);
     set_out(grads.add(b.F, b.D, b.T, 0, dgt, x, dgt, x), d.gate, d.ld_in, d.type, d.add);
     set_out(grads.add(b.F, b.D, b.T, 0, dut, x, dut, x), d.up, d.ld_in, d.type, d.add);
     set_out(grads.add(b.D, b.F, b.T, 0, dyt, h, dyt, h), d.down, d.ld_down, d.type, d.add);
-    return launch(grads, 0, sms, s, true);
+    return launch(grads, 0, sms, s);
 }
 
 bool aligned(const void *p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

@@ -174,6 +174,45 @@ def test_new_buffers_and_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
 
 
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_among_other_work(T):
+    """Calls in a row with nothing waited for, their inputs and weights written just before them by
+    other kernels, and their outputs read just after: the same as one at a time."""
+    import torch
+    D, F = 544, 1568
+    _, x, gate, up, down = _inputs(T, D, F)
+    q4 = [sg.q4_quantize(w.float(), 64, False) for w in (gate, down)]
+
+    def steps(wait):
+        w = [t.clone() for t in (gate, up, down)]
+        codes = [[t.clone() for t in q] for q in q4]
+        h = x.clone()
+        out = []
+        for i in range(12):
+            def then(v):
+                if wait:
+                    torch.cuda.synchronize()
+                return v
+            y, kept = then(sg.ffn(h, *w, keep=torch.bfloat16 if i % 3 else None))
+            if kept is not None:
+                grads = then(sg.ffn_backward((y * (0.5 / T)).contiguous(), h, *w, kept))
+                for a, g in zip(w, grads[1:]):
+                    a.add_(g, alpha=-0.01)
+            z = then(sg.q4_gemm(h, codes[0][0], codes[0][1], Z=codes[0][2], group=64))
+            z = then(sg.q4_gemm(z, codes[1][0], codes[1][1], Z=codes[1][2], group=64))
+            codes[0][1].mul_(1.01)
+            codes[1][0].bitwise_xor_(i)
+            h = torch.tanh(y.float() + z.float()).to(torch.bfloat16)
+            out.append(h)
+        torch.cuda.synchronize()
+        return out
+
+    want = steps(True)
+    assert all(bool(t.isfinite().all()) for t in want)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
+
+
 def test_captured_and_replayed():
     import torch
     dy, x, gate, up, down = _inputs(300, 136, 264)
