@@ -42,7 +42,7 @@ struct Params {
 };
 
 __device__ __forceinline__ void load8(const float *from, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(from)), b = __ldcs(reinterpret_cast<const float4 *>(from) + 1);
+    const float4 a = reinterpret_cast<const float4 *>(from)[0], b = reinterpret_cast<const float4 *>(from)[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -62,23 +62,45 @@ template <typename T, int G, bool ZEROS>
 __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
     constexpr int LANES = G / 8;               // of a group
     constexpr float INF = __builtin_huge_valf();
+    __shared__ __align__(16) float rows_of[THREADS / 32][ROWS * COLS];      // a warp's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *own = rows_of[warp];
     for (int64_t tile = (int64_t)blockIdx.x * (THREADS / 32) + warp; tile < p.tiles;
          tile += (int64_t)gridDim.x * (THREADS / 32)) {
         // (warps next to each other take rows next to each other: their scales are neighbours)
         const int col = (int)(tile % p.tiles_c) * COLS + 8 * lane;
         const int row0 = (int)(tile / p.tiles_c) * ROWS;
         const bool whole = col + 8 <= p.cols;
+        const int col0 = col - 8 * lane;
         float v[ROWS][8];
+        if (p.x_vec) {
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const T *from = static_cast<const T *>(p.X) + (row0 + r) * p.ldx + col;
-            if (row0 + r < p.rows && whole && p.x_vec) {
-                load8(from, v[r]);
-            } else {
+            for (int r = 0; r < ROWS; ++r) {
+                const T *from = static_cast<const T *>(p.X) + (row0 + r) * p.ldx + col;
+                if (row0 + r < p.rows && whole) {
+                    load8(from, v[r]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[r][i] = row0 + r < p.rows && col + i < p.cols ? load1(from + i) : 0.0f;
+                    for (int i = 0; i < 8; ++i) v[r][i] = row0 + r < p.rows && col + i < p.cols ? load1(from + i) : 0.0f;
+                }
             }
+        } else {
+            float e[ROWS][8];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = col0 + 32 * i + lane;
+                    e[r][i] = row0 + r < p.rows && c < p.cols ? load1(static_cast<const T *>(p.X) + (row0 + r) * p.ldx + c) : 0.0f;
+                }
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) own[r * COLS + 32 * i + lane] = e[r][i];
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) load8(own + r * COLS + 8 * lane, v[r]);
+            __syncwarp();
         }
         float scale[ROWS], zero[ROWS];
 #pragma unroll
@@ -107,11 +129,12 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
             uint32_t word = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float x = v[r][i];
-                float code = fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(x, inverse)), zero[r]), 0.0f), 15.0f);
-                if (x != x) code = zero[r];
-                word |= (uint32_t)code << (4 * i);
-                v[r][i] = __fmul_rn(__fsub_rn(code, zero[r]), scale[r]);
+                // rint by adding and taking off 1.5 2^23 (larger numbers are cut all the same), code
+                // and number from each other so too: without the conversions' slow unit
+                float n = __fsub_rn(__fadd_rn(__fmul_rn(v[r][i], inverse), 12582912.0f), 12582912.0f);
+                n = fminf(fmaxf(v[r][i] == v[r][i] ? n : 0.0f, -zero[r]), 15.0f - zero[r]);
+                word |= (__float_as_uint(__fadd_rn(n, 12582912.0f + zero[r])) & 15u) << (4 * i);
+                v[r][i] = __fmul_rn(n, scale[r]);
             }
             if (row0 + r >= p.rows) continue;
             uint8_t *q = p.Q + (row0 + r) * p.ldq + col / 2;
@@ -123,13 +146,13 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
                 for (int i = 0; i < 4; ++i)
                     if (col + 2 * i < p.cols) q[i] = (uint8_t)(word >> (8 * i));
             }
-            if (p.V) {
+            if (p.V && p.v_vec) {
                 const int64_t at = (row0 + r) * p.ldv + col;
-                if (whole && p.v_vec && !p.v_bf16) {
+                if (whole && !p.v_bf16) {
                     float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p.V) + at);
                     __stcs(to, make_float4(v[r][0], v[r][1], v[r][2], v[r][3]));
                     __stcs(to + 1, make_float4(v[r][4], v[r][5], v[r][6], v[r][7]));
-                } else if (whole && p.v_vec) {
+                } else if (whole) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -146,6 +169,27 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
                     }
                 }
             }
+        }
+        if (p.V && !p.v_vec) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                float4 *to = reinterpret_cast<float4 *>(own + r * COLS + 8 * lane);
+                to[0] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+                to[1] = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = col0 + 32 * i + lane;
+                    if (row0 + r >= p.rows || c >= p.cols) continue;
+                    const float x = own[r * COLS + 32 * i + lane];
+                    const int64_t at = (row0 + r) * p.ldv + c;
+                    if (p.v_bf16) static_cast<__nv_bfloat16 *>(p.V)[at] = __float2bfloat16_rn(x);
+                    else static_cast<float *>(p.V)[at] = x;
+                }
+            __syncwarp();
         }
         // a group's lanes store its rows' scales, a row each (4 lanes and rows at least)
         if (col / G * G < p.cols) {
