@@ -41,6 +41,9 @@ struct FewPlan {
 
 constexpr int kFewWarps = 8;
 constexpr int kFewStage = 4096;        // bytes of weights: 128 of each of 32 rows
+// Stages of each warp under way, 64 KB of an SM's with one CTA, 128 with two.  (A third made
+// the block of one token 4096 x 8192 43.8 us, not 35.5; one stage 39.8.)
+constexpr int kFewRing = 2;
 
 inline int64_t few_stage_k(int group) { return group ? 256 : 64; }
 inline int few_parts(int group, bool x_f32) { return group && x_f32 ? 2 : 1; }
@@ -59,26 +62,30 @@ inline FewPlan few_plan(int64_t M, int64_t N, int64_t K, int parts, bool gated, 
     p.nt = all <= 8 ? 1 : all <= 16 ? 2 : all <= 32 ? 4 : 8;
     const int64_t cols = std::min<int64_t>(M, 8 * p.nt / parts) * parts, x_stage = few_x_bytes(group, cols, p.nt);
     // Warps for the rows (32 each, or 16 of both matrices), times slices of the sum until
-    // there would be more than the GPU holds (a second round of CTAs starts late).  Few columns: the slices are a CTA's warps; with
-    // more, a cluster's CTAs first, since each CTA lays out x for its rows.
+    // there would be more than the GPU holds (a second round of CTAs starts late: 1 x 16384 x 8192
+    // with 4 slices, 256 CTAs, 19.2 us, with 8 24.5, with 2 20.9).
     const int64_t rows = (N + (gated ? 15 : 31)) / (gated ? 16 : 32);
     int64_t slices = 1;
     const int64_t warps = (int64_t)sms * kFewWarps * (p.nt <= 2 ? 2 : 1);        // that are resident
     while (slices < 64 && 2 * rows * slices <= warps && 2 * slices <= stages) slices *= 2;
-    if (p.nt == 1) {
+    if (cols * few_stage_k(group) <= 256) {
+        // little to lay out of x for a stage: the slices are a CTA's warps (4 bits, M = 1 19.2 us,
+        // not 20.0; bf16 block, 4 tokens 38.0, not 38.4)
         p.wk = (int)std::min<int64_t>(slices, kFewWarps);
         p.ks = (int)(slices / p.wk);
     } else {
-        // (clusters of 8 whole SMs: some of 16 have to wait for another to end)
-        p.ks = (int)std::min<int64_t>(slices, p.nt == 2 ? 8 : 4);
+        // else a cluster's CTAs first, so that a CTA lays out a part of x for more rows (M = 2
+        // 20.2 us, not 20.8, M = 8 23.0, not 34.9; bf16 block, 8 tokens 39.6, not 41.0).  Of
+        // clusters of 8 whole SMs some of 16 would have to wait for another to end.
+        p.ks = (int)std::min<int64_t>(slices, p.nt <= 2 ? 8 : 4);
         p.wk = (int)(slices / p.ks);
     }
-    // Shared memory, of which a CTA has half an SM's with few columns: the ring takes up to
-    // three stages of each warp, x its whole range where that leaves two.
+    // Shared memory, of which a CTA has half an SM's with few columns: the ring, and x's whole
+    // range where it fits beside it.
     const int64_t most = p.nt <= 2 ? 110 * 1024 : 216 * 1024, one = (int64_t)kFewWarps * kFewStage;
     const int64_t mine = (stages + p.ks - 1) / p.ks, each = (mine + p.wk - 1) / p.wk;
-    p.depth = (int)std::max<int64_t>(1, std::min<int64_t>(mine, (most - 2 * one) / x_stage));
-    p.ring = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(each, 4), (most - p.depth * x_stage) / one));
+    p.depth = (int)std::max<int64_t>(1, std::min<int64_t>(mine, (most - kFewRing * one) / x_stage));
+    p.ring = (int)std::max<int64_t>(1, std::min<int64_t>(each, kFewRing));
     return p;
 }
 

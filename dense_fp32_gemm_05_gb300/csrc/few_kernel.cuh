@@ -57,7 +57,6 @@ using namespace tc;
 constexpr int WARPS = kFewWarps;
 constexpr int THREADS = 32 * WARPS;
 constexpr int STAGE = kFewStage;
-constexpr int MOST_RING = 4;
 constexpr int RED = 36;                        // floats of a column of 32 partial sums: no bank twice
 constexpr uint64_t kDrainNs = 1000000000ull;
 
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     using R = Row<G>;
     constexpr int KC = R::KC, U = R::UNITS, GROUPS = 2 * R::GROUPS;       // groups of a stage
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t bars[WARPS][MOST_RING];
+    __shared__ uint64_t bars[WARPS][kFewRing];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint4 *xs = reinterpret_cast<uint4 *>(smem + p.ring * WARPS * STAGE);  // [chunk][piece][column][t]
     float *red = reinterpret_cast<float *>(smem);          // [warp][column][RED], after the products
