@@ -83,8 +83,9 @@ int run_few(const FewCall &c, int sms, cudaStream_t s, bool early) {
         return SGEMM_ERR_UNSUPPORTED;
     const int64_t bytes = c.group ? (c.K + 1) / 2 : 2 * c.K;
     const int box = gated ? 16 : 32;
-    if (!few::byte_map(&l.map[0], c.w, c.N, bytes, c.ldw, box) || !few::byte_map(&l.map[1], gated ? c.w2 : c.w, c.N, bytes, c.ldw, box))
-        return SGEMM_ERR_UNSUPPORTED;
+    if (!few::byte_map(&l.map[0], c.w, c.N, bytes, c.ldw, box)) return SGEMM_ERR_UNSUPPORTED;
+    l.map[1] = l.map[0];
+    if (gated && !few::byte_map(&l.map[1], c.w2, c.N, bytes, c.ldw, box)) return SGEMM_ERR_UNSUPPORTED;
     const int64_t cols = std::min<int64_t>(c.M, p.per_block) * parts;
     const int64_t hold = (int64_t)pl.ring * kFewWarps * kFewStage + pl.depth * few_x_bytes(c.group, cols, pl.nt);
     l.smem = 1024 + (int)std::max<int64_t>(hold, few_sums_bytes(pl.nt, std::min<int64_t>(c.M, p.per_block), pl.wk));
