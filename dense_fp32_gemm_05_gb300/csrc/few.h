@@ -49,7 +49,7 @@ inline int64_t few_stage_k(int group) { return group ? 256 : 64; }
 inline int few_parts(int group, bool x_f32) { return group && x_f32 ? 2 : 1; }
 // Shared memory of a stage of x: its pieces for `cols` columns, and for 4 bits their units for
 // all columns of a block; and of the partial sums, the warps' and the CTA's.
-inline int64_t few_x_bytes(int group, int64_t cols, int nt) { return few_stage_k(group) * 2 * cols + (group ? 2 * 32 * nt : 0); }
+inline int64_t few_x_bytes(int group, int64_t cols, int nt) { return few_stage_k(group) * 2 * cols + (group ? 8 * 16 + 2 * 32 * nt : 0); }
 inline int64_t few_sums_bytes(int nt, int64_t rows, int wk) {
     return (int64_t)kFewWarps * nt * 8 * 36 * 4 + 32 * (kFewWarps / wk) * rows * 4;
 }

@@ -119,10 +119,9 @@ struct Row {
     static constexpr int GROUPS = G ? 128 / (G ? G : 1) : 1;   // of a chunk
     static constexpr int IN_GROUP = 4 / GROUPS;            // words of a lane in a group
     static constexpr int UNITS = G ? 4 : 1;                // 16-byte pieces of x for a lane, column and chunk
-    // the first k of word i's 8 codes, or of a lane's 8 bf16
-    __device__ static __forceinline__ int k_of(int i, int t) {
-        return G ? i / IN_GROUP * G + t * (G / 4) + 8 * (i % IN_GROUP) : 8 * t;
-    }
+    // Of x's piece of 8 values from 8 p on in a chunk: the word whose codes it meets, and the lane.
+    __device__ static __forceinline__ int word_of(int p) { return G == 128 ? p % 4 : G == 64 ? p / 8 * 2 + p % 2 : p / 4; }
+    __device__ static __forceinline__ int lane_of(int p) { return G == 128 ? p / 4 : G == 64 ? p % 8 / 2 : p % 4; }
     // A lane's words of chunk `half` of a staged row: its 16-byte pieces are where TMA's
     // swizzle put them.
     __device__ static __forceinline__ void words(const uint8_t *stage, int row, int half, int t, uint32_t (&w)[4]) {
@@ -158,31 +157,43 @@ __device__ __forceinline__ void add4(float4 &a, const float4 &b) {
 }
 
 // Eight values of a row of x from k on (zero from K on): bf16 as they are, in pairs, or as fp32.
-__device__ __forceinline__ void load_bf16(const Params &p, int m, int k, uint32_t (&v)[4]) {
+// What does not start on 16 bytes, or ends inside them, goes element by element, in a
+// function of its own: laying out x runs through its code once, so code counts.
+static __device__ __noinline__ uint4 slow_bf16(const Params &p, int m, int k) {
     const uint16_t *from = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
-    if (p.x_vec && k + 8 <= p.K) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(from);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
+    uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = (k + 2 * e < p.K ? (uint32_t)from[2 * e] : 0u) | (k + 2 * e + 1 < p.K ? (uint32_t)from[2 * e + 1] << 16 : 0u);
-    }
+    for (int e = 0; e < 4; ++e)
+        v[e] = (k + 2 * e < p.K ? (uint32_t)from[2 * e] : 0u) | (k + 2 * e + 1 < p.K ? (uint32_t)from[2 * e + 1] << 16 : 0u);
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
+static __device__ __noinline__ float4 slow_f32(const Params &p, int m, int k) {
+    const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
+    return make_float4(k < p.K ? from[0] : 0.0f, k + 1 < p.K ? from[1] : 0.0f, k + 2 < p.K ? from[2] : 0.0f,
+                       k + 3 < p.K ? from[3] : 0.0f);
+}
+__device__ __forceinline__ uint4 load_bf16(const Params &p, int m, int k) {
+    if (p.x_vec && k + 8 <= p.K)
+        return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + m * p.ldx + k);
+    return slow_bf16(p, m, k);
+}
+template <bool F32>
 __device__ __forceinline__ void load_x(const Params &p, int m, int k, float (&v)[8]) {
-    if (p.x_f32) {
-        const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
+    if (F32) {
+        float4 a, b;
         if (p.x_vec && k + 8 <= p.K) {
-            const float4 a = *reinterpret_cast<const float4 *>(from), b = *reinterpret_cast<const float4 *>(from + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
+            a = *reinterpret_cast<const float4 *>(from);
+            b = *reinterpret_cast<const float4 *>(from + 4);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k + e < p.K ? from[e] : 0.0f;
+            a = slow_f32(p, m, k);
+            b = slow_f32(p, m, k + 4);
         }
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
-        uint32_t w[4];
-        load_bf16(p, m, k, w);
+        const uint4 a = load_bf16(p, m, k);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float(w[e] << 16);
@@ -200,6 +211,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     few_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1, const Params p) {
     using R = Row<G>;
     constexpr int KC = R::KC, U = R::UNITS, GROUPS = 2 * R::GROUPS;       // groups of a stage
+    constexpr int PAD = G ? 1 : 0;                         // 16 bytes: so that a quad's writes meet in no bank
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[WARPS][kFewRing];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,7 +226,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     const int parts = G && p.x_f32 ? 2 : 1;
     const int rows = min(p.per_block, p.M - m0), cols = rows * parts;
     // (4 bits) of each chunk, the power of two that each column is to be multiplied by
-    float *units = reinterpret_cast<float *>(xs + 2 * p.depth * U * cols * 4);
+    const int unit_step = 4 * cols + PAD;                  // from piece to piece
+    float *units = reinterpret_cast<float *>(xs + 2 * p.depth * U * unit_step);
     // this CTA's stages, and this warp's among them: kw, kw + wk, ..
     const int s_begin = (int)((int64_t)p.stages * rank / p.ks), s_end = (int)((int64_t)p.stages * (rank + 1) / p.ks);
     const int mine = max(0, (s_end - s_begin - kw + p.wk - 1) / p.wk);
@@ -288,90 +301,107 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
         if (s0 != s_begin) __syncthreads();                // x is no longer read
         // x into the order of the fragments: 64 quads of threads, each at (row, chunk) in turn
         const int chunks = 2 * (s1 - s0), quad = (int)threadIdx.x >> 2;
-        int m = quad / chunks, chunk = quad % chunks;
-        const int step_m = (THREADS / 4) / chunks, step = (THREADS / 4) % chunks;
+        int m = quad % rows, chunk = quad / rows;
+        const int step_m = (THREADS / 4) % rows, step = (THREADS / 4) / rows;
         auto next = [&]() {
             m += step_m;
             chunk += step;
-            if (chunk >= chunks) {
-                chunk -= chunks;
-                ++m;
+            if (m >= rows) {
+                m -= rows;
+                ++chunk;
             }
         };
         if (G == 0) {
-            while (m < rows) {
+            while (chunk < chunks) {
                 constexpr int BATCH = 4;                   // loads under way
                 int at[BATCH];
-                uint32_t v[BATCH][4];
+                uint4 v[BATCH];
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
-                    at[b] = m < rows ? (chunk * cols + m) * 4 + t : -1;
-                    if (m < rows) load_bf16(p, m0 + m, (2 * s0 + chunk) * KC + 8 * t, v[b]);
+                    at[b] = chunk < chunks ? chunk * unit_step + 4 * m + t : -1;
+                    if (chunk < chunks) v[b] = load_bf16(p, m0 + m, (2 * s0 + chunk) * KC + 8 * t);
                     next();
                 }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b)
-                    if (at[b] >= 0) xs[at[b]] = make_uint4(v[b][0], v[b][1], v[b][2], v[b][3]);
+                    if (at[b] >= 0) xs[at[b]] = v[b];
             }
         } else {
-            constexpr int BATCH = NT > 2 ? 2 : 1;          // chunks of 128 of a row for each quad, their loads under way
-            while (__any_sync(0xffffffffu, m < rows)) {
-                float v[BATCH][4][8];
-                int row[BATCH], place[BATCH];
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    row[b] = m;
-                    place[b] = chunk;
+            auto lay_out = [&](auto f32) {
+                constexpr bool F32 = decltype(f32)::value != 0;
+                constexpr int PARTS = F32 ? 2 : 1;
+#pragma unroll 1
+                while (__any_sync(0xffffffffu, chunk < chunks)) {
+                    // a chunk of 128 of a row for each quad: pieces next to each other by lanes
+                    // next to each other, 32 bytes a lane in 128 of a row (by the lane that
+                    // reads them, 4 lines for each quad's load, it took a third of 16 x 4096 x 8192)
+                    float v[4][8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (m < rows) {
-                            load_x(p, m0 + m, (2 * s0 + chunk) * KC + R::k_of(i, t), v[b][i]);
+                        if (chunk < chunks) {
+                            load_x<F32>(p, m0 + m, (2 * s0 + chunk) * KC + 8 * (4 * i + t), v[i]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[b][i][e] = 0.0f;
+                            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
                         }
                     }
-                    next();
-                }
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
                     uint32_t most = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t bits = __float_as_uint(v[b][i][e]) & 0x7fffffffu;
-                            most = max(most, bits < 0x7f800000u ? bits : 0u);
-                        }
-                    // (blocks below 2^-101 as if their largest were that: the factors stay normal)
-                    const int exponent = max((int)(quad_max(most) >> 23), 26);
-                    const float power = __uint_as_float((uint32_t)(268 - exponent) << 23);
-                    if (row[b] >= rows) continue;
-                    for (int part = 0; part < parts; ++part) {
-                        const int col = row[b] * parts + part;
-                        uint4 *to = xs + (place[b] * U * cols + col) * 4 + t;
+                        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[i][e]) & 0x7fffffffu);
+                    most = quad_max(most);
+                    const bool odd = most >= 0x7f800000u;          // not all finite: the largest that is
+                    if (__any_sync(0xffffffffu, odd)) {
+                        uint32_t finite = 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t h[8];
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                // (odd codes come out 16 times larger)
-                                const float x = part ? v[b][i][e] : v[b][i][e] * (e % 2 ? power * 0.0625f : power);
-                                const __half half = __float2half_rn(x);
-                                const float back = __half2float(half);
-                                h[e] = __half_as_ushort(half);
-                                // what a second part holds: nothing of what is not finite
-                                v[b][i][e] = fabsf(back) < __int_as_float(0x7f800000) ? (x - back) * 2048.0f : 0.0f;
+                                const uint32_t bits = __float_as_uint(v[i][e]) & 0x7fffffffu;
+                                finite = max(finite, bits < 0x7f800000u ? bits : 0u);
                             }
-                            // codes leave a word as (0, 4), (1, 5), (2, 6), (3, 7)
-                            to[i * 4 * cols] = make_uint4(h[0] | (h[4] << 16), h[1] | (h[5] << 16), h[2] | (h[6] << 16),
-                                                          h[3] | (h[7] << 16));
-                        }
-                        if (t == 0)
-                            units[place[b] * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
+                        most = quad_max(finite);
                     }
+                    // (blocks below 2^-101 as if their largest were that: the factors stay normal)
+                    const int exponent = max((int)(most >> 23), 26);
+                    const float power = __uint_as_float((uint32_t)(268 - exponent) << 23);
+                    if (chunk < chunks) {
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) {
+                            const int col = m * PARTS + part;
+                            uint4 *to = xs + chunk * U * unit_step + 4 * col;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // codes leave a word as (0, 4), (1, 5), (2, 6), (3, 7), the odd ones 16 times larger
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float &lower = v[i][e], &upper = v[i][e + 4];
+                                    if (part == 0) {
+                                        lower *= e % 2 ? power * 0.0625f : power;
+                                        upper *= e % 2 ? power * 0.0625f : power;
+                                    }
+                                    const __half2 h = __floats2half2_rn(lower, upper);
+                                    w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                    if (part + 1 < PARTS) {
+                                        // what a second part holds: nothing of what is not finite
+                                        const float2 back = __half22float2(h);
+                                        lower = odd && !(fabsf(back.x) < __int_as_float(0x7f800000)) ? 0.0f : (lower - back.x) * 2048.0f;
+                                        upper = odd && !(fabsf(back.y) < __int_as_float(0x7f800000)) ? 0.0f : (upper - back.y) * 2048.0f;
+                                    }
+                                }
+                                to[R::word_of(4 * i + t) * unit_step + R::lane_of(4 * i + t)] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            if (t == 0)
+                                units[chunk * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
+                        }
+                    }
+                    next();
                 }
-            }
+            };
+            if (p.x_f32) lay_out(act::Constant<1>());
+            else lay_out(act::Constant<0>());
         }
         __syncthreads();
 
@@ -386,9 +416,9 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
             ok = __all_sync(0xffffffffu, mbar_wait_for(bar0 + 8u * slot, phase, p.wait_ns, p.error));
             if (!ok) break;
             const uint8_t *stage = ring + slot * STAGE;
-            const uint4 *xc = xs + (s_begin + kw + done * p.wk - s0) * (2 * U * 4) * cols;
+            const uint4 *xc = xs + (s_begin + kw + done * p.wk - s0) * (2 * U) * unit_step;
 #pragma unroll
-            for (int half = 0; half < 2; ++half, xc += U * 4 * cols) {
+            for (int half = 0; half < 2; ++half, xc += U * unit_step) {
                 uint32_t w[2][2][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -438,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                                 }
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
-                                const uint4 b = xc[word * 4 * cols + column[j]];
+                                const uint4 b = xc[word * unit_step + column[j]];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
                                     if (k == 0) mma_first(sum[i][j], a[i][0][0], a[i][1][0], a[i][0][1], a[i][1][1], b.x, b.y);

@@ -213,6 +213,55 @@ def test_among_other_work(T):
         assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
 
 
+def test_two_at_a_time():
+    """Calls on two streams at once, forward, backward and with 4 bits, as alone."""
+    import torch
+    sets = []
+    for seed, (T, D, F) in enumerate(((900, 256, 1000), (5, 512, 2048))):
+        dy, x, gate, up, down = _inputs(T, D, F, seed)
+        q = sg.q4_quantize(gate.float())
+        y, kept = sg.ffn(x, gate, up, down, keep=torch.bfloat16)
+        alone = [sg.ffn(x, gate, up, down)[0], *sg.ffn_backward(dy, x, gate, up, down, kept), sg.q4_gemm(x[:20], *q[:2])]
+        sets.append((dy, x, gate, up, down, q, kept, alone, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (dy, x, gate, up, down, q, kept, _, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                got[i].append([sg.ffn(x, gate, up, down)[0], *sg.ffn_backward(dy, x, gate, up, down, kept),
+                               sg.q4_gemm(x[:20], *q[:2])])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, sets[i][7]))
+
+
+def test_one_token_captured_and_replayed():
+    """Two graphs of a block's decode step, one after the other and with new inputs."""
+    import torch
+    _, x, gate, up, down = _inputs(1, 520, 2056)
+    want = sg.ffn(x, gate, up, down)[0].clone()
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            y = x
+            for _ in range(3):
+                y = sg.ffn(x, gate, up, down)[0]
+            outs.append(y)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in outs)
+    x.copy_(_inputs(1, 520, 2056, seed=9)[1])
+    graphs[0].replay()
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    want = sg.ffn(x, gate, up, down)[0]
+    assert all(torch.equal(y, want) for y in outs)
+
+
 def test_captured_and_replayed():
     import torch
     dy, x, gate, up, down = _inputs(300, 136, 264)
