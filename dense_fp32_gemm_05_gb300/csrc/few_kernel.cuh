@@ -167,10 +167,9 @@ static __device__ __noinline__ uint4 slow_bf16(const Params &p, int m, int k) {
         v[e] = (k + 2 * e < p.K ? (uint32_t)from[2 * e] : 0u) | (k + 2 * e + 1 < p.K ? (uint32_t)from[2 * e + 1] << 16 : 0u);
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
-static __device__ __noinline__ float4 slow_f32(const Params &p, int m, int k) {
-    const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
-    return make_float4(k < p.K ? from[0] : 0.0f, k + 1 < p.K ? from[1] : 0.0f, k + 2 < p.K ? from[2] : 0.0f,
-                       k + 3 < p.K ? from[3] : 0.0f);
+static __device__ __noinline__ uint4 slow_f32(const Params &p, int m, int k) {
+    const uint32_t *from = static_cast<const uint32_t *>(p.x) + m * p.ldx + k;
+    return make_uint4(k < p.K ? from[0] : 0u, k + 1 < p.K ? from[1] : 0u, k + 2 < p.K ? from[2] : 0u, k + 3 < p.K ? from[3] : 0u);
 }
 __device__ __forceinline__ uint4 load_bf16(const Params &p, int m, int k) {
     if (p.x_vec && k + 8 <= p.K)
@@ -178,29 +177,27 @@ __device__ __forceinline__ uint4 load_bf16(const Params &p, int m, int k) {
     return slow_bf16(p, m, k);
 }
 template <bool F32>
-__device__ __forceinline__ void load_x(const Params &p, int m, int k, float (&v)[8]) {
-    if (F32) {
-        float4 a, b;
-        if (p.x_vec && k + 8 <= p.K) {
-            const float *from = static_cast<const float *>(p.x) + m * p.ldx + k;
-            a = *reinterpret_cast<const float4 *>(from);
-            b = *reinterpret_cast<const float4 *>(from + 4);
+struct Eight {                                 // values, as they are stored
+    uint4 a, b;
+    __device__ __forceinline__ void load(const Params &p, int m, int k) {
+        if (!F32) {
+            a = load_bf16(p, m, k);
+        } else if (p.x_vec && k + 8 <= p.K) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.x) + m * p.ldx + k);
+            a = from[0];
+            b = from[1];
         } else {
             a = slow_f32(p, m, k);
             b = slow_f32(p, m, k + 4);
         }
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = load_bf16(p, m, k);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = __uint_as_float(F32 ? w[e] : e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+};
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -330,21 +327,32 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
             auto lay_out = [&](auto f32) {
                 constexpr bool F32 = decltype(f32)::value != 0;
                 constexpr int PARTS = F32 ? 2 : 1;
+                constexpr bool AHEAD = !F32 && NT >= 4;
+                Eight<F32> there[4];
+                auto load = [&]() {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (chunk < chunks) there[i].load(p, m0 + m, (2 * s0 + chunk) * KC + 8 * (4 * i + t));
+                        else there[i].a = there[i].b = make_uint4(0, 0, 0, 0);
+                    }
+                };
+                if (AHEAD) load();
 #pragma unroll 1
                 while (__any_sync(0xffffffffu, chunk < chunks)) {
                     // a chunk of 128 of a row for each quad: pieces next to each other by lanes
                     // next to each other, 32 bytes a lane in 128 of a row (by the lane that
-                    // reads them, 4 lines for each quad's load, it took a third of 16 x 4096 x 8192)
+                    // reads them, 4 lines for each quad's load, it took a third of 16 x 4096 x 8192);
+                    // AHEAD: the next one's loads are under way meanwhile (bf16 32 x 4096 x 8192 18.3 us, not
+                    // 23.4; 64 x 8192 x 4096 29.8, not 34.3; with 16 rows, whose quads have half as much to do, 15.0, not 13.5, and
+                    // fp32 values take too many registers: 32 x 4096 x 8192 40.5 us, not 34.8)
+                    const int row = m, to_chunk = chunk;
+                    const bool live = chunk < chunks;
+                    if (!AHEAD) load();
                     float v[4][8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (chunk < chunks) {
-                            load_x<F32>(p, m0 + m, (2 * s0 + chunk) * KC + 8 * (4 * i + t), v[i]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-                        }
-                    }
+                    for (int i = 0; i < 4; ++i) there[i].values(v[i]);
+                    next();
+                    if (AHEAD) load();
                     uint32_t most = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -366,11 +374,11 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                     // (blocks below 2^-101 as if their largest were that: the factors stay normal)
                     const int exponent = max((int)(most >> 23), 26);
                     const float power = __uint_as_float((uint32_t)(268 - exponent) << 23);
-                    if (chunk < chunks) {
+                    if (live) {
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part) {
-                            const int col = m * PARTS + part;
-                            uint4 *to = xs + chunk * U * unit_step + 4 * col;
+                            const int col = row * PARTS + part;
+                            uint4 *to = xs + to_chunk * U * unit_step + 4 * col;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 // codes leave a word as (0, 4), (1, 5), (2, 6), (3, 7), the odd ones 16 times larger
@@ -394,10 +402,9 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                                 to[R::word_of(4 * i + t) * unit_step + R::lane_of(4 * i + t)] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                             if (t == 0)
-                                units[chunk * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
+                                units[to_chunk * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
                         }
                     }
-                    next();
                 }
             };
             if (p.x_f32) lay_out(act::Constant<1>());
