@@ -39,10 +39,10 @@ int few_take_device_error() {
     return v == 0 ? SGEMM_OK : (int)v;
 }
 
-int run_few(const FewCall &c, int sms, cudaStream_t s, bool early) {
+int run_few(const FewCall &c, cudaStream_t s, bool early) {
     const bool gated = c.w2 != nullptr;
     const int parts = few_parts(c.group, c.x_f32);
-    const FewPlan pl = few_plan(c.M, c.N, c.K, parts, gated, c.group, sms);
+    const FewPlan pl = few_plan(c.M, c.N, c.K, parts, gated, c.group, few_clusters);
     FewLaunch l{};
     few::Params &p = l.p;
     p.x = c.x;

@@ -30,7 +30,7 @@ struct FewCall {
 
 // early: the kernel before it in the stream is the library's, and writes none of its weights:
 // they may be read while that one still runs.
-int run_few(const FewCall &c, int sms, cudaStream_t s, bool early);
+int run_few(const FewCall &c, cudaStream_t s, bool early);
 
 // How a call is cut: blocks of 8 nt columns (rows of x, times their parts), wk warps of a
 // CTA and ks CTAs of a cluster along the sum, `depth` stages of k that a CTA holds of x at a
@@ -54,35 +54,45 @@ inline int64_t few_sums_bytes(int nt, int64_t rows, int wk) {
     return (int64_t)kFewWarps * nt * 8 * 36 * 4 + 32 * (kFewWarps / wk) * rows * 4;
 }
 
-inline FewPlan few_plan(int64_t M, int64_t N, int64_t K, int parts, bool gated, int group, int sms) {
+// Shared memory of a CTA, which has half an SM's with few columns.
+inline int64_t few_most_smem(int nt) { return (nt <= 2 ? 110 : 216) * 1024; }
+
+// The clusters of `ks` CTAs of nt tiles of columns that the current device runs together (0: an error).
+int few_clusters(int nt, int ks);
+
+// clusters(nt, ks): as few_clusters.
+template <typename Clusters>
+FewPlan few_plan(int64_t M, int64_t N, int64_t K, int parts, bool gated, int group, Clusters clusters) {
     FewPlan p;
     const int64_t stages = (K + few_stage_k(group) - 1) / few_stage_k(group);
     // columns for all rows of x, where their tiles' accumulators fit the registers
     const int64_t all = M * parts;
     p.nt = all <= 8 ? 1 : all <= 16 ? 2 : all <= 32 ? 4 : 8;
     const int64_t cols = std::min<int64_t>(M, 8 * p.nt / parts) * parts, x_stage = few_x_bytes(group, cols, p.nt);
-    // Warps for the rows (32 each, or 16 of both matrices), times slices of the sum until
-    // there would be more than the GPU holds (a second round of CTAs starts late: 1 x 16384 x 8192
-    // with 4 slices, 256 CTAs, 19.2 us, with 8 24.5, with 2 20.9).
-    const int64_t rows = (N + (gated ? 15 : 31)) / (gated ? 16 : 32);
-    int64_t slices = 1;
-    const int64_t warps = (int64_t)sms * kFewWarps * (p.nt <= 2 ? 2 : 1);        // that are resident
-    while (slices < 64 && 2 * rows * slices <= warps && 2 * slices <= stages) slices *= 2;
-    if (cols * few_stage_k(group) <= 256) {
-        // little to lay out of x for a stage: the slices are a CTA's warps (4 bits, M = 1 19.2 us,
-        // not 20.0; bf16 block, 4 tokens 38.0, not 38.4)
-        p.wk = (int)std::min<int64_t>(slices, kFewWarps);
-        p.ks = (int)(slices / p.wk);
-    } else {
-        // else a cluster's CTAs first, so that a CTA lays out a part of x for more rows (M = 2
-        // 20.2 us, not 20.8, M = 8 23.0, not 34.9; bf16 block, 8 tokens 39.6, not 41.0).  Of
-        // clusters of 8 whole SMs some of 16 would have to wait for another to end.
-        p.ks = (int)std::min<int64_t>(slices, p.nt <= 2 ? 8 : 4);
-        p.wk = (int)(slices / p.ks);
+    // Warps for the rows (32 each, or 16 of both matrices), times slices of the sum: the
+    // fewest stages a warp that CTAs which run together allow (a second round of CTAs starts late:
+    // 1 x 16384 x 8192 with 4 slices, 256 CTAs, 19.2 us, with 8 24.5, with 2 20.9; 1 x 20480 x
+    // 8192 with 3 24.2, with 2 30.6).  How many do is asked, since a cluster's CTAs
+    // are on neighbouring SMs: 48 clusters of 3 SMs, of the 50 that 152 SMs would hold, took
+    // two rounds (32 x 6144 x 4096 29.1 us, with 32 clusters of 4 19.3).  Slices are
+    // a CTA's warps where there is little to lay out of x for a stage (4 bits, M = 1 19.2 us,
+    // not 20.0; bf16 block, 4 tokens 38.0, not 38.4), else a cluster's CTAs first, so that a CTA
+    // lays out a part of x for more rows (M = 2 20.2 us, not 20.8, M = 8 23.0, not 34.9; bf16
+    // block, 8 tokens 39.6, not 41.0).
+    const bool little = cols * few_stage_k(group) <= 256;
+    const int most_ks = p.nt <= 2 ? 8 : 4;
+    int64_t fewest = stages + 1;
+    p.wk = p.ks = 1;
+    for (int i = 0; i < most_ks * 4; ++i) {
+        const int wk = 1 << (little ? 3 - i % 4 : i / most_ks), ks = little ? 1 + i / 4 : most_ks - i % most_ks;
+        const int64_t per_cta = (gated ? 16 : 32) * (kFewWarps / wk), each = ((stages + ks - 1) / ks + wk - 1) / wk;
+        if (ks > stages || each >= fewest || (N + per_cta - 1) / per_cta > clusters(p.nt, ks)) continue;
+        fewest = each;
+        p.wk = wk;
+        p.ks = ks;
     }
-    // Shared memory, of which a CTA has half an SM's with few columns: the ring, and x's whole
-    // range where it fits beside it.
-    const int64_t most = p.nt <= 2 ? 110 * 1024 : 216 * 1024, one = (int64_t)kFewWarps * kFewStage;
+    // the ring, and x's whole range where it fits beside it
+    const int64_t most = few_most_smem(p.nt), one = (int64_t)kFewWarps * kFewStage;
     const int64_t mine = (stages + p.ks - 1) / p.ks, each = (mine + p.wk - 1) / p.wk;
     p.depth = (int)std::max<int64_t>(1, std::min<int64_t>(mine, (most - kFewRing * one) / x_stage));
     p.ring = (int)std::max<int64_t>(1, std::min<int64_t>(each, kFewRing));

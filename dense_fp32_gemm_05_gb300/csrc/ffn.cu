@@ -1136,13 +1136,13 @@ int run_forward(const Block &b, void *y, int64_t ldy, cudaStream_t s) {
         c.w = b.gate.p; c.w2 = b.up.p; c.ldw = 2 * b.gate.ld;
         c.act = b.act;
         c.c = b.h; c.ldc = b.ldh;
-        st = run_few(c, sms, s, false);
+        st = run_few(c, s, false);
         if (st != SGEMM_OK) return st;
         c.N = b.D; c.K = b.F;
         c.x = b.h; c.ldx = b.ldh;
         c.w = b.down.p; c.w2 = nullptr; c.ldw = 2 * b.down.ld;
         c.c = y; c.ldc = ldy;
-        return run_few(c, sms, s, true);
+        return run_few(c, s, true);
     }
     const FfnPlan pl = ffn_plan(b.T, b.D, b.F, b.keep == 2, sms);
     Launch gated(pl.gated, ffn::GATED);

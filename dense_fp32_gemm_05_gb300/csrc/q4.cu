@@ -321,5 +321,5 @@ extern "C" int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_ty
     c.s = S; c.s2 = S2; c.z = Z; c.z2 = Z2; c.lds = lds;
     c.act = activation;
     c.c = C; c.c_f32 = c_f32; c.ldc = ldc;
-    return run_few(c, sms, s, false);
+    return run_few(c, s, false);
 }

@@ -568,8 +568,9 @@ int sgemm_moe(int64_t T, int64_t D, int64_t F, int64_t E, int64_t topk, const vo
  * x, gate, up, down and h are read by TMA: they start on 16 bytes and their leading
  * dimensions are multiples of 8 (pad rows where D or F is none), else
  * SGEMM_ERR_UNSUPPORTED; g, u, scales and y may lie anywhere.  The outputs may not
- * overlap one another or an input.  T or D zero: nothing is done (D zero with values to
- * keep: SGEMM_ERR_UNSUPPORTED); F zero: y = 0.  No library workspace.  Execution, errors
+ * overlap one another or an input.  Up to 16 tokens of which nothing is kept take D and F
+ * to 2^30 - 1024, else SGEMM_ERR_UNSUPPORTED.  T or D zero: nothing is done (D zero with values
+ * to keep: SGEMM_ERR_UNSUPPORTED); F zero: y = 0.  No library workspace.  Execution, errors
  * and the bounded waits as sgemm; needs compute capability 10.3.
  */
 int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t ldx, const void *gate,
@@ -665,7 +666,8 @@ int sgemm_q4_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int
  * whose largest is below 2^-101 as if it were that.  Products with code - zero are exact and
  * added in fp32 within a group, whose sum times its scale is added in fp32; C is rounded
  * once.  A fixed order, no atomics, no workspace.  NaN and infinities of X give the IEEE
- * result.  K == 0: C = 0.  Execution and errors as sgemm.
+ * result.  K == 0: C = 0.  K to 2^30 - 1024, M to 2^21 - 64, scales to 2^32 - 1 elements, else
+ * SGEMM_ERR_UNSUPPORTED.  Execution and errors as sgemm.
  */
 int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_type, int64_t ldx, const void *Q,
              const float *S, const uint8_t *Z, const void *Q2, const float *S2, const uint8_t *Z2,

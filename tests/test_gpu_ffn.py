@@ -262,6 +262,43 @@ def test_one_token_captured_and_replayed():
     assert all(torch.equal(y, want) for y in outs)
 
 
+def test_few_tokens_in_clusters_of_three():
+    """A width for which 152 SMs have room for three CTAs a cluster, and one of more CTAs than that."""
+    _forward(5, 192, 12032)
+    _forward(3, 16, 50000)
+
+
+def test_captured_behind_two_streams():
+    """A block whose operands come from two streams of a captured graph, replayed with new ones."""
+    import torch
+    for T in (3, 200):
+        dy, x, gate, up, down = _inputs(T, 256, 512)
+        sources = [t.clone() for t in (x, gate, down)]
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        y = sg.ffn(x, gate, up, down)[0]
+        with torch.cuda.graph(graph):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                for _ in range(8):
+                    gate.copy_(sources[1])
+                    down.copy_(sources[2])
+            for _ in range(8):
+                x.copy_(sources[0])
+            y.zero_()
+            main.wait_stream(side)
+            sg.ffn(x, gate, up, down, y=y)
+            for t in (x, gate, down):
+                t.zero_()
+        for seed in (5, 6):
+            _, *new = _inputs(T, 256, 512, seed)
+            for to, t in zip(sources, (new[0], new[1], new[3])):
+                to.copy_(t)
+            graph.replay()
+            torch.cuda.synchronize()
+            fp.close("y", y, *fp.forward(new[0], new[1], up, new[3], "silu")["y"])
+
+
 def test_captured_and_replayed():
     import torch
     dy, x, gate, up, down = _inputs(300, 136, 264)

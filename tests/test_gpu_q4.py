@@ -121,6 +121,14 @@ def test_every_kernel(M, group, zeros, two):
         _product(M, N, K, group, zeros, two)
 
 
+@pytest.mark.parametrize("M,N,K,two", [(1, 24000, 768, False), (4, 11776, 1536, False), (1, 14848, 1280, False),
+                                       (4, 9728, 1792, False), (4, 12032, 768, True), (30, 11700, 768, False),
+                                       (1, 40000, 300, False), (1, 80000, 520, False)])
+def test_clusters_of_any_size(M, N, K, two):
+    """Sums cut over 3, 6, 5, 7, 3 and 3 CTAs of a cluster, where 152 SMs have room, and more CTAs than that."""
+    _product(M, N, K, 64, True, two, "bf16", "bf16")
+
+
 SIZES = [(1, 1, 1), (1, 16, 32), (2, 17, 33), (1, 1000, 127), (3, 33, 129), (1, 40, 20000), (5, 5000, 300), (1, 2048, 4096),
          (70, 100, 700), (200, 50, 260), (64, 300, 9000), (1, 5, 300000)]
 
@@ -254,3 +262,33 @@ def test_trained_quantised_and_served():
         fp.close("h", h, want, e + 2.0 ** -24 * (want.abs() + e))
         exact = want @ v["down"].t()
         fp.close("y", y, exact, qp.product(h, v["down"], 64)[1] + (e + 2.0 ** -24 * want.abs()) @ v["down"].abs().t())
+
+
+def test_captured_behind_two_streams():
+    """A product whose operands come from two streams of a captured graph, replayed with new ones."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w, a, b = (torch.randn(s, device="cuda", generator=gen) for s in ((600, 1000), (600, 1000), (5, 1000)))
+    q, s, _ = sg.q4_quantize(w)
+    x, C = torch.zeros((5, 1000), device="cuda"), torch.zeros((5, 600), device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                w.copy_(a)
+            sg.q4_quantize(w, Q=q, S=s)
+        for _ in range(8):
+            x.copy_(b)
+        C.zero_()
+        main.wait_stream(side)
+        sg.q4_gemm(x, q, s, C)
+        x.zero_()
+    for _ in range(3):
+        a.normal_(generator=gen)
+        b.normal_(generator=gen)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, e = qp.product(b, qp.values(*sg.q4_quantize(a), 128, 1000), 128)
+        fp.close("c", C, want, e + 2.0 ** -24 * (want.abs() + e) + fp.TINY)
