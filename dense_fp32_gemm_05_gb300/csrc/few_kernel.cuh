@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     // scales and zero codes of a stage: lane l has those of the warp's row l
     const int which = p.gated ? lane >> 4 : 0;
     const uint32_t n = (uint32_t)min(row0 + (p.gated ? lane & 15 : lane), p.N - 1);     // (rows past N: any valid one)
-    float scale[G ? GROUPS : 1], zero[G ? GROUPS : 1];
+    float scale[G ? GROUPS : 1];
+    uint32_t zero[G ? GROUPS : 1];             // (as loaded: what is made of them here would wait for them)
     auto fetch = [&](int i) {
         if constexpr (G != 0) {
             if (i >= mine) return;
@@ -265,8 +266,7 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                 const uint32_t at = (uint32_t)group * p.lds + n;
                 const bool there = group < p.groups;
                 scale[g] = there ? __ldg(p.s[which] + at) : 0.0f;
-                // (a pair of fp16 numbers, as the codes)
-                if (ZEROS) zero[g] = __uint_as_float(there ? __ldg(p.z[which] + at) * 0x10001u + 0x64006400u : 0x64006400u);
+                if (ZEROS) zero[g] = there ? __ldg(p.z[which] + at) : 0u;
             }
         }
     };
@@ -413,11 +413,12 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
         __syncthreads();
 
         for (; ok && done < mine && s_begin + kw + done * p.wk < s1; ++done) {
-            float sc[G ? GROUPS : 1], ze[G ? GROUPS : 1];
+            float sc[G ? GROUPS : 1];
+            uint32_t ze[(GROUPS + 3) / 4];                 // four groups' zero codes in a word
 #pragma unroll
             for (int g = 0; g < (G ? GROUPS : 1); ++g) {
                 sc[g] = scale[g];
-                ze[g] = ZEROS ? zero[g] : 0.0f;
+                if (ZEROS) ze[g / 4] = (g % 4 ? ze[g / 4] : 0u) | zero[g] << (g % 4 * 8);
             }
             fetch(done + 1);
             ok = __all_sync(0xffffffffu, mbar_wait_for(bar0 + 8u * slot, phase, p.wait_ns, p.error));
@@ -444,18 +445,26 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                 } else {
                     const int chunk = 2 * (s_begin + kw + done * p.wk - s0) + half;
                     const float *unit = units + chunk * (8 * NT) + 2 * t;
+                    uint32_t packed[2][2];                 // of the chunk's first group on
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (ZEROS) packed[i][j] = __shfl_sync(0xffffffffu, ze[half * R::GROUPS / 4], 16 * i + 8 * j + lane / 4);
 #pragma unroll
                     for (int g = 0; g < R::GROUPS; ++g) {
+                        const int byte = (half * R::GROUPS + g) % 4;
                         float s[2][2];
-                        uint32_t z[2][2];
+                        uint32_t z[2][2], z16[2][2];       // zero codes as the codes are: pairs of fp16 numbers
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int from = 16 * i + 8 * j + lane / 4;
                                 s[i][j] = __shfl_sync(0xffffffffu, sc[half * R::GROUPS + g], from);
-                                z[i][j] = ZEROS ? __float_as_uint(__shfl_sync(0xffffffffu, ze[half * R::GROUPS + g], from))
-                                                : 0x64086408u;
+                                const uint32_t pick = 0x4040u | (uint32_t)byte << 8 | (uint32_t)byte;
+                                z[i][j] = ZEROS ? __byte_perm(packed[i][j], 0x64u, pick) : 0x64086408u;
+                                z16[i][j] = ZEROS ? __byte_perm(packed[i][j] << 4, 0x64u, pick) : 0x64806480u;
                             }
                         float sum[2][NT][4];
 #pragma unroll
@@ -466,12 +475,11 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                             for (int i = 0; i < 2; ++i)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const uint32_t first = w[i][j][word], second = first >> 8, z1 = z[i][j];
-                                    const uint32_t z16 = 0x64006400u + ((z1 & 0x000f000fu) << 4);
-                                    a[i][j][0] = subtract(codes_of(first, 0x000f000fu), z1);
-                                    a[i][j][1] = subtract(codes_of(first, 0x00f000f0u), z16);
-                                    a[i][j][2] = subtract(codes_of(second, 0x000f000fu), z1);
-                                    a[i][j][3] = subtract(codes_of(second, 0x00f000f0u), z16);
+                                    const uint32_t first = w[i][j][word], second = first >> 8;
+                                    a[i][j][0] = subtract(codes_of(first, 0x000f000fu), z[i][j]);
+                                    a[i][j][1] = subtract(codes_of(first, 0x00f000f0u), z16[i][j]);
+                                    a[i][j][2] = subtract(codes_of(second, 0x000f000fu), z[i][j]);
+                                    a[i][j][3] = subtract(codes_of(second, 0x00f000f0u), z16[i][j]);
                                 }
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
