@@ -244,6 +244,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     if (lane == 0) {
         for (int i = 0; i < p.ring; ++i) mbar_init(bar0 + 8u * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&map0);
+        if (p.gated) prefetch_map(&map1);
     }
     __syncwarp();
     int issued = 0;
