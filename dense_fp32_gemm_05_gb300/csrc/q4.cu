@@ -1,16 +1,18 @@
 // Matrices of 4-bit codes: the quantiser, and the entry point of products with few rows of x
 // (the kernel is few_kernel.cuh's).
 //
-// Quantiser: memory bound.  A thread takes 8 neighbours of a row (a word of codes), so a group of
-// 32, 64 or 128 is 4, 8 or 16 lanes, and a warp 256 columns of ROWS rows, whose loads are
-// under way together; the group's extremes meet by shuffles, and its scales for the rows
-// are stored together.  Rows that do not start on a thread's pieces go through shared
-// memory, so that a warp still moves neighbours together.  Each step is one rounded fp32
-// operation, so the result is defined bit for bit.
-//   8192 x 4096 fp32, groups of 128, with values: 47 us among other calls, 6.1 TB/s (0.90 of the
-// measured copy; 44 us on the GPU).  1537 x 4095 bf16, groups of 32 with zero codes, values in
-// fp32: 19 us (2.2 TB/s; 29 where each thread moved its own elements): element loads of 2
-// bytes, and ~150 instructions for the 8 values, of which the divisions are 40.
+// Quantiser: bound by memory for fp32, by instructions for bf16 (77 % of the issue slots).  A
+// thread takes 8 neighbours of a row (a word of codes), so a group of 32, 64 or 128 is 4, 8 or
+// 16 lanes, and a warp 256 columns of ROWS rows, whose loads are under way together; the
+// group's extremes meet by shuffles, and its scales for the rows are stored together.  Rows
+// that do not start on a thread's pieces go through shared memory, so that a warp still
+// moves neighbours together.  Each step is one rounded fp32 operation, so the result is
+// defined bit for bit.
+//   8192 x 4096 fp32, groups of 128, with values: 45.5 us among other calls, 6.3 TB/s (0.93 of the
+// measured copy).  1537 x 4095 bf16, groups of 32 with zero codes, values in fp32: 14.4 us
+// (2.9 TB/s; 29 where each thread moved its own elements).  16384 x 8192 bf16, groups of 128
+// with zero codes: 124 us (173 with a check of each value for infinity and NaN, 4 rows
+// a warp and a 64-bit division a tile).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +30,10 @@ namespace sgemm_gb300 {
 namespace q4 {
 
 constexpr int THREADS = 256;
-constexpr int ROWS = 4;                        // of a warp
+// Rows of a warp, and CTAs an SM (40 registers a thread).  1537 x 4095 with values and 16384 x 8192
+// bf16, us: 1 row and 8 CTAs 15.7, 128.7; 2 and 6 14.4, 123.9; 2 and 5 16.5, 129.3; 4 and 4 18.5, 139.3.
+constexpr int ROWS = 2;
+constexpr int CTAS = 6;
 constexpr int COLS = 256;
 
 struct Params {
@@ -41,8 +46,7 @@ struct Params {
     int64_t lds;
     void *V;
     int64_t ldv;
-    int rows, cols, tiles_c;
-    int64_t tiles;
+    int rows, cols, tiles_r, tiles_c, step_r, step_c;
     int x_vec, q_vec, v_vec, v_bf16;
 };
 
@@ -64,24 +68,28 @@ __device__ __forceinline__ float load1(const float *from) { return *from; }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *from) { return __bfloat162float(*from); }
 
 template <typename T, int G, bool ZEROS>
-__global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, CTAS) quantize_kernel(const Params p) {
     constexpr int LANES = G / 8;               // of a group
     constexpr float INF = __builtin_huge_valf();
     __shared__ __align__(16) float rows_of[THREADS / 32][ROWS * COLS];      // a warp's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *own = rows_of[warp];
-    for (int64_t tile = (int64_t)blockIdx.x * (THREADS / 32) + warp; tile < p.tiles;
-         tile += (int64_t)gridDim.x * (THREADS / 32)) {
-        // (warps next to each other take rows next to each other: their scales are neighbours)
-        const int col = (int)(tile % p.tiles_c) * COLS + 8 * lane;
-        const int row0 = (int)(tile / p.tiles_c) * ROWS;
+    // tiles in rows of tiles_c; the next one of this warp is step_r rows and step_c tiles on
+    // (a division for each tile was a quarter of the instructions)
+    const uint32_t first = blockIdx.x * (THREADS / 32) + warp;
+    int tile_r = (int)(first / (uint32_t)p.tiles_c), tile_c = (int)(first % (uint32_t)p.tiles_c);
+    for (; tile_r < p.tiles_r; tile_r += p.step_r, tile_c += p.step_c) {
+        if (tile_c >= p.tiles_c) {
+            tile_c -= p.tiles_c;
+            if (++tile_r >= p.tiles_r) break;
+        }
+        const int col0 = tile_c * COLS, col = col0 + 8 * lane, row0 = tile_r * ROWS;
         const bool whole = col + 8 <= p.cols;
-        const int col0 = col - 8 * lane;
         float v[ROWS][8];
         if (p.x_vec) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const T *from = static_cast<const T *>(p.X) + (row0 + r) * p.ldx + col;
+                const T *from = static_cast<const T *>(p.X) + row0 * p.ldx + col + r * p.ldx;
                 if (row0 + r < p.rows && whole) {
                     load8(from, v[r]);
                 } else {
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = col0 + 32 * i + lane;
-                    e[r][i] = row0 + r < p.rows && c < p.cols ? load1(static_cast<const T *>(p.X) + (row0 + r) * p.ldx + c) : 0.0f;
+                    e[r][i] = row0 + r < p.rows && c < p.cols ? load1(static_cast<const T *>(p.X) + row0 * p.ldx + c + r * p.ldx) : 0.0f;
                 }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r)
@@ -110,16 +118,24 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
         float scale[ROWS], zero[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            float high = 0.0f, low = 0.0f;     // (symmetric: high is the largest finite |value|)
+            // (0 x is NaN for an infinity or NaN: one operation a value finds a warp's rare rows of them)
+            float test = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = v[r][i];
-                const bool finite = fabsf(x) < INF;
-                if (ZEROS) {
-                    high = fmaxf(high, finite ? x : 0.0f);
-                    low = fminf(low, finite ? x : 0.0f);
-                } else {
-                    high = fmaxf(high, finite ? fabsf(x) : 0.0f);
+            for (int i = 0; i < 8; ++i) test = __fmaf_rn(v[r][i], 0.0f, test);
+            const bool odd = __any_sync(0xffffffffu, !(test == 0.0f));
+            float high = 0.0f, low = 0.0f;     // (symmetric: high is the largest finite |value|)
+            if (!odd) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    high = fmaxf(high, ZEROS ? v[r][i] : fabsf(v[r][i]));
+                    if (ZEROS) low = fminf(low, v[r][i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = fabsf(v[r][i]) < INF ? v[r][i] : 0.0f;
+                    high = fmaxf(high, ZEROS ? x : fabsf(x));
+                    if (ZEROS) low = fminf(low, x);
                 }
             }
 #pragma unroll
@@ -129,20 +145,33 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
             }
             const float s = ZEROS ? __fsub_rn(__fdiv_rn(high, 15.0f), __fdiv_rn(low, 15.0f)) : __fdiv_rn(high, 7.0f);
             scale[r] = fmaxf(s, 1.17549435e-38f);
-            const float inverse = __fdiv_rn(1.0f, scale[r]);
+            const float inverse = __frcp_rn(scale[r]);
             zero[r] = ZEROS ? fminf(rintf(__fmul_rn(-low, inverse)), 15.0f) : 8.0f;
-            uint32_t word = 0;
+            // Numbers are rint(x inverse), by adding and taking off 1.5 2^23.  Finite ones are
+            // -zero or more and, symmetric, 7 or less, but for roundings to half a step: with zero
+            // codes both ends may round away from 0, to 16 steps.
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // rint by adding and taking off 1.5 2^23 (larger numbers are cut all the same), code
-                // and number from each other so too: without the conversions' slow unit
                 float n = __fsub_rn(__fadd_rn(__fmul_rn(v[r][i], inverse), 12582912.0f), 12582912.0f);
-                n = fminf(fmaxf(v[r][i] == v[r][i] ? n : 0.0f, -zero[r]), 15.0f - zero[r]);
-                word |= (__float_as_uint(__fadd_rn(n, 12582912.0f + zero[r])) & 15u) << (4 * i);
-                v[r][i] = __fmul_rn(n, scale[r]);
+                if (odd) n = fmaxf(v[r][i] == v[r][i] ? n : 0.0f, -zero[r]);
+                if (odd || ZEROS) n = fminf(n, 15.0f - zero[r]);
+                v[r][i] = n;
+            }
+            // four codes, exactly, in a number's low 16 bits
+            uint32_t half[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float *n = v[r] + 4 * i;
+                const float sum = __fmaf_rn(n[3], 4096.0f, __fmaf_rn(n[2], 256.0f, __fmaf_rn(n[1], 16.0f, n[0])));
+                half[i] = __float_as_uint(__fadd_rn(sum, __fmaf_rn(zero[r], 4369.0f, 12582912.0f)));
+            }
+            uint32_t word = __byte_perm(half[0], half[1], 0x5410);
+            if (p.V) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[r][i] = __fmul_rn(v[r][i], scale[r]);
             }
             if (row0 + r >= p.rows) continue;
-            uint8_t *q = p.Q + (row0 + r) * p.ldq + col / 2;
+            uint8_t *q = p.Q + row0 * p.ldq + col / 2 + r * p.ldq;
             if (whole && p.q_vec) {
                 *reinterpret_cast<uint32_t *>(q) = word;
             } else {
@@ -152,7 +181,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
                     if (col + 2 * i < p.cols) q[i] = (uint8_t)(word >> (8 * i));
             }
             if (p.V && p.v_vec) {
-                const int64_t at = (row0 + r) * p.ldv + col;
+                const int64_t at = row0 * p.ldv + col + r * p.ldv;
                 if (whole && !p.v_bf16) {
                     float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p.V) + at);
                     __stcs(to, make_float4(v[r][0], v[r][1], v[r][2], v[r][3]));
@@ -190,13 +219,13 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Params p) {
                     const int c = col0 + 32 * i + lane;
                     if (row0 + r >= p.rows || c >= p.cols) continue;
                     const float x = own[r * COLS + 32 * i + lane];
-                    const int64_t at = (row0 + r) * p.ldv + c;
+                    const int64_t at = row0 * p.ldv + c + r * p.ldv;
                     if (p.v_bf16) static_cast<__nv_bfloat16 *>(p.V)[at] = __float2bfloat16_rn(x);
                     else static_cast<float *>(p.V)[at] = x;
                 }
             __syncwarp();
         }
-        // a group's lanes store its rows' scales, a row each (4 lanes and rows at least)
+        // a group's lanes store its rows' scales, a row each (there are 4 lanes at least)
         if (col / G * G < p.cols) {
             const int r = lane % LANES;
             float s = scale[0], z = zero[0];
@@ -269,13 +298,16 @@ extern "C" int sgemm_q4_quantize(int64_t rows, int64_t cols, const void *X, int 
     p.V = V; p.ldv = ldv;
     p.rows = (int)rows; p.cols = (int)cols;
     p.tiles_c = (int)((cols + q4::COLS - 1) / q4::COLS);
-    p.tiles = (rows + q4::ROWS - 1) / q4::ROWS * p.tiles_c;
+    p.tiles_r = (int)((rows + q4::ROWS - 1) / q4::ROWS);
     p.x_vec = aligned16(X) && ldx % (f32 ? 4 : 8) == 0;
     p.q_vec = q4::aligned(Q, 4) && ldq % 4 == 0;
     p.v_bf16 = v_type == SGEMM_TYPE_BF16;
     p.v_vec = aligned16(V) && ldv % (p.v_bf16 ? 8 : 4) == 0;
     const int warps = q4::THREADS / 32;
-    const int grid = (int)std::min<int64_t>((p.tiles + warps - 1) / warps, (int64_t)sms * 64);
+    const int64_t tiles = (int64_t)p.tiles_r * p.tiles_c;
+    const int grid = (int)std::min<int64_t>((tiles + warps - 1) / warps, (int64_t)sms * 64);
+    p.step_r = grid * warps / p.tiles_c;
+    p.step_c = grid * warps % p.tiles_c;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return f32 ? q4::launch<float>(p, group, grid, s) : q4::launch<__nv_bfloat16>(p, group, grid, s);
 }

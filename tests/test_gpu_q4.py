@@ -77,6 +77,17 @@ def test_quantize_extremes(symmetric):
     _quantize(w, 32, symmetric)
 
 
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_ties(dtype, symmetric):
+    """Halves of a step everywhere, and ranges whose both ends round away from 0 (16 steps)."""
+    import torch
+    w = (torch.arange(256, device="cuda") % 31 - 15).float() / 2
+    w = torch.stack([w, w.flip(0), w + 0.5, w - 0.5, w * 0.25, w.abs(), -w.abs(), w.clamp(-7, 7)] * 2)
+    _quantize(w.to(_dtype(dtype)), 32, symmetric)
+    _quantize(w.to(_dtype(dtype))[:, 1:], 128, symmetric)
+
+
 def _weights(gen, N, K, group, zeros):
     import torch
     half = (K + 1) // 2
