@@ -605,7 +605,7 @@ def _of_shape(name, t, types, shape, device):
     if t.shape == shape and t.get_device() == device:    # (0.3 us less than what _matrix looks at)
         rows, cols = shape
         ld, unit = t.stride()
-        code = _type_of(t.dtype)
+        code = _types.get(t.dtype)
         if code in types and (unit == 1 or cols <= 1) and (ld >= cols or rows <= 1):
             return t.data_ptr(), code, (ld if rows > 1 else cols) or 1
     p, code, ld, rows, cols = _matrix(name, t, types, device)
@@ -614,38 +614,41 @@ def _of_shape(name, t, types, shape, device):
     return p, code, ld
 
 
-def _same_step(name, a, b):
-    if a[2] != b[2]:
-        raise ValueError(f"{name} must have the same strides")
-
-
 def _ffn_weights(x, gate, up, down):
     """The checked arguments that both passes begin with."""
     device = x.get_device()
     px, _, ldx, T, D = _matrix("x", x, _BF16)
     _check_device(device)
     F = gate.shape[0] if gate.dim() == 2 else -1
-    g, u = (_of_shape(n, t, _BF16, (F, D), device) for n, t in (("gate", gate), ("up", up)))
-    _same_step("gate and up", g, u)
-    d = _of_shape("down", down, _BF16, (D, F), device)
-    return device, T, D, F, (px, ldx), (g[0], u[0], g[2], d[0], d[2])
+    shape = (F, D)
+    pg, _, ld_in = _of_shape("gate", gate, _BF16, shape, device)
+    pu, _, ld_up = _of_shape("up", up, _BF16, shape, device)
+    if ld_in != ld_up:
+        raise ValueError("gate and up must have the same strides")
+    pd, _, ld_down = _of_shape("down", down, _BF16, (D, F), device)
+    return device, T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down
 
 
 def _ffn_kept(kept, T, F, device):
     """(type, g, u, leading dimension, sg, su, leading dimension of the scales)."""
     if len(kept) not in (2, 4):
         raise ValueError("kept holds g and u, and with 8-bit codes their scales")
-    g, u = (_of_shape(n, t, _KEPT, (T, F), device) for n, t in zip(("kept g", "kept u"), kept))
-    _same_step("kept g and u", g, u)
-    if g[1] != u[1] or (g[1] == TYPE_E4M3) != (len(kept) == 4):
+    shape = (T, F)
+    pg, code, ld = _of_shape("kept g", kept[0], _KEPT, shape, device)
+    pu, code_u, ld_u = _of_shape("kept u", kept[1], _KEPT, shape, device)
+    if ld != ld_u:
+        raise ValueError("kept g and u must have the same strides")
+    if code != code_u or (code == TYPE_E4M3) != (len(kept) == 4):
         raise ValueError("kept holds g and u in bfloat16, or in float8_e4m3fn and their scales")
     if len(kept) == 2:
-        return g[1], g[0], u[0], g[2], None, None, 1
-    sg, su = (_of_shape(n, t, _BF16, ((F + 127) // 128, T), device) for n, t in zip(("scales of g", "scales of u"),
-                                                                                    kept[2:]))
-    _same_step("the scales", sg, su)
+        return code, pg, pu, ld, None, None, 1
+    shape = ((F + 127) // 128, T)
+    psg, _, lds = _of_shape("scales of g", kept[2], _BF16, shape, device)
+    psu, _, lds_u = _of_shape("scales of u", kept[3], _BF16, shape, device)
+    if lds != lds_u:
+        raise ValueError("the scales must have the same strides")
     # (one row of scales, whose stride means nothing, still has a token in each column)
-    return g[1], g[0], u[0], g[2], sg[0], su[0], sg[2]
+    return code, pg, pu, ld, psg, psu, lds
 
 
 def _scratch_rows(T, F, like, stream):
@@ -668,7 +671,7 @@ def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=
     The tensors are on the current device.  Asynchronous on ``stream`` (default:
     torch's current stream); raises SgemmError on any non-zero status.
     """
-    device, T, D, F, (px, ldx), (pg, pu, ld_in, pd, ld_down) = _ffn_weights(x, gate, up, down)
+    device, T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down = _ffn_weights(x, gate, up, down)
     if kept is None and keep is not None:
         import torch
         if keep not in (torch.bfloat16, torch.float8_e4m3fn):
@@ -702,7 +705,7 @@ def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgat
     then).  ``scratch``: three T x F bfloat16 buffers with the same strides, rows on
     16 bytes (on 128, as new ones have them, they are read faster).  Buffers, device, stream and errors as in ``ffn``.
     """
-    device, T, D, F, (px, ldx), (pg, pu, ld_in, pd, ld_down) = _ffn_weights(x, gate, up, down)
+    device, T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down = _ffn_weights(x, gate, up, down)
     pdy, _, lddy = _of_shape("dy", dy, _BF16, (T, D), device)
     k = _ffn_kept(kept, T, F, device)
     if accumulate and (dgate is None or dup is None or ddown is None):
@@ -717,20 +720,26 @@ def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgat
         ddown = _new((D, F), x.dtype, x.device, stream)
     if scratch is None:
         scratch = tuple(_scratch_rows(T, F, x, stream) for _ in range(3))
-    s = [_of_shape(f"scratch {i}", t, _BF16, (T, F), device) for i, t in enumerate(scratch)]
-    if len(s) != 3:
+    if len(scratch) != 3:
         raise ValueError("scratch is three buffers")
-    _same_step("the scratch buffers", s[0], s[1])
-    _same_step("the scratch buffers", s[0], s[2])
+    shape = (T, F)
+    p0, _, ld0 = _of_shape("scratch 0", scratch[0], _BF16, shape, device)
+    p1, _, ld1 = _of_shape("scratch 1", scratch[1], _BF16, shape, device)
+    p2, _, ld2 = _of_shape("scratch 2", scratch[2], _BF16, shape, device)
+    if ld0 != ld1 or ld0 != ld2:
+        raise ValueError("the scratch buffers must have the same strides")
     pdx, _, lddx = _of_shape("dx", dx, _BF16, (T, D), device)
-    dg, du = (_of_shape(n, t, _FLOATS, (F, D), device) for n, t in (("dgate", dgate), ("dup", dup)))
-    _same_step("dgate and dup", dg, du)
-    dd = _of_shape("ddown", ddown, _FLOATS, (D, F), device)
-    if dg[1] != du[1] or dg[1] != dd[1]:
+    shape = (F, D)
+    pdg, grad, ld_din = _of_shape("dgate", dgate, _FLOATS, shape, device)
+    pdu, grad_up, ld_dup = _of_shape("dup", dup, _FLOATS, shape, device)
+    if ld_din != ld_dup:
+        raise ValueError("dgate and dup must have the same strides")
+    pdd, grad_down, ld_ddown = _of_shape("ddown", ddown, _FLOATS, (D, F), device)
+    if grad != grad_up or grad != grad_down:
         raise ValueError("the weight gradients must be of one type")
     st = load().sgemm_ffn_backward(
-        T, D, F, pdy, lddy, px, ldx, pg, pu, ld_in, pd, ld_down, activation, *k, s[0][0], s[1][0], s[2][0],
-        s[0][2], pdx, lddx, dg[1], int(accumulate), dg[0], du[0], dg[2], dd[0], dd[2],
+        T, D, F, pdy, lddy, px, ldx, pg, pu, ld_in, pd, ld_down, activation, *k, p0, p1, p2, ld0,
+        pdx, lddx, grad, 1 if accumulate else 0, pdg, pdu, ld_din, pdd, ld_ddown,
         _current_stream(device) if stream is None else _stream(stream))
     if st != SGEMM_OK:
         raise SgemmError(st, "sgemm_ffn_backward")

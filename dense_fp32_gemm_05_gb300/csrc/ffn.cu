@@ -977,13 +977,32 @@ struct Launch {
         const int b_rows = t.ctas == 2 ? t.cols / 2 : t.cols;                // of B per CTA
         const int box_a = a0.across ? 64 : 128;
         const int box_b = b0.across ? 64 : gated && t.ctas == 1 ? b_rows / 2 : b_rows;
-        ok = ok && bf16_map(&maps.a[0], a0, box_a) && bf16_map(&maps.b[0], b0, box_b);
-        // (a map takes the host half a microsecond)
-        if (a1.p == a0.p) maps.a[1] = maps.a[0];
-        else ok = ok && bf16_map(&maps.a[1], a1, box_a);
-        if (b1.p == b0.p) maps.b[1] = maps.b[0];
-        else ok = ok && bf16_map(&maps.b[1], b1, box_b);
+        map(maps.a[0], a0, box_a);
+        map(maps.b[0], b0, box_b);
+        map(maps.a[1], a1, box_a);
+        map(maps.b[1], b1, box_b);
         return q;
+    }
+
+  private:
+    struct Made {
+        Operand o;
+        int box;
+        const CUtensorMap *map;
+    };
+    Made made[4 * ffn::PRODUCTS];
+    int count = 0;
+
+    // (a map takes the host half a microsecond: those of this launch are copied)
+    void map(CUtensorMap &to, const Operand &o, int box) {
+        for (int i = 0; i < count; ++i)
+            if (made[i].o.p == o.p && made[i].o.rows == o.rows && made[i].o.cols == o.cols && made[i].o.ld == o.ld &&
+                made[i].box == box) {
+                to = *made[i].map;
+                return;
+            }
+        ok = ok && bf16_map(&to, o, box);
+        made[count++] = Made{o, box, &to};
     }
 };
 
