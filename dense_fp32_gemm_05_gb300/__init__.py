@@ -380,16 +380,19 @@ def _check_device(device):
         raise ValueError(f"the operands are on device {device}, which is not the current one")
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, dtype, device, stream, ld=None):
     """A tensor for a call's result: of the stream that the call runs on, so that torch gives
-    it no memory that work on another stream still uses."""
+    it no memory that work on another stream still uses.  ld: a matrix' row stride."""
     import torch
-    if stream is None:
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        with torch.cuda.stream(stream):
+            return _new(shape, dtype, device, None, ld)
+    if ld is None or ld == shape[1]:
         return torch.empty(shape, device=device, dtype=dtype)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, device=device, dtype=dtype)
+    # (an empty tensor's columns taken off cost 2 us more)
+    return torch.empty_strided(shape, (ld, 1), device=device, dtype=dtype)
 
 
 def sgemm_fp8_quantize(rows, cols, X, x_type, ldx, group_rows, group_cols, Q, q_type, ldq, S, lds,
@@ -654,7 +657,7 @@ def _ffn_kept(kept, T, F, device):
 def _scratch_rows(T, F, like, stream):
     """A T x F bf16 matrix whose rows start on 128 bytes: TMA reads them in whole lines
     (gradients of 777 x 1000 x 2501 32.7 us, with rows on 16 bytes 40.9)."""
-    return _new((T, (F + 63) // 64 * 64), like.dtype, like.device, stream)[:, :F]
+    return _new((T, F), like.dtype, like.device, stream, (F + 63) // 64 * 64)
 
 
 def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=None, stream=None):
@@ -676,7 +679,7 @@ def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=
         import torch
         if keep not in (torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError("keep must be torch.bfloat16, torch.float8_e4m3fn or None")
-        kept = tuple(_new((T, (F + 15) // 16 * 16), keep, x.device, stream)[:, :F] for _ in range(2))
+        kept = tuple(_new((T, F), keep, x.device, stream, (F + 15) // 16 * 16) for _ in range(2))
         if keep != torch.bfloat16:
             kept += tuple(_new(((F + 127) // 128, T), torch.bfloat16, x.device, stream) for _ in range(2))
     elif kept is not None and keep is not None and kept[0].dtype != keep:
@@ -793,7 +796,7 @@ def q4_quantize(W, group=128, symmetric=True, Q=None, S=None, Z=None, V=None, st
     if Q is None or S is None or Z is None and not symmetric:
         import torch
     if Q is None:
-        Q = _new((rows, (half + 15) // 16 * 16), torch.uint8, W.device, stream)[:, :half]
+        Q = _new((rows, half), torch.uint8, W.device, stream, (half + 15) // 16 * 16)
     if S is None:
         S = _new((groups, rows), torch.float32, W.device, stream)
     if Z is None and not symmetric:
