@@ -42,7 +42,9 @@ int few_take_device_error() {
 int run_few(const FewCall &c, cudaStream_t s, bool early) {
     const bool gated = c.w2 != nullptr;
     const int parts = few_parts(c.group, c.x_f32);
-    const FewPlan pl = few_plan(c.M, c.N, c.K, parts, gated, c.group, few_clusters);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_status();
+    const FewPlan pl = few_plan(c.M, c.N, c.K, parts, gated, c.group, [dev](int nt, int ks) { return few_clusters(dev, nt, ks); });
     FewLaunch l{};
     few::Params &p = l.p;
     p.x = c.x;

@@ -57,8 +57,9 @@ inline int64_t few_sums_bytes(int nt, int64_t rows, int wk) {
 // Shared memory of a CTA, which has half an SM's with few columns.
 inline int64_t few_most_smem(int nt) { return (nt <= 2 ? 110 : 216) * 1024; }
 
-// The clusters of `ks` CTAs of nt tiles of columns that the current device runs together (0: an error).
-int few_clusters(int nt, int ks);
+// The clusters of `ks` CTAs of nt tiles of columns that the current device, dev, runs together
+// (0: an error).
+int few_clusters(int dev, int nt, int ks);
 
 // clusters(nt, ks): as few_clusters.
 template <typename Clusters>

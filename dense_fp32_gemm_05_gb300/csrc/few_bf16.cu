@@ -12,11 +12,9 @@ int launch_few<0>(const FewLaunch &l, cudaStream_t s) {
 
 // A CTA has the most shared memory that a plan gives it; registers are as all kernels of so
 // many tiles have them (two CTAs an SM, or one).
-int few_clusters(int nt, int ks) {
+int few_clusters(int dev, int nt, int ks) {
     static std::atomic<int> known[64][2][9];       // one more than the answer
     const int wide = nt > 2;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::atomic<int> *at = dev < 64 && ks <= 8 ? &known[dev][wide][ks] : nullptr;
     if (at && at->load(std::memory_order_relaxed)) return at->load(std::memory_order_relaxed) - 1;
     const auto kern = wide ? few::few_kernel<0, false, 4> : few::few_kernel<0, false, 1>;
