@@ -21,7 +21,7 @@
 //   the block's largest; fp32 in two parts, in columns of their own, the second 2^11
 //   times what the first leaves.  An MMA never spans two groups; a group's sum is scaled
 //   into the fp32 accumulator.
-//   Tried for 1 x 16384 x 8192, which takes 19.2 us among other calls: codes as bf16 numbers, 128 + code (11
+//   Tried for 1 x 16384 x 8192, which takes 18.8 us among other calls: codes as bf16 numbers, 128 + code (11
 //   operations a word, not 9), 27 us; as E4M3 bytes (3, but the MMA is made of conversions and
 //   fp16 MMAs) 29; zero codes taken off a group's sum instead (5 a word, but fp32 results
 //   2e-6 off, four times as much as fp32 arithmetic) 25, with loads into registers.  A code's
