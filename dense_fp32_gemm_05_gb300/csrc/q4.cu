@@ -329,7 +329,8 @@ extern "C" int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_ty
     if (ldq < std::max<int64_t>(1, (K + 1) / 2)) return -13;
     if (lds < std::max<int64_t>(1, N)) return -14;
     if (!q4::is_group(group)) return -15;
-    if (!act::is_activation(activation) || (!gated && activation != SGEMM_ACT_NONE)) return -16;
+    // (a second matrix without elements may have no address: then there is nothing to activate)
+    if (!act::is_activation(activation) || (all && !gated && activation != SGEMM_ACT_NONE)) return -16;
     if (!fp8::is_float_type(c_type)) return -18;
     const bool c_f32 = c_type == SGEMM_TYPE_F32;
     if (out && (C == nullptr || !q4::aligned(C, c_f32 ? 4 : 2))) return -17;
