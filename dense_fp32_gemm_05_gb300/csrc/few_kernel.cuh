@@ -59,6 +59,12 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int STAGE = kFewStage;
 constexpr int RED = 36;                        // floats of a column of 32 partial sums: no bank twice
 constexpr uint64_t kDrainNs = 1000000000ull;
+// (4 bits) Sums are held this many times smaller than they are until a warp has its own: a group's, 15 *
+// 128 times the largest of x at most, then stays below 2^128 before its scale is on it.  (What it
+// costs is bits of results below 2^-115.  Without it x from 2^117 on and a small scale gave an
+// infinity; scales multiplied first lose bits of results below 2^-101; found out and held smaller
+// for a CTA's range of x only where x is that large, 2 to 5 % of the time of every call.)
+constexpr float ACC = 2048.0f;
 
 struct Params {
     const void *x;
@@ -403,8 +409,9 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                                 }
                                 to[R::word_of(4 * i + t) * unit_step + R::lane_of(4 * i + t)] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
+                            // (2^11 smaller than they are: see ACC)
                             if (t == 0)
-                                units[to_chunk * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23);
+                                units[to_chunk * (8 * NT) + col] = __uint_as_float((uint32_t)(exponent - 14 - 11 * part) << 23) * (1.0f / ACC);
                         }
                     }
                 }
@@ -529,7 +536,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[(8 * j + 2 * t + k % 2) * RED + 16 * i + lane / 4 + 8 * (k / 2)] = acc[i][j][k];
+            for (int k = 0; k < 4; ++k)
+                to[(8 * j + 2 * t + k % 2) * RED + 16 * i + lane / 4 + 8 * (k / 2)] = G ? acc[i][j][k] * ACC : acc[i][j][k];
     __syncthreads();
     // (a CTA's rows are a power of two; four of them, next to each other in red and in a row
     // of C, at a time)

@@ -665,8 +665,10 @@ int sgemm_q4_quantize(int64_t rows, int64_t cols, const void *X, int x_type, int
  * in two parts, to the larger of 2^-23 of each and 2^-46 of their block's largest; blocks
  * whose largest is below 2^-101 as if it were that.  Products with code - zero are exact and
  * added in fp32 within a group, whose sum times its scale is added in fp32; C is rounded
- * once.  A fixed order, no atomics, no workspace.  NaN and infinities of X give the IEEE
- * result.  K == 0: C = 0, of one matrix or two (any activation).  K to 2^30 - 1024, M to 2^21 - 64, scales to 2^32 - 1 elements, else
+ * once; sums below 2^-115 are held to 2^-138.  A group's sum does not overflow before its
+ * scale is on it, however large finite X is.  A fixed order, no atomics, no
+ * workspace.  NaN and infinities of X give the IEEE result.  K == 0: C = 0, of one matrix or
+ * two (any activation).  K to 2^30 - 1024, M to 2^21 - 64, scales to 2^32 - 1 elements, else
  * SGEMM_ERR_UNSUPPORTED.  Execution and errors as sgemm.
  */
 int sgemm_q4(int64_t M, int64_t N, int64_t K, const void *X, int x_type, int64_t ldx, const void *Q,
