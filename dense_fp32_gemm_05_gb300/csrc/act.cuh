@@ -4,7 +4,9 @@
 //   relu  act(g) = max(g, 0)  gelu  act(g) = g p,  p = 1 / (1 + exp(-v)), v = 2 c (g + a g^3),
 //                             c = sqrt(2 / pi), a = 0.044715: the tanh form, (1 + tanh(v / 2)) / 2 = p
 //
-// act(g) = factor * g, and act'(g) = p (1 + g (1 - p) v'(g)): both from one exponential.
+// act(g) = factor * g, and act'(g) = p (1 + g (1 - p) v'(g)): both from one exponential (and in
+// gelu's from g cut to +-64, where p is 0 or 1: with a finite g past 4e35 its second term was
+// 0 times an infinity).
 // NaN passes through (relu: 0 at NaN's derivative, as a comparison has it).
 #pragma once
 
@@ -17,15 +19,16 @@ namespace act {
 
 inline bool is_activation(int a) { return a >= SGEMM_ACT_NONE && a <= SGEMM_ACT_GELU; }
 
-// p and v'(g) of silu and gelu.  gelu takes v from g cut to +-64, where p is 0 or 1 to
+// p, v'(g) and the g that both are of (t), of silu and gelu.  gelu takes v from g cut to +-64, where p is 0 or 1 to
 // the last bit: g^3 and v' stay finite.  __expf's error is 2 units and a few more as its
 // argument grows; where that counts p is far below a bf16 unit of 1.
 template <int A>
-__device__ __forceinline__ float factor_of(float g, float &dv) {
+__device__ __forceinline__ float factor_of(float g, float &t, float &dv) {
     float v = g;
+    t = g;
     dv = 1.0f;
     if (A == SGEMM_ACT_GELU) {
-        const float t = fabsf(g) > 64.0f ? copysignf(64.0f, g) : g;
+        t = fabsf(g) > 64.0f ? copysignf(64.0f, g) : g;
         const float s = t * t;
         v = 1.5957691216057308f * t * (1.0f + 0.044715f * s);
         dv = 1.5957691216057308f * (1.0f + 0.134145f * s);
@@ -37,8 +40,8 @@ template <int A>
 __device__ __forceinline__ float value(float g) {
     if (A == SGEMM_ACT_NONE) return g;
     if (A == SGEMM_ACT_RELU) return g < 0.0f ? 0.0f : g;
-    float dv;
-    return g * factor_of<A>(g, dv);
+    float t, dv;
+    return g * factor_of<A>(g, t, dv);
 }
 
 // act(g), and its derivative.
@@ -52,9 +55,9 @@ __device__ __forceinline__ float value_slope(float g, float &slope) {
         slope = g > 0.0f ? 1.0f : 0.0f;
         return g < 0.0f ? 0.0f : g;
     }
-    float dv;
-    const float p = factor_of<A>(g, dv);
-    slope = p * (1.0f + g * (1.0f - p) * dv);
+    float t, dv;
+    const float p = factor_of<A>(g, t, dv);
+    slope = p * (1.0f + t * (1.0f - p) * dv);
     return g * p;
 }
 
