@@ -84,7 +84,9 @@ typedef enum {
                                   sgemm_ffma_static_scratch holds            */
 } sgemm_status;
 
-/* Activation of the fused epilogue (sgemm_epilogue), and of gated feed-forward blocks. */
+/* Activation of the fused epilogue (sgemm_epilogue), and of gated feed-forward blocks.  SiLU and
+ * GELU are within 2^-20 (1 + |v|) of their value, v = x for SiLU, 2 sqrt(2/pi) (x + 0.044715 x^3)
+ * for GELU. */
 typedef enum {
     SGEMM_ACT_NONE = 0,
     SGEMM_ACT_RELU = 1,    /* max(x, 0); NaN passes through */
