@@ -554,7 +554,7 @@ def moe(x, router, gate, s_gate, up, s_up, down, s_down, topk, renormalize=True,
     if logits is None:
         logits = _new((T, E), f32, x.device, stream)
     if y is None:
-        y = _new((T, D), x.dtype, x.device, stream)
+        y = _rows_on_16(T, D, x, stream)
     if indices is None:
         indices = _new(chosen, i32, x.device, stream)
     if weights is None:
@@ -660,6 +660,11 @@ def _scratch_rows(T, F, like, stream):
     return _new((T, F), like.dtype, like.device, stream, (F + 63) // 64 * 64)
 
 
+def _rows_on_16(T, D, like, stream):
+    """A T x D bf16 matrix whose rows start on 16 bytes, so that it may be another block's x or dy."""
+    return _new((T, D), like.dtype, like.device, stream, (D + 7) // 8 * 8)
+
+
 def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=None, stream=None):
     """(y, kept): a gated feed-forward block, y = (act(x gate^T) * (x up^T)) down^T.
 
@@ -670,8 +675,9 @@ def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=
     ``ffn_backward`` as (g, u), or as (g, u, sg, su): codes, and bfloat16 scales
     of shape (ceil(F / 128), T) for each 128 columns of a row; None keeps nothing,
     and kept is None.  ``kept``, ``y`` and ``h`` (T x F, the product's other operand, rows on
-    16 bytes) take buffers to write into; new ones belong to the stream of the call.
-    The tensors are on the current device.  Asynchronous on ``stream`` (default:
+    16 bytes) take buffers to write into; new ones belong to the stream of the call, and
+    have rows that start on 16 bytes, as the next block's x does (y's are padded where D is no
+    multiple of 8).  The tensors are on the current device.  Asynchronous on ``stream`` (default:
     torch's current stream); raises SgemmError on any non-zero status.
     """
     device, T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down = _ffn_weights(x, gate, up, down)
@@ -686,7 +692,7 @@ def ffn(x, gate, up, down, activation=ACT_SILU, keep=None, kept=None, y=None, h=
         raise ValueError("kept is not of the type that keep asks for")
     k = (TYPE_BF16, None, None, max(F, 1), None, None, 1) if kept is None else _ffn_kept(kept, T, F, device)
     if y is None:
-        y = _new((T, D), x.dtype, x.device, stream)
+        y = _rows_on_16(T, D, x, stream)
     if h is None:
         h = _scratch_rows(T, F, x, stream)
     py, _, ldy = _of_shape("y", y, _BF16, (T, D), device)
@@ -706,7 +712,9 @@ def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgat
     them.  dx is bfloat16; dgate, dup and ddown are bfloat16 or, in buffers given,
     all float32.  ``accumulate`` adds to the three weight gradients (which are given
     then).  ``scratch``: three T x F bfloat16 buffers with the same strides, rows on
-    16 bytes (on 128, as new ones have them, they are read faster).  Buffers, device, stream and errors as in ``ffn``.
+    16 bytes (on 128, as new ones have them, they are read faster).  New weight gradients are
+    contiguous; a new dx has rows on 16 bytes, as the block before takes its dy.
+    Buffers, device, stream and errors as in ``ffn``.
     """
     device, T, D, F, px, ldx, pg, pu, ld_in, pd, ld_down = _ffn_weights(x, gate, up, down)
     pdy, _, lddy = _of_shape("dy", dy, _BF16, (T, D), device)
@@ -714,7 +722,7 @@ def ffn_backward(dy, x, gate, up, down, kept, activation=ACT_SILU, dx=None, dgat
     if accumulate and (dgate is None or dup is None or ddown is None):
         raise ValueError("accumulate needs the three weight gradients")
     if dx is None:
-        dx = _new((T, D), x.dtype, x.device, stream)
+        dx = _rows_on_16(T, D, x, stream)
     if dgate is None:
         dgate = _new((F, D), x.dtype, x.device, stream)
     if dup is None:
