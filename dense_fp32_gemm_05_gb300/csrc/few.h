@@ -84,10 +84,13 @@ FewPlan few_plan(int64_t M, int64_t N, int64_t K, int parts, bool gated, int gro
     const int most_ks = p.nt <= 2 ? 8 : 4;
     int64_t fewest = stages + 1;
     p.wk = p.ks = 1;
+    // Rows of x past a block's are blocks of CTAs beside it, and count (64 x 2048 x 4096 fp32 22.1 us, as
+    // if each had the GPU to itself 33.1; 512 x 8192 x 4096 bf16 168 and 216).
+    const int64_t blocks = (all + 8 * p.nt - 1) / (8 * p.nt);
     for (int i = 0; i < most_ks * 4; ++i) {
         const int wk = 1 << (little ? 3 - i % 4 : i / most_ks), ks = little ? 1 + i / 4 : most_ks - i % most_ks;
         const int64_t per_cta = (gated ? 16 : 32) * (kFewWarps / wk), each = ((stages + ks - 1) / ks + wk - 1) / wk;
-        if (ks > stages || each >= fewest || (N + per_cta - 1) / per_cta > clusters(p.nt, ks)) continue;
+        if (ks > stages || each >= fewest || (N + per_cta - 1) / per_cta * blocks > clusters(p.nt, ks)) continue;
         fewest = each;
         p.wk = wk;
         p.ks = ks;
