@@ -47,7 +47,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <new>
 #include <type_traits>
 
 #include "act.cuh"
@@ -1276,21 +1275,17 @@ extern "C" int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t
     if (!tma_rows(x, ldx, T) || !tma_rows(gate, ld_in, F) || !tma_rows(up, ld_in, F) || !tma_rows(down, ld_down, D) ||
         !tma_rows(h, ldh, T))
         return SGEMM_ERR_UNSUPPORTED;
-    try {
-        Block b{T, D, F};
-        b.x = Operand{x, T, D, up8(ldx), false};
-        b.gate = Operand{gate, F, D, up8(ld_in), false};
-        b.up = Operand{up, F, D, up8(ld_in), false};
-        b.down = Operand{down, D, F, up8(ld_down), false};
-        b.act = activation;
-        b.keep = !keep ? 0 : codes ? 2 : 1;
-        b.g = g; b.u = u; b.sg = sg; b.su = su;
-        b.ld_kept = ld_kept; b.ld_scales = ld_scales;
-        b.h = h; b.ldh = up8(ldh);
-        return run_forward(b, y, ldy, s);
-    } catch (const std::bad_alloc &) {
-        return SGEMM_ERR_NOMEM;
-    }
+    Block b{T, D, F};
+    b.x = Operand{x, T, D, up8(ldx), false};
+    b.gate = Operand{gate, F, D, up8(ld_in), false};
+    b.up = Operand{up, F, D, up8(ld_in), false};
+    b.down = Operand{down, D, F, up8(ld_down), false};
+    b.act = activation;
+    b.keep = !keep ? 0 : codes ? 2 : 1;
+    b.g = g; b.u = u; b.sg = sg; b.su = su;
+    b.ld_kept = ld_kept; b.ld_scales = ld_scales;
+    b.h = h; b.ldh = up8(ldh);
+    return run_forward(b, y, ldy, s);
 }
 
 extern "C" int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *dy, int64_t lddy, const void *x, int64_t ldx,
@@ -1348,23 +1343,19 @@ extern "C" int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *d
     if (!tma_rows(dy, lddy, T) || !tma_rows(x, ldx, T) || !tma_rows(gate, ld_in, F) || !tma_rows(up, ld_in, F) ||
         !tma_rows(down, ld_down, D) || !tma_rows(dg, ldh, T) || !tma_rows(du, ldh, T) || !tma_rows(h, ldh, T))
         return SGEMM_ERR_UNSUPPORTED;
-    try {
-        Block b{T, D, F};
-        b.x = Operand{x, T, D, up8(ldx), false};
-        b.gate = Operand{gate, F, D, up8(ld_in), false};
-        b.up = Operand{up, F, D, up8(ld_in), false};
-        b.down = Operand{down, D, F, up8(ld_down), false};
-        b.act = activation;
-        b.keep = codes ? 2 : 1;
-        b.g = const_cast<void *>(g); b.u = const_cast<void *>(u);
-        b.sg = const_cast<void *>(sg); b.su = const_cast<void *>(su);
-        b.ld_kept = ld_kept; b.ld_scales = ld_scales;
-        b.h = h; b.ldh = up8(ldh);
-        return run_backward(b, Operand{dy, T, D, up8(lddy), false},
-                            Gradients{dg, du, dx, lddx, dgate, dup, ld_din, ddown, ld_ddown, grad_type, accumulate != 0}, s);
-    } catch (const std::bad_alloc &) {
-        return SGEMM_ERR_NOMEM;
-    }
+    Block b{T, D, F};
+    b.x = Operand{x, T, D, up8(ldx), false};
+    b.gate = Operand{gate, F, D, up8(ld_in), false};
+    b.up = Operand{up, F, D, up8(ld_in), false};
+    b.down = Operand{down, D, F, up8(ld_down), false};
+    b.act = activation;
+    b.keep = codes ? 2 : 1;
+    b.g = const_cast<void *>(g); b.u = const_cast<void *>(u);
+    b.sg = const_cast<void *>(sg); b.su = const_cast<void *>(su);
+    b.ld_kept = ld_kept; b.ld_scales = ld_scales;
+    b.h = h; b.ldh = up8(ldh);
+    return run_backward(b, Operand{dy, T, D, up8(lddy), false},
+                        Gradients{dg, du, dx, lddx, dgate, dup, ld_din, ddown, ld_ddown, grad_type, accumulate != 0}, s);
 }
 
 extern "C" int sgemm_ffn_plan(int64_t T, int64_t D, int64_t F, int kept_type, int num_sms, int *out_rows, int *out_cols,

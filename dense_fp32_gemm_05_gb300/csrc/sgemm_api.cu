@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <map>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -73,7 +74,13 @@ static int device_state(DeviceState **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
-    DeviceState &d = g_dev[dev];
+    DeviceState *found = nullptr;
+    try {                                          // (a device's first call allocates its entry)
+        found = &g_dev[dev];
+    } catch (const std::bad_alloc &) {
+        return SGEMM_ERR_NOMEM;
+    }
+    DeviceState &d = *found;
     if (!d.ready) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
