@@ -21,13 +21,16 @@
 //   the block's largest; fp32 in two parts, in columns of their own, the second 2^11
 //   times what the first leaves.  An MMA never spans two groups; a group's sum is scaled
 //   into the fp32 accumulator.
-//   Tried for 1 x 16384 x 8192, which takes 18.8 us among other calls: codes as bf16 numbers, 128 + code (11
-//   operations a word, not 9), 27 us; as E4M3 bytes (3, but the MMA is made of conversions and
-//   fp16 MMAs) 29; zero codes taken off a group's sum instead (5 a word, but fp32 results
-//   2e-6 off, four times as much as fp32 arithmetic) 25, with loads into registers.  A code's
-//   bits alone are an fp16 number, too, but a subnormal one, which the MMA aligns with the
-//   smallest normal numbers: sums lose up to 7 bits (1.4e-6 off).
-//   8-bit integer MMAs take 65 clocks each, 8 times these.
+//   (Integers made into numbers by the exponent's bits, and odd ones left 16 times larger, are a
+//   published way with 4-bit weights: Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't
+//   Run", 2022.  The order of k, the exact zero codes and the factor on x's side are this kernel's.)
+//   Tried for 1 x 16384 x 8192 on earlier forms of the kernel, which took 33 us with weights loaded into
+//   registers and 22.5 when the rings were new (18.9 now): codes as bf16 numbers, 128 + code (11
+//   operations a word, not 9), 27 us; as E4M3 bytes (3) 29; zero codes taken off a group's sum
+//   instead (5 a word, but fp32 results 2e-6 off, four times as much as fp32 arithmetic) 25,
+//   with loads into registers.  A code's bits alone are an fp16 number, too, but a subnormal
+//   one, and sums came out with up to 7 bits fewer (1.4e-6 off).  8-bit integer MMAs take 65
+//   clocks each, 8 times these.
 // The sum is cut over the warps of a CTA (which take stages in turn, so that neighbours in
 // memory are read together) and over a cluster of CTAs; the partial sums meet
 // through (distributed) shared memory in a fixed order: no workspace, no atomics.
@@ -84,7 +87,7 @@ struct Params {
     unsigned long long wait_ns;
 };
 
-// The same from sums of zero.
+// 16 rows of W times 8 columns of x over 16 of k: the first of a sum, and one added to it.
 __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
@@ -104,8 +107,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (word & mask) | the exponents of 1024, in one operation (as C++ it became two, each with a
-// constant of its own).
+// (word & mask) | the exponents of 1024.
 __device__ __forceinline__ uint32_t codes_of(uint32_t word, uint32_t mask) {
     uint32_t v;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word), "r"(mask), "r"(0x64006400u));

@@ -27,7 +27,8 @@
 // What bounds it (4096 tokens x 2048 x 8192, values kept as codes; alone, us, and the tensor
 // pipe's busy cycles): GATED 150, 92 %; the down product 82, 89 %; SLOPE 118, 58 %: its epilogue reads two and writes three
 // matrices through the shared memory and L2 that feed the MMAs (95 without its stores, 105
-// without its loads, 111 without its arithmetic, 75 without it); the gradients 353, 97 %.  Tiles on pairs
+// without its loads, 111 without its arithmetic, 75 without it, in copies made to measure that); the
+// gradients 353, 97 %.  Tiles on pairs
 // take half the operand traffic of single SMs' for each MMA (4096 x 4096 x 8192 down 164 us,
 // with 128 x 128 tiles 225, 128 x 64 350); small calls have too few of them (ffn_plan.h), and where
 // one product has few tiles of any size its sum is cut over a cluster (SPLIT: 100 x 1001 x 2731
@@ -329,7 +330,7 @@ __device__ __forceinline__ float larger(float m, float v) {
     return a < __int_as_float(0x7f800000) ? fmaxf(m, a) : m;
 }
 // A group's scale: rounded to bf16, so that it costs a 64th of the codes; a value may then
-// be past 448 scales by 2^-9, where it still rounds to 448.
+// be past 448 scales by 2^-8 of that (449.75), where it still rounds to 448.
 __device__ __forceinline__ float kept_scale(float amax) {
     return __bfloat162float(__float2bfloat16_rn(fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f)));
 }

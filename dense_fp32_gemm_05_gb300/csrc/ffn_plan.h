@@ -6,8 +6,8 @@
 
 namespace sgemm_gb300 {
 
-// One product: an M x N result in tiles, summed over nk blocks of 64.  `halves`: the
-// tile's columns are two matrices' (gate and up), so N counts both.
+// One product: an m x n result in tiles, summed over nk blocks of 64.  Of the gated product n
+// counts the columns of both matrices, gate and up, which share its tiles.
 struct FfnShape {
     int64_t m, n, nk;
 };
@@ -44,7 +44,8 @@ struct FfnCut {
 // The cut of a launch of `count` products: the shortest time of that model, a lane's share
 // of the tiles, or the longest tile with what its lane gets beside it.  One product with
 // few tiles may be cut along the sum, over clusters that the GPU holds at once (clusters
-// of 8 whole SMs: 14 of 19); they add the partial sums in 1500 clocks.
+// of 8 whole SMs: 14 of 19, as a GB300 answers; the plan is also asked for without a GPU. One
+// that held fewer would run the rest after them); they add the partial sums in 1500 clocks.
 // `whole_groups`: only tiles with 128 columns of gate and of up.
 inline FfnCut ffn_cut(FfnKind kind, const FfnShape *s, int count, bool whole_groups, bool may_split, int sms) {
     FfnCut best{0, 1, 0};

@@ -30,7 +30,8 @@ namespace sgemm_gb300 {
 namespace q4 {
 
 constexpr int THREADS = 256;
-// Rows of a warp, and CTAs an SM (40 registers a thread).  1537 x 4095 with values and 16384 x 8192
+// Rows of a warp, and CTAs an SM (40 registers a thread; the symmetric kernels spill 44 bytes of
+// theirs).  1537 x 4095 with values and 16384 x 8192
 // bf16, us: 1 row and 8 CTAs 15.7, 128.7; 2 and 6 14.4, 123.9; 2 and 5 16.5, 129.3; 4 and 4 18.5, 139.3.
 constexpr int ROWS = 2;
 constexpr int CTAS = 6;

@@ -593,7 +593,7 @@ int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t ldx, const
  * nonzero: they are added to what is there (in fp32, rounded once), as for a batch in
  * parts.  dg, du and h (T x F bf16, all with leading dimension ldh >= F) are scratch of
  * the call: dg, du and h are rounded to bf16 for the products that read them, which
- * is most of the error of fp32 gradients (2^-9 of each of their terms).
+ * is most of the error of fp32 gradients (up to 2^-8 of each of their terms).
  * relu's derivative at 0 is 0.  With kept codes g and u are code * scale.
  *
  * No atomics: the same result every time.  dy, x, gate, up, down and the scratch start on
