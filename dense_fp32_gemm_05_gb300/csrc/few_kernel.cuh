@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
     };
     if (p.early) fill();                                   // (the kernel before writes no weights)
 
-    // scales and zero codes of a stage: lane l has those of the warp's row l
+    // scales and zero codes of a stage: lane l has those of the warp's row l (by plain loads: the kernel
+    // before may still be writing them when this one starts, so they are no constants of it)
     const int which = p.gated ? lane >> 4 : 0;
     const uint32_t n = (uint32_t)min(row0 + (p.gated ? lane & 15 : lane), p.N - 1);     // (rows past N: any valid one)
     float scale[G ? GROUPS : 1];
@@ -275,8 +276,8 @@ __global__ void __launch_bounds__(THREADS, NT <= 2 ? 2 : 1)
                 const int group = (s_begin + kw + i * p.wk) * GROUPS + g;
                 const uint32_t at = (uint32_t)group * p.lds + n;
                 const bool there = group < p.groups;
-                scale[g] = there ? __ldg(p.s[which] + at) : 0.0f;
-                if (ZEROS) zero[g] = there ? __ldg(p.z[which] + at) : 0u;
+                scale[g] = there ? p.s[which][at] : 0.0f;
+                if (ZEROS) zero[g] = there ? p.z[which][at] : 0u;
             }
         }
     };
