@@ -1276,6 +1276,10 @@ extern "C" int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t
     if (!tma_rows(x, ldx, T) || !tma_rows(gate, ld_in, F) || !tma_rows(up, ld_in, F) || !tma_rows(down, ld_down, D) ||
         !tma_rows(h, ldh, T))
         return SGEMM_ERR_UNSUPPORTED;
+    // (one buffer for two results: tiles that run together would write over each other)
+    if (keep && u == g) return -14;
+    if (keep && codes && su == sg) return -17;
+    if (y == h) return -21;
     Block b{T, D, F};
     b.x = Operand{x, T, D, up8(ldx), false};
     b.gate = Operand{gate, F, D, up8(ld_in), false};
@@ -1344,6 +1348,11 @@ extern "C" int sgemm_ffn_backward(int64_t T, int64_t D, int64_t F, const void *d
     if (!tma_rows(dy, lddy, T) || !tma_rows(x, ldx, T) || !tma_rows(gate, ld_in, F) || !tma_rows(up, ld_in, F) ||
         !tma_rows(down, ld_down, D) || !tma_rows(dg, ldh, T) || !tma_rows(du, ldh, T) || !tma_rows(h, ldh, T))
         return SGEMM_ERR_UNSUPPORTED;
+    // (one buffer for two results, such as two tied weights' gradients, which would both be added to at once)
+    if (du == dg) return -22;
+    if (h == dg || h == du) return -23;
+    if (dup == dgate) return -30;
+    if (ddown == dgate || ddown == dup) return -32;
     Block b{T, D, F};
     b.x = Operand{x, T, D, up8(ldx), false};
     b.gate = Operand{gate, F, D, up8(ld_in), false};

@@ -570,10 +570,10 @@ int sgemm_moe(int64_t T, int64_t D, int64_t F, int64_t E, int64_t topk, const vo
  * x, gate, up, down and h are read by TMA: they start on 16 bytes and their leading
  * dimensions are multiples of 8 (pad rows where D or F is none), else
  * SGEMM_ERR_UNSUPPORTED; g, u, scales and y may lie anywhere.  The outputs may not
- * overlap one another or an input.  Up to 16 tokens of which nothing is kept take D and F
- * to 2^30 - 1024, else SGEMM_ERR_UNSUPPORTED.  T or D zero: nothing is done (D zero with values
- * to keep: SGEMM_ERR_UNSUPPORTED); F zero: y = 0.  No library workspace.  Execution, errors
- * and the bounded waits as sgemm; needs compute capability 10.3.
+ * overlap one another or an input (one address for two of them is refused).  Up to 16 tokens
+ * of which nothing is kept take D and F to 2^30 - 1024, else SGEMM_ERR_UNSUPPORTED.  T or D
+ * zero: nothing is done (D zero with values to keep: SGEMM_ERR_UNSUPPORTED); F zero: y = 0.
+ * No library workspace.  Execution, errors and the bounded waits as sgemm; needs compute capability 10.3.
  */
 int sgemm_ffn(int64_t T, int64_t D, int64_t F, const void *x, int64_t ldx, const void *gate,
               const void *up, int64_t ld_in, const void *down, int64_t ld_down, int activation,
